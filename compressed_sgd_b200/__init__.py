@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Optional, Sequence, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -85,6 +85,14 @@ _SIGNATURES = {
                                                   _i32, _i32, _vp, _vp, _sz, _vp, _vp]),
     "gsparse_combine_local": (ctypes.c_int, [_vp, _vp, _vp, _i64, _f32, _f32, _i32, _vp, _vp, _vp, _i64, _vp,
                                              _vp]),
+    "gsparse_token_logprobs": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+                                              _vp, _i64, _vp, _vp, _vp, _vp]),
+    "gsparse_token_logprobs_backward": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp,
+                                                       _i32, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "gsparse_distill_topk": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _i32, _i32, _i32, _vp, _vp,
+                                            _vp, _i64, _vp, _vp, _vp]),
+    "gsparse_distill_topk_backward": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _i32,
+                                                     _i32, _vp, _vp, _i64, _vp, _vp]),
 }
 
 _lib = None
@@ -455,3 +463,190 @@ def combine_local(G: torch.Tensor, L: torch.Tensor, out: Optional[torch.Tensor] 
                                      _ptr(own_val), _ptr(own_count), own_capacity, _ptr(d_status), _stream(dev))
     _check(st, "gsparse_combine_local")
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# losses over vocabulary rows
+
+MAX_VOCAB = 1 << 24
+MAX_ALTERNATIVES = 256
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]
+    entropy: Optional[torch.Tensor]
+    top_idx: Optional[torch.Tensor]
+    top_logprob: Optional[torch.Tensor]
+    stats: Optional[torch.Tensor]
+    dlogits: Optional[torch.Tensor]
+
+
+class DistillTopk(NamedTuple):
+    loss: torch.Tensor
+    stats: Optional[torch.Tensor]
+    dlogits: Optional[torch.Tensor]
+
+
+def _logits(t: torch.Tensor, name="logits"):
+    """(rows, vocab, row stride, dtype code) of a matrix whose rows are contiguous."""
+    if not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise GsparseError(f"{name} must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
+    return t.shape[0], t.shape[1], t.stride(0), _DTYPES[t.dtype]
+
+
+def _like(t: Optional[torch.Tensor], dtype, shape, device, name):
+    """Checks an argument's type, device and shape; None stays None."""
+    if t is None:
+        return None
+    _dev(t, dtype, name)
+    if t.device != device or tuple(t.shape) != shape:
+        raise GsparseError(f"{name} must have the shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _inverse(temperature: float) -> float:
+    return 1.0 / temperature if temperature else 0.0    # the library refuses 0
+
+
+def _new_dlogits(logits: torch.Tensor) -> torch.Tensor:
+    """A gradient laid out as the logits are: rows start at the same offset from a 16-byte boundary."""
+    rows, vocab = logits.shape
+    stride = logits.stride(0)
+    if stride < vocab or stride > vocab + max(64, vocab // 8):
+        stride = vocab                              # broadcast or far apart rows: a dense gradient
+    first = (logits.data_ptr() % 16) // logits.element_size()
+    if stride == vocab and first == 0:
+        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    flat = torch.empty(first + max(rows, 1) * stride, dtype=logits.dtype, device=logits.device)
+    return flat.as_strided((rows, vocab), (stride, 1), first)
+
+
+def _grad_out(dlogits: Optional[torch.Tensor], logits: torch.Tensor) -> torch.Tensor:
+    if dlogits is None:
+        return _new_dlogits(logits)
+    _logits(dlogits, "dlogits")
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.device != logits.device:
+        raise GsparseError("dlogits must have the type, shape and device of logits")
+    return dlogits
+
+
+def _on_device(device, name, *args):
+    """Calls the entry point with the tensors' device current, on that device's current stream."""
+    fn = getattr(_lib or lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != 0:
+        _check(st, name)
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, top_k: int = 0,
+                   want_entropy: bool = False, want_stats: bool = False, temperature: float = 1.0,
+                   want_grad: bool = False, grad_logprob: Optional[torch.Tensor] = None,
+                   grad_entropy: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                   d_status: Optional[torch.Tensor] = None) -> TokenLogprobs:
+    """Log probabilities of `targets` (int32[rows], -1: none) under softmax(logits / temperature) of
+    each row, the rows' entropy, and their top_k most likely tokens (largest first, ties to the lower
+    index). `want_stats`: the row statistics that token_logprobs_backward takes. `want_grad` (or a
+    `dlogits` to write to, which may be the logits): also the gradient of sum(grad_logprob * logprob)
+    + sum(grad_entropy * entropy) by the logits, laid out as the logits are."""
+    rows, vocab, stride, dt = _logits(logits)
+    dev = logits.device
+    p_t = _like(targets, torch.int32, (rows,), dev, "targets")
+    p_g = _like(grad_logprob, torch.float32, (rows,), dev, "grad_logprob")
+    p_h = _like(grad_entropy, torch.float32, (rows,), dev, "grad_entropy")
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    logprob = entropy = stats = top_idx = top_logprob = None
+    if targets is not None:
+        logprob = torch.empty(rows, dtype=torch.float32, device=dev)
+    if want_entropy:
+        entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    if want_stats:
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    if top_k > 0:
+        top_idx = torch.empty((rows, top_k), dtype=torch.int32, device=dev)
+        top_logprob = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+    if want_grad or dlogits is not None:
+        dlogits = _grad_out(dlogits, logits)
+    _on_device(dev, "gsparse_token_logprobs", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature), p_t,
+               _ptr(logprob), _ptr(entropy), _ptr(stats), top_k, _ptr(top_idx), _ptr(top_logprob), _ptr(dlogits),
+               0 if dlogits is None else dlogits.stride(0), p_g, p_h, p_s)
+    return TokenLogprobs(logprob, entropy, top_idx, top_logprob, stats, dlogits)
+
+
+def token_logprobs_backward(logits: torch.Tensor, stats: torch.Tensor, targets: Optional[torch.Tensor] = None,
+                            grad_logprob: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                            grad_entropy: Optional[torch.Tensor] = None, top_idx: Optional[torch.Tensor] = None,
+                            grad_top: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                            dlogits: Optional[torch.Tensor] = None,
+                            d_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient by the logits from the saved stats (and entropy, with grad_entropy) of
+    token_logprobs at the same temperature; grad_top is that of top_logprob at top_idx."""
+    rows, vocab, stride, dt = _logits(logits)
+    dev = logits.device
+    if (top_idx is None) != (grad_top is None):
+        raise GsparseError("top_idx and grad_top come together")
+    top_k = 0 if top_idx is None else top_idx.shape[-1]
+    p = (_like(stats, torch.float32, (rows, 2), dev, "stats"), _like(targets, torch.int32, (rows,), dev, "targets"),
+         _like(grad_logprob, torch.float32, (rows,), dev, "grad_logprob"),
+         _like(entropy, torch.float32, (rows,), dev, "entropy"),
+         _like(grad_entropy, torch.float32, (rows,), dev, "grad_entropy"), top_k,
+         _like(top_idx, torch.int32, (rows, top_k), dev, "top_idx"),
+         _like(grad_top, torch.float32, (rows, top_k), dev, "grad_top"))
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    dlogits = _grad_out(dlogits, logits)
+    _on_device(dev, "gsparse_token_logprobs_backward", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature),
+               *p, dlogits.data_ptr(), dlogits.stride(0), p_s)
+    return dlogits
+
+
+def _teacher(teacher_idx, teacher_val, rows, dev):
+    if teacher_idx.dim() != 2 or teacher_val.dtype not in _DTYPES:
+        raise GsparseError("teacher_idx must be a matrix, teacher_val fp32, bf16 or fp16")
+    k = teacher_idx.shape[1]
+    return (_like(teacher_idx, torch.int32, (rows, k), dev, "teacher_idx"),
+            _like(teacher_val, teacher_val.dtype, (rows, k), dev, "teacher_val"), _DTYPES[teacher_val.dtype], k)
+
+
+def distill_topk(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_val: torch.Tensor, tail: bool = False,
+                 temperature: float = 1.0, grad_loss: Optional[torch.Tensor] = None, want_grad: bool = False,
+                 want_stats: bool = False, dlogits: Optional[torch.Tensor] = None,
+                 d_status: Optional[torch.Tensor] = None) -> DistillTopk:
+    """Loss of each row against a teacher's list of tokens (teacher_idx int32[rows, k], -1: absent):
+    the divergence from the list's softmax at that temperature, or with `tail` from the list's log
+    probabilities with the mass the list leaves as one more class. `want_grad` (or a `dlogits` to
+    write to, which may be the logits): also the gradient of sum(grad_loss * loss)."""
+    rows, vocab, stride, dt = _logits(logits)
+    dev = logits.device
+    lists = _teacher(teacher_idx, teacher_val, rows, dev)
+    p_g = _like(grad_loss, torch.float32, (rows,), dev, "grad_loss")
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 4 if tail else 2), dtype=torch.float32, device=dev) if want_stats else None
+    if want_grad or dlogits is not None:
+        dlogits = _grad_out(dlogits, logits)
+    _on_device(dev, "gsparse_distill_topk", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature), *lists,
+               int(tail), loss.data_ptr(), _ptr(stats), _ptr(dlogits), 0 if dlogits is None else dlogits.stride(0), p_g,
+               p_s)
+    return DistillTopk(loss, stats, dlogits)
+
+
+def distill_topk_backward(logits: torch.Tensor, stats: torch.Tensor, teacher_idx: torch.Tensor,
+                          teacher_val: torch.Tensor, grad_loss: torch.Tensor, tail: bool = False,
+                          temperature: float = 1.0, dlogits: Optional[torch.Tensor] = None,
+                          d_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of sum(grad_loss * loss) by the logits from the saved stats of distill_topk with
+    the same list, `tail` and temperature."""
+    rows, vocab, stride, dt = _logits(logits)
+    dev = logits.device
+    p_st = _like(stats, torch.float32, (rows, 4 if tail else 2), dev, "stats")
+    lists = _teacher(teacher_idx, teacher_val, rows, dev)
+    p_g = _like(grad_loss, torch.float32, (rows,), dev, "grad_loss")
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    dlogits = _grad_out(dlogits, logits)
+    _on_device(dev, "gsparse_distill_topk_backward", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature),
+               p_st, *lists, int(tail), p_g, dlogits.data_ptr(), dlogits.stride(0), p_s)
+    return dlogits

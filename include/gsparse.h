@@ -402,6 +402,102 @@ int gsparse_combine_local(const float* G, const float* L, float* out, int64_t n,
                           const int64_t* d_own_count, int64_t own_capacity, int32_t* d_status,
                           gsparse_stream stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Losses over vocabulary rows  (no counterpart in the pages: these calls make the gradient of an
+ * output layer over a vocabulary, which the calls above compress, and the (index, value) lists a
+ * teacher sends)
+ *
+ * logits       [rows] rows of `vocab` entries of type dtype, entry v of row r at logits[r * row_stride
+ *              + v]; any row_stride >= 0 (0: every row the same) and any alignment of the element.
+ *              What stands between the rows is neither read nor written.
+ * z_v = x_v * inv_temperature, p = softmax(z); -inf entries have p = 0. A row with nothing but -inf
+ * has no distribution: its log probabilities are -inf, its entropy and gradient 0. A row that holds
+ * NaN or +inf gives NaN.
+ * dlogits      gradient of the logits, same type and shape, entry v of row r at dlogits[r *
+ *              dlogits_stride + v] (dlogits_stride >= vocab); may be logits itself with the same
+ *              stride, must not overlap it otherwise. Rows of logits and dlogits that start at the
+ *              same offset from a 16-byte boundary are fastest. A row whose incoming gradients are
+ *              all zero gets zeros, whatever its logits hold.
+ * Arithmetic: the exponential of fp32 differences and sums in fp32 within a thread, joined in fp64
+ * in a fixed order: the same call on the same layout gives the same bits on every run, within a few
+ * fp32 roundings of the formula (a gradient in 16 bits is rounded once). 1 <= vocab <= GSPARSE_MAX_VOCAB, 0 <= rows <
+ * 2^28. These calls need no workspace.
+ */
+enum gsparse_dtype { GSPARSE_F32 = 0, GSPARSE_BF16 = 1, GSPARSE_F16 = 2 };
+
+#define GSPARSE_MAX_VOCAB (1 << 24)
+#define GSPARSE_MAX_ALTERNATIVES 256
+
+/* Log probabilities of given tokens, entropy, most likely tokens; optionally the gradient.
+ * targets      int32[rows] or NULL: the token of each row, -1 for none (its logprob is 0 and its
+ *              grad_logprob is ignored). Others outside [0, vocab) raise GSPARSE_DERR_INDEX_RANGE and
+ *              count as -1.
+ * logprob      fp32[rows] or NULL: log p of the token.
+ * entropy      fp32[rows] or NULL: -sum_v p_v log p_v.
+ * stats        fp32[rows][2] or NULL, for the backward call: the row's largest logit x (before the
+ *              temperature; the lowest fp32 value for a row with nothing but -inf) and the sum of
+ *              exp(z - its z).
+ * top_k        0 <= top_k <= min(vocab, GSPARSE_MAX_ALTERNATIVES): the top_k largest entries of each
+ *              row, largest first, ties to the lower index (-0 ties with +0, NaN ranks above +inf);
+ *              top_idx int32[rows][top_k], top_logprob fp32[rows][top_k]. -inf entries are never
+ *              among them: places left over hold -1 and -inf.
+ * dlogits      NULL, or with grad_logprob g and grad_entropy h (fp32[rows], either may be NULL = 0):
+ *              inv_temperature * (g (1[v = target] - p_v) - h p_v (log p_v + entropy)).
+ */
+int gsparse_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                           int64_t row_stride, float inv_temperature, const int32_t* targets,
+                           float* logprob, float* entropy, float* stats, int32_t top_k,
+                           int32_t* top_idx, float* top_logprob, void* dlogits,
+                           int64_t dlogits_stride, const float* grad_logprob,
+                           const float* grad_entropy, int32_t* d_status, gsparse_stream stream);
+
+/* The gradient from the saved stats (and entropy, where grad_entropy is given), when the incoming
+ * gradients are known only after the log probabilities. grad_top fp32[rows][top_k] is the gradient
+ * of top_logprob at top_idx (as returned; -1 places are ignored, an index may stand there more than
+ * once): each adds inv_temperature * grad_top_j (1[v = top_idx_j] - p_v). */
+int gsparse_token_logprobs_backward(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                    int64_t row_stride, float inv_temperature, const float* stats,
+                                    const int32_t* targets, const float* grad_logprob,
+                                    const float* entropy, const float* grad_entropy, int32_t top_k,
+                                    const int32_t* top_idx, const float* grad_top, void* dlogits,
+                                    int64_t dlogits_stride, int32_t* d_status,
+                                    gsparse_stream stream);
+
+/* Distillation from a teacher's most likely tokens: the loss of each row against the teacher's list
+ * (teacher_idx int32[rows][k], teacher_val [rows][k] of type val_dtype; index -1: absent; others
+ * outside [0, vocab) raise GSPARSE_DERR_INDEX_RANGE and count as absent; any order; an index given
+ * twice counts as two entries), 1 <= k <= GSPARSE_MAX_ALTERNATIVES.
+ *
+ * mode GSPARSE_DISTILL_RENORM: q = softmax(teacher_val * inv_temperature) over the list (logits or
+ *   log probabilities); loss = sum_j q_j (log q_j - log p_{i_j}).
+ * mode GSPARSE_DISTILL_TAIL: teacher_val are log probabilities at that temperature, q_j =
+ *   exp(teacher_val_j), and the mass the list leaves, rho = max(0, 1 - sum q), is one more class
+ *   against R = the sum of p outside the list: loss = sum_j q_j (log q_j - log p_{i_j}) + rho (log
+ *   rho - log R). Where no entry outside the list has p > 0 the rho term is dropped.
+ * Entries with q = 0 add nothing; an empty list has loss 0 and gradient 0. Both are the
+ * Kullback-Leibler divergence from the teacher, in nats, not multiplied by the temperature.
+ *
+ * loss     fp32[rows].
+ * stats    fp32[rows][2], with the tail [rows][4], or NULL: as in gsparse_token_logprobs; the tail's
+ *          other two are the same for the entries outside the list.
+ * dlogits  NULL, or with grad_loss fp32[rows]: grad_loss * d loss / d logits.
+ */
+enum gsparse_distill_mode { GSPARSE_DISTILL_RENORM = 0, GSPARSE_DISTILL_TAIL = 1 };
+
+int gsparse_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t row_stride, float inv_temperature, const int32_t* teacher_idx,
+                         const void* teacher_val, int32_t val_dtype, int32_t k, int32_t mode,
+                         float* loss, float* stats, void* dlogits, int64_t dlogits_stride,
+                         const float* grad_loss, int32_t* d_status, gsparse_stream stream);
+
+/* The gradient from the saved stats (of the same mode). */
+int gsparse_distill_topk_backward(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                  int64_t row_stride, float inv_temperature, const float* stats,
+                                  const int32_t* teacher_idx, const void* teacher_val,
+                                  int32_t val_dtype, int32_t k, int32_t mode,
+                                  const float* grad_loss, void* dlogits, int64_t dlogits_stride,
+                                  int32_t* d_status, gsparse_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

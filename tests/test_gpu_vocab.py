@@ -1,0 +1,568 @@
+"""Losses over vocabulary rows on the GPU against their formulas in 64 bits (oracle/vocab.py), at the
+sizes, types, masks, layouts and lists where a row kernel can go wrong.
+
+Tolerances count roundings, u = 2^-24 (half a step of fp32):
+ - an exponential 2^q, q = (x - M) c: the hardware's 2^q is within 4 u (its documented 2^-22), and q carries
+   the roundings of c and of the product, 2 |q| u, in the exponent: ln2 * 2 |q| u relative. The entries that
+   carry a softmax's weight have sum p |q| <= log2 V + entropy <= 2 log2 V.
+ - a thread adds at most n = max(64, V / 512) entries in fp32: n u.
+ So log S, and with it a log probability, is within LSE(V) = (4 + 2 * 2 log2 V + n) u, plus u |result| for the
+ result's own rounding; the entropy log S - T / S within LSE (2 + ln V) as T weighs the same errors by |q|.
+ - a gradient p (A + B log p) + a: p is off by the exponential's error at its own q' = log2 p and by log S's,
+   P(p) = (4 + 3 |log2 p| + 4 log2 V) u + LSE (the exponent is the sum of three rounded terms), the products
+   and the bracket by 4 u each, a by 2 u; it is rounded once to its type (half a step, eps / 2, and where that
+   type's smallest steps begin half of one).
+ - a loss is summed in 64 bits: LSE (mass of q + rest <= 2) + u |loss|."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import compressed_sgd_b200 as gs
+from oracle import vocab
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+TINY = {"fp32": 2.0 ** -126, "bf16": 2.0 ** -126, "fp16": 2.0 ** -25}   # fp32 results below 2^-126 may be flushed
+
+
+def lse_tol(V):
+    return (4 + 4 * math.log2(V + 1) + max(64, V / 512)) * U
+
+
+def close(got, want, tol, what):
+    got = got.detach().float().cpu().numpy().astype(np.float64) if torch.is_tensor(got) else got
+    assert got.shape == want.shape, what
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan), what
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf]) and not np.isinf(got[~inf]).any(), what
+    fine = ~nan & ~inf
+    off = np.abs(got - want)[fine] - np.broadcast_to(tol, want.shape)[fine]
+    assert off.size == 0 or off.max() <= 0, (what, off.max(), np.abs(got - want)[fine].max())
+
+
+def grad_tol(x, it, want, dtype, A, B, extra):
+    """A, B, extra: sizes of the bracket's parts and of the added entries, by row, already with it."""
+    V = x.shape[1]
+    lp = vocab.log_softmax(x, it)
+    p = np.where(np.isfinite(lp), np.exp(lp), 0.0)
+    l2 = np.where(np.isfinite(lp), np.abs(lp) / math.log(2), 0.0)
+    rel = (4 + 3 * l2 + 4 * math.log2(V + 1)) * U + lse_tol(V)
+    size = np.abs(A)[:, None] + np.abs(B)[:, None] * (l2 * math.log(2))
+    # the bracket itself: the entropy and log p carry LSE's error into it
+    body = p * (size * (rel + 8 * U) + np.abs(B)[:, None] * (rel + lse_tol(V) * (2 + math.log(V + 1))))
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    body = body + 2 * U * np.abs(extra)[:, None] * (want != 0)
+    return body + half * (np.abs(want) + body) + TINY[dtype]
+
+
+def make(rows, V, dtype, seed=0, scale=3.0, stride=None, first=0):
+    """Logits with rows `stride` apart, the first `first` elements into a buffer whose other elements are NaN."""
+    rng = np.random.default_rng([seed, rows, V])
+    x = torch.from_numpy(rng.normal(size=(rows, V)).astype(np.float32) * scale).to(TYPES[dtype])
+    stride = V if stride is None else stride
+    buf = torch.full((first + max(rows, 1) * stride + 16,), float("nan"), dtype=TYPES[dtype], device="cuda")
+    view = buf.as_strided((rows, V), (stride, 1), first)
+    view.copy_(x)
+    return view, buf
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def dev(a, dtype=torch.float32):
+    return torch.as_tensor(np.asarray(a)).to(dtype).cuda()
+
+
+def weights(rows, seed=1):
+    rng = np.random.default_rng([seed, rows])
+    w = rng.normal(size=(2, rows)).astype(np.float32)
+    w[:, 3::7] = 0.0
+    return w
+
+
+def check_tokens(x, dtype, temperature=1.0, targets=None, top_k=0, grad=True, dlogits=None):
+    rows, V = x.shape
+    it = float(np.float32(1.0 / temperature))
+    h = f64(x)
+    if targets is None:
+        targets = np.random.default_rng([5, rows, V]).integers(-1, V, size=rows)
+    t = dev(targets, torch.int32)
+    w = weights(rows)
+    g, e = dev(w[0]), dev(w[1])
+    st = gs.status_tensor()
+    r = gs.token_logprobs(x, t, top_k=top_k, want_entropy=True, want_stats=True, temperature=temperature, want_grad=grad,
+                          grad_logprob=g if grad else None, grad_entropy=e if grad else None, dlogits=dlogits, d_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    lp, ent, idx, val = vocab.token_logprobs(h, it, targets, top_k)
+    tol = lse_tol(V)
+    close(r.logprob, lp, tol + 4 * U * np.abs(np.where(np.isfinite(lp), lp, 0)), "logprob")
+    close(r.entropy, ent, tol * (2 + math.log(V + 1)) + U * np.abs(np.nan_to_num(ent)), "entropy")
+    if top_k:
+        assert np.array_equal(r.top_idx.cpu().numpy(), idx)
+        close(r.top_logprob, val, tol + 4 * U * np.abs(np.where(np.isfinite(val), val, 0)), "top_logprob")
+    if grad:
+        want = vocab.token_logprobs_grad(h, it, targets, w[0].astype(np.float64), w[1].astype(np.float64))
+        want[(np.where(targets < 0, 0, w[0]) == 0) & (w[1] == 0)] = 0.0
+        ent0 = np.nan_to_num(ent)
+        tolg = grad_tol(h, it, want, dtype, it * (np.abs(w[0]) + np.abs(w[1]) * ent0), it * w[1], it * w[0])
+        close(r.dlogits, want, tolg, "dlogits")
+    return r
+
+
+SIZES = [(1, 1), (3, 2), (2, 3), (5, 7), (2, 8), (3, 9), (2, 31), (1, 64), (4, 65), (2, 255), (3, 1000), (2, 1001),
+         (2, 4099), (1, 16385), (2, 50021)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,V", SIZES)
+def test_tokens_sizes(rows, V, dtype):
+    x, _ = make(rows, V, dtype)
+    check_tokens(x, dtype, top_k=min(V, 5))
+
+
+@pytest.mark.parametrize("rows", [0, 1, 37, 150, 700])
+def test_tokens_rows(rows):
+    x, _ = make(rows, 4200, "bf16")
+    check_tokens(x, "bf16", top_k=3) if rows else gs.token_logprobs(x, dev(np.zeros(0), torch.int32), top_k=3)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("stride,first", [(1003, 0), (1003, 3), (1040, 5), (1004, 1)])
+def test_tokens_layouts_and_what_stands_between_rows(stride, first, dtype):
+    V = 1003
+    x, buf = make(5, V, dtype, stride=stride, first=first)
+    before = buf.clone()
+    check_tokens(x, dtype, top_k=4)
+    assert torch.equal(torch.nan_to_num(buf.float(), 7.0), torch.nan_to_num(before.float(), 7.0))
+    # a gradient laid out in another way, and one in the logits' place
+    other, obuf = make(5, V, dtype, stride=1050, first=2)
+    outside = torch.ones(obuf.numel(), dtype=torch.bool, device="cuda")
+    outside.as_strided((5, V), (1050, 1), 2).fill_(False)
+    check_tokens(x, dtype, dlogits=other)
+    assert bool(torch.isnan(obuf[outside]).all())
+    w = weights(5)
+    t = dev([0, V - 1, 500, -1, 7], torch.int32)
+    kw = dict(grad_logprob=dev(w[0]), grad_entropy=dev(w[1]))
+    want = gs.token_logprobs(x, t, top_k=4, want_grad=True, **kw)
+    got = gs.token_logprobs(x, t, top_k=4, dlogits=x, **kw)
+    assert got.dlogits.data_ptr() == x.data_ptr() and torch.equal(got.dlogits, want.dlogits)
+    assert torch.equal(got.top_idx, want.top_idx) and torch.equal(got.logprob, want.logprob)
+
+
+def test_tokens_of_one_row_for_all():
+    x, _ = make(1, 777, "bf16")
+    # (rows that start at other offsets from 16 bytes add in another order: compared by the tolerance)
+    r = check_tokens(x.expand(6, 777), "bf16", targets=np.array([0, 5, 776, -1, 8, 9]), top_k=3)
+    assert bool((r.top_idx == r.top_idx[0]).all()) and r.dlogits.stride(0) == 777
+
+
+@pytest.mark.parametrize("temperature", [0.25, 1.25, 3.0])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_tokens_temperature(dtype, temperature):
+    x, _ = make(4, 2003, dtype, scale=2.0)
+    check_tokens(x, dtype, temperature=temperature, top_k=9)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_tokens_masks(dtype):
+    V = 1200
+    x, _ = make(9, V, dtype)
+    low = torch.finfo(TYPES[dtype]).min
+    x[0] = float("-inf")                                  # nothing left
+    x[1, :] = float("-inf"); x[1, 700] = 2.0              # one token left
+    x[2, 1:] = float("-inf")
+    x[3, torch.arange(V) % 2 == 0] = float("-inf")
+    x[4, 5:] = low                                        # the type's lowest value as a mask
+    x[5] = low                                            # all of it: a uniform row
+    x[6, 3] = float("nan")
+    x[7, 1100] = float("inf")
+    x[8, :40] = float("-inf")
+    check_tokens(x, dtype, targets=np.array([3, 700, 1, 4, 2, 9, 8, 8, 39]), top_k=7)
+    check_tokens(x, dtype, targets=np.array([-1, 5, 0, -1, 6, 1199, -1, 1100, 41]), top_k=128, grad=False)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,V", [(2, 9000), (1, 40000), (300, 2100)])
+@pytest.mark.parametrize("k", [1, 20, 256])
+def test_alternatives_with_ties(rows, V, k, dtype):
+    rng = np.random.default_rng(3)
+    a = rng.integers(0, 6, size=(rows, V)).astype(np.float32)     # many equal entries
+    a[0] = 1.5                                                    # one value
+    if rows > 1:
+        a[1] = np.where(np.arange(V) % 512 == 7, 100.0 + np.arange(V) / V, 0.0)   # large entries in step
+    if rows > 2:
+        a[2] = -np.arange(V) / 64.0                               # large entries side by side
+        a[3] = np.where(np.arange(V) < V - 300, 0.0, -0.0)
+    x = torch.from_numpy(a).to(TYPES[dtype]).cuda()
+    r = gs.token_logprobs(x, top_k=k)
+    want = np.argsort(-f64(x), axis=1, kind="stable")[:, :k]
+    assert np.array_equal(r.top_idx.cpu().numpy(), want)
+    lp = vocab.log_softmax(f64(x), 1.0)
+    val = np.take_along_axis(lp, want, 1)
+    close(r.top_logprob, val, lse_tol(V) + 4 * U * np.abs(val), "top_logprob")
+    assert r.logprob is None and r.entropy is None and r.dlogits is None
+
+
+def test_alternatives_few_left_and_many_asked():
+    V = 30000
+    x = torch.full((3, V), float("-inf"), device="cuda")
+    x[0, [5, 29999, 17]] = torch.tensor([1.0, 2.0, 1.0], device="cuda")
+    x[1, 100:100 + 2000] = 0.25
+    x[2, ::3] = torch.arange(10000, device="cuda").float()
+    r = gs.token_logprobs(x, top_k=200)
+    want = vocab.token_logprobs(f64(x), 1.0, None, 200)
+    assert np.array_equal(r.top_idx.cpu().numpy(), want[2])
+    close(r.top_logprob, want[3], lse_tol(V) + 4 * U * np.abs(np.nan_to_num(want[3], neginf=0.0)), "top_logprob")
+
+
+def test_tokens_outside_the_vocabulary_are_reported_and_left_out():
+    x, _ = make(4, 100, "fp32")
+    for bad in ([100, 1, 2, 3], [0, -2, 2, 3], [0, 1, 2, 2 ** 31 - 1]):
+        st = gs.status_tensor()
+        ok = [t if 0 <= t < 100 else -1 for t in bad]
+        g = dev(np.ones(4))
+        a = gs.token_logprobs(x, dev(bad, torch.int64).to(torch.int32), want_grad=True, grad_logprob=g, d_status=st)
+        b = gs.token_logprobs(x, dev(ok, torch.int32), want_grad=True, grad_logprob=g)
+        assert int(st.item()) == gs.DERR_INDEX_RANGE
+        assert torch.equal(a.logprob, b.logprob) and torch.equal(a.dlogits, b.dlogits)
+
+
+def test_zero_weights_give_zeros_whatever_the_row_holds():
+    x, _ = make(3, 500, "bf16")
+    x[1] = float("nan")
+    r = gs.token_logprobs(x, dev([1, 2, 3], torch.int32), want_grad=True, grad_logprob=dev([1.0, 0.0, 1.0]))
+    assert bool((r.dlogits[1] == 0).all()) and bool(torch.isnan(r.logprob[1])) and bool((r.dlogits[0] != 0).any())
+    r = gs.token_logprobs(x, dev([1, 2, 3], torch.int32), want_grad=True)
+    assert bool((r.dlogits == 0).all())
+
+
+def test_same_bits_every_time():
+    x, _ = make(5, 60001, "bf16", scale=1.0)
+    idx = torch.randint(0, 60001, (5, 100), device="cuda", dtype=torch.int32)
+    val = torch.randn(5, 100, device="cuda")
+    a = gs.token_logprobs(x, idx[:, 0].contiguous(), top_k=100, want_entropy=True, want_grad=True,
+                          grad_logprob=val[:, 0].contiguous())
+    d = gs.distill_topk(x, idx, val - 6, tail=True, want_grad=True, grad_loss=val[:, 0].contiguous())
+    for _ in range(3):
+        b = gs.token_logprobs(x, idx[:, 0].contiguous(), top_k=100, want_entropy=True, want_grad=True,
+                              grad_logprob=val[:, 0].contiguous())
+        e = gs.distill_topk(x, idx, val - 6, tail=True, want_grad=True, grad_loss=val[:, 0].contiguous())
+        for u, v in zip([a.logprob, a.entropy, a.top_idx, a.top_logprob, a.dlogits, d.loss, d.dlogits],
+                        [b.logprob, b.entropy, b.top_idx, b.top_logprob, b.dlogits, e.loss, e.dlogits]):
+            assert torch.equal(u, v)
+
+
+# ---- backward pass of its own ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,V,k", [(1, 1, 1), (3, 9, 4), (4, 1000, 0), (3, 4099, 20), (2, 50021, 256), (400, 2100, 3)])
+def test_tokens_backward(rows, V, k, dtype):
+    x, _ = make(rows, V, dtype, stride=V + 3, first=2)
+    if rows > 2:
+        x[2, : V // 2] = float("-inf")
+    h = f64(x)
+    it = float(np.float32(1 / 1.25))
+    rng = np.random.default_rng([9, rows, V])
+    t = rng.integers(-1, V, size=rows)
+    w = weights(rows)
+    r = gs.token_logprobs(x, dev(t, torch.int32), top_k=k, want_entropy=True, want_stats=True, temperature=1.25)
+    gt = rng.normal(size=(rows, k)).astype(np.float32)
+    gt[3::7] = 0.0
+    got = gs.token_logprobs_backward(x, r.stats, dev(t, torch.int32), dev(w[0]), r.entropy, dev(w[1]),
+                                     r.top_idx, dev(gt) if k else None, temperature=1.25)
+    want = vocab.token_logprobs_grad(h, it, t, w[0].astype(np.float64), w[1].astype(np.float64),
+                                     r.top_idx.cpu().numpy() if k else None, gt.astype(np.float64) if k else None)
+    ent = vocab.token_logprobs(h, it)[1]
+    extra = np.abs(w[0]) + np.abs(gt).sum(1)
+    tol = grad_tol(h, it, want, dtype, it * (extra + np.abs(w[1]) * ent), it * w[1], it * extra)
+    close(got, want, tol, "dlogits")
+    # in the logits' place
+    if k:
+        again = gs.token_logprobs_backward(x, r.stats, dev(t, torch.int32), dev(w[0]), r.entropy, dev(w[1]), r.top_idx,
+                                           dev(gt), temperature=1.25, dlogits=x)
+        assert torch.equal(again, got)
+
+
+def test_alternatives_whose_gradients_cancel():
+    x, _ = make(1, 50, "fp32")
+    s = gs.token_logprobs(x, top_k=2, want_stats=True)
+    g = gs.token_logprobs_backward(x, s.stats, top_idx=s.top_idx, grad_top=dev([[0.5, -0.5]]))
+    i = s.top_idx.cpu().numpy()[0]
+    want = np.zeros(50)
+    want[i] = [0.5, -0.5]
+    assert np.array_equal(f64(g)[0], want)
+    twice = gs.token_logprobs_backward(x, s.stats, targets=s.top_idx[:, 0].contiguous(), grad_logprob=dev([1.0]),
+                                       top_idx=s.top_idx[:, :1].repeat(1, 3), grad_top=dev([[0.25, 0.5, 0.25]]))
+    once = gs.token_logprobs_backward(x, s.stats, targets=s.top_idx[:, 0].contiguous(), grad_logprob=dev([2.0]))
+    assert torch.equal(twice, once)
+
+
+# ---- distillation -----------------------------------------------------------------------------------
+
+def lists(x, k, it, tail, seed=0, ragged=True):
+    rows, V = x.shape
+    rng = np.random.default_rng([seed, rows, V, k])
+    y = f64(x) + rng.normal(size=x.shape) * 0.7
+    lp = vocab.log_softmax(np.where(np.isfinite(y), y, -50.0), it)
+    idx = np.argsort(-lp, axis=1, kind="stable")[:, :k].astype(np.int32)
+    if idx.shape[1] < k:                                  # more places than tokens
+        idx = np.concatenate([idx, np.full((rows, k - idx.shape[1]), -1, np.int32)], 1)
+    val = np.take_along_axis(lp, np.maximum(idx, 0), 1).astype(np.float32)
+    if ragged:
+        idx[:, k // 2:][rng.random((rows, k - k // 2)) < 0.3] = -1
+        if rows > 2:
+            idx[1] = -1
+    for r in range(rows):
+        p = rng.permutation(k)
+        idx[r], val[r] = idx[r, p], val[r, p]
+    return idx, val
+
+
+def check_distill(x, dtype, idx, val, tail, temperature=1.0, val_dtype="fp32", w=None):
+    rows, V = x.shape
+    it = float(np.float32(1.0 / temperature))
+    h = f64(x)
+    tv = torch.from_numpy(val).to(TYPES[val_dtype]).cuda()
+    ti = dev(idx, torch.int32)
+    w = weights(rows)[0] if w is None else w
+    st = gs.status_tensor()
+    r = gs.distill_topk(x, ti, tv, tail=tail, temperature=temperature, grad_loss=dev(w), want_grad=True, want_stats=True,
+                        d_status=st)
+    assert int(st.item()) == 0
+    v64 = f64(tv)
+    want = vocab.distill(h, it, idx, v64, tail)
+    close(r.loss, want, 2 * lse_tol(V) + 2 * U * np.abs(np.where(np.isfinite(want), want, 0)), "loss")
+    grad = vocab.distill_grad(h, it, idx, v64, tail, w.astype(np.float64))
+    grad[w == 0] = 0.0
+    q = vocab.teacher(idx, v64, it, tail)[1].sum(1)
+    size = it * np.abs(w) * np.maximum(q, 1.0)
+    # with the tail, an entry outside the list has (mass + rest) p - rest p / R: two terms of p's accuracy
+    tol = grad_tol(h, it, grad, dtype, size, 0 * size, size)
+    if tail:
+        lp = vocab.log_softmax(h, it)
+        for row in range(rows):
+            lr = vocab._log_rest(lp[row], idx[row]) if np.isfinite(lp[row]).any() else -np.inf
+            if np.isfinite(lr):
+                l2 = np.abs(np.where(np.isfinite(lp[row]), lp[row] - lr, 0)) / math.log(2)
+                pt = np.exp(np.where(np.isfinite(lp[row]), lp[row] - lr, -np.inf))
+                tol[row] += 2 * size[row] * pt * ((8 + 3 * l2 + 4 * math.log2(V + 1)) * U + lse_tol(V)) * max(0.0, 1 - q[row])
+    close(r.dlogits, grad, tol, "dlogits")
+    back = gs.distill_topk_backward(x, r.stats, ti, tv, dev(w), tail=tail, temperature=temperature)
+    # the statistics were rounded to fp32 on the way: the tolerance has room for it (LSE holds 64 u)
+    close(back, grad, tol, "backward")
+    plain = gs.distill_topk(x, ti, tv, tail=tail, temperature=temperature)
+    assert torch.equal(plain.loss, r.loss) or bool(torch.isnan(r.loss).any())
+    return r
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,V,k", [(1, 1, 1), (3, 2, 2), (3, 9, 4), (4, 65, 13), (5, 1000, 8), (3, 1001, 64),
+                                      (3, 4099, 32), (2, 50021, 256), (1, 40000, 100), (350, 2100, 5), (3, 5, 9)])
+def test_distill_sizes(rows, V, k, dtype, tail):
+    x, _ = make(rows, V, dtype, stride=V + 5, first=3)
+    idx, val = lists(x, k, 1.0, tail)
+    check_distill(x, dtype, idx, val, tail)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("temperature,val_dtype", [(0.5, "fp32"), (2.0, "bf16"), (1.25, "fp16"), (4.0, "fp32")])
+def test_distill_temperature_and_value_types(temperature, val_dtype, tail):
+    x, _ = make(4, 3001, "bf16")
+    idx, val = lists(x, 24, float(np.float32(1 / temperature)), tail)
+    check_distill(x, "bf16", idx, val, tail, temperature, val_dtype)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_a_confident_student(tail):
+    # the list holds all but 1e-9 of the student's mass: what it leaves must not be a difference of sums
+    V = 3000
+    x = torch.zeros(4, V, device="cuda")
+    x[:, 7] = 30.0
+    x[1, 8] = 29.0
+    x[2, 9] = 80.0
+    x[3, 7] = 200.0
+    idx = np.array([[7, 8], [8, 7], [9, 7], [7, 3]], np.int32)
+    val = np.log(np.array([[0.9, 0.05], [0.3, 0.6], [0.5, 0.25], [0.99, 0.001]])).astype(np.float32)
+    check_distill(x, "fp32", idx, val, tail, w=np.ones(4, np.float32))
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_distill_masks_and_lists(dtype, tail):
+    V = 1100
+    x, _ = make(10, V, dtype)
+    idx = np.tile(np.array([[3, 900, 14, 15]], np.int32), (10, 1))
+    val = np.tile(np.log(np.array([[0.4, 0.3, 0.1, 0.05]], np.float32)), (10, 1))
+    x[0] = float("-inf")                                  # nothing left, and a list: no probability for it
+    x[1] = float("-inf"); idx[1] = -1                     # nothing left and nothing wanted
+    x[2, [i for i in range(V) if i not in (3, 900, 14, 15)]] = float("-inf")   # the list is all there is
+    x[3, 900] = float("-inf")                             # a wanted token is ruled out
+    val[4, 1] = -np.inf                                   # an entry without mass on a token ruled out
+    x[4, 900] = float("-inf")
+    val[5] = -np.inf                                      # no mass in the list at all
+    idx[6] = [3, 3, 14, 3]                                # an index several times
+    idx[7] = [-1, -1, 5, -1]
+    val[8] += 0.3                                         # with the tail: more mass than one
+    x[9, 40] = float("nan")
+    check_distill(x, dtype, idx, val, tail, w=np.linspace(0.5, 1.5, 10).astype(np.float32))
+
+
+def test_distill_bad_indices_are_reported_and_left_out():
+    x, _ = make(2, 100, "fp32")
+    val = dev(np.log([[0.5, 0.2, 0.1], [0.5, 0.2, 0.1]]))
+    for tail in (False, True):
+        for bad in ([[1, 100, 3], [4, 5, 6]], [[1, 2, -5], [4, 5, 6]], [[1, 2 ** 31 - 1, 3], [-2 ** 31, 5, 6]]):
+            ok = [[i if 0 <= i < 100 else -1 for i in row] for row in bad]
+            st = gs.status_tensor()
+            g = dev(np.ones(2))
+            a = gs.distill_topk(x, dev(bad, torch.int64).to(torch.int32), val, tail=tail, grad_loss=g, want_grad=True, d_status=st)
+            b = gs.distill_topk(x, dev(ok, torch.int32), val, tail=tail, grad_loss=g, want_grad=True, want_stats=True)
+            assert int(st.item()) == gs.DERR_INDEX_RANGE
+            assert torch.equal(a.loss, b.loss) and torch.equal(a.dlogits, b.dlogits)
+            st.zero_()
+            gs.distill_topk_backward(x, b.stats, dev(bad, torch.int64).to(torch.int32), val, g, tail=tail, d_status=st)
+            assert int(st.item()) == gs.DERR_INDEX_RANGE
+
+
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_in_place(tail):
+    for rows, V in [(3, 2000), (1, 40001), (400, 1500)]:
+        x, _ = make(rows, V, "bf16", first=1)
+        idx, val = lists(x, 17, 1.0, tail)
+        ti, tv, w = dev(idx, torch.int32), dev(val), dev(weights(rows)[0])
+        want = gs.distill_topk(x, ti, tv, tail=tail, grad_loss=w, want_grad=True, want_stats=True)
+        y = x.clone()
+        gs.distill_topk_backward(y, want.stats, ti, tv, w, tail=tail, dlogits=y)
+        got = gs.distill_topk(x, ti, tv, tail=tail, grad_loss=w, dlogits=x)
+        assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.loss, want.loss)
+        half = torch.finfo(torch.bfloat16).eps
+        assert bool(((y.float() - want.dlogits.float()).abs() <= half * want.dlogits.float().abs() + 1e-6).all())
+
+
+# ---- as a run ---------------------------------------------------------------------------------------
+
+def test_teacher_to_student_to_compressed_gradient():
+    """A teacher's alternatives are the student's lists, and the student's gradient is what the residual
+    top-k compresses."""
+    rows, V, k, T = 24, 3001, 16, 2.0
+    teacher, _ = make(rows, V, "fp32", seed=1)
+    student = teacher + 0.3 * make(rows, V, "fp32", seed=2)[0]
+    top = gs.token_logprobs(teacher, top_k=k, temperature=T)
+    same = gs.distill_topk(teacher, top.top_idx, top.top_logprob, tail=True, temperature=T, want_grad=True,
+                           grad_loss=dev(np.ones(rows)))
+    # the list's values were rounded to fp32 (u |log q| each) and carry log S's error
+    assert float(same.loss.abs().max()) < 4 * lse_tol(V) and float(same.dlogits.abs().max()) < 16 * U * 10 + lse_tol(V)
+    w = np.full(rows, T * T / rows, np.float32)
+    r = gs.distill_topk(student, top.top_idx, top.top_logprob, tail=True, temperature=T, want_grad=True, grad_loss=dev(w))
+    it = 1.0 / T
+    want = vocab.distill(f64(student), it, top.top_idx.cpu().numpy(), f64(top.top_logprob), True)
+    close(r.loss, want, 2 * lse_tol(V) + 2 * U * np.abs(want), "loss")
+    flat = r.dlogits.reshape(-1)
+    pad = (-flat.numel()) % 4
+    g = torch.nn.functional.pad(flat, (0, pad))
+    residual = torch.zeros_like(g)
+    idx, val, off = gs.residual_topk(g, residual, (1, 100))
+    K = int(off[-1])
+    order = torch.argsort(g.abs(), descending=True, stable=True)[:K]
+    assert torch.equal(idx[:K].long(), order.sort().values) and torch.equal(val[:K], g[idx[:K].long()])
+    # moving the student against its gradient lowers the loss by about the gradient's square
+    step = 0.05
+    after = gs.distill_topk(student - step * r.dlogits, top.top_idx, top.top_logprob, tail=True, temperature=T)
+    down = float((dev(w) * (r.loss - after.loss)).sum())
+    square = float((r.dlogits.double() ** 2).sum())
+    assert 0.9 * step * square < down < 1.0 * step * square + 1e-6
+
+
+def test_streams_and_two_calls_at_once():
+    sets = []
+    for s in range(2):
+        x, _ = make(200, 20001, "bf16", seed=10 + s)
+        idx, val = lists(x[:4], 8, 1.0, True)
+        sets.append((x, dev(np.tile(idx, (50, 1)), torch.int32), dev(np.tile(val, (50, 1)))))
+    want = [gs.distill_topk(x, i, v, tail=True, want_grad=True, grad_loss=torch.ones(200, device="cuda")) for x, i, v in sets]
+    tops = [gs.token_logprobs(x, top_k=50) for x, _, _ in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got, gtops = [None, None], [None, None]
+    ones = torch.ones(200, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (x, i, v) in enumerate(sets):
+            with torch.cuda.stream(streams[s]):
+                got[s] = gs.distill_topk(x, i, v, tail=True, want_grad=True, grad_loss=ones)
+                gtops[s] = gs.token_logprobs(x, top_k=50)
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert torch.equal(got[s].loss, want[s].loss) and torch.equal(got[s].dlogits, want[s].dlogits)
+        assert torch.equal(gtops[s].top_idx, tops[s].top_idx) and torch.equal(gtops[s].top_logprob, tops[s].top_logprob)
+
+
+def test_captured_and_replayed():
+    x, _ = make(3, 30000, "bf16", seed=20)
+    idx, val = lists(x, 9, 1.0, True)
+    ti, tv, w = dev(idx, torch.int32), dev(val), dev(np.ones(3))
+    t = ti[:, 0].clamp_min(0).contiguous()
+
+    def step():
+        a = gs.token_logprobs(x, t, top_k=6, want_entropy=True, want_stats=True)
+        b = gs.token_logprobs_backward(x, a.stats, t, w, a.entropy, w)
+        c = gs.distill_topk(x, ti, tv, tail=True, want_grad=True, want_stats=True, grad_loss=w)
+        d = gs.distill_topk_backward(x, c.stats, ti, tv, w, tail=True)
+        return [a.logprob, a.entropy, a.top_idx, a.top_logprob, b, c.loss, c.dlogits, d]
+
+    step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        graphs.append((g, out))
+    for s in range(3):
+        x.copy_(make(3, 30000, "bf16", seed=30 + s)[0])
+        want = step()
+        for g, out in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for g, out in graphs:
+            for a, b in zip(out, want):
+                assert torch.equal(a, b)
+
+
+def test_rows_beyond_32_bits_of_elements():
+    V, stride = 1000, (1 << 31) + 24
+    buf = torch.zeros(stride + V, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((2, V), (stride, 1), 0)
+    x.copy_(make(2, V, "bf16")[0])
+    t = dev([5, 999], torch.int32)
+    got = gs.token_logprobs(x, t, top_k=5, dlogits=x, grad_logprob=dev([1.0, 2.0]))
+    y = make(2, V, "bf16")[0].clone()
+    want = gs.token_logprobs(y, t, top_k=5, want_grad=True, grad_logprob=dev([1.0, 2.0]))
+    assert torch.equal(got.top_idx, want.top_idx) and torch.equal(got.logprob, want.logprob)
+    assert torch.equal(got.dlogits, want.dlogits)
+    assert bool((buf[V:stride] == 0).all())
+
+
+def test_the_binding_refuses():
+    x, _ = make(2, 10, "fp32")
+    i, v = dev([[1], [2]], torch.int32), dev([[0.0], [0.0]])
+    E = gs.GsparseError
+    for call in (lambda: gs.token_logprobs(x.double()), lambda: gs.token_logprobs(x.t()), lambda: gs.token_logprobs(x[0]),
+                 lambda: gs.token_logprobs(x, dev([1, 2], torch.int64)), lambda: gs.token_logprobs(x, dev([1], torch.int32)),
+                 lambda: gs.token_logprobs(x, temperature=0.0), lambda: gs.token_logprobs(x, temperature=-1.0),
+                 lambda: gs.token_logprobs(x, top_k=11), lambda: gs.token_logprobs(x, grad_logprob=v[:, 0].contiguous()),
+                 lambda: gs.token_logprobs(x, dlogits=x.half()), lambda: gs.token_logprobs(x, dlogits=x[:1]),
+                 lambda: gs.token_logprobs_backward(x, v), lambda: gs.token_logprobs_backward(x, dev(np.ones((2, 2))), top_idx=i),
+                 lambda: gs.distill_topk(x, i, v[:1]), lambda: gs.distill_topk(x, i[:, 0], v), lambda: gs.distill_topk(x, i, i),
+                 lambda: gs.distill_topk(x, i, v, want_grad=True),
+                 lambda: gs.distill_topk_backward(x, dev(np.ones((2, 2))), i, v, v[:, 0].contiguous(), tail=True)):
+        with pytest.raises(E):
+            call()
