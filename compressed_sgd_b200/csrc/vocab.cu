@@ -25,15 +25,16 @@ namespace cg = cooperative_groups;
 
 constexpr int kVocThreads = 512;
 constexpr int kVocWarps = kVocThreads / 32;
-constexpr int kVocUnroll = 4;                     // 16-byte loads in flight per thread
+constexpr int kUnroll = 4;                        // vectors of 16 bytes per lane and chunk
+constexpr int kChunk = 32 * kUnroll;              // vectors per chunk
+constexpr int kStages = 3;                        // chunks per warp in shared memory
 constexpr int kCand = 1024;                       // candidates for the alternatives, per CTA and in all
-constexpr int kList = GSPARSE_MAX_ALTERNATIVES + 1;   // a row's list and its target
-constexpr int kTable = 1024;                      // hash table over the list (load <= 1/4)
-constexpr int kFilterWords = 512;                 // one bit per vector of the row, modulo 16384
 
 constexpr float kLowest = -3.402823466e38f;       // the maximum of a row that holds nothing but -inf
-constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: exponents are clamped here, so that
-                                                  // 0 * exponent stays 0 where the logit is -inf
+constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: where a sum weighs by the exponent it is
+                                                  // clamped here, so that -inf logits add 0
+constexpr float kLowestSafe = 1.0e38f;
+constexpr float kWildBits = 1.2676506e30f;        // 2^100: maxima beyond it (in bits) take the careful route
 
 enum { kLogprob = 0, kRenorm = 1, kTail = 2 };    // what is computed
 enum { kForward = 0, kFused = 1, kBackward = 2 }; // loss; loss and gradient; gradient from saved statistics
@@ -45,7 +46,8 @@ struct VocArgs {
   int32_t rows, vocab, split;    // split = CTAs per row
   int32_t k;                     // list length: alternatives wanted (forward), given (backward), or the teacher's
   int32_t val_dtype;
-  float it, c, c_lo, far;        // c + c_lo = it log2(e); far = kFarBits / c
+  float it, c, c_lo;             // c + c_lo = it log2(e)
+  float far, ref_min;            // kFarBits / c, -kWildBits / c
   const int32_t* targets;
   const int32_t* list_idx;       // teacher's list, or the alternatives of the backward pass
   const void* list_val;          // teacher's values, or the gradient of the alternatives
@@ -66,12 +68,20 @@ struct VocArgs {
 template <class T> struct Elem;
 template <> struct Elem<float> {
   static constexpr int N = 4;
-  static constexpr uint32_t kNegInf = 0xff800000u;
   static __device__ __forceinline__ float to(float x) { return x; }
   static __device__ __forceinline__ float from(float x) { return x; }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
     x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
     x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  }
+  // Largest entry of n vectors, NaN passed over (-inf or NaN if there is nothing else).
+  template <int NV> static __device__ __forceinline__ float high(const uint4* v) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v[u].x)), __uint_as_float(v[u].y)),
+                fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w)));
+    return m;
   }
   static __device__ __forceinline__ uint4 pack(const float* x) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -79,9 +89,20 @@ template <> struct Elem<float> {
 };
 template <> struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
-  static constexpr uint32_t kNegInf = 0xff80ff80u;
   static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+  template <int NV> static __device__ __forceinline__ float high(const uint4* v) {
+    __nv_bfloat162 m = as2(v[0].x);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (u) m = __hmax2(m, as2(v[u].x));
+      m = __hmax2(m, as2(v[u].y));
+      m = __hmax2(m, as2(v[u].z));
+      m = __hmax2(m, as2(v[u].w));
+    }
+    return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
+  }
+  static __device__ __forceinline__ __nv_bfloat162 as2(const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -102,9 +123,20 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<__half> {
   static constexpr int N = 8;
-  static constexpr uint32_t kNegInf = 0xfc00fc00u;
   static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
+  template <int NV> static __device__ __forceinline__ float high(const uint4* v) {
+    __half2 m = as2(v[0].x);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (u) m = __hmax2(m, as2(v[u].x));
+      m = __hmax2(m, as2(v[u].y));
+      m = __hmax2(m, as2(v[u].z));
+      m = __hmax2(m, as2(v[u].w));
+    }
+    return fmaxf(__half2float(m.x), __half2float(m.y));
+  }
+  static __device__ __forceinline__ __half2 as2(const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -181,55 +213,62 @@ constexpr uint32_t kKeyNegInf = 0x007fffffu;      // order_key(-inf): never an a
 
 // ---- block-wide reductions, in a fixed order ------------------------------------------------
 
-struct Scratch {
-  float f[kVocWarps];
-  double a[kVocWarps], b[kVocWarps];
-  int i[kVocWarps];
-};
-
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
   return v;
 }
 
-// Each leaves its scratch free for the next call (the sync at the start).
-__device__ __forceinline__ float block_max(float v, Scratch& sh) {
+// One reduction's partial results. Every reduction of the kernel has its own, so that one barrier
+// each is enough.
+struct PartMax { float w[kVocWarps]; };
+struct PartSum { double a[kVocWarps], b[kVocWarps]; };
+
+// Maximum over the block, to every thread.
+__device__ __forceinline__ float block_max(float v, PartMax& p) {
   v = warp_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.f[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) p.w[threadIdx.x >> 5] = v;
   __syncthreads();
   const int nw = blockDim.x >> 5;
-  float m = sh.f[0];
-  for (int w = 1; w < nw; ++w) m = fmaxf(m, sh.f[w]);
+  float m = p.w[0];
+  for (int w = 1; w < nw; ++w) m = fmaxf(m, p.w[w]);
   return m;
 }
-__device__ __forceinline__ void block_sum2(double& x, double& y, Scratch& sh) {
+// Two sums over the block: put, a barrier, and any thread may get.
+__device__ __forceinline__ void sum_put(double x, double y, PartSum& p) {
   x = warp_sum(x);
   y = warp_sum(y);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) {
-    sh.a[threadIdx.x >> 5] = x;
-    sh.b[threadIdx.x >> 5] = y;
-  }
-  __syncthreads();
-  const int nw = blockDim.x >> 5;
-  x = sh.a[0];
-  y = sh.b[0];
-  for (int w = 1; w < nw; ++w) {
-    x += sh.a[w];
-    y += sh.b[w];
+    p.a[threadIdx.x >> 5] = x;
+    p.b[threadIdx.x >> 5] = y;
   }
 }
-__device__ __forceinline__ int block_count(int v, Scratch& sh) {
+__device__ __forceinline__ void sum_get(double& x, double& y, const PartSum& p) {
+  const int nw = blockDim.x >> 5;
+  x = p.a[0];
+  y = p.b[0];
+  for (int w = 1; w < nw; ++w) {
+    x += p.a[w];
+    y += p.b[w];
+  }
+}
+// Count over the block, to every thread; the barriers at both ends let the array be used again.
+__device__ __forceinline__ int block_count(int v, int* part) {
   v = warp_sum(v);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.i[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   const int nw = blockDim.x >> 5;
   int n = 0;
-  for (int w = 0; w < nw; ++w) n += sh.i[w];
+  for (int w = 0; w < nw; ++w) n += part[w];
   return n;
+}
+
+// 2^x for a small x to 64 bits' accuracy without the library's long route.
+__device__ __forceinline__ double exp2_small(double x) {
+  if (fabs(x) > 1.0e-4) return exp2(x);
+  const double y = x * 0.6931471805599453;
+  return 1.0 + y * (1.0 + y * (0.5 + y * (1.0 / 6.0)));   // next term below 1e-18
 }
 
 // ---- a row and its parts --------------------------------------------------------------------
@@ -261,14 +300,10 @@ struct Row {
     if (last && t >= 32 && e < V) return e;
     return -1;
   }
-  // Vector number of element e, the head being vector 0 and the body starting at 1.
-  __device__ __forceinline__ int vec_of(int e) const { return e < head ? 0 : (e - head) / Elem<T>::N + 1; }
-  __device__ __forceinline__ int lane_of(int e) const { return e < head ? e : (e - head) % Elem<T>::N; }
   __device__ __forceinline__ bool owns(int e) const {
-    const int v = vec_of(e);
-    if (v == 0) return first;
-    if (v == nv + 1) return last;
-    return v - 1 >= v0 && v - 1 < v1;
+    if (e < head) return first;
+    const int v = (e - head) / Elem<T>::N;
+    return v >= nv ? last : v >= v0 && v < v1;
   }
 };
 
@@ -276,92 +311,120 @@ struct Row {
 
 struct Running {
   float m;        // largest entry so far, -inf if none (NaN is passed over; it reaches s)
-  f2 s, t;        // sums over entries of e = 2^((x - ref) c) and of e (x - ref) c, ref = max(m, lowest)
+  float rc;       // fl(max(m, ref_min) c), what the exponents are taken from
+  f2 s, t;        // sums over entries of e = 2^q and of e q, q = fl(x c - rc)
 };
 
-__device__ __forceinline__ void running_init(Running& r) {
+__device__ __forceinline__ void running_init(Running& r, const VocArgs& a) {
   r.m = -INFINITY;
+  r.rc = a.ref_min * a.c;
   r.s = r.t = pair(0.0f, 0.0f);
 }
 
-// Moves the sums to the maximum m2 >= m.
-__device__ __forceinline__ void running_raise(Running& r, float m2, float c) {
-  const float dd = max_nan((fmaxf(r.m, kLowest) - fmaxf(m2, kLowest)) * c, -kFarBits);
+// Moves the sums to the reference rc2 >= rc.
+__device__ __forceinline__ void running_shift(Running& r, float rc2) {
+  const float dd = max_nan(r.rc - rc2, -kFarBits);
   const float f = ex2(dd);
   r.t = mul2(fma2(r.s, pair(dd, dd), r.t), pair(f, f));
   r.s = mul2(r.s, pair(f, f));
-  r.m = m2;
+  r.rc = rc2;
 }
 
-// Adds n entries (n even). FINE: the product with c in two parts, so that the rounding of c does
-// not shift every exponent the same way (the distillation loss is a small difference of logs).
-template <int NE, bool ENT, bool FINE>
-__device__ __forceinline__ void running_add(Running& r, const float* x, const VocArgs& a) {
-  const float ref = fmaxf(r.m, kLowest);
-  const f2 nref = pair(-ref, -ref), c2 = pair(a.c, a.c);
-#pragma unroll
-  for (int i = 0; i < NE; i += 2) {
-    float d0, d1;
-    unpair(add2(pair(x[i], x[i + 1]), nref), &d0, &d1);
-    const f2 d = pair(max_nan(d0, -a.far), max_nan(d1, -a.far));
-    f2 q = mul2(d, c2);
-    if (FINE) q = fma2(d, pair(a.c_lo, a.c_lo), q);
-    float q0, q1;
-    unpair(q, &q0, &q1);
-    const f2 e = pair(ex2(q0), ex2(q1));
-    r.s = add2(r.s, e);
-    if (ENT) r.t = fma2(e, q, r.t);
+// Adds NV vectors. An exponent is one fused multiply-add (one rounding), entry by entry four and a
+// half instructions: unpack, half a maximum, half an exponent, 2^q, half an addition each to s and t.
+// 0 * -inf makes t NaN when -inf is among the entries; those NV vectors are then added again with the
+// exponents clamped, which costs rows without -inf one comparison per NV vectors.
+template <class T, int NV>
+__device__ __forceinline__ void running_add(Running& r, const uint4* v, const VocArgs& a) {
+  constexpr int N = Elem<T>::N;
+  const float high = Elem<T>::template high<NV>(v);
+  if (high > r.m) {
+    r.m = high;
+    running_shift(r, fmaxf(high, a.ref_min) * a.c);
   }
+  const f2 c2 = pair(a.c, a.c), nrc = pair(-r.rc, -r.rc), before = r.t;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    float x[N];
+    Elem<T>::unpack(v[u], x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const f2 q = fma2(pair(x[i], x[i + 1]), c2, nrc);
+      float q0, q1;
+      unpair(q, &q0, &q1);
+      const f2 e = pair(ex2(q0), ex2(q1));
+      r.s = add2(r.s, e);
+      r.t = fma2(e, q, r.t);
+    }
+  }
+  float t0, t1;
+  unpair(r.t, &t0, &t1);
+  t0 += t1;
+  if (t0 != t0) {
+    r.t = before;
+#pragma unroll 1
+    for (int u = 0; u < NV; ++u) {
+      float x[N];
+      Elem<T>::unpack(v[u], x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        float q0, q1;
+        unpair(fma2(pair(x[i], x[i + 1]), c2, nrc), &q0, &q1);
+        r.t = fma2(pair(ex2(q0), ex2(q1)), pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), r.t);
+      }
+    }
+  }
+}
+
+// Adds one entry.
+__device__ __forceinline__ void running_add_one(Running& r, float x, const VocArgs& a) {
+  if (x > r.m) {
+    r.m = x;
+    running_shift(r, fmaxf(x, a.ref_min) * a.c);
+  }
+  const float q = fmaf(x, a.c, -r.rc), e = ex2(q);
+  r.s = add2(r.s, pair(e, 0.0f));
+  r.t = fma2(pair(e, 0.0f), pair(max_nan(q, -kFarBits), 0.0f), r.t);
 }
 
 // ---- list of a row ------------------------------------------------------------------------------
 
-struct ListShared {
-  int32_t idx[kList];      // -1: absent
-  float x[kList];          // the row's entry there
-  float add[kList];        // what the gradient gets there besides the dense part
-  uint32_t table[kTable];  // (vector + 1) << 8 | entries of that vector in the list
-  uint32_t filter[kFilterWords];
-  int repeats;             // an index stands in the list twice
+struct List {              // in dynamic shared memory, for n entries
+  double* q;               // the teacher's probability
+  int32_t* idx;            // -1: absent
+  float* x;                // the row's entry there
+  float* v;                // the teacher's value, or the incoming gradient of the entry
+  uint32_t* table;         // which indices are in the list: index + 1, open addressing, at most half full
+  int slots;
+  __host__ __device__ __forceinline__ static int table_slots(int n) {
+    int t = 64;
+    while (t < 2 * n) t *= 2;
+    return t;
+  }
+  __host__ __device__ __forceinline__ static size_t bytes(int n) {
+    return (size_t)round_up(n, 4) * 20 + (size_t)table_slots(n) * 4;
+  }
+  __device__ __forceinline__ void carve(void* at, int n) {
+    const int m = (int)round_up(n, 4);
+    q = static_cast<double*>(at);
+    idx = reinterpret_cast<int32_t*>(q + m);
+    x = reinterpret_cast<float*>(idx + m);
+    v = x + m;
+    table = reinterpret_cast<uint32_t*>(v + m);
+    slots = table_slots(n);
+  }
+  // Enters index e; true if it was there.
+  __device__ __forceinline__ bool add(int e) const {
+    const uint32_t key = (uint32_t)e + 1u;
+    uint32_t s = (key * 2654435761u) >> 16;
+    for (int n = 0; n < slots; ++n, ++s) {
+      const uint32_t old = atomicCAS(&table[s & (slots - 1)], 0u, key);
+      if (old == 0u) return false;
+      if (old == key) return true;
+    }
+    return false;
+  }
 };
-
-__device__ __forceinline__ uint32_t table_slot(uint32_t v) { return (v * 2654435761u) >> 22; }   // kTable = 2^10
-
-// Enters element (vector v, place l) into the table; true if it was there.
-__device__ __forceinline__ bool table_add(ListShared& L, int v, int l) {
-  const uint32_t tag = (uint32_t)(v + 1) << 8, bit = 1u << l;
-  uint32_t s = table_slot((uint32_t)v);
-  for (int n = 0; n < kTable; ++n, s = (s + 1) & (kTable - 1)) {
-    const uint32_t old = atomicCAS(&L.table[s], 0u, tag | bit);
-    if (old == 0u) break;
-    if ((old & ~255u) == tag) return (atomicOr(&L.table[s], bit) & bit) != 0;
-  }
-  atomicOr(&L.filter[((uint32_t)v >> 5) & (kFilterWords - 1)], 1u << (v & 31));
-  return false;
-}
-
-// Which entries of vector v are in the list.
-__device__ __forceinline__ uint32_t table_mask(const ListShared& L, int v) {
-  if (!((L.filter[((uint32_t)v >> 5) & (kFilterWords - 1)] >> (v & 31)) & 1u)) return 0;
-  const uint32_t tag = (uint32_t)(v + 1) << 8;
-  uint32_t s = table_slot((uint32_t)v);
-  for (int n = 0; n < kTable; ++n, s = (s + 1) & (kTable - 1)) {
-    const uint32_t w = L.table[s];
-    if (w == 0u) return 0;
-    if ((w & ~255u) == tag) return w & 255u;
-  }
-  return 0;
-}
-
-template <class T>
-__device__ __forceinline__ uint4 masked(uint4 u, uint32_t mask) {
-  float x[Elem<T>::N];
-  Elem<T>::unpack(u, x);
-#pragma unroll
-  for (int i = 0; i < Elem<T>::N; ++i)
-    if ((mask >> i) & 1u) x[i] = -INFINITY;
-  return Elem<T>::pack(x);
-}
 
 // ---- most likely tokens ---------------------------------------------------------------------------
 
@@ -395,7 +458,7 @@ __device__ uint32_t kth_key_of_block(uint32_t key, int k) {
 
 // Entries of the whole row with key >= t (the CTA reads all of it).
 template <class T>
-__device__ int count_ge(const Row<T>& row, uint32_t t, Scratch& sh) {
+__device__ int count_ge(const Row<T>& row, uint32_t t, int* sh) {
   int n = 0;
   const uint4* p = row.vec();
   for (int i = threadIdx.x; i < row.nv; i += blockDim.x) {
@@ -413,7 +476,7 @@ __device__ int count_ge(const Row<T>& row, uint32_t t, Scratch& sh) {
 // NaN): bisection on the key for the k-th largest, then everything above it, then the entries equal
 // to it from the lowest index on. Every step reads the row, which L2 holds by now.
 template <class T>
-__device__ __noinline__ void exact_top(const Row<T>& row, int k, uint32_t lower, TopShared& top, Scratch& sh) {
+__device__ __noinline__ void exact_top(const Row<T>& row, int k, uint32_t lower, TopShared& top, int* sh) {
   constexpr uint32_t kLeast = kKeyNegInf + 1;
   uint32_t lo = lower > kLeast ? lower : kLeast;      // at least k at or above lo, or lo = kLeast
   int above_lo = count_ge(row, lo, sh);
@@ -466,18 +529,98 @@ __device__ __noinline__ void exact_top(const Row<T>& row, int k, uint32_t lower,
     const bool hit = e < row.V && order_key(Elem<T>::to(row.x[e])) == lo;
     const uint32_t b = __ballot_sync(kFull, hit);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.i[threadIdx.x >> 5] = __popc(b);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = __popc(b);
     __syncthreads();
     int before = 0, all = 0;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-      if (w < (int)(threadIdx.x >> 5)) before += sh.i[w];
-      all += sh.i[w];
+      if (w < (int)(threadIdx.x >> 5)) before += sh[w];
+      all += sh[w];
     }
     before += __popc(b & lanemask_lt());
     if (hit && found + before < need) cand_push(top, lo, e);
     found += all;
   }
   __syncthreads();
+}
+
+// ---- a warp's chunks in shared memory ------------------------------------------------------------------
+
+// Warp w of nw takes chunks w, w + nw, ... of its CTA's slice, each kChunk vectors (2 KB), copied
+// by bulk asynchronous copies into a ring of its own: no warp waits for another, and kStages
+// chunks per warp are on their way whatever the registers hold.
+struct Ring {
+  uint4* slots;
+  uint64_t* bars;
+  const uint4* from;      // the slice
+  int own, n;             // vectors of the slice, chunks of this warp
+  int warp, nw;
+  uint32_t phase;         // parity of the next fill of each slot
+  bool ok;
+  __device__ __forceinline__ void init(uint4* s, uint64_t* b, const uint4* src, int vectors) {
+    warp = threadIdx.x >> 5;
+    nw = blockDim.x >> 5;
+    slots = s + warp * kStages * kChunk;
+    bars = b + warp * kStages;
+    from = src;
+    own = vectors;
+    const int chunks = (vectors + kChunk - 1) / kChunk;
+    n = chunks > warp ? (chunks - warp + nw - 1) / nw : 0;
+    phase = 0;
+    ok = true;
+    if ((threadIdx.x & 31) == 0) {
+      for (int q = 0; q < kStages; ++q) mbar_init(&bars[q], 1);
+      fence_mbarrier_init();
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ int first(int k) const { return (warp + nw * k) * kChunk; }   // vector of the slice
+  __device__ __forceinline__ uint4* at(int k) const { return slots + (k % kStages) * kChunk; }
+  // Requests chunk k (the slot's last readers have passed a __syncwarp).
+  __device__ __forceinline__ void issue(int k) const {
+    if ((threadIdx.x & 31) == 0) {
+      const int o = first(k);
+      const uint32_t bytes = 16u * (uint32_t)min(kChunk, own - o);
+      mbar_arrive_expect_tx(&bars[k % kStages], bytes);
+      bulk_load(at(k), from + o, bytes, &bars[k % kStages]);
+    }
+  }
+  // Waits for the requested chunk k. A wait that runs out ends all later ones: the call reports it and
+  // goes on with what the slot holds.
+  __device__ __forceinline__ void wait(int k, int32_t* d_status) {
+    const int q = k % kStages;
+    if (ok && !mbar_wait_bounded(&bars[q], (phase >> q) & 1u)) {
+      ok = false;
+      raise(d_status, GSPARSE_DERR_TIMEOUT);
+    }
+    phase ^= 1u << q;
+  }
+  // No copy may land after the CTA is gone.
+  __device__ __forceinline__ void drain() const {
+    if (ok) return;
+    for (int q = 0; q < kStages; ++q)
+      for (uint32_t p = 0; p < 2; ++p) mbar_wait_bounded(&bars[q], p);
+  }
+};
+
+// The thread's sums over the CTA's slice relative to M, entry by entry with the difference taken first: for rows
+// whose maximum times c is beyond 2^100, where fl(x c - rc) would overflow. out: entries left out.
+template <class T>
+__device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocArgs& a, const int32_t* out, int n_out,
+                                          double& S, double& Tt) {
+  double s = 0.0, t = 0.0;
+  auto one = [&](int e) {
+    float x = Elem<T>::to(row.x[e]);
+    for (int j = 0; j < n_out; ++j)
+      if (out[j] == e) x = -INFINITY;
+    const float q = max_nan(max_nan(x - M, -a.far) * a.c, -kFarBits), y = ex2(q);
+    s += (double)y;
+    t += (double)y * (double)q;
+  };
+  for (int e = row.head + row.v0 * Elem<T>::N + threadIdx.x; e < row.head + row.v1 * Elem<T>::N; e += blockDim.x) one(e);
+  const int edge = row.edge(threadIdx.x);
+  if (edge >= 0) one(edge);
+  S = s;
+  Tt = t;
 }
 
 // ---- the kernel -----------------------------------------------------------------------------------
@@ -488,36 +631,85 @@ struct Exchange {      // what the CTAs of a row tell each other
   uint32_t kth;
 };
 
-template <bool LIST> struct ListPart { ListShared list; };
-template <> struct ListPart<false> {};
-template <bool TOP> struct TopPart { TopShared top; };
-template <> struct TopPart<false> {};
+constexpr int kHitWords = 16;
+
+// What one thread works out for all: 64-bit arithmetic by every thread would cost more than the row.
+struct RowShared {
+  PartMax max_row, max_list;
+  PartSum sum_row, sum_list, sum_loss;
+  int part[kVocWarps];
+  int repeats;         // an index stands in the list twice
+  uint32_t hit[kHitWords];   // chunks of the slice that hold entries of the list (modulo 32 kHitWords)
+  float M;             // of the entries that S and T sum
+  double S, T;
+  uint32_t kth;
+  double Q, rho;       // mass of the list and what it leaves
+  double list_max, list_log;
+  float ref, ref_row, ent;
+  double S_row;
+  // the dense gradient p (A + Bl log2 p) = 2^q (A + Bl q), q = fl(x c - k)
+  float k, A, Bl, A_list;
+  int wild;
+};
+
+// The factors of the dense gradient for p = 2^((x - ref) c) / S, g = p (A + Bl log2 p).
+// With S = 2^E s, 1 <= s < 2, p = 2^(x c - k) f for k = fl(fl(ref c) + E) and f = 2^(k - E - ref c) / s: no
+// logarithm, and no rounding of k is left in p.
+__device__ __forceinline__ void dense_factors(RowShared& R, float ref, double S, double A, double Bl, const VocArgs& a) {
+  R.ref = ref;
+  R.wild = !(fabsf(ref) * a.c <= kWildBits);
+  if (S == 0.0) {                                 // -inf alone, and entries that the list writes
+    R.k = R.A = R.Bl = 0.0f;
+    R.wild = 0;
+    return;
+  }
+  int E;
+  const double s = 2.0 * frexp(S, &E);
+  E -= 1;
+  const float k = ref * a.c + (float)E;
+  const double off = R.wild ? 0.0 : (double)k - (double)E - (double)ref * (double)a.c;
+  const double f = exp2_small(off) / s;
+  R.k = R.wild ? (float)E : k;                    // careful entries take (x - ref) c - E
+  R.A = (float)(f * (A + (Bl != 0.0 ? Bl * (off - (double)log2f((float)s)) : 0.0)));
+  R.Bl = (float)(f * Bl);
+}
+
+// Dynamic shared memory: the warps' rings; the list; the candidates, over the rings where no
+// gradient needs them again.
+__host__ __device__ __forceinline__ size_t ring_bytes(int threads) { return (size_t)threads / 32 * kStages * kChunk * 16; }
 
 template <class T, int OP, bool TOP, int MODE>
 __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_constant__ VocArgs a) {
-  constexpr int N = Elem<T>::N, U = kVocUnroll;
+  constexpr int N = Elem<T>::N, U = kUnroll;
   constexpr bool LIST = OP != kLogprob || MODE == kBackward;
-  constexpr bool FINE = OP != kLogprob;
-  constexpr bool ENT = OP == kLogprob;
-  __shared__ Scratch sh;
+  constexpr bool GRAD = MODE != kForward;
+  extern __shared__ __align__(16) uint4 dyn[];
+  __shared__ RowShared R;
   __shared__ Exchange ex;
-  __shared__ ListPart<LIST> lp;
-  __shared__ TopPart<TOP> tp;
+  __shared__ uint64_t bars[kVocWarps * kStages];
 
   const int C = a.split, part = (int)(blockIdx.x % (unsigned)C), r = (int)(blockIdx.x / (unsigned)C);
-  const int tid = threadIdx.x, B = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, B = blockDim.x;
   const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C);
   const uint4* vec = row.vec();
+  const int own = row.v1 - row.v0;
+  const int edge = row.edge(tid);
+  char* beyond = reinterpret_cast<char*>(dyn) + ring_bytes(B);
+  Ring ring;
+  ring.init(dyn, bars, vec + row.v0, own);
   pdl_begin();
+  if (MODE != kBackward)
+    for (int q = 0; q < min(kStages, ring.n); ++q) ring.issue(q);
 
   // -- the row's list ---------------------------------------------------------------------------
   float w = 0.0f, w_h = 0.0f;                     // gradient weights of the row
-  if (MODE != kForward) {
+  if (GRAD) {
     w = a.weight ? a.weight[r] : 0.0f;
     w_h = OP == kLogprob && a.weight_entropy ? a.weight_entropy[r] : 0.0f;
   }
   int target = -1;
-  float x_target = 0.0f;
+  float x_target = 0.0f, x_edge = 0.0f;
+  if (edge >= 0) x_edge = Elem<T>::to(row.x[edge]);
   if (OP == kLogprob && a.targets) {
     target = a.targets[r];
     if (target < -1 || target >= a.vocab) {
@@ -526,22 +718,23 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
     }
     if (target >= 0) x_target = Elem<T>::to(row.x[target]);
   }
-  if (target < 0 && OP == kLogprob) w = 0.0f;
-  double Q = 0.0, rho = 0.0;                      // mass of the list and what it leaves
-  double list_max = 0.0, list_log = 0.0;          // renormalised list: maximum and log of the sum
-  double w_list = 0.0, w_size = 0.0;              // sum of the alternatives' gradients; of the list's magnitudes
+  if (OP == kLogprob && target < 0) w = 0.0f;
+  // the backward pass reads nothing of a row without weights (where the list has none of its own)
+  const bool early = MODE == kBackward && (OP == kLogprob || w != 0.0f);
+  if (early)
+    for (int q = 0; q < min(kStages, ring.n); ++q) ring.issue(q);
   const int nl = LIST ? (OP == kLogprob ? a.k + 1 : a.k) : 0;
+  List L;
   if constexpr (LIST) {
-    ListShared& L = lp.list;
-    if (OP == kTail || MODE != kForward) {
-      for (int i = tid; i < kTable; i += B) L.table[i] = 0;
-      for (int i = tid; i < kFilterWords; i += B) L.filter[i] = 0;
-    }
-    if (tid == 0) L.repeats = 0;
+    L.carve(beyond, nl);
+    if (OP == kTail || GRAD)
+      for (int i = tid; i < L.slots; i += B) L.table[i] = 0;
+    if (tid == 0) R.repeats = 0;
+    if (OP == kTail && tid < kHitWords) R.hit[tid] = 0;
     float vmax = -INFINITY;
     for (int j = tid; j < nl; j += B) {
       int e;
-      float v = 0.0f;
+      float v;
       if (OP == kLogprob) {
         e = j == 0 ? target : a.list_idx[(int64_t)r * a.k + j - 1];
         v = j == 0 ? w : static_cast<const float*>(a.list_val)[(int64_t)r * a.k + j - 1];
@@ -555,123 +748,175 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
       }
       L.idx[j] = e;
       L.x[j] = e >= 0 && (MODE != kBackward || row.owns(e)) ? Elem<T>::to(row.x[e]) : 0.0f;
-      L.add[j] = v;
+      L.v[j] = v;
       if (e >= 0) vmax = fmaxf(vmax, v);
     }
-    if (OP == kRenorm) list_max = (double)fmaxf(block_max(vmax, sh), kLowest);
-    __syncthreads();
+    float list_max = 0.0f;
+    if (OP == kRenorm) list_max = fmaxf(block_max(vmax, R.max_list), kLowest);
+    else __syncthreads();
+    // sum of the probabilities (of the renormalised list: not yet divided); of the incoming gradients
+    // and their sizes
     double sum = 0.0, size = 0.0;
     for (int j = tid; j < nl; j += B) {
       const int e = L.idx[j];
       if (e < 0) continue;
       if (OP == kLogprob) {
-        if (j > 0) sum += (double)L.add[j];
-        size += fabs((double)L.add[j]);
+        if (j > 0) sum += (double)L.v[j];
+        size += fabs((double)L.v[j]);
+      } else {
+        const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)list_max) * (double)a.it : (double)L.v[j]);
+        L.q[j] = q;
+        sum += q;
       }
-      else if (OP == kRenorm) sum += exp(((double)L.add[j] - list_max) * (double)a.it);
-      else sum += exp((double)L.add[j]);
-      if (OP == kTail || MODE != kForward)
-        if (table_add(L, row.vec_of(e), row.lane_of(e))) L.repeats = 1;
+      if (OP == kTail || GRAD)
+        if (L.add(e)) R.repeats = 1;
+      if (OP == kTail && MODE != kBackward && e >= row.head) {
+        const int v = (e - row.head) / N - row.v0;
+        if (v >= 0 && v < own) atomicOr(&R.hit[(v / kChunk >> 5) & (kHitWords - 1)], 1u << ((v / kChunk) & 31));
+      }
     }
-    block_sum2(sum, size, sh);
-    if (OP == kLogprob) {
-      w_list = sum;
-      w_size = size;
-    } else if (OP == kRenorm) {
-      list_log = log(sum);
-      Q = sum != 0.0 ? 1.0 : 0.0;                 // NaN in the list: Q = 1, the entries are NaN
-      if (sum != sum) Q = sum;
-    } else {
-      Q = sum;
-      rho = fmax(1.0 - sum, 0.0);
-      if (sum != sum) rho = sum;
+    sum_put(sum, size, R.sum_list);
+    __syncthreads();
+    if (tid == 0) {
+      sum_get(sum, size, R.sum_list);
+      R.Q = sum;
+      R.rho = size;                               // kLogprob: sum of the gradients and of their sizes
+      if (OP == kRenorm) {
+        R.list_max = (double)list_max;
+        R.list_log = sum;                         // the loss takes its logarithm
+        R.Q = sum == 0.0 ? 0.0 : sum == sum ? 1.0 : sum;
+        R.rho = 0.0;
+      }
+      if (OP == kTail) R.rho = sum == sum ? fmax(1.0 - sum, 0.0) : sum;
     }
+    if (OP == kTail) __syncthreads();             // hit
   }
 
   // -- maximum and sums ----------------------------------------------------------------------------
   // Of the whole row; with kTail of the entries outside the list, whose sum as the difference of
   // two others would lose its digits when the list holds nearly all of the mass.
-  float M = -INFINITY;
-  double S = 0.0, Tt = 0.0;
-  if (MODE != kBackward) {
+  if constexpr (MODE != kBackward) {
     Running run;
-    running_init(run);
-    for (int i = row.v0 + tid; i < row.v1; i += U * B) {
-      uint4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int q = i + u * B;
-        v[u] = q < row.v1 ? __ldcg(vec + q) : make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
-      }
-      if constexpr (OP == kTail) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t mask = table_mask(lp.list, i + u * B + 1);
-          if (mask) v[u] = masked<T>(v[u], mask);
+    running_init(run, a);
+    for (int q = 0; q < ring.n; ++q) {
+      ring.wait(q, a.d_status);
+      const uint4* at = ring.at(q);
+      const int left = own - ring.first(q);
+      if constexpr (OP == kTail) {                // the list's entries leave the chunk
+        const int c = ring.warp + ring.nw * q;
+        if ((R.hit[(c >> 5) & (kHitWords - 1)] >> (c & 31)) & 1u) {
+          const int e0 = row.head + (row.v0 + c * kChunk) * N;
+          for (int j = lane; j < nl; j += 32) {
+            const int e = L.idx[j] - e0;
+            if (L.idx[j] >= 0 && e >= 0 && e < min(kChunk, left) * N)
+              reinterpret_cast<T*>(ring.at(q))[e] = Elem<T>::from(-INFINITY);
+          }
+          fence_proxy_async_smem();               // before the slot's next copy
+          __syncwarp();
         }
       }
-      float high = run.m;
+      if (left >= kChunk) {
+        uint4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[N];
-        Elem<T>::unpack(v[u], x);
-#pragma unroll
-        for (int j = 0; j < N; ++j) high = fmaxf(high, x[j]);
+        for (int u = 0; u < U; ++u) v[u] = at[u * 32 + lane];
+        running_add<T, U>(run, v, a);
+      } else {
+        for (int u = lane; u < left; u += 32) {
+          const uint4 v = at[u];
+          running_add<T, 1>(run, &v, a);
+        }
       }
-      if (high > run.m) running_raise(run, high, a.c);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[N];
-        Elem<T>::unpack(v[u], x);
-        running_add<N, ENT, FINE>(run, x, a);
-      }
+      __syncwarp();
+      if (q + kStages < ring.n) ring.issue(q + kStages);
     }
-    const int edge = row.edge(tid);
     if (edge >= 0) {
-      float x[2] = {Elem<T>::to(row.x[edge]), -INFINITY};
-      if constexpr (OP == kTail)
-        if ((table_mask(lp.list, row.vec_of(edge)) >> row.lane_of(edge)) & 1u) x[0] = -INFINITY;
-      if (x[0] > run.m) running_raise(run, x[0], a.c);
-      running_add<2, ENT, FINE>(run, x, a);
+      float x = x_edge;
+      if constexpr (OP == kTail) {
+        for (int j = 0; j < nl; ++j)
+          if (L.idx[j] == edge) x = -INFINITY;
+      }
+      running_add_one(run, x, a);
     }
     const float mine = run.m;
-    M = block_max(run.m, sh);
-    running_raise(run, M, a.c);
-    float s0, s1, t0, t1;
-    unpair(run.s, &s0, &s1);
-    unpair(run.t, &t0, &t1);
-    S = (double)s0 + (double)s1;
-    Tt = (double)t0 + (double)t1;
-    block_sum2(S, Tt, sh);
+    const float M = block_max(run.m, R.max_row);
+    const float ref = fmaxf(M, a.ref_min);
+    const bool wild = !(fabsf(M) * a.c <= kWildBits) && fabsf(M) < INFINITY;
+    if (wild) {
+      const int32_t* out = nullptr;
+      if constexpr (OP == kTail) out = L.idx;
+      double s, t;
+      careful_sums(row, M, a, out, OP == kTail ? nl : 0, s, t);
+      sum_put(s, t, R.sum_row);
+    } else {
+      running_shift(run, ref * a.c);
+      float s0, s1, t0, t1;
+      unpair(run.s, &s0, &s1);
+      unpair(run.t, &t0, &t1);
+      s0 = warp_sum(s0 + s1);
+      t0 = warp_sum(t0 + t1);
+      if ((tid & 31) == 0) {
+        R.sum_row.a[tid >> 5] = (double)s0;
+        R.sum_row.b[tid >> 5] = (double)t0;
+      }
+    }
     uint32_t kth = 0;
     if constexpr (TOP) kth = kth_key_of_block(order_key(mine), a.k);
+    __syncthreads();
+    if (tid == 0) {
+      double S, t;
+      sum_get(S, t, R.sum_row);
+      if (!wild && M != -INFINITY) {
+        // the exponents were taken from fl(ref c) instead of ref c
+        const double off = (double)run.rc - (double)ref * (double)a.c, f = exp2_small(off);
+        t = f * (t + off * S);
+        S *= f;
+      }
+      if (C > 1) {
+        ex = Exchange{M, S, t, kth};
+      } else {
+        // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
+        R.M = M;
+        R.S = S + ((double)a.c_lo / (double)a.c) * 0.6931471805599453 * t;
+        R.T = t;
+        R.kth = kth;
+      }
+    }
     if (C > 1) {
       cg::cluster_group cl = cg::this_cluster();
-      if (tid == 0) ex = Exchange{M, S, Tt, kth};
       cl.sync();
-      float all = -INFINITY;
-      for (int q = 0; q < C; ++q) {
-        const Exchange* o = cl.map_shared_rank(&ex, q);
-        all = fmaxf(all, o->m);
-        kth = max(kth, o->kth);
+      if (tid == 0) {
+        float all = -INFINITY;
+        double S = 0.0, t = 0.0;
+        for (int q = 0; q < C; ++q) {
+          const Exchange* o = cl.map_shared_rank(&ex, q);
+          all = fmaxf(all, o->m);
+          kth = max(kth, o->kth);
+        }
+        for (int q = 0; q < C; ++q) {
+          const Exchange* o = cl.map_shared_rank(&ex, q);
+          const float m = o->m;
+          const double os = o->s, ot = o->t;
+          if (m == -INFINITY) continue;
+          const double dd = fmax(((double)m - (double)all) * (double)a.c, -(double)kFarBits);
+          const double f = m == all ? 1.0 : exp2(dd);
+          S += os * f;
+          t += f * (ot + (m == all ? 0.0 : dd * os));
+        }
+        R.M = all;
+        R.S = S + ((double)a.c_lo / (double)a.c) * 0.6931471805599453 * t;
+        R.T = t;
+        R.kth = kth;
       }
-      S = Tt = 0.0;
-      for (int q = 0; q < C; ++q) {
-        const Exchange* o = cl.map_shared_rank(&ex, q);
-        const float dd = max_nan((fmaxf(o->m, kLowest) - fmaxf(all, kLowest)) * a.c, -kFarBits);
-        const double f = (double)ex2(dd);
-        S += o->s * f;
-        Tt += f * (o->t + (double)dd * o->s);
-      }
-      M = all;
     }
+    __syncthreads();
 
     // -- most likely tokens ----------------------------------------------------------------------
     // A thread's maximum is one entry, so the k-th largest of the threads' maxima is a lower bound of
     // the row's k-th largest entry; only threads whose maximum reaches it own candidates, and those
     // read their entries again (from L2).
     if constexpr (TOP) {
-      TopShared& top = tp.top;
+      TopShared& top = *reinterpret_cast<TopShared*>(GRAD ? beyond : reinterpret_cast<char*>(dyn));
+      kth = R.kth;
       if (tid == 0) top.count = 0;
       __syncthreads();
       const uint32_t bound = max(kth, kKeyNegInf + 1);
@@ -680,21 +925,25 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
       while (owners) {
         const int l = __ffs(owners) - 1;
         owners &= owners - 1;
-        for (int i = row.v0 + (tid & ~31) + l + (tid & 31) * B; i < row.v1; i += 32 * B) {
+        // vector j of lane l: chunk j / U of its warp, row j % U of the chunk
+        for (int j = lane; j < ring.n * U; j += 32) {
+          const int i = row.v0 + ring.first(j / U) + (j % U) * 32 + l;
+          if (i >= row.v1) break;
           float x[N];
           Elem<T>::unpack(__ldcg(vec + i), x);
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const uint32_t key = order_key(x[j]);
-            if (key >= bound) cand_push(top, key, row.head + i * N + j);
+          for (int b = 0; b < N; ++b) {
+            const uint32_t key = order_key(x[b]);
+            if (key >= bound) cand_push(top, key, row.head + i * N + b);
           }
         }
       }
       if (owner && edge >= 0) {
-        const uint32_t key = order_key(Elem<T>::to(row.x[edge]));
+        const uint32_t key = order_key(x_edge);
         if (key >= bound) cand_push(top, key, edge);
       }
       __syncthreads();
+      const double S = R.S;
       bool again = top.count > kCand || !(S == S);
       if (C > 1) {
         cg::cluster_group cl = cg::this_cluster();
@@ -703,7 +952,7 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
           int at = top.count;
           __syncthreads();
           for (int q = 1; q < C; ++q) {
-            const TopShared* o = cl.map_shared_rank(&tp.top, q);
+            const TopShared* o = cl.map_shared_rank(&top, q);
             const int n = o->count;
             if (n > kCand || at + n > kCand) again = true;
             if (again) break;
@@ -715,12 +964,11 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
         }
       }
       if (part == 0) {
-        if (again) exact_top(row, a.k, kth, top, sh);
+        if (again) exact_top(row, a.k, kth, top, R.part);
         const int n = top.count;
         // rank of a candidate = how many are larger; `per` neighbouring lanes share one
         int per = 1;
         while (per < 32 && 2 * per * n <= B) per *= 2;
-        const double log_s = log(S);
         for (int base = 0; base < n; base += B / per) {
           const int i = base + tid / per;
           int above = 0;
@@ -731,7 +979,7 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
             const int e = (int)~(uint32_t)me;
             const int64_t o = (int64_t)r * a.k + above;
             a.top_idx[o] = e;
-            a.top_val[o] = (float)(((double)Elem<T>::to(row.x[e]) - (double)M) * (double)a.it - log_s);
+            a.top_val[o] = (float)(((double)Elem<T>::to(row.x[e]) - (double)R.M) * (double)a.it - log(S));
           }
         }
         for (int j = n + tid; j < a.k; j += B) {
@@ -741,211 +989,262 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
       }
       // the row is read whole above: no gradient may be written before that is done
       if (C > 1) cg::this_cluster().sync();
+      else __syncthreads();
     }
   }
 
-  // -- statistics of the row, its loss -------------------------------------------------------------
-  float ref = fmaxf(M, kLowest);                  // of the dense part of the gradient
-  double S_dense = S;
-  float ref_row = ref;                            // of the whole row
-  double S_row = S;
-  float ent = 0.0f;
-  if (MODE == kBackward) {
-    const float* st = a.stats_in + (int64_t)r * (OP == kTail ? 4 : 2);
-    ref_row = ref = fmaxf(st[0], kLowest);
-    S_row = S_dense = (double)st[1];
-    if (OP == kTail) {
-      ref = fmaxf(st[2], kLowest);
-      S_dense = (double)st[3];
-    }
-    if (OP == kLogprob && a.weight_entropy) ent = a.entropy_in[r];
-  }
+  // -- the list's part of the loss -------------------------------------------------------------------
   if constexpr (LIST && MODE != kBackward) {
-    ListShared& L = lp.list;
-    if (OP == kTail) {                            // the list's entries join the others'
+    float ref_row = fmaxf(R.M, kLowest);
+    if (OP == kTail) {                            // the list's entries join the others
       float high = -INFINITY;
       for (int j = tid; j < nl; j += B)
         if (L.idx[j] >= 0) high = fmaxf(high, L.x[j]);
-      ref_row = fmaxf(fmaxf(block_max(high, sh), M), kLowest);
-      double sum = 0.0, unused = 0.0;
-      for (int j = tid; j < nl; j += B) {
-        bool count = L.idx[j] >= 0;
-        if (count && L.repeats)
-          for (int i = 0; i < j; ++i) count = count && L.idx[i] != L.idx[j];
-        if (count) sum += exp(((double)L.x[j] - (double)ref_row) * (double)a.it);
-      }
-      block_sum2(sum, unused, sh);
-      S_row = sum + (S != 0.0 ? S * exp(((double)ref - (double)ref_row) * (double)a.it) : 0.0);
+      ref_row = fmaxf(block_max(high, R.max_list), ref_row);
     }
-    if (OP == kTail && S_dense == 0.0) rho = 0.0; // no entry is left for the rest
-    double loss = 0.0, unused = 0.0;
-    const double log_s = log(S_row);
+    double loss = 0.0, sum = 0.0;                 // sum q (log q - z_j), with z from ref_row; sum of exp(z_j)
     for (int j = tid; j < nl; j += B) {
-      if (L.idx[j] < 0 || Q == 0.0) continue;
-      const double lq = OP == kRenorm ? ((double)L.add[j] - list_max) * (double)a.it - list_log : (double)L.add[j];
-      const double q = exp(lq);
-      const double lp_j = S_row == 0.0 ? -(double)INFINITY : ((double)L.x[j] - (double)ref_row) * (double)a.it - log_s;
-      if (!(q == 0.0)) loss += q * (lq - lp_j);
-    }
-    block_sum2(loss, unused, sh);
-    if (!(rho == 0.0))
-      loss += rho * (log(rho) - (((double)ref - (double)ref_row) * (double)a.it + log(S_dense) - log_s));
-    if (Q == 0.0 && rho == 0.0) loss = 0.0;
-    if (part == 0 && tid == 0) {
-      a.out[r] = (float)loss;
-      if (a.stats) {
-        float* st = a.stats + (int64_t)r * (OP == kTail ? 4 : 2);
-        st[0] = ref_row;
-        st[1] = (float)S_row;
-        if (OP == kTail) {
-          st[2] = ref;
-          st[3] = (float)S_dense;
-        }
+      if (L.idx[j] < 0) continue;
+      const double z = ((double)L.x[j] - (double)ref_row) * (double)a.it;
+      const double lq = OP == kRenorm ? ((double)L.v[j] - R.list_max) * (double)a.it : (double)L.v[j];
+      const double q = L.q[j];
+      if (!(q == 0.0)) loss += q * (lq - z);
+      if (OP == kTail) {
+        bool count = true;
+        if (R.repeats)
+          for (int i = 0; i < j; ++i) count = count && L.idx[i] != L.idx[j];
+        if (count) sum += exp(z);
       }
+    }
+    sum_put(loss, sum, R.sum_loss);
+    __syncthreads();
+    if (tid == 0) {
+      double unused;
+      R.ref_row = ref_row;
+      if (OP == kTail) {
+        const float ref = fmaxf(R.M, kLowest);
+        sum_get(unused, sum, R.sum_loss);
+        R.S_row = sum + (R.S != 0.0 ? R.S * (ref == ref_row ? 1.0 : exp(((double)ref - (double)ref_row) * (double)a.it)) : 0.0);
+        if (R.S == 0.0) R.rho = 0.0;              // no entry is left for the rest
+      } else {
+        R.S_row = R.S;
+      }
+    }
+  } else if constexpr (MODE != kBackward) {
+    if (tid == 0) {
+      R.ref_row = fmaxf(R.M, kLowest);
+      R.S_row = R.S;
     }
   }
-  if (OP == kTail && MODE == kBackward && S_dense == 0.0) rho = 0.0;
-  if (OP == kLogprob && MODE != kBackward) {
-    const double log_s = log(S);
-    const bool nothing = S == 0.0;
-    ent = nothing ? 0.0f : (float)(log_s - 0.6931471805599453 * (Tt / S));
-    if (part == 0 && tid == 0) {
+
+  // -- the dense gradient's factors ----------------------------------------------------------------
+  if constexpr (GRAD) {
+    if (tid == 0) {
+      float ref;
+      double S;
+      float ent = 0.0f;
+      if (MODE == kBackward) {
+        const float* st = a.stats_in + (int64_t)r * (OP == kTail ? 4 : 2);
+        R.ref_row = ref = fmaxf(st[0], kLowest);
+        R.S_row = S = (double)st[1];
+        if (OP == kTail) {
+          ref = fmaxf(st[2], kLowest);
+          S = (double)st[3];
+          if (S == 0.0) R.rho = 0.0;
+        }
+        if (OP == kLogprob && w_h != 0.0f) ent = a.entropy_in[r];
+      } else {
+        ref = fmaxf(R.M, kLowest);
+        S = R.S;
+        if (OP == kLogprob && w_h != 0.0f) ent = (float)(log(S) - 0.6931471805599453 * (R.T / S));
+      }
+      double A, Bl = 0.0;
+      const double it = (double)a.it;
+      if (OP == kLogprob) {
+        A = -it * ((double)w + (LIST ? R.Q : 0.0) + (w_h != 0.0f ? (double)w_h * (double)ent : 0.0));
+        Bl = -it * (double)w_h * 0.6931471805599453;
+        R.A_list = (float)A;
+      } else if (OP == kRenorm) {
+        A = it * (double)w * R.Q;
+        R.A_list = (float)A;
+      } else {
+        const double Rr = S == 0.0 ? 0.0
+                          : S / R.S_row * (ref == R.ref_row ? 1.0 : exp(((double)ref - (double)R.ref_row) * it));
+        A = it * (double)w * ((R.Q + R.rho) * Rr - R.rho);
+        R.A_list = (float)(it * (double)w * (R.Q + R.rho));
+      }
+      dense_factors(R, ref, S, A, Bl, a);
+    }
+  }
+  // every CTA of the row has read its list's and target's entries; with no gradient: the others may
+  // still read this CTA's shared memory
+  if (C > 1 && MODE != kBackward) cg::this_cluster().sync();
+  else __syncthreads();
+
+  // -- results per row, by a thread that nothing waits for -----------------------------------------
+  if (MODE != kBackward && part == 0 && tid == 32) {
+    const double S = R.S, S_row = R.S_row, log_s = log(S_row);
+    const float ref = fmaxf(R.M, kLowest);
+    if (OP == kLogprob) {
+      const bool nothing = S == 0.0;
       if (a.out)
         a.out[r] = target < 0 ? 0.0f
                    : nothing  ? -INFINITY
-                              : (float)(((double)x_target - (double)M) * (double)a.it - log_s);
-      if (a.entropy) a.entropy[r] = ent;
-      if (a.stats) {
-        a.stats[2 * (int64_t)r] = ref;
-        a.stats[2 * (int64_t)r + 1] = (float)S;
+                              : (float)(((double)x_target - (double)ref) * (double)a.it - log_s);
+      if (a.entropy) a.entropy[r] = nothing ? 0.0f : (float)(log_s - 0.6931471805599453 * (R.T / S));
+    } else {
+      double loss, unused;
+      sum_get(loss, unused, R.sum_loss);
+      if (OP == kRenorm) {
+        const double sum = R.list_log;            // of the probabilities before their division by it
+        loss = R.Q == 0.0 ? 0.0 : loss / sum - log(sum) + (S_row == 0.0 ? (double)INFINITY : log_s);
+      } else {
+        const double rho = R.rho;
+        if (R.Q == 0.0 && rho == 0.0) {
+          loss = 0.0;
+        } else if (S_row == 0.0) {
+          loss = R.Q != 0.0 ? (double)INFINITY : 0.0;
+        } else {
+          loss += (R.Q + rho) * log_s;
+          if (!(rho == 0.0)) loss += rho * (log(rho) - ((double)ref - (double)R.ref_row) * (double)a.it - log(S));
+        }
+      }
+      a.out[r] = (float)loss;
+    }
+    if (a.stats) {
+      float* st = a.stats + (int64_t)r * (OP == kTail ? 4 : 2);
+      st[0] = R.ref_row;
+      st[1] = (float)S_row;
+      if (OP == kTail) {
+        st[2] = ref;
+        st[3] = (float)S;
       }
     }
   }
 
-  // the others may still read this CTA's shared memory
-  if (MODE == kForward && !TOP && C > 1) cg::this_cluster().sync();
-
   // -- gradient ----------------------------------------------------------------------------------
-  if constexpr (MODE != kForward) {
-    // dense: g = p (A + Bl log2 p), p = 2^((x - ref) c - l2)
-    float A, Bl = 0.0f, A_list;
-    if (OP == kLogprob) {
-      A = (float)(-(double)a.it * ((double)w + w_list + (double)w_h * (double)ent));
-      Bl = -a.it * w_h * 0.69314718f;
-      A_list = A;
-    } else if (OP == kRenorm) {
-      A_list = A = (float)((double)a.it * (double)w * Q);
-    } else {
-      const double R = S_dense != 0.0 ? S_dense / S_row * exp(((double)ref - (double)ref_row) * (double)a.it) : 0.0;
-      A_list = (float)((double)a.it * (double)w * (Q + rho));
-      A = (float)((double)a.it * (double)w * ((Q + rho) * R - rho));
-    }
-    const bool nothing = S_row == 0.0;            // nothing but -inf: no distribution, no gradient
-    if (nothing) A = A_list = Bl = 0.0f;
-    const float l2 = S_dense == 0.0 ? 0.0f : (float)log2(S_dense);
+  if constexpr (GRAD) {
+    const float kf = R.k, A = R.A, Bl = R.Bl, ref = R.ref;
+    const bool nothing = R.S_row == 0.0;          // nothing but -inf: no distribution, no gradient
     // no weight: zeros, whatever the row holds
-    const bool none = OP == kLogprob ? (w == 0.0f && w_h == 0.0f && w_size == 0.0) : w == 0.0f;
+    const bool none = nothing || (OP == kLogprob ? (w == 0.0f && w_h == 0.0f && (!LIST || R.rho == 0.0)) : w == 0.0f);
+    const bool wild = R.wild;
     T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
-    if (C > 1 && MODE == kFused) {
-      if (!TOP) cg::this_cluster().sync();        // every CTA has read the list's and target's entries
-    } else {
-      __syncthreads();
-    }
-    if (none) A = Bl = 0.0f;
-    const f2 nref = pair(-ref, -ref), c2 = pair(a.c, a.c), nl2 = pair(-l2, -l2), A2 = pair(A, A), B2 = pair(Bl, Bl);
-    auto grad = [&](float* x, int n) {
+    const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
+    auto grad = [&](uint4 v) {
+      float x[N];
+      Elem<T>::unpack(v, x);
 #pragma unroll
-      for (int i = 0; i < n; i += 2) {
-        float d0, d1;
-        unpair(add2(pair(x[i], x[i + 1]), nref), &d0, &d1);
-        const f2 d = pair(max_nan(d0, -a.far), max_nan(d1, -a.far));
-        const f2 q = fma2(d, c2, nl2);
+      for (int i = 0; i < N; i += 2) {
         float q0, q1;
+        f2 q = fma2(pair(x[i], x[i + 1]), c2, nk), g = A2;
         unpair(q, &q0, &q1);
-        const f2 p = pair(ex2(q0), ex2(q1));
-        const f2 g = OP == kLogprob ? mul2(p, fma2(q, B2, A2)) : mul2(p, A2);
-        unpair(g, &x[i], &x[i + 1]);
+        if (OP == kLogprob && Bl != 0.0f) g = fma2(pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), B2, A2);
+        unpair(mul2(pair(ex2(q0), ex2(q1)), g), &x[i], &x[i + 1]);
       }
+      return Elem<T>::pack(x);
     };
-    if (((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0) {
-      uint4* dvec = reinterpret_cast<uint4*>(dx + row.head);
-      for (int i = row.v0 + tid; i < row.v1; i += U * B) {
-        uint4 v[U];
+    auto grad_one = [&](float x) {
+      float q = fmaf(x, a.c, -kf);
+      if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
+      return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
+    };
+    const int e0 = row.head + row.v0 * N, e1 = row.head + row.v1 * N;
+    const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
+    uint4* dvec = reinterpret_cast<uint4*>(dx + row.head) + row.v0;
+    if (early && (none || wild || !in_step))
+      for (int q = 0; q < min(kStages, ring.n); ++q) ring.wait(q, a.d_status);
+    if (none) {
+      if (in_step) {
+        for (int i = tid; i < own; i += B) __stcs(dvec + i, make_uint4(0, 0, 0, 0));
+      } else {
+        for (int e = e0 + tid; e < e1; e += B) dx[e] = Elem<T>::from(0.0f);
+      }
+      if (edge >= 0) dx[edge] = Elem<T>::from(0.0f);
+    } else {
+      if (in_step && !wild) {
+        // forward: the row's last chunks are still in the ring, so it goes backwards
+        for (int j = 0; j < ring.n; ++j) {
+          const int q = MODE == kFused ? ring.n - 1 - j : j;
+          if (MODE == kBackward || j >= kStages) ring.wait(q, a.d_status);
+          const uint4* at = ring.at(q);
+          uint4* to = dvec + ring.first(q);
+          const int left = own - ring.first(q);
+          if (left >= kChunk) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int q = i + u * B;
-          if (q < row.v1 && !none) v[u] = __ldcs(vec + q);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int q = i + u * B;
-          if (q >= row.v1) break;
-          float x[N];
-          if (none) {
-            v[u] = make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < U; ++u) __stcs(to + u * 32 + lane, grad(at[u * 32 + lane]));
           } else {
-            Elem<T>::unpack(v[u], x);
-            grad(x, N);
-            v[u] = Elem<T>::pack(x);
+            for (int u = lane; u < left; u += 32) __stcs(to + u, grad(at[u]));
           }
-          __stcs(dvec + q, v[u]);
+          __syncwarp();
+          const int next = MODE == kFused ? q - kStages : q + kStages;
+          if (next >= 0 && next < ring.n) ring.issue(next);
         }
+      } else {                                    // rows that start at different offsets from 16 bytes
+        for (int e = e0 + tid; e < e1; e += B) dx[e] = grad_one(Elem<T>::to(row.x[e]));
       }
-    } else {                                      // rows that start at different offsets from 16 bytes
-      for (int e = row.head + row.v0 * N + tid; e < row.head + row.v1 * N; e += B) {
-        float x[2] = {none ? 0.0f : Elem<T>::to(row.x[e]), -INFINITY};
-        if (!none) grad(x, 2);
-        dx[e] = Elem<T>::from(x[0]);
-      }
+      if (edge >= 0) dx[edge] = grad_one(x_edge);
     }
-    const int edge = row.edge(tid);
-    if (edge >= 0) {
-      float x[2] = {none ? 0.0f : Elem<T>::to(row.x[edge]), -INFINITY};
-      if (!none) grad(x, 2);
-      dx[edge] = Elem<T>::from(x[0]);
-    }
+    ring.drain();
+    if (none) return;
     __syncthreads();
     // the list's entries, over what the dense part wrote there
-    if (none || nothing) return;
     auto value = [&](float x, double add) {
-      const double lp2 = ((double)x - (double)ref_row) * (double)a.it - log(S_row);
-      const double p = exp(lp2);
-      double g = p * (double)A_list + add;
-      if (OP == kLogprob && Bl != 0.0f && p != 0.0) g -= (double)a.it * (double)w_h * p * lp2;
+      const double lp2 = ((double)x - (double)R.ref_row) * (double)a.it;
+      const double p = exp(lp2) / R.S_row;
+      double g = p * (double)R.A_list + (double)a.it * add;
+      if (OP == kLogprob && w_h != 0.0f && p != 0.0) g -= (double)a.it * (double)w_h * p * (lp2 - log(R.S_row));
       return (float)g;
     };
     if constexpr (LIST) {
-      ListShared& L = lp.list;
+      const double per = OP == kRenorm ? -(double)w / R.list_log : -(double)w;
       for (int j = tid; j < nl; j += B) {
         const int e = L.idx[j];
         if (e < 0 || !row.owns(e)) continue;
         double add = 0.0;
         bool mine = true;
-        for (int i = L.repeats ? 0 : j; i < (L.repeats ? nl : j + 1); ++i) {
+        for (int i = R.repeats ? 0 : j; i < (R.repeats ? nl : j + 1); ++i) {
           if (L.idx[i] != e) continue;
           if (i < j) mine = false;
-          if (OP == kLogprob) add += (double)a.it * (double)L.add[i];
-          else if (Q != 0.0) {
-            const double lq = OP == kRenorm ? ((double)L.add[i] - list_max) * (double)a.it - list_log : (double)L.add[i];
-            add -= (double)a.it * (double)w * exp(lq);
-          }
+          if (OP == kLogprob) add += (double)L.v[i];
+          else if (R.Q != 0.0) add += per * L.q[i];
         }
         if (mine) dx[e] = Elem<T>::from(value(L.x[j], add));
       }
     } else {
-      if (tid == 0 && target >= 0 && row.owns(target))
-        dx[target] = Elem<T>::from(value(x_target, (double)a.it * (double)w));
+      if (tid == 0 && target >= 0 && row.owns(target)) dx[target] = Elem<T>::from(value(x_target, (double)w));
     }
   }
 }
 
 // ---- launch -----------------------------------------------------------------------------------------
 
+constexpr size_t kSliceMost = 200 << 10;          // a slice whose second read still finds it in L2
+
 template <class T, int OP, bool TOP, int MODE>
-int voc_launch(const VocArgs& a, int threads, cudaStream_t st) {
+int voc_of_type(VocArgs a, cudaStream_t st) {
+  const int64_t nv = cdiv(a.vocab, Elem<T>::N);
+  // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
+  int split = 1;
+  while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
+  if (MODE == kFused)
+    while (split < 8 && (size_t)nv * 16 > split * kSliceMost) split *= 2;
+  a.split = split;
+  int threads = 64;
+  while (threads < 256 && (int64_t)threads * kUnroll * split < nv) threads *= 2;
+  if (TOP) while (threads < kVocThreads && threads < 2 * a.k) threads *= 2;
+  size_t smem = ring_bytes(threads);
+  if (OP != kLogprob || MODE == kBackward) smem += List::bytes(OP == kLogprob ? a.k + 1 : a.k);
+  if (TOP) smem = MODE == kFused ? smem + sizeof(TopShared) : smem > sizeof(TopShared) ? smem : sizeof(TopShared);
+  auto* kernel = voc_kernel<T, OP, TOP, MODE>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return GSPARSE_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.rows * a.split));
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -955,7 +1254,7 @@ int voc_launch(const VocArgs& a, int threads, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = MODE != kBackward && a.split > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, voc_kernel<T, OP, TOP, MODE>, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
     cudaGetLastError();
     return GSPARSE_ERR_CUDA;
   }
@@ -963,19 +1262,10 @@ int voc_launch(const VocArgs& a, int threads, cudaStream_t st) {
 }
 
 template <int OP, bool TOP, int MODE>
-int voc_by_type(int32_t dtype, VocArgs a, cudaStream_t st) {
-  const int n = dtype == GSPARSE_F32 ? 4 : 8;
-  const int64_t nv = cdiv(a.vocab, n);
-  // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
-  int split = 1;
-  while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
-  a.split = split;
-  int threads = 64;
-  while (threads < kVocThreads && (int64_t)threads * kVocUnroll * split < nv) threads *= 2;
-  if (TOP) while (threads < kVocThreads && threads < 2 * a.k) threads *= 2;
-  if (dtype == GSPARSE_F32) return voc_launch<float, OP, TOP, MODE>(a, threads, st);
-  if (dtype == GSPARSE_BF16) return voc_launch<__nv_bfloat16, OP, TOP, MODE>(a, threads, st);
-  return voc_launch<__half, OP, TOP, MODE>(a, threads, st);
+int voc_by_type(int32_t dtype, const VocArgs& a, cudaStream_t st) {
+  if (dtype == GSPARSE_F32) return voc_of_type<float, OP, TOP, MODE>(a, st);
+  if (dtype == GSPARSE_BF16) return voc_of_type<__nv_bfloat16, OP, TOP, MODE>(a, st);
+  return voc_of_type<__half, OP, TOP, MODE>(a, st);
 }
 
 bool voc_dtype(int32_t t) { return t == GSPARSE_F32 || t == GSPARSE_BF16 || t == GSPARSE_F16; }
@@ -996,7 +1286,9 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
   a.c = (float)c;
   a.c_lo = (float)(c - (double)a.c);
   a.far = kFarBits / a.c;
+  a.ref_min = -kWildBits / a.c;
   if (!isfinite(a.c) || !isfinite(a.far) || a.far == 0.0f) return GSPARSE_ERR_UNSUPPORTED;
+  if (a.ref_min < -kLowestSafe) a.ref_min = -kLowestSafe;
   a.it = inv_temperature;
   a.logits = logits;
   a.dlogits = dlogits;

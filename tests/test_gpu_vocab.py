@@ -357,8 +357,9 @@ def check_distill(x, dtype, idx, val, tail, temperature=1.0, val_dtype="fp32", w
     back = gs.distill_topk_backward(x, r.stats, ti, tv, dev(w), tail=tail, temperature=temperature)
     # the statistics were rounded to fp32 on the way: the tolerance has room for it (LSE holds 64 u)
     close(back, grad, tol, "backward")
+    # without the gradient the row may be added in another order: the loss to the same tolerance
     plain = gs.distill_topk(x, ti, tv, tail=tail, temperature=temperature)
-    assert torch.equal(plain.loss, r.loss) or bool(torch.isnan(r.loss).any())
+    close(plain.loss, want, 2 * lse_tol(V) + 2 * U * np.abs(np.where(np.isfinite(want), want, 0)), "loss alone")
     return r
 
 
