@@ -44,6 +44,7 @@ struct VocArgs {
   void* dlogits;
   int64_t stride, dstride;       // elements
   int32_t rows, vocab, split;    // split = CTAs per row
+  int32_t slice;                 // vectors of a CTA's slice in shared memory
   int32_t k;                     // list length: alternatives wanted (forward), given (backward), or the teacher's
   int32_t val_dtype;
   float it, c, c_lo;             // c + c_lo = it log2(e)
@@ -68,6 +69,7 @@ struct VocArgs {
 template <class T> struct Elem;
 template <> struct Elem<float> {
   static constexpr int N = 4;
+  static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }   // -inf
   static __device__ __forceinline__ float to(float x) { return x; }
   static __device__ __forceinline__ float from(float x) { return x; }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
@@ -89,6 +91,7 @@ template <> struct Elem<float> {
 };
 template <> struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
+  static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }   // -inf
   static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
   template <int NV> static __device__ __forceinline__ float high(const uint4* v) {
@@ -123,6 +126,7 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<__half> {
   static constexpr int N = 8;
+  static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u); }   // -inf
   static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
   template <int NV> static __device__ __forceinline__ float high(const uint4* v) {
@@ -602,11 +606,24 @@ struct Ring {
   }
 };
 
+// The thread's maximum over the slice, NaN passed over; the entries in `out` left out.
+template <class T>
+__device__ __noinline__ float careful_max(const Row<T>& row, const int32_t* out, int n_out, int tid, int threads) {
+  float m = -INFINITY;
+  for (int e = tid; e < row.V; e += threads) {
+    float x = Elem<T>::to(row.x[e]);
+    for (int j = 0; j < n_out; ++j)
+      if (out[j] == e) x = -INFINITY;
+    m = fmaxf(m, x);
+  }
+  return m;
+}
+
 // The thread's sums over the CTA's slice relative to M, entry by entry with the difference taken first: for rows
 // whose maximum times c is beyond 2^100, where fl(x c - rc) would overflow. out: entries left out.
 template <class T>
-__device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocArgs& a, const int32_t* out, int n_out,
-                                          double& S, double& Tt) {
+__device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocArgs& a, const int32_t* out, int n_out, int tid,
+                                          int threads, double& S, double& Tt) {
   double s = 0.0, t = 0.0;
   auto one = [&](int e) {
     float x = Elem<T>::to(row.x[e]);
@@ -616,9 +633,11 @@ __device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocA
     s += (double)y;
     t += (double)y * (double)q;
   };
-  for (int e = row.head + row.v0 * Elem<T>::N + threadIdx.x; e < row.head + row.v1 * Elem<T>::N; e += blockDim.x) one(e);
-  const int edge = row.edge(threadIdx.x);
-  if (edge >= 0) one(edge);
+  for (int e = row.head + row.v0 * Elem<T>::N + tid; e < row.head + row.v1 * Elem<T>::N; e += threads) one(e);
+  if (row.first)
+    for (int e = tid; e < row.head; e += threads) one(e);
+  if (row.last)
+    for (int e = row.tail0() + tid; e < row.V; e += threads) one(e);
   S = s;
   Tt = t;
 }
@@ -655,7 +674,8 @@ struct RowShared {
 // The factors of the dense gradient for p = 2^((x - ref) c) / S, g = p (A + Bl log2 p).
 // With S = 2^E s, 1 <= s < 2, p = 2^(x c - k) f for k = fl(fl(ref c) + E) and f = 2^(k - E - ref c) / s: no
 // logarithm, and no rounding of k is left in p.
-__device__ __forceinline__ void dense_factors(RowShared& R, float ref, double S, double A, double Bl, const VocArgs& a) {
+template <class Out>
+__device__ __forceinline__ void dense_factors(Out& R, float ref, double S, double A, double Bl, const VocArgs& a) {
   R.ref = ref;
   R.wild = !(fabsf(ref) * a.c <= kWildBits);
   if (S == 0.0) {                                 // -inf alone, and entries that the list writes
@@ -845,7 +865,7 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
       const int32_t* out = nullptr;
       if constexpr (OP == kTail) out = L.idx;
       double s, t;
-      careful_sums(row, M, a, out, OP == kTail ? nl : 0, s, t);
+      careful_sums(row, M, a, out, OP == kTail ? nl : 0, tid, B, s, t);
       sum_put(s, t, R.sum_row);
     } else {
       running_shift(run, ref * a.c);
@@ -1217,18 +1237,849 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
   }
 }
 
+// ---- sums without a running maximum ---------------------------------------------------------------------
+
+// Sums over a lane's entries of e = 2^q and e q, q = fl(x c - rc). rc starts as the largest entry of the
+// warp's first chunk; fp32 takes entries far above it, and a chunk that takes the sums beyond 2^60
+// moves it. Saves half an instruction per entry and a branch per chunk against the running maximum.
+struct Sums {
+  float rc;
+  f2 s, t;
+  // entries before rc is set that are below ref_min (a row of the type's lowest value, say), with
+  // their own maximum and the difference taken first; they count where the row has no others
+  float low_m, low_s, low_t;
+  bool have, huge;        // rc is set; an entry is beyond -ref_min
+};
+
+// What the fast sums cannot take: -inf (0 * -inf makes t NaN), or entries far above rc. The vectors
+// again, with rc moved up to them and the exponents clamped.
+template <class T, int NV>
+__device__ __noinline__ void sums_slow(Sums& r, const uint4* v, f2 s, f2 t, const VocArgs& a) {
+  constexpr int N = Elem<T>::N;
+  Running m{0.0f, r.rc, s, t};
+  float high = -INFINITY;
+  for (int u = 0; u < NV; ++u) {
+    float x[N];
+    Elem<T>::unpack(v[u], x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) high = fmaxf(high, x[i]);
+  }
+  if (high > -a.ref_min) r.huge = true;
+  else if (high * a.c > m.rc) running_shift(m, high * a.c);
+  const f2 c2 = pair(a.c, a.c), nrc = pair(-m.rc, -m.rc);
+  for (int u = 0; u < NV; ++u) {
+    float x[N];
+    Elem<T>::unpack(v[u], x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float q0, q1;
+      unpair(fma2(pair(x[i], x[i + 1]), c2, nrc), &q0, &q1);
+      q0 = max_nan(q0, -kFarBits);
+      q1 = max_nan(q1, -kFarBits);
+      const f2 e = pair(ex2(q0), ex2(q1));
+      m.s = add2(m.s, e);
+      m.t = fma2(e, pair(q0, q1), m.t);
+    }
+  }
+  r.rc = m.rc;
+  r.s = m.s;
+  r.t = m.t;
+}
+
+// Adds NV vectors. Entry by entry: unpack, half a fused multiply-add, 2^q, half an addition, half a
+// fused multiply-add.
+template <class T, int NV>
+__device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs& a) {
+  constexpr int N = Elem<T>::N;
+  const f2 c2 = pair(a.c, a.c), nrc = pair(-r.rc, -r.rc);
+  f2 s = r.s, t = r.t;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    float x[N];
+    Elem<T>::unpack(v[u], x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const f2 q = fma2(pair(x[i], x[i + 1]), c2, nrc);
+      float q0, q1;
+      unpair(q, &q0, &q1);
+      const f2 e = pair(ex2(q0), ex2(q1));
+      s = add2(s, e);
+      t = fma2(e, q, t);
+    }
+  }
+  float t0, t1;
+  unpair(t, &t0, &t1);
+  if (!(fabsf(t0 + t1) < 1.0e18f)) {
+    Sums again = r;                               // copies: what a call may touch must not live in registers' stead
+    uint4 w[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) w[u] = v[u];
+    sums_slow<T, NV>(again, w, r.s, r.t, a);
+    r = again;
+  } else {
+    r.s = s;
+    r.t = t;
+  }
+}
+
+// A chunk before rc is set whose largest entry over the warp, top, is not from ref_min to -ref_min.
+template <class T, int NV>
+__device__ __noinline__ void sums_odd(Sums& r, const uint4* v, float top, const VocArgs& a) {
+  constexpr int N = Elem<T>::N;
+  if (top > 0.0f) r.huge = true;
+  for (int u = 0; u < NV; ++u) {
+    float x[N];
+    Elem<T>::unpack(v[u], x);
+    for (int i = 0; i < N; ++i) {
+      if (x[i] != x[i]) r.s = pair(NAN, NAN);
+      if (!(x[i] > -INFINITY) || r.huge) continue;
+      if (x[i] > r.low_m) {
+        const float d = fmaxf((r.low_m - x[i]) * a.c, -kFarBits), f = ex2(d);
+        r.low_t = f * (r.low_t + d * r.low_s);
+        r.low_s *= f;
+        r.low_m = x[i];
+      }
+      const float d = fmaxf((x[i] - r.low_m) * a.c, -kFarBits), e = ex2(d);
+      r.low_s += e;
+      r.low_t = fmaf(e, d, r.low_t);
+    }
+  }
+}
+
+// Sets rc from a chunk's largest entry over the warp; false if the chunk is not for the sums.
+template <class T, int NV>
+__device__ __forceinline__ bool sums_start(Sums& r, const uint4* v, const VocArgs& a) {
+  const float top = warp_max(Elem<T>::template high<NV>(v));
+  if (top >= a.ref_min && top <= -a.ref_min) {
+    r.rc = top * a.c;
+    r.have = true;
+    return true;
+  }
+  Sums again = r;
+  uint4 w[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) w[u] = v[u];
+  sums_odd<T, NV>(again, w, top, a);
+  r = again;
+  return false;
+}
+
+// Reads a row's vector past L1. (Kept coherent: the gradient may take the logits' place.)
+__device__ __forceinline__ uint4 ld_row(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// ---- a row per cluster, streamed -----------------------------------------------------------------------
+
+// A cluster of C CTAs takes a row; W warps of a CTA stream its slice chunk by chunk (U vectors per lane, the
+// next chunk's loads in registers while one is worked on) and one more warp reads the row's list and
+// writes its results. The warps meet once: each leaves its partial sums with every CTA of the row, and
+// joins the partial sums of all by itself.
+// What was measured (4000 rows of 85000 bf16): plain loads through registers with 64 KB a SM on their way read
+// the rows in 95 us; bulk and cp.async copies with 96 to 192 KB on their way took 109 to 120 us, rings of
+// them under this kernel 133 to 190 us.
+// RES (the gradient): the slice stays in shared memory between the sums and the gradient. Reading it again from
+// L2 costs half as much traffic again between L2 and the SMs, which is what bounds that form.
+constexpr int kRowWarps = 7;                      // streaming warps, at most
+constexpr int kRowCtas = 4;                       // per SM
+constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at most
+
+struct StreamShared {
+  uint64_t listed, sums, ready;                   // the list is there; all partial sums; results in 64 bits
+  float rc[kParts], s[kParts], t[kParts];
+  int kind[kParts];                               // 0 none, 1 sums, 2 beyond range, 3 below ref_min
+  int repeats;                                    // an index stands in the list twice
+  uint32_t hit[kHitWords];                        // chunks of the slice that hold entries of the list (modulo)
+  float w, w_h, x_target;
+  int target;
+  double Q, rho, list_max, list_sum;
+  float list_high;                                // kTail: largest logit at the list's entries
+  double list_exp;                                // and the sum of exp(z - its z) over them
+  // the results of the careful route
+  float k, A, Bl, ref, ref_row;
+  int wild, none;
+  double A_list, S_row, per, log_s;
+};
+
+// Stores to and arrivals at another CTA of the cluster.
+__device__ __forceinline__ uint32_t peer(const void* p, int q) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
+  return r;
+}
+__device__ __forceinline__ void peer_store(float* p, int q, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(p, q)), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store(int* p, int q, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer(p, q)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint64_t* bar, int q) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer(bar, q)) : "memory");
+}
+__device__ __forceinline__ bool peer_wait_bounded(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > kWaitCycles) return false;
+  }
+}
+
+// Shared memory: RES: the slice; else a chunk per warp for those that hold entries of the list. Then the list.
+template <class T, int OP, int MODE, bool RES>
+__global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_kernel(const __grid_constant__ VocArgs a) {
+  constexpr int N = Elem<T>::N, U = kUnroll;
+  constexpr bool LIST = OP != kLogprob;
+  constexpr bool GRAD = MODE == kFused;
+  extern __shared__ __align__(16) uint4 dyn[];
+  __shared__ StreamShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = (blockDim.x >> 5) - 1;
+  const int C = a.split, part = (int)(blockIdx.x % (unsigned)C), r = (int)(blockIdx.x / (unsigned)C);
+  const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C);
+  const int own = row.v1 - row.v0, step = W * kChunk;
+  uint4* const buf = RES ? dyn : dyn + warp * kChunk;
+  List L;
+  if constexpr (LIST) L.carve(dyn + (RES ? a.slice : W * kChunk), a.k);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.listed, 1);
+    mbar_init(&sh.sums, GRAD || part == 0 ? C * W : 1);
+    mbar_init(&sh.ready, 1);
+    fence_mbarrier_init();
+  }
+  pdl_begin();
+  // the first chunk is on its way before the CTAs meet
+  const uint4* at = row.vec() + row.v0 + warp * kChunk + lane;
+  uint4 nx[U];
+  auto request = [&](int left) {                  // of the slice, from the chunk's first vector on
+    if (left >= kChunk) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) nx[u] = ld_row(at + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * 32 + lane < left) nx[u] = ld_row(at + u * 32);
+    }
+    at += step;
+  };
+  if (warp < W) request(own - warp * kChunk);
+  // the first warp's lanes take the head and the tail, one entry each
+  int edge = -1;
+  if (warp == 0) {
+    if (row.first && lane < row.head) edge = lane;
+    else if (row.last && lane >= 8 && row.tail0() + lane - 8 < row.V) edge = row.tail0() + lane - 8;
+  }
+  float x_edge = -INFINITY;
+  if (edge >= 0) x_edge = Elem<T>::to(row.x[edge]);
+  if (C > 1) cg::this_cluster().sync();
+  else __syncthreads();
+
+  bool ok = true;                                 // a wait that runs out ends all later ones
+  auto wait = [&](uint64_t* bar) {
+    if (ok && !peer_wait_bounded(bar, 0)) {
+      ok = false;
+      raise(a.d_status, GSPARSE_DERR_TIMEOUT);
+    }
+  };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+  };
+
+  if (warp == W) {
+    // -- the row's list ----------------------------------------------------------------------------
+    float w = 0.0f, w_h = 0.0f;
+    if (GRAD) {
+      w = a.weight ? a.weight[r] : 0.0f;
+      w_h = OP == kLogprob && a.weight_entropy ? a.weight_entropy[r] : 0.0f;
+    }
+    if (OP == kLogprob) {
+      int target = a.targets ? a.targets[r] : -1;
+      if (target < -1 || target >= a.vocab) {
+        if (lane == 0 && part == 0) raise(a.d_status, GSPARSE_DERR_INDEX_RANGE);
+        target = -1;
+      }
+      w = target >= 0 ? w : 0.0f;
+      if (lane == 0) {
+        sh.target = target;
+        sh.x_target = target >= 0 ? Elem<T>::to(row.x[target]) : 0.0f;
+        sh.w = w;
+        sh.w_h = w_h;
+      }
+    }
+    if constexpr (LIST) {
+      if (GRAD || OP == kTail)
+        for (int i = lane; i < L.slots; i += 32) L.table[i] = 0;
+      if (lane < kHitWords) sh.hit[lane] = 0;
+      float vmax = -INFINITY;
+#pragma unroll 4
+      for (int j = lane; j < a.k; j += 32) {
+        const int64_t o = (int64_t)r * a.k + j;
+        int e = a.list_idx[o];
+        const float v = list_value(a.list_val, a.val_dtype, o);
+        if (e < -1 || e >= a.vocab) {
+          if (part == 0) raise(a.d_status, GSPARSE_DERR_INDEX_RANGE);
+          e = -1;
+        }
+        L.idx[j] = e;
+        L.v[j] = v;
+        if (e >= 0) vmax = fmaxf(vmax, v);
+      }
+#pragma unroll 4
+      for (int j = lane; j < a.k; j += 32) {
+        const int e = L.idx[j];
+        L.x[j] = e >= 0 ? Elem<T>::to(row.x[e]) : 0.0f;
+      }
+      vmax = fmaxf(warp_max(vmax), kLowest);
+      __syncwarp();
+      double sum = 0.0;
+      bool repeats = false;
+      for (int j = lane; j < a.k; j += 32) {
+        const int e = L.idx[j];
+        if (e < 0) continue;
+        const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)vmax) * (double)a.it : (double)L.v[j]);
+        L.q[j] = q;
+        sum += q;
+        if (GRAD || OP == kTail) {
+          repeats |= L.add(e);
+          const int at = e < row.head ? -1 : (e - row.head) / N - row.v0;   // vector of the slice
+          if (at >= 0 && at < row.v1 - row.v0) {
+            const int c = at / kChunk;
+            atomicOr(&sh.hit[(c >> 5) & (kHitWords - 1)], 1u << (c & 31));
+          }
+        }
+      }
+      sum = warp_sum(sum);
+      repeats = __any_sync(kFull, repeats);
+      if (lane == 0) {
+        sh.w = w;
+        sh.repeats = repeats;
+        sh.list_max = (double)vmax;
+        sh.list_sum = sum;
+        sh.Q = OP == kTail ? sum : sum == 0.0 ? 0.0 : sum == sum ? 1.0 : sum;
+        sh.rho = OP == kTail ? (sum == sum ? fmax(1.0 - sum, 0.0) : sum) : 0.0;
+      }
+    }
+    if constexpr (OP == kTail && GRAD) {
+      // what the entries add to the row's sum, from the largest of them
+      float high = -INFINITY;
+      for (int j = lane; j < a.k; j += 32)
+        if (L.idx[j] >= 0) high = fmaxf(high, L.x[j]);
+      high = warp_max(high);
+      double add = 0.0;
+      __syncwarp();
+      for (int j = lane; j < a.k; j += 32) {
+        if (L.idx[j] < 0) continue;
+        bool count = true;
+        if (sh.repeats)
+          for (int i = 0; i < j; ++i) count = count && L.idx[i] != L.idx[j];
+        if (count && !(L.x[j] == -INFINITY)) add += exp(((double)L.x[j] - (double)high) * (double)a.it);
+      }
+      add = warp_sum(add);
+      if (lane == 0) {
+        sh.list_high = high;
+        sh.list_exp = add;
+      }
+    }
+    arrive(&sh.listed);
+    if (!GRAD && part != 0) {
+      if (C > 1) cg::this_cluster().sync();
+      return;
+    }
+
+    // -- the row's results in 64 bits ------------------------------------------------------------------
+    wait(&sh.sums);
+    int kind = 0;
+    float M = -INFINITY;                          // what the sums are taken from
+    double Sd = 0.0, Td = 0.0;
+    {
+      const int n = C * W, k0 = lane < n ? sh.kind[lane] : 0, k1 = lane + 32 < n ? sh.kind[lane + 32] : 0;
+      const bool huge = __any_sync(kFull, k0 == 2 || k1 == 2), normal = __any_sync(kFull, k0 == 1 || k1 == 1);
+      // of the parts with a normal reference (kind 1) where there are any, else of those below ref_min
+      const int which = normal ? 1 : 3;
+      kind = huge ? 2 : normal ? 1 : __any_sync(kFull, k0 == 3 || k1 == 3) ? 3 : 0;
+      M = warp_max(fmaxf(k0 == which ? sh.rc[lane] : -INFINITY, k1 == which ? sh.rc[lane + 32] : -INFINITY));
+      for (int q = lane; q < n; q += 32) {
+        if (sh.kind[q] != which) continue;
+        // a normal reference is fl(x c), the other an entry
+        const double off = fmax(((double)sh.rc[q] - (double)M) * (normal ? 1.0 : (double)a.c), -(double)kFarBits);
+        const double f = exp2_small(off);
+        Sd += f * (double)sh.s[q];
+        Td += f * ((double)sh.t[q] + off * (double)sh.s[q]);
+      }
+      Sd = warp_sum(Sd);
+      Td = warp_sum(Td);
+      if (kind == 1) {
+        const double rc = (double)M;
+        M = M / a.c;
+        const double off = rc - (double)M * (double)a.c, f = exp2_small(off);
+        Td = f * (Td + off * Sd);
+        Sd *= f;
+      }
+    }
+    const bool careful = kind == 2;
+    if (careful) {                                // logits beyond 2^100 / c
+      const int32_t* out = nullptr;
+      if constexpr (OP == kTail) out = L.idx;
+      const Row<T> whole(row.x, a.vocab, 0, 1);
+      M = careful_max(whole, out, OP == kTail ? a.k : 0, lane, 32);
+      M = warp_max(M);
+      careful_sums(whole, M, a, out, OP == kTail ? a.k : 0, lane, 32, Sd, Td);
+      Sd = warp_sum(Sd);
+      Td = warp_sum(Td);
+    }
+    const float ref = fmaxf(M, kLowest);
+    // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
+    Sd += ((double)a.c_lo / (double)a.c) * 0.6931471805599453 * Td;
+    float ref_row = ref;
+    double S_row = Sd, loss = 0.0, rho = 0.0, Q = 0.0;
+    if constexpr (LIST) {
+      Q = sh.Q;
+      rho = sh.rho;
+      if (OP == kTail) {                          // the list's entries join the others
+        float high = -INFINITY;
+        for (int j = lane; j < a.k; j += 32)
+          if (L.idx[j] >= 0) high = fmaxf(high, L.x[j]);
+        ref_row = fmaxf(warp_max(high), ref);
+      }
+      double sum = 0.0;                           // loss: sum q (log q - z_j), z from ref_row; sum of exp(z_j)
+      for (int j = lane; j < a.k; j += 32) {
+        if (L.idx[j] < 0) continue;
+        const double z = ((double)L.x[j] - (double)ref_row) * (double)a.it;
+        const double lq = OP == kRenorm ? ((double)L.v[j] - sh.list_max) * (double)a.it : (double)L.v[j];
+        const double q = L.q[j];
+        if (!(q == 0.0)) loss += q * (lq - z);
+        if (OP == kTail) {
+          bool count = true;
+          if (sh.repeats)
+            for (int i = 0; i < j; ++i) count = count && L.idx[i] != L.idx[j];
+          if (count) sum += exp(z);
+        }
+      }
+      loss = warp_sum(loss);
+      if (OP == kTail) {
+        sum = warp_sum(sum);
+        S_row = sum + (Sd != 0.0 ? Sd * (ref == ref_row ? 1.0 : exp(((double)ref - (double)ref_row) * (double)a.it)) : 0.0);
+        if (Sd == 0.0) rho = 0.0;                 // no entry is left for the rest
+      }
+    }
+    double log_s = 0.0;
+    if (GRAD) {
+      double A, Bl = 0.0;
+      const double itd = (double)a.it;
+      if (OP == kLogprob) {
+        double ent = 0.0;
+        if (w_h != 0.0f) {
+          log_s = log(S_row);
+          ent = (double)(float)(log_s - 0.6931471805599453 * (Td / Sd));
+        }
+        A = -itd * ((double)w + (double)w_h * ent);
+        Bl = -itd * (double)w_h * 0.6931471805599453;
+      } else if (OP == kRenorm) {
+        A = itd * (double)w * Q;
+      } else {
+        const double Rr = Sd == 0.0 ? 0.0 : Sd / S_row * (ref == ref_row ? 1.0 : exp(((double)ref - (double)ref_row) * itd));
+        A = itd * (double)w * ((Q + rho) * Rr - rho);
+      }
+      if (lane == 0) {
+        dense_factors(sh, ref, Sd, A, Bl, a);
+        sh.A_list = OP == kTail ? itd * (double)w * (Q + rho) : A;
+        sh.ref_row = ref_row;
+        sh.S_row = S_row;
+        sh.log_s = log_s;
+        sh.per = OP == kRenorm ? -(double)w / sh.list_sum : -(double)w;
+        sh.none = S_row == 0.0 || (w == 0.0f && w_h == 0.0f);
+      }
+    }
+    if (GRAD) arrive(&sh.ready);
+    if (lane == 0 && part == 0) {
+      if (w_h == 0.0f) log_s = log(S_row);
+      if constexpr (OP == kLogprob) {
+        if (a.out)
+          a.out[r] = sh.target < 0     ? 0.0f
+                     : S_row == 0.0 ? -INFINITY
+                                    : (float)(((double)sh.x_target - (double)ref) * (double)a.it - log_s);
+        if (a.entropy) a.entropy[r] = S_row == 0.0 ? 0.0f : (float)(log_s - 0.6931471805599453 * (Td / Sd));
+      } else if constexpr (OP == kRenorm) {
+        a.out[r] = Q == 0.0 ? 0.0f
+                            : (float)(loss / sh.list_sum - log(sh.list_sum) + (S_row == 0.0 ? (double)INFINITY : log_s));
+      } else {
+        if (Q == 0.0 && rho == 0.0) loss = 0.0;
+        else if (S_row == 0.0) loss = Q != 0.0 ? (double)INFINITY : 0.0;
+        else {
+          loss += (Q + rho) * log_s;
+          if (!(rho == 0.0)) loss += rho * (log(rho) - ((double)ref - (double)ref_row) * (double)a.it - log(Sd));
+        }
+        a.out[r] = (float)loss;
+      }
+      if (a.stats) {
+        float* st = a.stats + (int64_t)r * (OP == kTail ? 4 : 2);
+        st[0] = ref_row;
+        st[1] = (float)S_row;
+        if (OP == kTail) {
+          st[2] = ref;
+          st[3] = (float)Sd;
+        }
+      }
+
+    }
+    if (C > 1) cg::this_cluster().sync();
+    return;
+  }
+
+  // Entries of the list in elements [e0, e0 + n) of the row: f(place in that range, entry).
+  auto listed_in = [&](int e0, int n, auto f) {
+    for (int j = lane; j < a.k; j += 32) {
+      const int e = L.idx[j] - e0;
+      if (L.idx[j] >= 0 && e >= 0 && e < n) f(e, j);
+    }
+  };
+  auto hits = [&](int o) -> bool { return (sh.hit[(o / kChunk >> 5) & (kHitWords - 1)] >> ((o / kChunk) & 31)) & 1u; };
+
+  // -- sums --------------------------------------------------------------------------------------------
+  if (OP == kTail) wait(&sh.listed);
+  Sums run;
+  run.s = run.t = pair(0.0f, 0.0f);
+  run.have = run.huge = false;
+  run.rc = run.low_s = run.low_t = 0.0f;
+  run.low_m = -INFINITY;
+  for (int left = own - warp * kChunk; left > 0; left -= step) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = nx[u];
+    request(left - step);
+    const int o = own - left;                     // first vector of the chunk
+    const bool hit = OP == kTail && hits(o);
+    if (RES || hit) {
+      uint4* chunk = RES ? buf + o : buf;
+      if (hit) __syncwarp();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (left >= kChunk || u * 32 + lane < left) chunk[u * 32 + lane] = v[u];
+      if (hit) {                                  // the list's entries leave the sums
+        T* el = reinterpret_cast<T*>(chunk);
+        __syncwarp();
+        listed_in(row.head + (row.v0 + o) * N, min(kChunk, left) * N, [&](int e, int) { el[e] = Elem<T>::from(-INFINITY); });
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (left >= kChunk || u * 32 + lane < left) v[u] = chunk[u * 32 + lane];
+      }
+    }
+    if (left >= kChunk) {
+      if (run.have || sums_start<T, U>(run, v, a)) sums_add<T, U>(run, v, a);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * 32 >= left) break;
+        const bool there = u * 32 + lane < left;
+        if (!there) v[u] = Elem<T>::nothing();
+        if (run.have || sums_start<T, 1>(run, &v[u], a))
+          if (there) sums_add<T, 1>(run, &v[u], a);
+      }
+    }
+  }
+  if (warp == 0 && __any_sync(kFull, edge >= 0)) {   // the entries before the first and after the last vector
+    float x[N];
+    x[0] = x_edge;
+    if (OP == kTail && edge >= 0)
+      for (int j = 0; j < a.k; ++j)
+        if (L.idx[j] == edge) x[0] = -INFINITY;
+#pragma unroll
+    for (int i = 1; i < N; ++i) x[i] = -INFINITY;
+    const uint4 v = Elem<T>::pack(x);
+    if ((run.have || sums_start<T, 1>(run, &v, a)) && edge >= 0) sums_add<T, 1>(run, &v, a);
+  }
+  {                                               // the lanes' sums together, to the CTAs of the row
+    const float rc = warp_max(run.rc);
+    Running all{0.0f, run.rc, run.s, run.t};
+    if (run.have) running_shift(all, rc);
+    float s0, s1, t0, t1;
+    unpair(all.s, &s0, &s1);
+    unpair(all.t, &t0, &t1);
+    s0 = warp_sum(s0 + s1);
+    t0 = warp_sum(t0 + t1);
+    float ref = rc;
+    int kind = __any_sync(kFull, run.huge) ? 2 : run.have || s0 != s0 ? 1 : 0;
+    if (kind == 0) {
+      const float low = warp_max(run.low_m);
+      if (low > -INFINITY) {
+        const float d = fmaxf((run.low_m - low) * a.c, -kFarBits), f = ex2(d);
+        const bool any = run.low_m > -INFINITY;
+        s0 = warp_sum(any ? f * run.low_s : 0.0f);
+        t0 = warp_sum(any ? f * (run.low_t + d * run.low_s) : 0.0f);
+        ref = low;
+        kind = 3;
+      }
+    }
+    if (lane < (GRAD ? C : 1)) {
+      const int q = part * W + warp;
+      peer_store(&sh.kind[q], lane, kind);
+      peer_store(&sh.rc[q], lane, ref);
+      peer_store(&sh.s[q], lane, s0);
+      peer_store(&sh.t[q], lane, t0);
+      peer_arrive(&sh.sums, lane);
+    }
+  }
+
+  // -- gradient ------------------------------------------------------------------------------------------
+  if constexpr (GRAD) {
+    at = row.vec() + row.v0 + warp * kChunk + lane;
+    if (!RES) request(own - warp * kChunk);
+    wait(&sh.listed);
+    wait(&sh.sums);
+    float kf, A, Bl, ref = 0.0f;
+    bool wild = false, none;
+    double A_list, S_row, x0, log_s = 0.0;        // for the list's entries: p = exp((x - x0) it) / S_row
+    const double itd = (double)a.it, w = (double)sh.w, w_h = OP == kLogprob ? (double)sh.w_h : 0.0;
+    // a warp's own way to the factors: in fp32, the parts in a fixed order
+    const int n = C * W, k0 = lane < n ? sh.kind[lane] : 0, k1 = lane + 32 < n ? sh.kind[lane + 32] : 0;
+    const bool plain_sums = __any_sync(kFull, k0 == 1 || k1 == 1) && !__any_sync(kFull, k0 == 2 || k1 == 2);
+    if (plain_sums) {
+      const float rc0 = k0 == 1 ? sh.rc[lane] : -INFINITY, rc1 = k1 == 1 ? sh.rc[lane + 32] : -INFINITY;
+      const float rcm = warp_max(fmaxf(rc0, rc1));
+      float s = 0.0f, t = 0.0f;
+      if (k0 == 1) {
+        const float d = fmaxf(rc0 - rcm, -kFarBits), f = ex2(d);
+        s = f * sh.s[lane];
+        t = f * fmaf(d, sh.s[lane], sh.t[lane]);
+      }
+      if (k1 == 1) {
+        const float d = fmaxf(rc1 - rcm, -kFarBits), f = ex2(d);
+        s = fmaf(f, sh.s[lane + 32], s);
+        t = fmaf(f, fmaf(d, sh.s[lane + 32], sh.t[lane + 32]), t);
+      }
+      s = warp_sum(s);
+      t = warp_sum(t);
+      s = fmaf(a.c_lo / a.c * 0.69314718f, t, s); // c is rounded: to first order S + d ln2 T
+      x0 = (double)rcm / (double)a.c;
+      float Af;
+      Bl = 0.0f;
+      if (OP == kLogprob) {
+        float ent = 0.0f;
+        if (w_h != 0.0) ent = 0.69314718f * (log2f(s) - t / s);
+        Af = -a.it * fmaf((float)w_h, ent, (float)w);
+        Bl = -a.it * (float)w_h * 0.69314718f;
+        S_row = (double)s;
+        if (w_h != 0.0) log_s = (double)logf(s);
+      } else if (OP == kRenorm) {
+        Af = a.it * (float)w * (float)sh.Q;
+        S_row = (double)s;
+      } else {
+        // the list's sum to the same reference; the share of the others
+        const float d = (float)(((double)sh.list_high - x0) * ((double)a.c + (double)a.c_lo));
+        const float Q = (float)sh.Q, rho = (float)sh.rho;
+        float list = 0.0f, R = 1.0f;
+        S_row = (double)s;
+        if (!(sh.list_exp == 0.0)) {
+          if (d < 100.0f) {
+            list = (float)sh.list_exp * ex2(d);
+            R = s / (s + list);
+            S_row = (double)s + (double)list;
+          } else {                                // the others are below 2^-100 of the row
+            R = s * ex2(-d) / (float)sh.list_exp;
+            x0 = (double)sh.list_high;
+            S_row = sh.list_exp;
+          }
+        }
+        Af = a.it * (float)w * ((Q + rho) * R - rho);
+      }
+      A_list = OP == kTail ? itd * w * (sh.Q + sh.rho) : (double)Af;
+      // p = 2^(x c - rcm) / s with s = 2^E m: 2^(x c - k) f, k = fl(rcm + E), f = 2^(k - E - rcm) / m
+      const int E = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
+      const float m = s * __uint_as_float((uint32_t)(127 - E) << 23);
+      kf = rcm + (float)E;
+      const float off = (float)((double)kf - (double)E - (double)rcm), f = fmaf(off, 0.69314718f, 1.0f) / m;
+      A = f * (Bl != 0.0f ? fmaf(Bl, off - log2f(m), Af) : Af);
+      Bl *= f;
+      none = w == 0.0 && w_h == 0.0;
+    } else {
+      wait(&sh.ready);
+      kf = sh.k;
+      A = sh.A;
+      Bl = sh.Bl;
+      ref = sh.ref;
+      wild = sh.wild;
+      none = sh.none;
+      A_list = sh.A_list;
+      S_row = sh.S_row;
+      x0 = (double)sh.ref_row;
+      log_s = sh.log_s;
+    }
+    T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
+    const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
+    const bool plain = in_step && !wild && !none;
+    uint4* dvec = reinterpret_cast<uint4*>(dx + row.head) + row.v0;
+    const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
+    auto grad = [&](uint4 v) {
+      float x[N];
+      Elem<T>::unpack(v, x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        float q0, q1;
+        f2 q = fma2(pair(x[i], x[i + 1]), c2, nk), g = A2;
+        unpair(q, &q0, &q1);
+        if (OP == kLogprob && Bl != 0.0f) g = fma2(pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), B2, A2);
+        unpair(mul2(pair(ex2(q0), ex2(q1)), g), &x[i], &x[i + 1]);
+      }
+      return Elem<T>::pack(x);
+    };
+    auto grad_one = [&](float x) {
+      float q = fmaf(x, a.c, -kf);
+      if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
+      return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
+    };
+    // an entry of the list in 64 bits: `add` is what it gets besides p's part
+    auto listed_one = [&](float x, double add) {
+      const double z = ((double)x - x0) * itd, p = exp(z) / S_row;
+      double g = p * A_list + itd * add;
+      if (OP == kLogprob && w_h != 0.0 && p != 0.0) g -= itd * w_h * p * (z - log_s);
+      return Elem<T>::from((float)g);
+    };
+    auto list_entry = [&](int j) {
+      double add = 0.0;
+      if (sh.Q != 0.0) {
+        const double per = OP == kRenorm ? -w / sh.list_sum : -w;
+        if (!sh.repeats) add = per * L.q[j];
+        else
+          for (int i = 0; i < a.k; ++i)
+            if (L.idx[i] == L.idx[j]) add += per * L.q[i];
+      }
+      return listed_one(L.x[j], add);
+    };
+    for (int left = own - warp * kChunk; left > 0; left -= step) {
+      const int o = own - left, e0 = row.head + (row.v0 + o) * N;   // first vector and element
+      uint4* chunk = RES ? buf + o : buf;
+      T* el = reinterpret_cast<T*>(chunk);
+      uint4 v[U];
+      if constexpr (!RES) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = nx[u];
+        request(left - step);
+      }
+      uint4* to = dvec + o + lane;
+      bool hit;
+      if (LIST) hit = hits(o);
+      else hit = sh.target >= e0 && sh.target < e0 + kChunk * N;
+      if (plain && !hit && left >= kChunk) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(RES ? chunk[u * 32 + lane] : v[u]));
+      } else {
+        // through shared memory: the list's entries over the dense gradient
+        const int n = min(left, kChunk);
+        if (!RES) __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u * 32 + lane >= n) break;
+          if (RES) v[u] = chunk[u * 32 + lane];
+          chunk[u * 32 + lane] = none ? make_uint4(0, 0, 0, 0) : wild ? v[u] : grad(v[u]);
+        }
+        __syncwarp();
+        if (!none) {
+          if (wild) {
+            for (int e = lane; e < n * N; e += 32) el[e] = grad_one(Elem<T>::to(el[e]));
+            __syncwarp();
+          }
+          if constexpr (LIST) {
+            if (hit) listed_in(e0, n * N, [&](int e, int j) { el[e] = list_entry(j); });
+          } else {
+            if (lane == 0 && hit && sh.target - e0 < n * N) el[sh.target - e0] = listed_one(sh.x_target, w);
+          }
+          __syncwarp();
+        }
+        if (in_step) {
+          for (int u = lane; u < n; u += 32) __stcs(to + u - lane, chunk[u]);
+        } else {
+          for (int e = lane; e < n * N; e += 32) dx[e0 + e] = el[e];
+        }
+      }
+    }
+    if (edge >= 0) {
+      T g = none ? Elem<T>::from(0.0f) : grad_one(x_edge);
+      if (!none) {
+        if constexpr (LIST) {
+          for (int j = 0; j < a.k; ++j)
+            if (L.idx[j] == edge) g = list_entry(j);
+        } else {
+          if (sh.target == edge) g = listed_one(sh.x_target, w);
+        }
+      }
+      dx[edge] = g;
+    }
+  }
+  if (C > 1) cg::this_cluster().sync();           // stores to this CTA may still be on their way
+}
+
 // ---- launch -----------------------------------------------------------------------------------------
 
-constexpr size_t kSliceMost = 200 << 10;          // a slice whose second read still finds it in L2
+template <class T, int OP, int MODE, bool RES>
+int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
+  const int64_t own = cdiv(nv, split), chunks = cdiv(own, kChunk);
+  int warps = (int)(chunks < kRowWarps ? (chunks > 0 ? chunks : 1) : kRowWarps);
+  a.split = split;
+  a.slice = (int32_t)(chunks * kChunk);
+  const size_t smem = (RES ? (size_t)a.slice : (size_t)warps * kChunk) * 16 + (OP == kLogprob ? 0 : List::bytes(a.k));
+  auto* kernel = voc_stream_kernel<T, OP, MODE, RES>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return GSPARSE_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.rows * split));
+  cfg.blockDim = dim3((unsigned)((warps + 1) * 32));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return GSPARSE_ERR_CUDA;
+  }
+  return launch_status();
+}
 
-template <class T, int OP, bool TOP, int MODE>
-int voc_of_type(VocArgs a, cudaStream_t st) {
+constexpr int64_t kSliceBytes = 48 << 10;         // four CTAs per SM
+constexpr int64_t kSliceMost = 200 << 10;         // one
+
+template <class T, int OP, int MODE>
+int voc_stream(const VocArgs& a, cudaStream_t st) {
   const int64_t nv = cdiv(a.vocab, Elem<T>::N);
   // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
   int split = 1;
   while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
-  if (MODE == kFused)
-    while (split < 8 && (size_t)nv * 16 > split * kSliceMost) split *= 2;
+  if constexpr (MODE == kFused) {
+    const int64_t need = cdiv(nv * 16, kSliceBytes);
+    if (split < need) split = need < 8 ? (int)need : 8;
+    if (nv * 16 <= split * kSliceMost) return voc_stream_launch<T, OP, MODE, true>(a, nv, split, st);
+  }
+  return voc_stream_launch<T, OP, MODE, false>(a, nv, split, st);
+}
+
+template <class T, int OP, bool TOP, int MODE>
+int voc_of_type(VocArgs a, cudaStream_t st) {
+  if constexpr (!TOP && MODE != kBackward)
+    return voc_stream<T, OP, MODE>(a, st);
+  else {
+  const int64_t nv = cdiv(a.vocab, Elem<T>::N);
+  // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
+  int split = 1;
+  while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
+  if (MODE == kFused)                             // a slice whose second read still finds it in L2
+    while (split < 8 && nv * 16 > split * (200 << 10)) split *= 2;
   a.split = split;
   int threads = 64;
   while (threads < 256 && (int64_t)threads * kUnroll * split < nv) threads *= 2;
@@ -1259,6 +2110,7 @@ int voc_of_type(VocArgs a, cudaStream_t st) {
     return GSPARSE_ERR_CUDA;
   }
   return launch_status();
+  }
 }
 
 template <int OP, bool TOP, int MODE>
@@ -1275,6 +2127,7 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
                float inv_temperature, void* dlogits, int64_t dstride, int32_t* d_status) {
   if (!voc_dtype(dtype) || rows < 0 || vocab < 1 || stride < 0) return GSPARSE_ERR_INVALID_ARG;
   if (!(inv_temperature > 0.0f) || !isfinite(inv_temperature)) return GSPARSE_ERR_INVALID_ARG;
+  if (inv_temperature < 0x1p-64f || inv_temperature > 0x1p64f) return GSPARSE_ERR_UNSUPPORTED;
   if (rows > INT32_MAX / 8 || vocab > GSPARSE_MAX_VOCAB) return GSPARSE_ERR_UNSUPPORTED;
   const uintptr_t align = dtype == GSPARSE_F32 ? 3 : 1;
   if (rows > 0 && !logits) return GSPARSE_ERR_INVALID_ARG;
@@ -1287,7 +2140,6 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
   a.c_lo = (float)(c - (double)a.c);
   a.far = kFarBits / a.c;
   a.ref_min = -kWildBits / a.c;
-  if (!isfinite(a.c) || !isfinite(a.far) || a.far == 0.0f) return GSPARSE_ERR_UNSUPPORTED;
   if (a.ref_min < -kLowestSafe) a.ref_min = -kLowestSafe;
   a.it = inv_temperature;
   a.logits = logits;

@@ -116,6 +116,27 @@ def check_tokens(x, dtype, temperature=1.0, targets=None, top_k=0, grad=True, dl
     return r
 
 
+MANY = [(301, 1), (160, 3), (200, 7), (333, 9), (170, 130), (1000, 1000), (449, 1031), (300, 4099), (160, 12347), (150, 70001)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,V", MANY)
+def test_tokens_many_rows(rows, V, dtype):
+    """More rows than the GPU holds at once; rows at every offset from 16 bytes."""
+    x, buf = make(rows, V, dtype, stride=V + 1, first=1)
+    before = buf.clone()
+    check_tokens(x, dtype, temperature=1.25)
+    check_tokens(x, dtype, grad=False)
+    other, _ = make(rows, V, dtype, stride=V + 3)            # a gradient out of step with the logits
+    check_tokens(x, dtype, dlogits=other)
+    assert torch.equal(torch.nan_to_num(buf.float(), 7.0), torch.nan_to_num(before.float(), 7.0))
+    t = dev(np.arange(rows) % V, torch.int32)
+    kw = dict(grad_logprob=dev(weights(rows)[0]), grad_entropy=dev(weights(rows)[1]))
+    want = gs.token_logprobs(x, t, want_grad=True, **kw)
+    got = gs.token_logprobs(x, t, dlogits=x, **kw)
+    assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.logprob, want.logprob)
+
+
 SIZES = [(1, 1), (3, 2), (2, 3), (5, 7), (2, 8), (3, 9), (2, 31), (1, 64), (4, 65), (2, 255), (3, 1000), (2, 1001),
          (2, 4099), (1, 16385), (2, 50021)]
 
@@ -170,8 +191,9 @@ def test_tokens_temperature(dtype, temperature):
     check_tokens(x, dtype, temperature=temperature, top_k=9)
 
 
+@pytest.mark.parametrize("times", [1, 20])     # few rows, and enough for every CTA to take several
 @pytest.mark.parametrize("dtype", list(TYPES))
-def test_tokens_masks(dtype):
+def test_tokens_masks(dtype, times):
     V = 1200
     x, _ = make(9, V, dtype)
     low = torch.finfo(TYPES[dtype]).min
@@ -184,8 +206,11 @@ def test_tokens_masks(dtype):
     x[6, 3] = float("nan")
     x[7, 1100] = float("inf")
     x[8, :40] = float("-inf")
-    check_tokens(x, dtype, targets=np.array([3, 700, 1, 4, 2, 9, 8, 8, 39]), top_k=7)
-    check_tokens(x, dtype, targets=np.array([-1, 5, 0, -1, 6, 1199, -1, 1100, 41]), top_k=128, grad=False)
+    x = x.repeat(times, 1)
+    check_tokens(x, dtype, targets=np.tile([3, 700, 1, 4, 2, 9, 8, 8, 39], times), top_k=7)
+    check_tokens(x, dtype, targets=np.tile([-1, 5, 0, -1, 6, 1199, -1, 1100, 41], times), top_k=128, grad=False)
+    check_tokens(x, dtype, targets=np.tile([-1, 700, 0, 4, 6, 1199, 8, 1100, 41], times))
+    check_tokens(x, dtype, targets=np.tile([-1, 700, 0, 4, 6, 1199, 8, 1100, 41], times), grad=False)
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
@@ -366,7 +391,9 @@ def check_distill(x, dtype, idx, val, tail, temperature=1.0, val_dtype="fp32", w
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows,V,k", [(1, 1, 1), (3, 2, 2), (3, 9, 4), (4, 65, 13), (5, 1000, 8), (3, 1001, 64),
-                                      (3, 4099, 32), (2, 50021, 256), (1, 40000, 100), (350, 2100, 5), (3, 5, 9)])
+                                      (3, 4099, 32), (2, 50021, 256), (1, 40000, 100), (350, 2100, 5), (3, 5, 9),
+                                      (301, 1, 1), (200, 9, 4), (1000, 1000, 8), (449, 1031, 40), (160, 12347, 256),
+                                      (150, 70001, 64)])
 def test_distill_sizes(rows, V, k, dtype, tail):
     x, _ = make(rows, V, dtype, stride=V + 5, first=3)
     idx, val = lists(x, k, 1.0, tail)
@@ -381,8 +408,9 @@ def test_distill_temperature_and_value_types(temperature, val_dtype, tail):
     check_distill(x, "bf16", idx, val, tail, temperature, val_dtype)
 
 
+@pytest.mark.parametrize("times", [1, 50])
 @pytest.mark.parametrize("tail", [False, True])
-def test_distill_a_confident_student(tail):
+def test_distill_a_confident_student(tail, times):
     # the list holds all but 1e-9 of the student's mass: what it leaves must not be a difference of sums
     V = 3000
     x = torch.zeros(4, V, device="cuda")
@@ -392,12 +420,14 @@ def test_distill_a_confident_student(tail):
     x[3, 7] = 200.0
     idx = np.array([[7, 8], [8, 7], [9, 7], [7, 3]], np.int32)
     val = np.log(np.array([[0.9, 0.05], [0.3, 0.6], [0.5, 0.25], [0.99, 0.001]])).astype(np.float32)
-    check_distill(x, "fp32", idx, val, tail, w=np.ones(4, np.float32))
+    check_distill(x.repeat(times, 1), "fp32", np.tile(idx, (times, 1)), np.tile(val, (times, 1)), tail,
+                  w=np.ones(4 * times, np.float32))
 
 
+@pytest.mark.parametrize("times", [1, 20])
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", list(TYPES))
-def test_distill_masks_and_lists(dtype, tail):
+def test_distill_masks_and_lists(dtype, tail, times):
     V = 1100
     x, _ = make(10, V, dtype)
     idx = np.tile(np.array([[3, 900, 14, 15]], np.int32), (10, 1))
@@ -413,7 +443,8 @@ def test_distill_masks_and_lists(dtype, tail):
     idx[7] = [-1, -1, 5, -1]
     val[8] += 0.3                                         # with the tail: more mass than one
     x[9, 40] = float("nan")
-    check_distill(x, dtype, idx, val, tail, w=np.linspace(0.5, 1.5, 10).astype(np.float32))
+    check_distill(x.repeat(times, 1), dtype, np.tile(idx, (times, 1)), np.tile(val, (times, 1)), tail,
+                  w=np.tile(np.linspace(0.5, 1.5, 10), times).astype(np.float32))
 
 
 def test_distill_bad_indices_are_reported_and_left_out():
