@@ -49,6 +49,8 @@ struct VocArgs {
   int32_t val_dtype;
   float it, c, c_lo;             // c + c_lo = it log2(e)
   float far, ref_min;            // kFarBits / c, -kWildBits / c
+  float fine;                    // ln2 c_lo / c
+  double inv_c;                  // 1 / c
   const int32_t* targets;
   const int32_t* list_idx;       // teacher's list, or the alternatives of the backward pass
   const void* list_val;          // teacher's values, or the gradient of the alternatives
@@ -217,10 +219,11 @@ constexpr uint32_t kKeyNegInf = 0x007fffffu;      // order_key(-inf): never an a
 
 // ---- block-wide reductions, in a fixed order ------------------------------------------------
 
+// Largest of the warp's values, NaN passed over.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // One reduction's partial results. Every reduction of the kernel has its own, so that one barrier
@@ -896,7 +899,7 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
       } else {
         // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
         R.M = M;
-        R.S = S + ((double)a.c_lo / (double)a.c) * 0.6931471805599453 * t;
+        R.S = S + (double)a.fine * t;
         R.T = t;
         R.kth = kth;
       }
@@ -923,7 +926,7 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
           t += f * (ot + (m == all ? 0.0 : dd * os));
         }
         R.M = all;
-        R.S = S + ((double)a.c_lo / (double)a.c) * 0.6931471805599453 * t;
+        R.S = S + (double)a.fine * t;
         R.T = t;
         R.kth = kth;
       }
@@ -1387,9 +1390,8 @@ constexpr int kRowCtas = 4;                       // per SM
 constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at most
 
 struct StreamShared {
-  uint64_t listed, sums, ready;                   // the list is there; all partial sums; results in 64 bits
-  float rc[kParts], s[kParts], t[kParts];
-  int kind[kParts];                               // 0 none, 1 sums, 2 beyond range, 3 below ref_min
+  uint64_t listed, weighed, sums, ready;          // the list's indices; its weights; all partial sums; results in 64 bits
+  float4 part[kParts];                            // rc, s, t, and as an int: 0 none, 1 sums, 2 beyond range, 3 below ref_min
   int repeats;                                    // an index stands in the list twice
   uint32_t hit[kHitWords];                        // chunks of the slice that hold entries of the list (modulo)
   float w, w_h, x_target;
@@ -1409,11 +1411,9 @@ __device__ __forceinline__ uint32_t peer(const void* p, int q) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
   return r;
 }
-__device__ __forceinline__ void peer_store(float* p, int q, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(p, q)), "f"(v) : "memory");
-}
-__device__ __forceinline__ void peer_store(int* p, int q, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer(p, q)), "r"(v) : "memory");
+__device__ __forceinline__ void peer_store(float4* p, int q, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer(p, q)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 __device__ __forceinline__ void peer_arrive(uint64_t* bar, int q) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer(bar, q)) : "memory");
@@ -1451,6 +1451,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.listed, 1);
+    mbar_init(&sh.weighed, 1);
     mbar_init(&sh.sums, GRAD || part == 0 ? C * W : 1);
     mbar_init(&sh.ready, 1);
     fence_mbarrier_init();
@@ -1479,8 +1480,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   }
   float x_edge = -INFINITY;
   if (edge >= 0) x_edge = Elem<T>::to(row.x[edge]);
-  if (C > 1) cg::this_cluster().sync();
-  else __syncthreads();
+  __syncthreads();
+  // the CTAs meet without waiting; what is sent to another waits for its start
+  if (C > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  auto started = [&]() {
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  };
 
   bool ok = true;                                 // a wait that runs out ends all later ones
   auto wait = [&](uint64_t* bar) {
@@ -1492,6 +1497,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+  };
+
+  // What others send here is waited for, so that a CTA may leave when it is done; if a wait has run out it
+  // stays until the others have left.
+  auto leave = [&]() {
+    if (C > 1 && !__all_sync(kFull, ok)) cg::this_cluster().sync();
   };
 
   if (warp == W) {
@@ -1540,28 +1551,33 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
       vmax = fmaxf(warp_max(vmax), kLowest);
       __syncwarp();
-      double sum = 0.0;
       bool repeats = false;
+      if (GRAD || OP == kTail) {
+        for (int j = lane; j < a.k; j += 32) {
+          const int e = L.idx[j];
+          if (e < 0) continue;
+          repeats |= L.add(e);
+          const int at = e < row.head ? -1 : (e - row.head) / N - row.v0;   // vector of the slice
+          if (at >= 0 && at < own) {
+            const int c = at / kChunk;
+            atomicOr(&sh.hit[(c >> 5) & (kHitWords - 1)], 1u << (c & 31));
+          }
+        }
+        repeats = __any_sync(kFull, repeats);
+        if (lane == 0) sh.repeats = repeats;
+      }
+      arrive(&sh.listed);
+      double sum = 0.0;
       for (int j = lane; j < a.k; j += 32) {
         const int e = L.idx[j];
         if (e < 0) continue;
         const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)vmax) * (double)a.it : (double)L.v[j]);
         L.q[j] = q;
         sum += q;
-        if (GRAD || OP == kTail) {
-          repeats |= L.add(e);
-          const int at = e < row.head ? -1 : (e - row.head) / N - row.v0;   // vector of the slice
-          if (at >= 0 && at < row.v1 - row.v0) {
-            const int c = at / kChunk;
-            atomicOr(&sh.hit[(c >> 5) & (kHitWords - 1)], 1u << (c & 31));
-          }
-        }
       }
       sum = warp_sum(sum);
-      repeats = __any_sync(kFull, repeats);
       if (lane == 0) {
         sh.w = w;
-        sh.repeats = repeats;
         sh.list_max = (double)vmax;
         sh.list_sum = sum;
         sh.Q = OP == kTail ? sum : sum == 0.0 ? 0.0 : sum == sum ? 1.0 : sum;
@@ -1589,11 +1605,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         sh.list_exp = add;
       }
     }
-    arrive(&sh.listed);
-    if (!GRAD && part != 0) {
-      if (C > 1) cg::this_cluster().sync();
-      return;
-    }
+    arrive(&sh.weighed);
+    started();
+    if (!GRAD && part != 0) return;
 
     // -- the row's results in 64 bits ------------------------------------------------------------------
     wait(&sh.sums);
@@ -1601,25 +1615,26 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
     {
-      const int n = C * W, k0 = lane < n ? sh.kind[lane] : 0, k1 = lane + 32 < n ? sh.kind[lane + 32] : 0;
+      const int n = C * W, k0 = lane < n ? __float_as_int(sh.part[lane].w) : 0;
+      const int k1 = lane + 32 < n ? __float_as_int(sh.part[lane + 32].w) : 0;
       const bool huge = __any_sync(kFull, k0 == 2 || k1 == 2), normal = __any_sync(kFull, k0 == 1 || k1 == 1);
       // of the parts with a normal reference (kind 1) where there are any, else of those below ref_min
       const int which = normal ? 1 : 3;
       kind = huge ? 2 : normal ? 1 : __any_sync(kFull, k0 == 3 || k1 == 3) ? 3 : 0;
-      M = warp_max(fmaxf(k0 == which ? sh.rc[lane] : -INFINITY, k1 == which ? sh.rc[lane + 32] : -INFINITY));
+      M = warp_max(fmaxf(k0 == which ? sh.part[lane].x : -INFINITY, k1 == which ? sh.part[lane + 32].x : -INFINITY));
       for (int q = lane; q < n; q += 32) {
-        if (sh.kind[q] != which) continue;
+        const float4 p = sh.part[q];
+        if (__float_as_int(p.w) != which) continue;
         // a normal reference is fl(x c), the other an entry
-        const double off = fmax(((double)sh.rc[q] - (double)M) * (normal ? 1.0 : (double)a.c), -(double)kFarBits);
-        const double f = exp2_small(off);
-        Sd += f * (double)sh.s[q];
-        Td += f * ((double)sh.t[q] + off * (double)sh.s[q]);
+        const float off = fmaxf(normal ? p.x - M : (p.x - M) * a.c, -kFarBits), f = ex2(off);
+        Sd += (double)f * (double)p.y;
+        Td += (double)f * ((double)p.z + (double)off * (double)p.y);
       }
       Sd = warp_sum(Sd);
       Td = warp_sum(Td);
       if (kind == 1) {
         const double rc = (double)M;
-        M = M / a.c;
+        M = (float)(rc * a.inv_c);
         const double off = rc - (double)M * (double)a.c, f = exp2_small(off);
         Td = f * (Td + off * Sd);
         Sd *= f;
@@ -1638,7 +1653,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     }
     const float ref = fmaxf(M, kLowest);
     // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
-    Sd += ((double)a.c_lo / (double)a.c) * 0.6931471805599453 * Td;
+    Sd += (double)a.fine * Td;
     float ref_row = ref;
     double S_row = Sd, loss = 0.0, rho = 0.0, Q = 0.0;
     if constexpr (LIST) {
@@ -1672,7 +1687,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
     }
     double log_s = 0.0;
-    if (GRAD) {
+    if (GRAD && kind != 1) {
       double A, Bl = 0.0;
       const double itd = (double)a.it;
       if (OP == kLogprob) {
@@ -1701,7 +1716,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     }
     if (GRAD) arrive(&sh.ready);
     if (lane == 0 && part == 0) {
-      if (w_h == 0.0f) log_s = log(S_row);
+      log_s = log(S_row);
       if constexpr (OP == kLogprob) {
         if (a.out)
           a.out[r] = sh.target < 0     ? 0.0f
@@ -1731,7 +1746,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
 
     }
-    if (C > 1) cg::this_cluster().sync();
+    leave();
     return;
   }
 
@@ -1758,32 +1773,31 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     request(left - step);
     const int o = own - left;                     // first vector of the chunk
     const bool hit = OP == kTail && hits(o);
-    if (RES || hit) {
-      uint4* chunk = RES ? buf + o : buf;
-      if (hit) __syncwarp();
+    uint4* chunk = RES ? buf + o : buf;
+    if (RES || hit || left < kChunk) {
+      if (!RES) __syncwarp();
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (left >= kChunk || u * 32 + lane < left) chunk[u * 32 + lane] = v[u];
-      if (hit) {                                  // the list's entries leave the sums
-        T* el = reinterpret_cast<T*>(chunk);
-        __syncwarp();
-        listed_in(row.head + (row.v0 + o) * N, min(kChunk, left) * N, [&](int e, int) { el[e] = Elem<T>::from(-INFINITY); });
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (left >= kChunk || u * 32 + lane < left) v[u] = chunk[u * 32 + lane];
-      }
+    }
+    if (hit) {                                    // the list's entries leave the sums
+      T* el = reinterpret_cast<T*>(chunk);
+      __syncwarp();
+      listed_in(row.head + (row.v0 + o) * N, min(kChunk, left) * N, [&](int e, int) { el[e] = Elem<T>::from(-INFINITY); });
+      __syncwarp();
     }
     if (left >= kChunk) {
+      if (hit) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = chunk[u * 32 + lane];
+      }
       if (run.have || sums_start<T, U>(run, v, a)) sums_add<T, U>(run, v, a);
     } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u * 32 >= left) break;
-        const bool there = u * 32 + lane < left;
-        if (!there) v[u] = Elem<T>::nothing();
-        if (run.have || sums_start<T, 1>(run, &v[u], a))
-          if (there) sums_add<T, 1>(run, &v[u], a);
+#pragma unroll 1
+      for (int u = lane; u - lane < left; u += 32) {
+        const uint4 one = u < left ? chunk[u] : Elem<T>::nothing();
+        if (run.have || sums_start<T, 1>(run, &one, a))
+          if (u < left) sums_add<T, 1>(run, &one, a);
       }
     }
   }
@@ -1820,12 +1834,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         kind = 3;
       }
     }
+    started();
     if (lane < (GRAD ? C : 1)) {
-      const int q = part * W + warp;
-      peer_store(&sh.kind[q], lane, kind);
-      peer_store(&sh.rc[q], lane, ref);
-      peer_store(&sh.s[q], lane, s0);
-      peer_store(&sh.t[q], lane, t0);
+      peer_store(&sh.part[part * W + warp], lane, make_float4(ref, s0, t0, __int_as_float(kind)));
       peer_arrive(&sh.sums, lane);
     }
   }
@@ -1834,33 +1845,34 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   if constexpr (GRAD) {
     at = row.vec() + row.v0 + warp * kChunk + lane;
     if (!RES) request(own - warp * kChunk);
-    wait(&sh.listed);
+    wait(&sh.weighed);
     wait(&sh.sums);
     float kf, A, Bl, ref = 0.0f;
     bool wild = false, none;
     double A_list, S_row, x0, log_s = 0.0;        // for the list's entries: p = exp((x - x0) it) / S_row
     const double itd = (double)a.it, w = (double)sh.w, w_h = OP == kLogprob ? (double)sh.w_h : 0.0;
     // a warp's own way to the factors: in fp32, the parts in a fixed order
-    const int n = C * W, k0 = lane < n ? sh.kind[lane] : 0, k1 = lane + 32 < n ? sh.kind[lane + 32] : 0;
+    const float4 none4 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    const float4 p0 = lane < C * W ? sh.part[lane] : none4, p1 = lane + 32 < C * W ? sh.part[lane + 32] : none4;
+    const int k0 = __float_as_int(p0.w), k1 = __float_as_int(p1.w);
     const bool plain_sums = __any_sync(kFull, k0 == 1 || k1 == 1) && !__any_sync(kFull, k0 == 2 || k1 == 2);
     if (plain_sums) {
-      const float rc0 = k0 == 1 ? sh.rc[lane] : -INFINITY, rc1 = k1 == 1 ? sh.rc[lane + 32] : -INFINITY;
-      const float rcm = warp_max(fmaxf(rc0, rc1));
+      const float rcm = warp_max(fmaxf(k0 == 1 ? p0.x : -INFINITY, k1 == 1 ? p1.x : -INFINITY));
       float s = 0.0f, t = 0.0f;
       if (k0 == 1) {
-        const float d = fmaxf(rc0 - rcm, -kFarBits), f = ex2(d);
-        s = f * sh.s[lane];
-        t = f * fmaf(d, sh.s[lane], sh.t[lane]);
+        const float d = fmaxf(p0.x - rcm, -kFarBits), f = ex2(d);
+        s = f * p0.y;
+        t = f * fmaf(d, p0.y, p0.z);
       }
       if (k1 == 1) {
-        const float d = fmaxf(rc1 - rcm, -kFarBits), f = ex2(d);
-        s = fmaf(f, sh.s[lane + 32], s);
-        t = fmaf(f, fmaf(d, sh.s[lane + 32], sh.t[lane + 32]), t);
+        const float d = fmaxf(p1.x - rcm, -kFarBits), f = ex2(d);
+        s = fmaf(f, p1.y, s);
+        t = fmaf(f, fmaf(d, p1.y, p1.z), t);
       }
       s = warp_sum(s);
       t = warp_sum(t);
-      s = fmaf(a.c_lo / a.c * 0.69314718f, t, s); // c is rounded: to first order S + d ln2 T
-      x0 = (double)rcm / (double)a.c;
+      s = fmaf(a.fine, t, s);                     // c is rounded: to first order S + d ln2 T
+      x0 = (double)rcm * a.inv_c;
       float Af;
       Bl = 0.0f;
       if (OP == kLogprob) {
@@ -1969,9 +1981,15 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       bool hit;
       if (LIST) hit = hits(o);
       else hit = sh.target >= e0 && sh.target < e0 + kChunk * N;
-      if (plain && !hit && left >= kChunk) {
+      if (plain && !hit) {
+        if (left >= kChunk) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(RES ? chunk[u * 32 + lane] : v[u]));
+          for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(RES ? chunk[u * 32 + lane] : v[u]));
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (u * 32 + lane < left) __stcs(to + u * 32, grad(RES ? chunk[u * 32 + lane] : v[u]));
+        }
       } else {
         // through shared memory: the list's entries over the dense gradient
         const int n = min(left, kChunk);
@@ -2015,7 +2033,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       dx[edge] = g;
     }
   }
-  if (C > 1) cg::this_cluster().sync();           // stores to this CTA may still be on their way
+  leave();
 }
 
 // ---- launch -----------------------------------------------------------------------------------------
@@ -2139,6 +2157,8 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
   a.c = (float)c;
   a.c_lo = (float)(c - (double)a.c);
   a.far = kFarBits / a.c;
+  a.fine = (float)((double)a.c_lo / (double)a.c * 0.6931471805599453);
+  a.inv_c = 1.0 / (double)a.c;
   a.ref_min = -kWildBits / a.c;
   if (a.ref_min < -kLowestSafe) a.ref_min = -kLowestSafe;
   a.it = inv_temperature;
