@@ -490,18 +490,22 @@ class DistillTopk(NamedTuple):
 
 def _logits(t: torch.Tensor, name="logits"):
     """(rows, vocab, row stride, dtype code) of a matrix whose rows are contiguous."""
-    if not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    code = _DTYPES.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != 2:
         raise GsparseError(f"{name} must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
-    return t.shape[0], t.shape[1], t.stride(0), _DTYPES[t.dtype]
+    rows, vocab = t.shape
+    stride, unit = t.stride()
+    if unit != 1 and vocab > 1:
+        raise GsparseError(f"{name} must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
+    return rows, vocab, stride, code
 
 
 def _like(t: Optional[torch.Tensor], dtype, shape, device, name):
-    """Checks an argument's type, device and shape; None stays None."""
+    """The pointer of an argument of that type, device and shape; None stays None."""
     if t is None:
         return None
-    _dev(t, dtype, name)
-    if t.device != device or tuple(t.shape) != shape:
-        raise GsparseError(f"{name} must have the shape {shape} on {device}")
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise GsparseError(f"{name} must be a contiguous {dtype} tensor of the shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
 
@@ -534,13 +538,19 @@ def _grad_out(dlogits: Optional[torch.Tensor], logits: torch.Tensor) -> torch.Te
 def _on_device(device, name, *args):
     """Calls the entry point with the tensors' device current, on that device's current stream."""
     fn = getattr(_lib or lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != 0:
         _check(st, name)
+
+
+# the current stream's handle without the Stream object around it (2 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, top_k: int = 0,

@@ -27,6 +27,8 @@ constexpr int kVocThreads = 512;
 constexpr int kVocWarps = kVocThreads / 32;
 constexpr int kUnroll = 4;                        // vectors of 16 bytes per lane and chunk
 constexpr int kChunk = 32 * kUnroll;              // vectors per chunk
+constexpr int kChunkLog = 7;
+static_assert(kChunk == 1 << kChunkLog, "");
 constexpr int kStages = 3;                        // chunks per warp in shared memory
 constexpr int kCand = 1024;                       // candidates for the alternatives, per CTA and in all
 
@@ -45,6 +47,7 @@ struct VocArgs {
   int64_t stride, dstride;       // elements
   int32_t rows, vocab, split;    // split = CTAs per row
   int32_t slice;                 // vectors of a CTA's slice in shared memory
+  uint32_t inv_split;            // ceil(2^32 / split)
   int32_t k;                     // list length: alternatives wanted (forward), given (backward), or the teacher's
   int32_t val_dtype;
   float it, c, c_lo;             // c + c_lo = it log2(e)
@@ -288,13 +291,14 @@ struct Row {
   const T* x;
   int V, head, nv, v0, v1;
   bool first, last;
-  __device__ __forceinline__ Row(const T* p, int vocab, int part, int split) : x(p), V(vocab) {
+  // inv: ceil(2^32 / split), for n / split = (n inv) >> 32, exact for n split < 2^32.
+  __device__ __forceinline__ Row(const T* p, int vocab, int part, int split, uint32_t inv) : x(p), V(vocab) {
     constexpr int N = Elem<T>::N;
     head = (int)(((16u - ((uint32_t)reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / sizeof(T));
     if (head > V) head = V;
     nv = (V - head) / N;
-    v0 = (int)((int64_t)nv * part / split);
-    v1 = (int)((int64_t)nv * (part + 1) / split);
+    v0 = split == 1 ? 0 : (int)__umulhi((uint32_t)nv * (uint32_t)part, inv);
+    v1 = split == 1 ? nv : (int)__umulhi((uint32_t)nv * (uint32_t)(part + 1), inv);
     first = part == 0;
     last = part == split - 1;
   }
@@ -711,9 +715,9 @@ __global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_consta
   __shared__ Exchange ex;
   __shared__ uint64_t bars[kVocWarps * kStages];
 
-  const int C = a.split, part = (int)(blockIdx.x % (unsigned)C), r = (int)(blockIdx.x / (unsigned)C);
+  const int C = a.split, r = C == 1 ? (int)blockIdx.x : (int)__umulhi(blockIdx.x, a.inv_split), part = (int)blockIdx.x - r * C;
   const int tid = threadIdx.x, lane = tid & 31, B = blockDim.x;
-  const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C);
+  const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C, a.inv_split);
   const uint4* vec = row.vec();
   const int own = row.v1 - row.v0;
   const int edge = row.edge(tid);
@@ -1418,19 +1422,23 @@ __device__ __forceinline__ void peer_store(float4* p, int q, float4 v) {
 __device__ __forceinline__ void peer_arrive(uint64_t* bar, int q) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer(bar, q)) : "memory");
 }
-__device__ __forceinline__ bool peer_wait_bounded(uint64_t* bar, uint32_t parity) {
+// Waits, asleep, until the barrier's first phase is complete; false after kWaitCycles.
+__device__ __forceinline__ bool peer_try_wait(uint64_t* bar) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0, 1000000;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar))
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool peer_wait_bounded(uint64_t* bar) {
+  if (peer_try_wait(bar)) return true;
   const long long t0 = clock64();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+  while (!peer_try_wait(bar))
     if (clock64() - t0 > kWaitCycles) return false;
-  }
+  return true;
 }
 
 // Shared memory: RES: the slice; else a chunk per warp for those that hold entries of the list. Then the list.
@@ -1442,8 +1450,8 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   extern __shared__ __align__(16) uint4 dyn[];
   __shared__ StreamShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = (blockDim.x >> 5) - 1;
-  const int C = a.split, part = (int)(blockIdx.x % (unsigned)C), r = (int)(blockIdx.x / (unsigned)C);
-  const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C);
+  const int C = a.split, r = C == 1 ? (int)blockIdx.x : (int)__umulhi(blockIdx.x, a.inv_split), part = (int)blockIdx.x - r * C;
+  const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C, a.inv_split);
   const int own = row.v1 - row.v0, step = W * kChunk;
   uint4* const buf = RES ? dyn : dyn + warp * kChunk;
   List L;
@@ -1456,8 +1464,13 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     mbar_init(&sh.ready, 1);
     fence_mbarrier_init();
   }
+  __syncthreads();
+  // the CTAs meet without waiting; what is sent to another waits for its start
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  auto started = [&]() {
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  };
   pdl_begin();
-  // the first chunk is on its way before the CTAs meet
   const uint4* at = row.vec() + row.v0 + warp * kChunk + lane;
   uint4 nx[U];
   auto request = [&](int left) {                  // of the slice, from the chunk's first vector on
@@ -1480,16 +1493,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   }
   float x_edge = -INFINITY;
   if (edge >= 0) x_edge = Elem<T>::to(row.x[edge]);
-  __syncthreads();
-  // the CTAs meet without waiting; what is sent to another waits for its start
-  if (C > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  auto started = [&]() {
-    if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-  };
-
   bool ok = true;                                 // a wait that runs out ends all later ones
   auto wait = [&](uint64_t* bar) {
-    if (ok && !peer_wait_bounded(bar, 0)) {
+    if (ok && !peer_wait_bounded(bar)) {
       ok = false;
       raise(a.d_status, GSPARSE_DERR_TIMEOUT);
     }
@@ -1644,7 +1650,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     if (careful) {                                // logits beyond 2^100 / c
       const int32_t* out = nullptr;
       if constexpr (OP == kTail) out = L.idx;
-      const Row<T> whole(row.x, a.vocab, 0, 1);
+      const Row<T> whole(row.x, a.vocab, 0, 1, 0u);
       M = careful_max(whole, out, OP == kTail ? a.k : 0, lane, 32);
       M = warp_max(M);
       careful_sums(whole, M, a, out, OP == kTail ? a.k : 0, lane, 32, Sd, Td);
@@ -1815,7 +1821,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   {                                               // the lanes' sums together, to the CTAs of the row
     const float rc = warp_max(run.rc);
     Running all{0.0f, run.rc, run.s, run.t};
-    if (run.have) running_shift(all, rc);
+    if (__any_sync(kFull, run.rc != rc)) running_shift(all, rc);   // (a lane that had entries far above the first chunk)
     float s0, s1, t0, t1;
     unpair(all.s, &s0, &s1);
     unpair(all.t, &t0, &t1);
@@ -1852,19 +1858,26 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     double A_list, S_row, x0, log_s = 0.0;        // for the list's entries: p = exp((x - x0) it) / S_row
     const double itd = (double)a.it, w = (double)sh.w, w_h = OP == kLogprob ? (double)sh.w_h : 0.0;
     // a warp's own way to the factors: in fp32, the parts in a fixed order
-    const float4 none4 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-    const float4 p0 = lane < C * W ? sh.part[lane] : none4, p1 = lane + 32 < C * W ? sh.part[lane + 32] : none4;
-    const int k0 = __float_as_int(p0.w), k1 = __float_as_int(p1.w);
-    const bool plain_sums = __any_sync(kFull, k0 == 1 || k1 == 1) && !__any_sync(kFull, k0 == 2 || k1 == 2);
+    const int parts = C * W;
+    const float4 p = lane < parts ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    bool normal = __float_as_int(p.w) == 1, huge = __float_as_int(p.w) == 2;
+    float rcm = warp_max(normal ? p.x : -INFINITY);
+    float4 p1 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    if (parts > 32) {
+      if (lane + 32 < parts) p1 = sh.part[lane + 32];
+      normal |= __float_as_int(p1.w) == 1;
+      huge |= __float_as_int(p1.w) == 2;
+      rcm = fmaxf(rcm, warp_max(__float_as_int(p1.w) == 1 ? p1.x : -INFINITY));
+    }
+    const bool plain_sums = __any_sync(kFull, normal) && !__any_sync(kFull, huge);
     if (plain_sums) {
-      const float rcm = warp_max(fmaxf(k0 == 1 ? p0.x : -INFINITY, k1 == 1 ? p1.x : -INFINITY));
       float s = 0.0f, t = 0.0f;
-      if (k0 == 1) {
-        const float d = fmaxf(p0.x - rcm, -kFarBits), f = ex2(d);
-        s = f * p0.y;
-        t = f * fmaf(d, p0.y, p0.z);
+      if (__float_as_int(p.w) == 1) {
+        const float d = fmaxf(p.x - rcm, -kFarBits), f = ex2(d);
+        s = f * p.y;
+        t = f * fmaf(d, p.y, p.z);
       }
-      if (k1 == 1) {
+      if (parts > 32 && __float_as_int(p1.w) == 1) {
         const float d = fmaxf(p1.x - rcm, -kFarBits), f = ex2(d);
         s = fmaf(f, p1.y, s);
         t = fmaf(f, fmaf(d, p1.y, p1.z), t);
@@ -1877,11 +1890,11 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       Bl = 0.0f;
       if (OP == kLogprob) {
         float ent = 0.0f;
-        if (w_h != 0.0) ent = 0.69314718f * (log2f(s) - t / s);
+        if (w_h != 0.0) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
         Af = -a.it * fmaf((float)w_h, ent, (float)w);
         Bl = -a.it * (float)w_h * 0.69314718f;
         S_row = (double)s;
-        if (w_h != 0.0) log_s = (double)logf(s);
+        if (w_h != 0.0) log_s = (double)(0.69314718f * __log2f(s));
       } else if (OP == kRenorm) {
         Af = a.it * (float)w * (float)sh.Q;
         S_row = (double)s;
@@ -1909,8 +1922,8 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       const int E = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
       const float m = s * __uint_as_float((uint32_t)(127 - E) << 23);
       kf = rcm + (float)E;
-      const float off = (float)((double)kf - (double)E - (double)rcm), f = fmaf(off, 0.69314718f, 1.0f) / m;
-      A = f * (Bl != 0.0f ? fmaf(Bl, off - log2f(m), Af) : Af);
+      const float off = (float)((double)kf - (double)E - (double)rcm), f = __fdividef(fmaf(off, 0.69314718f, 1.0f), m);
+      A = f * (Bl != 0.0f ? fmaf(Bl, off - __log2f(m), Af) : Af);
       Bl *= f;
       none = w == 0.0 && w_h == 0.0;
     } else {
@@ -1967,7 +1980,34 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
       return listed_one(L.x[j], add);
     };
-    for (int left = own - warp * kChunk; left > 0; left -= step) {
+    // The whole chunks without entries of the list, in a loop of their own that holds little else (one loop
+    // for all chunks took 160 instructions per chunk more); the others after it.
+    uint32_t rest = 0xffffffffu;
+    if constexpr (RES) {
+      if (plain) {
+        const int target_chunk = LIST ? -1 : sh.target < row.head ? -1 : ((sh.target - row.head) / N - row.v0) >> kChunkLog;
+        const uint4* from = buf + warp * kChunk + lane;
+        uint4* to = dvec + warp * kChunk + lane;
+        rest = 0;
+        int c = warp;
+        for (int left = own - warp * kChunk; left > 0; left -= step, c += W, from += step, to += step) {
+          bool apart = left < kChunk;
+          if (LIST) apart |= (sh.hit[(c >> 5) & (kHitWords - 1)] >> (c & 31)) & 1u;
+          else apart |= c == target_chunk;
+          if (apart) {
+            rest |= 1u << (c / W);
+            continue;
+          }
+          uint4 v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[u] = from[u * 32];
+#pragma unroll
+          for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(v[u]));
+        }
+      }
+    }
+    for (int left = own - warp * kChunk; left > 0; left -= step, rest >>= RES ? 1 : 0) {
+      if (RES && !(rest & 1u)) continue;
       const int o = own - left, e0 = row.head + (row.v0 + o) * N;   // first vector and element
       uint4* chunk = RES ? buf + o : buf;
       T* el = reinterpret_cast<T*>(chunk);
@@ -1976,30 +2016,29 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = nx[u];
         request(left - step);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = chunk[u * 32 + lane];
       }
       uint4* to = dvec + o + lane;
       bool hit;
       if (LIST) hit = hits(o);
       else hit = sh.target >= e0 && sh.target < e0 + kChunk * N;
+      if (!wild) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = grad(v[u]);
+      }
       if (plain && !hit) {
-        if (left >= kChunk) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(RES ? chunk[u * 32 + lane] : v[u]));
-        } else {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (u * 32 + lane < left) __stcs(to + u * 32, grad(RES ? chunk[u * 32 + lane] : v[u]));
-        }
+        for (int u = 0; u < U; ++u)
+          if (u * 32 + lane < left) __stcs(to + u * 32, v[u]);
       } else {
         // through shared memory: the list's entries over the dense gradient
         const int n = min(left, kChunk);
         if (!RES) __syncwarp();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (u * 32 + lane >= n) break;
-          if (RES) v[u] = chunk[u * 32 + lane];
-          chunk[u * 32 + lane] = none ? make_uint4(0, 0, 0, 0) : wild ? v[u] : grad(v[u]);
-        }
+        for (int u = 0; u < U; ++u)
+          if (u * 32 + lane < n) chunk[u * 32 + lane] = none ? make_uint4(0, 0, 0, 0) : v[u];
         __syncwarp();
         if (!none) {
           if (wild) {
@@ -2044,9 +2083,11 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
   int warps = (int)(chunks < kRowWarps ? (chunks > 0 ? chunks : 1) : kRowWarps);
   a.split = split;
   a.slice = (int32_t)(chunks * kChunk);
+  a.inv_split = (uint32_t)(((1ull << 32) + split - 1) / split);
   const size_t smem = (RES ? (size_t)a.slice : (size_t)warps * kChunk) * 16 + (OP == kLogprob ? 0 : List::bytes(a.k));
   auto* kernel = voc_stream_kernel<T, OP, MODE, RES>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+  if (smem > (32 << 10) &&                        // beyond what needs no leave, with the static part
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return GSPARSE_ERR_CUDA;
   }
@@ -2099,6 +2140,7 @@ int voc_of_type(VocArgs a, cudaStream_t st) {
   if (MODE == kFused)                             // a slice whose second read still finds it in L2
     while (split < 8 && nv * 16 > split * (200 << 10)) split *= 2;
   a.split = split;
+  a.inv_split = (uint32_t)(((1ull << 32) + split - 1) / split);
   int threads = 64;
   while (threads < 256 && (int64_t)threads * kUnroll * split < nv) threads *= 2;
   if (TOP) while (threads < kVocThreads && threads < 2 * a.k) threads *= 2;
@@ -2106,7 +2148,8 @@ int voc_of_type(VocArgs a, cudaStream_t st) {
   if (OP != kLogprob || MODE == kBackward) smem += List::bytes(OP == kLogprob ? a.k + 1 : a.k);
   if (TOP) smem = MODE == kFused ? smem + sizeof(TopShared) : smem > sizeof(TopShared) ? smem : sizeof(TopShared);
   auto* kernel = voc_kernel<T, OP, TOP, MODE>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+  if (smem > (32 << 10) &&                        // beyond what needs no leave, with the static part
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return GSPARSE_ERR_CUDA;
   }
@@ -2146,7 +2189,7 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
   if (!voc_dtype(dtype) || rows < 0 || vocab < 1 || stride < 0) return GSPARSE_ERR_INVALID_ARG;
   if (!(inv_temperature > 0.0f) || !isfinite(inv_temperature)) return GSPARSE_ERR_INVALID_ARG;
   if (inv_temperature < 0x1p-64f || inv_temperature > 0x1p64f) return GSPARSE_ERR_UNSUPPORTED;
-  if (rows > INT32_MAX / 8 || vocab > GSPARSE_MAX_VOCAB) return GSPARSE_ERR_UNSUPPORTED;
+  if (rows >= (1 << 26) || vocab > GSPARSE_MAX_VOCAB) return GSPARSE_ERR_UNSUPPORTED;
   const uintptr_t align = dtype == GSPARSE_F32 ? 3 : 1;
   if (rows > 0 && !logits) return GSPARSE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(logits) & align) || (reinterpret_cast<uintptr_t>(dlogits) & align))

@@ -421,7 +421,7 @@ int gsparse_combine_local(const float* G, const float* L, float* out, int64_t n,
  * Arithmetic: the exponential of fp32 differences and sums in fp32 within a thread, joined in fp64
  * in a fixed order: the same call on the same layout gives the same bits on every run, within a few
  * fp32 roundings of the formula (a gradient in 16 bits is rounded once). 1 <= vocab <= GSPARSE_MAX_VOCAB, 0 <= rows <
- * 2^28. These calls need no workspace.
+ * 2^26. These calls need no workspace.
  */
 enum gsparse_dtype { GSPARSE_F32 = 0, GSPARSE_BF16 = 1, GSPARSE_F16 = 2 };
 
