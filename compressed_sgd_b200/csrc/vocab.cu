@@ -23,14 +23,14 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVocThreads = 512;
+constexpr int kVocThreads = 256;
 constexpr int kVocWarps = kVocThreads / 32;
 constexpr int kUnroll = 4;                        // vectors of 16 bytes per lane and chunk
 constexpr int kChunk = 32 * kUnroll;              // vectors per chunk
 constexpr int kChunkLog = 7;
 static_assert(kChunk == 1 << kChunkLog, "");
 constexpr int kStages = 3;                        // chunks per warp in shared memory
-constexpr int kCand = 1024;                       // candidates for the alternatives, per CTA and in all
+constexpr int kCand = 2048;                       // candidates for a row's alternatives
 
 constexpr float kLowest = -3.402823466e38f;       // the maximum of a row that holds nothing but -inf
 constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: where a sum weighs by the exponent it is
@@ -74,6 +74,12 @@ struct VocArgs {
 template <class T> struct Elem;
 template <> struct Elem<float> {
   static constexpr int N = 4;
+  using Max = float;                              // a running maximum, NaN passed over
+  static __device__ __forceinline__ Max least() { return -INFINITY; }
+  static __device__ __forceinline__ void rise(Max& m, const uint4& v) {
+    m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v.x)), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  static __device__ __forceinline__ float top(const Max& m) { return m; }
   static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }   // -inf
   static __device__ __forceinline__ float to(float x) { return x; }
   static __device__ __forceinline__ float from(float x) { return x; }
@@ -96,6 +102,12 @@ template <> struct Elem<float> {
 };
 template <> struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
+  using Max = __nv_bfloat162;
+  static __device__ __forceinline__ Max least() { return as2(0xff80ff80u); }
+  static __device__ __forceinline__ void rise(Max& m, const uint4& v) {
+    m = __hmax2(__hmax2(m, as2(v.x)), __hmax2(__hmax2(as2(v.y), as2(v.z)), as2(v.w)));
+  }
+  static __device__ __forceinline__ float top(const Max& m) { return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y)); }
   static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }   // -inf
   static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
@@ -110,7 +122,7 @@ template <> struct Elem<__nv_bfloat16> {
     }
     return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
   }
-  static __device__ __forceinline__ __nv_bfloat162 as2(const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  static __device__ __forceinline__ __nv_bfloat162 as2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -131,6 +143,12 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<__half> {
   static constexpr int N = 8;
+  using Max = __half2;
+  static __device__ __forceinline__ Max least() { return as2(0xfc00fc00u); }
+  static __device__ __forceinline__ void rise(Max& m, const uint4& v) {
+    m = __hmax2(__hmax2(m, as2(v.x)), __hmax2(__hmax2(as2(v.y), as2(v.z)), as2(v.w)));
+  }
+  static __device__ __forceinline__ float top(const Max& m) { return fmaxf(__half2float(m.x), __half2float(m.y)); }
   static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u); }   // -inf
   static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
@@ -145,7 +163,7 @@ template <> struct Elem<__half> {
     }
     return fmaxf(__half2float(m.x), __half2float(m.y));
   }
-  static __device__ __forceinline__ __half2 as2(const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); }
+  static __device__ __forceinline__ __half2 as2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -326,12 +344,6 @@ struct Running {
   f2 s, t;        // sums over entries of e = 2^q and of e q, q = fl(x c - rc)
 };
 
-__device__ __forceinline__ void running_init(Running& r, const VocArgs& a) {
-  r.m = -INFINITY;
-  r.rc = a.ref_min * a.c;
-  r.s = r.t = pair(0.0f, 0.0f);
-}
-
 // Moves the sums to the reference rc2 >= rc.
 __device__ __forceinline__ void running_shift(Running& r, float rc2) {
   const float dd = max_nan(r.rc - rc2, -kFarBits);
@@ -339,63 +351,6 @@ __device__ __forceinline__ void running_shift(Running& r, float rc2) {
   r.t = mul2(fma2(r.s, pair(dd, dd), r.t), pair(f, f));
   r.s = mul2(r.s, pair(f, f));
   r.rc = rc2;
-}
-
-// Adds NV vectors. An exponent is one fused multiply-add (one rounding), entry by entry four and a
-// half instructions: unpack, half a maximum, half an exponent, 2^q, half an addition each to s and t.
-// 0 * -inf makes t NaN when -inf is among the entries; those NV vectors are then added again with the
-// exponents clamped, which costs rows without -inf one comparison per NV vectors.
-template <class T, int NV>
-__device__ __forceinline__ void running_add(Running& r, const uint4* v, const VocArgs& a) {
-  constexpr int N = Elem<T>::N;
-  const float high = Elem<T>::template high<NV>(v);
-  if (high > r.m) {
-    r.m = high;
-    running_shift(r, fmaxf(high, a.ref_min) * a.c);
-  }
-  const f2 c2 = pair(a.c, a.c), nrc = pair(-r.rc, -r.rc), before = r.t;
-#pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    float x[N];
-    Elem<T>::unpack(v[u], x);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const f2 q = fma2(pair(x[i], x[i + 1]), c2, nrc);
-      float q0, q1;
-      unpair(q, &q0, &q1);
-      const f2 e = pair(ex2(q0), ex2(q1));
-      r.s = add2(r.s, e);
-      r.t = fma2(e, q, r.t);
-    }
-  }
-  float t0, t1;
-  unpair(r.t, &t0, &t1);
-  t0 += t1;
-  if (t0 != t0) {
-    r.t = before;
-#pragma unroll 1
-    for (int u = 0; u < NV; ++u) {
-      float x[N];
-      Elem<T>::unpack(v[u], x);
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        float q0, q1;
-        unpair(fma2(pair(x[i], x[i + 1]), c2, nrc), &q0, &q1);
-        r.t = fma2(pair(ex2(q0), ex2(q1)), pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), r.t);
-      }
-    }
-  }
-}
-
-// Adds one entry.
-__device__ __forceinline__ void running_add_one(Running& r, float x, const VocArgs& a) {
-  if (x > r.m) {
-    r.m = x;
-    running_shift(r, fmaxf(x, a.ref_min) * a.c);
-  }
-  const float q = fmaf(x, a.c, -r.rc), e = ex2(q);
-  r.s = add2(r.s, pair(e, 0.0f));
-  r.t = fma2(pair(e, 0.0f), pair(max_nan(q, -kFarBits), 0.0f), r.t);
 }
 
 // ---- list of a row ------------------------------------------------------------------------------
@@ -450,21 +405,6 @@ __device__ __forceinline__ unsigned long long cand_of(uint32_t key, int e) {
 __device__ __forceinline__ void cand_push(TopShared& t, uint32_t key, int e) {
   const int n = atomicAdd(&t.count, 1);
   if (n < kCand) t.cand[n] = cand_of(key, e);
-}
-
-// The largest key with at least k of the block's keys at or above it; 0 if there are not k valid
-// keys (a key at or below -inf's is not valid). Stops as soon as exactly k are above.
-__device__ uint32_t kth_key_of_block(uint32_t key, int k) {
-  const bool valid = key > kKeyNegInf;
-  if (__syncthreads_count(valid) < k) return 0;
-  uint32_t res = 0;
-  for (int b = 31; b >= 0; --b) {
-    const uint32_t trial = res | (1u << b);
-    const int n = __syncthreads_count(valid && key >= trial);
-    if (n >= k) res = trial;
-    if (n == k) break;
-  }
-  return res;
 }
 
 // Entries of the whole row with key >= t (the CTA reads all of it).
@@ -649,34 +589,9 @@ __device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocA
   Tt = t;
 }
 
-// ---- the kernel -----------------------------------------------------------------------------------
-
-struct Exchange {      // what the CTAs of a row tell each other
-  float m;
-  double s, t;
-  uint32_t kth;
-};
+// ---- gradient from saved statistics ----------------------------------------------------------------
 
 constexpr int kHitWords = 16;
-
-// What one thread works out for all: 64-bit arithmetic by every thread would cost more than the row.
-struct RowShared {
-  PartMax max_row, max_list;
-  PartSum sum_row, sum_list, sum_loss;
-  int part[kVocWarps];
-  int repeats;         // an index stands in the list twice
-  uint32_t hit[kHitWords];   // chunks of the slice that hold entries of the list (modulo 32 kHitWords)
-  float M;             // of the entries that S and T sum
-  double S, T;
-  uint32_t kth;
-  double Q, rho;       // mass of the list and what it leaves
-  double list_max, list_log;
-  float ref, ref_row, ent;
-  double S_row;
-  // the dense gradient p (A + Bl log2 p) = 2^q (A + Bl q), q = fl(x c - k)
-  float k, A, Bl, A_list;
-  int wild;
-};
 
 // The factors of the dense gradient for p = 2^((x - ref) c) / S, g = p (A + Bl log2 p).
 // With S = 2^E s, 1 <= s < 2, p = 2^(x c - k) f for k = fl(fl(ref c) + E) and f = 2^(k - E - ref c) / s: no
@@ -701,546 +616,221 @@ __device__ __forceinline__ void dense_factors(Out& R, float ref, double S, doubl
   R.Bl = (float)(f * Bl);
 }
 
-// Dynamic shared memory: the warps' rings; the list; the candidates, over the rings where no
-// gradient needs them again.
+// What one thread works out for all: 64-bit arithmetic by every thread would cost more than the row.
+struct RowShared {
+  PartMax max_list;
+  PartSum sum_list;
+  int repeats;         // an index stands in the list twice
+  double Q, rho;       // mass of the list and what it leaves; kLogprob: sum of the gradients and of their sizes
+  double list_max, list_sum;
+  float ref, ref_row;
+  double S_row;
+  float k, A, Bl, A_list;
+  int wild;
+};
+
+// Dynamic shared memory: the warps' rings, then the list.
 __host__ __device__ __forceinline__ size_t ring_bytes(int threads) { return (size_t)threads / 32 * kStages * kChunk * 16; }
 
-template <class T, int OP, bool TOP, int MODE>
-__global__ void __launch_bounds__(kVocThreads, 2) voc_kernel(const __grid_constant__ VocArgs a) {
+// C CTAs take a row, each a slice, with nothing to tell each other. One read and one write per entry:
+// 4096 x 32000 fp32 in 156 us, 6.73 TB/s; through registers, without the rings, 187 us.
+template <class T, int OP>
+__global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __grid_constant__ VocArgs a) {
   constexpr int N = Elem<T>::N, U = kUnroll;
-  constexpr bool LIST = OP != kLogprob || MODE == kBackward;
-  constexpr bool GRAD = MODE != kForward;
   extern __shared__ __align__(16) uint4 dyn[];
   __shared__ RowShared R;
-  __shared__ Exchange ex;
   __shared__ uint64_t bars[kVocWarps * kStages];
 
   const int C = a.split, r = C == 1 ? (int)blockIdx.x : (int)__umulhi(blockIdx.x, a.inv_split), part = (int)blockIdx.x - r * C;
   const int tid = threadIdx.x, lane = tid & 31, B = blockDim.x;
   const Row<T> row(static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, part, C, a.inv_split);
-  const uint4* vec = row.vec();
-  const int own = row.v1 - row.v0;
-  const int edge = row.edge(tid);
-  char* beyond = reinterpret_cast<char*>(dyn) + ring_bytes(B);
+  const int own = row.v1 - row.v0, edge = row.edge(tid);
   Ring ring;
-  ring.init(dyn, bars, vec + row.v0, own);
+  ring.init(dyn, bars, row.vec() + row.v0, own);
   pdl_begin();
-  if (MODE != kBackward)
-    for (int q = 0; q < min(kStages, ring.n); ++q) ring.issue(q);
 
   // -- the row's list ---------------------------------------------------------------------------
-  float w = 0.0f, w_h = 0.0f;                     // gradient weights of the row
-  if (GRAD) {
-    w = a.weight ? a.weight[r] : 0.0f;
-    w_h = OP == kLogprob && a.weight_entropy ? a.weight_entropy[r] : 0.0f;
-  }
-  int target = -1;
-  float x_target = 0.0f, x_edge = 0.0f;
+  float w = a.weight ? a.weight[r] : 0.0f;        // gradient weights of the row
+  const float w_h = OP == kLogprob && a.weight_entropy ? a.weight_entropy[r] : 0.0f;
+  float x_edge = 0.0f;
   if (edge >= 0) x_edge = Elem<T>::to(row.x[edge]);
+  int target = -1;
   if (OP == kLogprob && a.targets) {
     target = a.targets[r];
     if (target < -1 || target >= a.vocab) {
       if (tid == 0 && part == 0) raise(a.d_status, GSPARSE_DERR_INDEX_RANGE);
       target = -1;
     }
-    if (target >= 0) x_target = Elem<T>::to(row.x[target]);
   }
   if (OP == kLogprob && target < 0) w = 0.0f;
-  // the backward pass reads nothing of a row without weights (where the list has none of its own)
-  const bool early = MODE == kBackward && (OP == kLogprob || w != 0.0f);
+  // nothing is read of a row without weights (where the list has none of its own)
+  const bool early = OP == kLogprob || w != 0.0f;
   if (early)
     for (int q = 0; q < min(kStages, ring.n); ++q) ring.issue(q);
-  const int nl = LIST ? (OP == kLogprob ? a.k + 1 : a.k) : 0;
+  const int nl = OP == kLogprob ? a.k + 1 : a.k;
   List L;
-  if constexpr (LIST) {
-    L.carve(beyond, nl);
-    if (OP == kTail || GRAD)
-      for (int i = tid; i < L.slots; i += B) L.table[i] = 0;
-    if (tid == 0) R.repeats = 0;
-    if (OP == kTail && tid < kHitWords) R.hit[tid] = 0;
-    float vmax = -INFINITY;
-    for (int j = tid; j < nl; j += B) {
-      int e;
-      float v;
-      if (OP == kLogprob) {
-        e = j == 0 ? target : a.list_idx[(int64_t)r * a.k + j - 1];
-        v = j == 0 ? w : static_cast<const float*>(a.list_val)[(int64_t)r * a.k + j - 1];
-      } else {
-        e = a.list_idx[(int64_t)r * a.k + j];
-        v = list_value(a.list_val, a.val_dtype, (int64_t)r * a.k + j);
-      }
-      if (e < -1 || e >= a.vocab) {
-        if (part == 0) raise(a.d_status, GSPARSE_DERR_INDEX_RANGE);
-        e = -1;
-      }
-      L.idx[j] = e;
-      L.x[j] = e >= 0 && (MODE != kBackward || row.owns(e)) ? Elem<T>::to(row.x[e]) : 0.0f;
-      L.v[j] = v;
-      if (e >= 0) vmax = fmaxf(vmax, v);
+  L.carve(reinterpret_cast<char*>(dyn) + ring_bytes(B), nl);
+  for (int i = tid; i < L.slots; i += B) L.table[i] = 0;
+  if (tid == 0) R.repeats = 0;
+  float vmax = -INFINITY;
+  for (int j = tid; j < nl; j += B) {
+    int e;
+    float v;
+    if (OP == kLogprob) {
+      e = j == 0 ? target : a.list_idx[(int64_t)r * a.k + j - 1];
+      v = j == 0 ? w : static_cast<const float*>(a.list_val)[(int64_t)r * a.k + j - 1];
+    } else {
+      e = a.list_idx[(int64_t)r * a.k + j];
+      v = list_value(a.list_val, a.val_dtype, (int64_t)r * a.k + j);
     }
-    float list_max = 0.0f;
-    if (OP == kRenorm) list_max = fmaxf(block_max(vmax, R.max_list), kLowest);
-    else __syncthreads();
-    // sum of the probabilities (of the renormalised list: not yet divided); of the incoming gradients
-    // and their sizes
-    double sum = 0.0, size = 0.0;
-    for (int j = tid; j < nl; j += B) {
-      const int e = L.idx[j];
-      if (e < 0) continue;
-      if (OP == kLogprob) {
-        if (j > 0) sum += (double)L.v[j];
-        size += fabs((double)L.v[j]);
-      } else {
-        const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)list_max) * (double)a.it : (double)L.v[j]);
-        L.q[j] = q;
-        sum += q;
-      }
-      if (OP == kTail || GRAD)
-        if (L.add(e)) R.repeats = 1;
-      if (OP == kTail && MODE != kBackward && e >= row.head) {
-        const int v = (e - row.head) / N - row.v0;
-        if (v >= 0 && v < own) atomicOr(&R.hit[(v / kChunk >> 5) & (kHitWords - 1)], 1u << ((v / kChunk) & 31));
-      }
+    if (e < -1 || e >= a.vocab) {
+      if (part == 0) raise(a.d_status, GSPARSE_DERR_INDEX_RANGE);
+      e = -1;
     }
-    sum_put(sum, size, R.sum_list);
-    __syncthreads();
-    if (tid == 0) {
-      sum_get(sum, size, R.sum_list);
-      R.Q = sum;
-      R.rho = size;                               // kLogprob: sum of the gradients and of their sizes
-      if (OP == kRenorm) {
-        R.list_max = (double)list_max;
-        R.list_log = sum;                         // the loss takes its logarithm
-        R.Q = sum == 0.0 ? 0.0 : sum == sum ? 1.0 : sum;
-        R.rho = 0.0;
-      }
-      if (OP == kTail) R.rho = sum == sum ? fmax(1.0 - sum, 0.0) : sum;
-    }
-    if (OP == kTail) __syncthreads();             // hit
+    L.idx[j] = e;
+    L.x[j] = e >= 0 && row.owns(e) ? Elem<T>::to(row.x[e]) : 0.0f;
+    L.v[j] = v;
+    if (e >= 0) vmax = fmaxf(vmax, v);
   }
+  float list_max = 0.0f;
+  if (OP == kRenorm) list_max = fmaxf(block_max(vmax, R.max_list), kLowest);
+  else __syncthreads();
+  // sum of the probabilities (of the renormalised list: not yet divided); of the incoming gradients and
+  // their sizes
+  double sum = 0.0, size = 0.0;
+  for (int j = tid; j < nl; j += B) {
+    const int e = L.idx[j];
+    if (e < 0) continue;
+    if (OP == kLogprob) {
+      if (j > 0) sum += (double)L.v[j];
+      size += fabs((double)L.v[j]);
+    } else {
+      const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)list_max) * (double)a.it : (double)L.v[j]);
+      L.q[j] = q;
+      sum += q;
+    }
+    if (L.add(e)) R.repeats = 1;
+  }
+  sum_put(sum, size, R.sum_list);
+  __syncthreads();
 
-  // -- maximum and sums ----------------------------------------------------------------------------
-  // Of the whole row; with kTail of the entries outside the list, whose sum as the difference of
-  // two others would lose its digits when the list holds nearly all of the mass.
-  if constexpr (MODE != kBackward) {
-    Running run;
-    running_init(run, a);
+  // -- the dense gradient's factors ----------------------------------------------------------------
+  if (tid == 0) {
+    sum_get(sum, size, R.sum_list);
+    R.Q = sum;
+    R.rho = size;
+    R.list_sum = sum;
+    if (OP == kRenorm) R.Q = sum == 0.0 ? 0.0 : sum == sum ? 1.0 : sum;
+    if (OP == kTail) R.rho = sum == sum ? fmax(1.0 - sum, 0.0) : sum;
+    const float* st = a.stats_in + (int64_t)r * (OP == kTail ? 4 : 2);
+    float ref = fmaxf(st[0], kLowest);
+    double S = (double)st[1];
+    R.ref_row = ref;
+    R.S_row = S;
+    if (OP == kTail) {
+      ref = fmaxf(st[2], kLowest);
+      S = (double)st[3];
+      if (S == 0.0) R.rho = 0.0;                  // no entry is left for the rest
+    }
+    const double it = (double)a.it;
+    double A, Bl = 0.0;
+    if (OP == kLogprob) {
+      A = -it * ((double)w + R.Q + (w_h != 0.0f ? (double)w_h * (double)a.entropy_in[r] : 0.0));
+      Bl = -it * (double)w_h * 0.6931471805599453;
+      R.A_list = (float)A;
+    } else if (OP == kRenorm) {
+      A = it * (double)w * R.Q;
+      R.A_list = (float)A;
+    } else {
+      const double Rr = S == 0.0 ? 0.0
+                        : S / R.S_row * (ref == R.ref_row ? 1.0 : exp(((double)ref - (double)R.ref_row) * it));
+      A = it * (double)w * ((R.Q + R.rho) * Rr - R.rho);
+      R.A_list = (float)(it * (double)w * (R.Q + R.rho));
+    }
+    dense_factors(R, ref, S, A, Bl, a);
+  }
+  __syncthreads();
+
+  // -- gradient ------------------------------------------------------------------------------------
+  const float kf = R.k, A = R.A, Bl = R.Bl, ref = R.ref;
+  const bool nothing = R.S_row == 0.0;            // nothing but -inf: no distribution, no gradient
+  // no weight: zeros, whatever the row holds
+  const bool none = nothing || (OP == kLogprob ? w_h == 0.0f && R.rho == 0.0 : w == 0.0f);
+  const bool wild = R.wild;
+  T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
+  const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
+  auto grad = [&](uint4 v) {
+    float x[N];
+    Elem<T>::unpack(v, x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float q0, q1;
+      f2 q = fma2(pair(x[i], x[i + 1]), c2, nk), g = A2;
+      unpair(q, &q0, &q1);
+      if (OP == kLogprob && Bl != 0.0f) g = fma2(pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), B2, A2);
+      unpair(mul2(pair(ex2(q0), ex2(q1)), g), &x[i], &x[i + 1]);
+    }
+    return Elem<T>::pack(x);
+  };
+  auto grad_one = [&](float x) {
+    float q = fmaf(x, a.c, -kf);
+    if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
+    return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
+  };
+  const int e0 = row.head + row.v0 * N, e1 = row.head + row.v1 * N;
+  const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
+  uint4* dvec = reinterpret_cast<uint4*>(dx + row.head) + row.v0;
+  if (early && (none || wild || !in_step))
+    for (int q = 0; q < min(kStages, ring.n); ++q) ring.wait(q, a.d_status);
+  if (none) {
+    if (in_step) {
+      for (int i = tid; i < own; i += B) __stcs(dvec + i, make_uint4(0, 0, 0, 0));
+    } else {
+      for (int e = e0 + tid; e < e1; e += B) dx[e] = Elem<T>::from(0.0f);
+    }
+    if (edge >= 0) dx[edge] = Elem<T>::from(0.0f);
+    ring.drain();
+    return;
+  }
+  if (in_step && !wild) {
     for (int q = 0; q < ring.n; ++q) {
       ring.wait(q, a.d_status);
       const uint4* at = ring.at(q);
+      uint4* to = dvec + ring.first(q);
       const int left = own - ring.first(q);
-      if constexpr (OP == kTail) {                // the list's entries leave the chunk
-        const int c = ring.warp + ring.nw * q;
-        if ((R.hit[(c >> 5) & (kHitWords - 1)] >> (c & 31)) & 1u) {
-          const int e0 = row.head + (row.v0 + c * kChunk) * N;
-          for (int j = lane; j < nl; j += 32) {
-            const int e = L.idx[j] - e0;
-            if (L.idx[j] >= 0 && e >= 0 && e < min(kChunk, left) * N)
-              reinterpret_cast<T*>(ring.at(q))[e] = Elem<T>::from(-INFINITY);
-          }
-          fence_proxy_async_smem();               // before the slot's next copy
-          __syncwarp();
-        }
-      }
       if (left >= kChunk) {
-        uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = at[u * 32 + lane];
-        running_add<T, U>(run, v, a);
+        for (int u = 0; u < U; ++u) __stcs(to + u * 32 + lane, grad(at[u * 32 + lane]));
       } else {
-        for (int u = lane; u < left; u += 32) {
-          const uint4 v = at[u];
-          running_add<T, 1>(run, &v, a);
-        }
+        for (int u = lane; u < left; u += 32) __stcs(to + u, grad(at[u]));
       }
       __syncwarp();
       if (q + kStages < ring.n) ring.issue(q + kStages);
     }
-    if (edge >= 0) {
-      float x = x_edge;
-      if constexpr (OP == kTail) {
-        for (int j = 0; j < nl; ++j)
-          if (L.idx[j] == edge) x = -INFINITY;
-      }
-      running_add_one(run, x, a);
-    }
-    const float mine = run.m;
-    const float M = block_max(run.m, R.max_row);
-    const float ref = fmaxf(M, a.ref_min);
-    const bool wild = !(fabsf(M) * a.c <= kWildBits) && fabsf(M) < INFINITY;
-    if (wild) {
-      const int32_t* out = nullptr;
-      if constexpr (OP == kTail) out = L.idx;
-      double s, t;
-      careful_sums(row, M, a, out, OP == kTail ? nl : 0, tid, B, s, t);
-      sum_put(s, t, R.sum_row);
-    } else {
-      running_shift(run, ref * a.c);
-      float s0, s1, t0, t1;
-      unpair(run.s, &s0, &s1);
-      unpair(run.t, &t0, &t1);
-      s0 = warp_sum(s0 + s1);
-      t0 = warp_sum(t0 + t1);
-      if ((tid & 31) == 0) {
-        R.sum_row.a[tid >> 5] = (double)s0;
-        R.sum_row.b[tid >> 5] = (double)t0;
-      }
-    }
-    uint32_t kth = 0;
-    if constexpr (TOP) kth = kth_key_of_block(order_key(mine), a.k);
-    __syncthreads();
-    if (tid == 0) {
-      double S, t;
-      sum_get(S, t, R.sum_row);
-      if (!wild && M != -INFINITY) {
-        // the exponents were taken from fl(ref c) instead of ref c
-        const double off = (double)run.rc - (double)ref * (double)a.c, f = exp2_small(off);
-        t = f * (t + off * S);
-        S *= f;
-      }
-      if (C > 1) {
-        ex = Exchange{M, S, t, kth};
-      } else {
-        // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
-        R.M = M;
-        R.S = S + (double)a.fine * t;
-        R.T = t;
-        R.kth = kth;
-      }
-    }
-    if (C > 1) {
-      cg::cluster_group cl = cg::this_cluster();
-      cl.sync();
-      if (tid == 0) {
-        float all = -INFINITY;
-        double S = 0.0, t = 0.0;
-        for (int q = 0; q < C; ++q) {
-          const Exchange* o = cl.map_shared_rank(&ex, q);
-          all = fmaxf(all, o->m);
-          kth = max(kth, o->kth);
-        }
-        for (int q = 0; q < C; ++q) {
-          const Exchange* o = cl.map_shared_rank(&ex, q);
-          const float m = o->m;
-          const double os = o->s, ot = o->t;
-          if (m == -INFINITY) continue;
-          const double dd = fmax(((double)m - (double)all) * (double)a.c, -(double)kFarBits);
-          const double f = m == all ? 1.0 : exp2(dd);
-          S += os * f;
-          t += f * (ot + (m == all ? 0.0 : dd * os));
-        }
-        R.M = all;
-        R.S = S + (double)a.fine * t;
-        R.T = t;
-        R.kth = kth;
-      }
-    }
-    __syncthreads();
-
-    // -- most likely tokens ----------------------------------------------------------------------
-    // A thread's maximum is one entry, so the k-th largest of the threads' maxima is a lower bound of
-    // the row's k-th largest entry; only threads whose maximum reaches it own candidates, and those
-    // read their entries again (from L2).
-    if constexpr (TOP) {
-      TopShared& top = *reinterpret_cast<TopShared*>(GRAD ? beyond : reinterpret_cast<char*>(dyn));
-      kth = R.kth;
-      if (tid == 0) top.count = 0;
-      __syncthreads();
-      const uint32_t bound = max(kth, kKeyNegInf + 1);
-      const bool owner = order_key(mine) >= bound;
-      uint32_t owners = __ballot_sync(kFull, owner);
-      while (owners) {
-        const int l = __ffs(owners) - 1;
-        owners &= owners - 1;
-        // vector j of lane l: chunk j / U of its warp, row j % U of the chunk
-        for (int j = lane; j < ring.n * U; j += 32) {
-          const int i = row.v0 + ring.first(j / U) + (j % U) * 32 + l;
-          if (i >= row.v1) break;
-          float x[N];
-          Elem<T>::unpack(__ldcg(vec + i), x);
-#pragma unroll
-          for (int b = 0; b < N; ++b) {
-            const uint32_t key = order_key(x[b]);
-            if (key >= bound) cand_push(top, key, row.head + i * N + b);
-          }
-        }
-      }
-      if (owner && edge >= 0) {
-        const uint32_t key = order_key(x_edge);
-        if (key >= bound) cand_push(top, key, edge);
-      }
-      __syncthreads();
-      const double S = R.S;
-      bool again = top.count > kCand || !(S == S);
-      if (C > 1) {
-        cg::cluster_group cl = cg::this_cluster();
-        cl.sync();
-        if (part == 0) {
-          int at = top.count;
-          __syncthreads();
-          for (int q = 1; q < C; ++q) {
-            const TopShared* o = cl.map_shared_rank(&top, q);
-            const int n = o->count;
-            if (n > kCand || at + n > kCand) again = true;
-            if (again) break;
-            for (int i = tid; i < n; i += B) top.cand[at + i] = o->cand[i];
-            at += n;
-          }
-          if (tid == 0) top.count = at;
-          __syncthreads();
-        }
-      }
-      if (part == 0) {
-        if (again) exact_top(row, a.k, kth, top, R.part);
-        const int n = top.count;
-        // rank of a candidate = how many are larger; `per` neighbouring lanes share one
-        int per = 1;
-        while (per < 32 && 2 * per * n <= B) per *= 2;
-        for (int base = 0; base < n; base += B / per) {
-          const int i = base + tid / per;
-          int above = 0;
-          const unsigned long long me = i < n ? top.cand[i] : 0ull;
-          for (int j = tid % per; j < n; j += per) above += top.cand[j] > me;
-          for (int d = per >> 1; d > 0; d >>= 1) above += __shfl_xor_sync(kFull, above, d);
-          if (i < n && tid % per == 0 && above < a.k) {
-            const int e = (int)~(uint32_t)me;
-            const int64_t o = (int64_t)r * a.k + above;
-            a.top_idx[o] = e;
-            a.top_val[o] = (float)(((double)Elem<T>::to(row.x[e]) - (double)R.M) * (double)a.it - log(S));
-          }
-        }
-        for (int j = n + tid; j < a.k; j += B) {
-          a.top_idx[(int64_t)r * a.k + j] = -1;
-          a.top_val[(int64_t)r * a.k + j] = -INFINITY;
-        }
-      }
-      // the row is read whole above: no gradient may be written before that is done
-      if (C > 1) cg::this_cluster().sync();
-      else __syncthreads();
-    }
+  } else {                                        // rows that start at different offsets from 16 bytes
+    for (int e = e0 + tid; e < e1; e += B) dx[e] = grad_one(Elem<T>::to(row.x[e]));
   }
-
-  // -- the list's part of the loss -------------------------------------------------------------------
-  if constexpr (LIST && MODE != kBackward) {
-    float ref_row = fmaxf(R.M, kLowest);
-    if (OP == kTail) {                            // the list's entries join the others
-      float high = -INFINITY;
-      for (int j = tid; j < nl; j += B)
-        if (L.idx[j] >= 0) high = fmaxf(high, L.x[j]);
-      ref_row = fmaxf(block_max(high, R.max_list), ref_row);
+  if (edge >= 0) dx[edge] = grad_one(x_edge);
+  ring.drain();
+  __syncthreads();
+  // the list's entries, in 64 bits, over what the dense part wrote there
+  const double per = OP == kRenorm ? -(double)w / R.list_sum : -(double)w;
+  for (int j = tid; j < nl; j += B) {
+    const int e = L.idx[j];
+    if (e < 0 || !row.owns(e)) continue;
+    double add = 0.0;
+    bool mine = true;
+    for (int i = R.repeats ? 0 : j; i < (R.repeats ? nl : j + 1); ++i) {
+      if (L.idx[i] != e) continue;
+      if (i < j) mine = false;
+      if (OP == kLogprob) add += (double)L.v[i];
+      else if (R.Q != 0.0) add += per * L.q[i];
     }
-    double loss = 0.0, sum = 0.0;                 // sum q (log q - z_j), with z from ref_row; sum of exp(z_j)
-    for (int j = tid; j < nl; j += B) {
-      if (L.idx[j] < 0) continue;
-      const double z = ((double)L.x[j] - (double)ref_row) * (double)a.it;
-      const double lq = OP == kRenorm ? ((double)L.v[j] - R.list_max) * (double)a.it : (double)L.v[j];
-      const double q = L.q[j];
-      if (!(q == 0.0)) loss += q * (lq - z);
-      if (OP == kTail) {
-        bool count = true;
-        if (R.repeats)
-          for (int i = 0; i < j; ++i) count = count && L.idx[i] != L.idx[j];
-        if (count) sum += exp(z);
-      }
-    }
-    sum_put(loss, sum, R.sum_loss);
-    __syncthreads();
-    if (tid == 0) {
-      double unused;
-      R.ref_row = ref_row;
-      if (OP == kTail) {
-        const float ref = fmaxf(R.M, kLowest);
-        sum_get(unused, sum, R.sum_loss);
-        R.S_row = sum + (R.S != 0.0 ? R.S * (ref == ref_row ? 1.0 : exp(((double)ref - (double)ref_row) * (double)a.it)) : 0.0);
-        if (R.S == 0.0) R.rho = 0.0;              // no entry is left for the rest
-      } else {
-        R.S_row = R.S;
-      }
-    }
-  } else if constexpr (MODE != kBackward) {
-    if (tid == 0) {
-      R.ref_row = fmaxf(R.M, kLowest);
-      R.S_row = R.S;
-    }
-  }
-
-  // -- the dense gradient's factors ----------------------------------------------------------------
-  if constexpr (GRAD) {
-    if (tid == 0) {
-      float ref;
-      double S;
-      float ent = 0.0f;
-      if (MODE == kBackward) {
-        const float* st = a.stats_in + (int64_t)r * (OP == kTail ? 4 : 2);
-        R.ref_row = ref = fmaxf(st[0], kLowest);
-        R.S_row = S = (double)st[1];
-        if (OP == kTail) {
-          ref = fmaxf(st[2], kLowest);
-          S = (double)st[3];
-          if (S == 0.0) R.rho = 0.0;
-        }
-        if (OP == kLogprob && w_h != 0.0f) ent = a.entropy_in[r];
-      } else {
-        ref = fmaxf(R.M, kLowest);
-        S = R.S;
-        if (OP == kLogprob && w_h != 0.0f) ent = (float)(log(S) - 0.6931471805599453 * (R.T / S));
-      }
-      double A, Bl = 0.0;
-      const double it = (double)a.it;
-      if (OP == kLogprob) {
-        A = -it * ((double)w + (LIST ? R.Q : 0.0) + (w_h != 0.0f ? (double)w_h * (double)ent : 0.0));
-        Bl = -it * (double)w_h * 0.6931471805599453;
-        R.A_list = (float)A;
-      } else if (OP == kRenorm) {
-        A = it * (double)w * R.Q;
-        R.A_list = (float)A;
-      } else {
-        const double Rr = S == 0.0 ? 0.0
-                          : S / R.S_row * (ref == R.ref_row ? 1.0 : exp(((double)ref - (double)R.ref_row) * it));
-        A = it * (double)w * ((R.Q + R.rho) * Rr - R.rho);
-        R.A_list = (float)(it * (double)w * (R.Q + R.rho));
-      }
-      dense_factors(R, ref, S, A, Bl, a);
-    }
-  }
-  // every CTA of the row has read its list's and target's entries; with no gradient: the others may
-  // still read this CTA's shared memory
-  if (C > 1 && MODE != kBackward) cg::this_cluster().sync();
-  else __syncthreads();
-
-  // -- results per row, by a thread that nothing waits for -----------------------------------------
-  if (MODE != kBackward && part == 0 && tid == 32) {
-    const double S = R.S, S_row = R.S_row, log_s = log(S_row);
-    const float ref = fmaxf(R.M, kLowest);
-    if (OP == kLogprob) {
-      const bool nothing = S == 0.0;
-      if (a.out)
-        a.out[r] = target < 0 ? 0.0f
-                   : nothing  ? -INFINITY
-                              : (float)(((double)x_target - (double)ref) * (double)a.it - log_s);
-      if (a.entropy) a.entropy[r] = nothing ? 0.0f : (float)(log_s - 0.6931471805599453 * (R.T / S));
-    } else {
-      double loss, unused;
-      sum_get(loss, unused, R.sum_loss);
-      if (OP == kRenorm) {
-        const double sum = R.list_log;            // of the probabilities before their division by it
-        loss = R.Q == 0.0 ? 0.0 : loss / sum - log(sum) + (S_row == 0.0 ? (double)INFINITY : log_s);
-      } else {
-        const double rho = R.rho;
-        if (R.Q == 0.0 && rho == 0.0) {
-          loss = 0.0;
-        } else if (S_row == 0.0) {
-          loss = R.Q != 0.0 ? (double)INFINITY : 0.0;
-        } else {
-          loss += (R.Q + rho) * log_s;
-          if (!(rho == 0.0)) loss += rho * (log(rho) - ((double)ref - (double)R.ref_row) * (double)a.it - log(S));
-        }
-      }
-      a.out[r] = (float)loss;
-    }
-    if (a.stats) {
-      float* st = a.stats + (int64_t)r * (OP == kTail ? 4 : 2);
-      st[0] = R.ref_row;
-      st[1] = (float)S_row;
-      if (OP == kTail) {
-        st[2] = ref;
-        st[3] = (float)S;
-      }
-    }
-  }
-
-  // -- gradient ----------------------------------------------------------------------------------
-  if constexpr (GRAD) {
-    const float kf = R.k, A = R.A, Bl = R.Bl, ref = R.ref;
-    const bool nothing = R.S_row == 0.0;          // nothing but -inf: no distribution, no gradient
-    // no weight: zeros, whatever the row holds
-    const bool none = nothing || (OP == kLogprob ? (w == 0.0f && w_h == 0.0f && (!LIST || R.rho == 0.0)) : w == 0.0f);
-    const bool wild = R.wild;
-    T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
-    const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
-    auto grad = [&](uint4 v) {
-      float x[N];
-      Elem<T>::unpack(v, x);
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        float q0, q1;
-        f2 q = fma2(pair(x[i], x[i + 1]), c2, nk), g = A2;
-        unpair(q, &q0, &q1);
-        if (OP == kLogprob && Bl != 0.0f) g = fma2(pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), B2, A2);
-        unpair(mul2(pair(ex2(q0), ex2(q1)), g), &x[i], &x[i + 1]);
-      }
-      return Elem<T>::pack(x);
-    };
-    auto grad_one = [&](float x) {
-      float q = fmaf(x, a.c, -kf);
-      if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
-      return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
-    };
-    const int e0 = row.head + row.v0 * N, e1 = row.head + row.v1 * N;
-    const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
-    uint4* dvec = reinterpret_cast<uint4*>(dx + row.head) + row.v0;
-    if (early && (none || wild || !in_step))
-      for (int q = 0; q < min(kStages, ring.n); ++q) ring.wait(q, a.d_status);
-    if (none) {
-      if (in_step) {
-        for (int i = tid; i < own; i += B) __stcs(dvec + i, make_uint4(0, 0, 0, 0));
-      } else {
-        for (int e = e0 + tid; e < e1; e += B) dx[e] = Elem<T>::from(0.0f);
-      }
-      if (edge >= 0) dx[edge] = Elem<T>::from(0.0f);
-    } else {
-      if (in_step && !wild) {
-        // forward: the row's last chunks are still in the ring, so it goes backwards
-        for (int j = 0; j < ring.n; ++j) {
-          const int q = MODE == kFused ? ring.n - 1 - j : j;
-          if (MODE == kBackward || j >= kStages) ring.wait(q, a.d_status);
-          const uint4* at = ring.at(q);
-          uint4* to = dvec + ring.first(q);
-          const int left = own - ring.first(q);
-          if (left >= kChunk) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) __stcs(to + u * 32 + lane, grad(at[u * 32 + lane]));
-          } else {
-            for (int u = lane; u < left; u += 32) __stcs(to + u, grad(at[u]));
-          }
-          __syncwarp();
-          const int next = MODE == kFused ? q - kStages : q + kStages;
-          if (next >= 0 && next < ring.n) ring.issue(next);
-        }
-      } else {                                    // rows that start at different offsets from 16 bytes
-        for (int e = e0 + tid; e < e1; e += B) dx[e] = grad_one(Elem<T>::to(row.x[e]));
-      }
-      if (edge >= 0) dx[edge] = grad_one(x_edge);
-    }
-    ring.drain();
-    if (none) return;
-    __syncthreads();
-    // the list's entries, over what the dense part wrote there
-    auto value = [&](float x, double add) {
-      const double lp2 = ((double)x - (double)R.ref_row) * (double)a.it;
-      const double p = exp(lp2) / R.S_row;
-      double g = p * (double)R.A_list + (double)a.it * add;
-      if (OP == kLogprob && w_h != 0.0f && p != 0.0) g -= (double)a.it * (double)w_h * p * (lp2 - log(R.S_row));
-      return (float)g;
-    };
-    if constexpr (LIST) {
-      const double per = OP == kRenorm ? -(double)w / R.list_log : -(double)w;
-      for (int j = tid; j < nl; j += B) {
-        const int e = L.idx[j];
-        if (e < 0 || !row.owns(e)) continue;
-        double add = 0.0;
-        bool mine = true;
-        for (int i = R.repeats ? 0 : j; i < (R.repeats ? nl : j + 1); ++i) {
-          if (L.idx[i] != e) continue;
-          if (i < j) mine = false;
-          if (OP == kLogprob) add += (double)L.v[i];
-          else if (R.Q != 0.0) add += per * L.q[i];
-        }
-        if (mine) dx[e] = Elem<T>::from(value(L.x[j], add));
-      }
-    } else {
-      if (tid == 0 && target >= 0 && row.owns(target)) dx[target] = Elem<T>::from(value(x_target, (double)w));
-    }
+    if (!mine) continue;
+    const double z = ((double)L.x[j] - (double)R.ref_row) * (double)a.it, p = exp(z) / R.S_row;
+    double g = p * (double)R.A_list + (double)a.it * add;
+    if (OP == kLogprob && w_h != 0.0f && p != 0.0) g -= (double)a.it * (double)w_h * p * (z - log(R.S_row));
+    dx[e] = Elem<T>::from((float)g);
   }
 }
 
@@ -1395,6 +985,11 @@ constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at m
 
 struct StreamShared {
   uint64_t listed, weighed, sums, ready;          // the list's indices; its weights; all partial sums; results in 64 bits
+  uint64_t bounded, pushed;                       // alternatives: the bound is there; all candidates
+  uint32_t bound;
+  int nan, scratch[kRowWarps + 1];
+  float top_ref;
+  double top_log_s;
   float4 part[kParts];                            // rc, s, t, and as an int: 0 none, 1 sums, 2 beyond range, 3 below ref_min
   int repeats;                                    // an index stands in the list twice
   uint32_t hit[kHitWords];                        // chunks of the slice that hold entries of the list (modulo)
@@ -1441,8 +1036,16 @@ __device__ __forceinline__ bool peer_wait_bounded(uint64_t* bar) {
   return true;
 }
 
-// Shared memory: RES: the slice; else a chunk per warp for those that hold entries of the list. Then the list.
-template <class T, int OP, int MODE, bool RES>
+// A candidate to the first CTA of the row.
+__device__ __forceinline__ void peer_push(TopShared* top, uint32_t key, int e) {
+  uint32_t n;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(peer(&top->count, 0)) : "memory");
+  if (n < kCand) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer(&top->cand[n], 0)), "l"(cand_of(key, e)) : "memory");
+}
+
+// Shared memory: RES: the slice; else a chunk per warp for those that hold entries of the list. Then the
+// list; with the alternatives, the maxima and the candidates.
+template <class T, int OP, int MODE, bool RES, bool TOP>
 __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_kernel(const __grid_constant__ VocArgs a) {
   constexpr int N = Elem<T>::N, U = kUnroll;
   constexpr bool LIST = OP != kLogprob;
@@ -1456,12 +1059,22 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   uint4* const buf = RES ? dyn : dyn + warp * kChunk;
   List L;
   if constexpr (LIST) L.carve(dyn + (RES ? a.slice : W * kChunk), a.k);
+  // alternatives: the largest entries of parts of the row (a lane's vectors, for one CTA a lane's vectors of
+  // one place in the chunks), later their keys
+  float* maxima = reinterpret_cast<float*>(dyn + W * kChunk);
+  const int n_maxima = C == 1 ? W * 128 : C * W * 32;
+  TopShared& top = *reinterpret_cast<TopShared*>(maxima + n_maxima);
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.listed, 1);
     mbar_init(&sh.weighed, 1);
     mbar_init(&sh.sums, GRAD || part == 0 ? C * W : 1);
     mbar_init(&sh.ready, 1);
+    if (TOP) {
+      mbar_init(&sh.bounded, 1);
+      mbar_init(&sh.pushed, part == 0 ? C * W : 1);
+      top.count = 0;
+    }
     fence_mbarrier_init();
   }
   __syncthreads();
@@ -1617,6 +1230,34 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 
     // -- the row's results in 64 bits ------------------------------------------------------------------
     wait(&sh.sums);
+    if constexpr (TOP) {
+      // Each maximum is an entry, so a value that k of them reach is a lower bound of the row's k-th
+      // largest: the largest such one, or one that a few more reach.
+      uint32_t* keys = reinterpret_cast<uint32_t*>(maxima);
+      for (int i = lane; i < n_maxima; i += 32) keys[i] = order_key(maxima[i]);
+      __syncwarp();
+      auto reach = [&](uint32_t t) {
+        int n = 0;
+#pragma unroll 4
+        for (int i = lane; i < n_maxima; i += 32) n += keys[i] >= t;
+        return __reduce_add_sync(kFull, n);
+      };
+      uint32_t bound = kKeyNegInf + 1;
+      if (reach(bound) >= a.k) {
+        uint32_t res = 0;
+        for (int b = 31; b >= 0; --b) {
+          const uint32_t trial = res | (1u << b);
+          const int n = reach(trial);
+          if (n >= a.k) res = trial;
+          if (n >= a.k && n <= a.k + a.k / 4 + 2) break;
+        }
+        bound = max(bound, res);
+      }
+      if (lane < C) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(&sh.bound, lane)), "r"(bound) : "memory");
+        peer_arrive(&sh.bounded, lane);
+      }
+    }
     int kind = 0;
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
@@ -1752,9 +1393,18 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
 
     }
-    leave();
-    return;
-  }
+    if constexpr (TOP) {
+      if (lane == 0) {
+        sh.nan = !(Sd == Sd);
+        sh.top_ref = ref;
+        sh.top_log_s = log(Sd);
+      }
+      wait(&sh.pushed);
+    } else {
+      leave();
+      return;
+    }
+  } else {
 
   // Entries of the list in elements [e0, e0 + n) of the row: f(place in that range, entry).
   auto listed_in = [&](int e0, int n, auto f) {
@@ -1772,6 +1422,11 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   run.have = run.huge = false;
   run.rc = run.low_s = run.low_t = 0.0f;
   run.low_m = -INFINITY;
+  typename Elem<T>::Max high[U];
+  if (TOP) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) high[u] = Elem<T>::least();
+  }
   for (int left = own - warp * kChunk; left > 0; left -= step) {
     uint4 v[U];
 #pragma unroll
@@ -1791,6 +1446,11 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       __syncwarp();
       listed_in(row.head + (row.v0 + o) * N, min(kChunk, left) * N, [&](int e, int) { el[e] = Elem<T>::from(-INFINITY); });
       __syncwarp();
+    }
+    if (TOP) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (left >= kChunk || u * 32 + lane < left) Elem<T>::rise(high[u], v[u]);
     }
     if (left >= kChunk) {
       if (hit) {
@@ -1841,10 +1501,70 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
     }
     started();
+    if constexpr (TOP) {
+      if (C == 1) {
+        reinterpret_cast<float4*>(maxima)[warp * 32 + lane] =
+            make_float4(Elem<T>::top(high[0]), Elem<T>::top(high[1]), Elem<T>::top(high[2]), Elem<T>::top(high[3]));
+      } else {
+        const float m = fmaxf(fmaxf(Elem<T>::top(high[0]), Elem<T>::top(high[1])), fmaxf(Elem<T>::top(high[2]), Elem<T>::top(high[3])));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(&maxima[(part * W + warp) * 32 + lane], 0)), "f"(m) : "memory");
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      }
+      __syncwarp();
+    }
     if (lane < (GRAD ? C : 1)) {
       peer_store(&sh.part[part * W + warp], lane, make_float4(ref, s0, t0, __int_as_float(kind)));
       peer_arrive(&sh.sums, lane);
     }
+  }
+
+  // -- candidates for the alternatives ------------------------------------------------------------------
+  // Only parts whose maximum reaches the bound hold any; those are read again, from L2.
+  if constexpr (TOP) {
+    wait(&sh.bounded);
+    const uint32_t bound = sh.bound;
+    const int chunks = (own + kChunk - 1) / kChunk, mine = chunks > warp ? (chunks - warp + W - 1) / W : 0;
+    const int each = C == 1 ? mine : mine * U;    // vectors of a part
+    const int width = each <= 8 ? 8 : each <= 16 ? 16 : 32;
+    for (int place = 0; place < (C == 1 ? U : 1); ++place) {
+      float m;
+      if (C == 1) {
+        m = place == 0 ? Elem<T>::top(high[0]) : place == 1 ? Elem<T>::top(high[1])
+            : place == 2 ? Elem<T>::top(high[2]) : Elem<T>::top(high[3]);
+      } else {
+        m = fmaxf(fmaxf(Elem<T>::top(high[0]), Elem<T>::top(high[1])), fmaxf(Elem<T>::top(high[2]), Elem<T>::top(high[3])));
+      }
+      uint32_t owners = __ballot_sync(kFull, order_key(m) >= bound);
+      while (owners) {
+        int l = -1;                               // the lane whose part this lane reads: several at once
+        for (int g = 0; g < 32 / width; ++g) {
+          if (lane / width == g && owners) l = __ffs(owners) - 1;
+          owners &= owners - 1;
+        }
+        if (l < 0) continue;
+        for (int j = lane % width; j < each; j += width) {
+          const int c = C == 1 ? j : j / U, u = C == 1 ? place : j % U;
+          const int i = (warp + W * c) * kChunk + u * 32 + l;
+          if (i >= own) break;
+          float x[N];
+          Elem<T>::unpack(ld_row(row.vec() + row.v0 + i), x);
+#pragma unroll
+          for (int b = 0; b < N; ++b) {
+            const uint32_t key = order_key(x[b]);
+            if (key >= bound) peer_push(&top, key, row.head + (row.v0 + i) * N + b);
+          }
+        }
+      }
+    }
+    if (edge >= 0 && order_key(x_edge) >= bound) peer_push(&top, order_key(x_edge), edge);
+    if (C > 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) peer_arrive(&sh.pushed, 0);
+    if (part != 0) {
+      leave();
+      return;
+    }
+    wait(&sh.pushed);
   }
 
   // -- gradient ------------------------------------------------------------------------------------------
@@ -2072,21 +1792,88 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       dx[edge] = g;
     }
   }
-  leave();
+  if constexpr (!TOP) {
+    leave();
+    return;
+  }
+  }
+
+  // -- the alternatives, by all warps of the first CTA ---------------------------------------------------
+  if constexpr (TOP) {
+    const int tid = threadIdx.x, B = blockDim.x;
+    __syncthreads();
+    if (top.count > kCand || sh.nan) {
+      const Row<T> whole(row.x, a.vocab, 0, 1, 0u);
+      exact_top(whole, a.k, sh.bound, top, sh.scratch);
+    }
+    int n = top.count;
+    unsigned long long* cand = top.cand;
+    if (n > 192 && n > 2 * a.k) {
+      // too many to rank one against all: those from their own k-th key on, or a little below
+      uint32_t res = 0;
+      int reached = n;
+      for (int b = 31; b >= 0; --b) {
+        const uint32_t trial = res | (1u << b);
+        int c = 0;
+        for (int i = tid; i < n; i += B) c += (uint32_t)(cand[i] >> 32) >= trial;
+        c = block_count(c, sh.scratch);
+        if (c >= a.k) {
+          res = trial;
+          reached = c;
+          if (c <= a.k + a.k / 2 + 16) break;
+        }
+      }
+      unsigned long long* to = reinterpret_cast<unsigned long long*>(dyn);
+      if (reached <= W * kChunk * 2) {
+        __syncthreads();
+        if (tid == 0) sh.scratch[0] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += B)
+          if ((uint32_t)(cand[i] >> 32) >= res) to[atomicAdd(&sh.scratch[0], 1)] = cand[i];
+        __syncthreads();
+        cand = to;
+        n = reached;
+      }
+    }
+    // rank of a candidate = how many are larger; `per` neighbouring lanes share one
+    int per = 1;
+    while (per < 32 && 2 * per * n <= B) per *= 2;
+    for (int base = 0; base < n; base += B / per) {
+      const int i = base + tid / per;
+      int above = 0;
+      const unsigned long long me = i < n ? cand[i] : 0ull;
+      for (int j = tid % per; j < n; j += per) above += cand[j] > me;
+      for (int d = per >> 1; d > 0; d >>= 1) above += __shfl_xor_sync(kFull, above, d);
+      if (i < n && tid % per == 0 && above < a.k) {
+        const int e = (int)~(uint32_t)me;
+        const int64_t o = (int64_t)r * a.k + above;
+        a.top_idx[o] = e;
+        a.top_val[o] = (float)(((double)Elem<T>::to(row.x[e]) - (double)sh.top_ref) * (double)a.it - sh.top_log_s);
+      }
+    }
+    for (int j = n + tid; j < a.k; j += B) {
+      a.top_idx[(int64_t)r * a.k + j] = -1;
+      a.top_val[(int64_t)r * a.k + j] = -INFINITY;
+    }
+    leave();
+  }
 }
 
 // ---- launch -----------------------------------------------------------------------------------------
 
-template <class T, int OP, int MODE, bool RES>
+constexpr size_t kPlainBytes = 32 << 10;          // dynamic shared memory that needs no leave beside the static part
+
+template <class T, int OP, int MODE, bool RES, bool TOP>
 int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
   const int64_t own = cdiv(nv, split), chunks = cdiv(own, kChunk);
   int warps = (int)(chunks < kRowWarps ? (chunks > 0 ? chunks : 1) : kRowWarps);
   a.split = split;
   a.slice = (int32_t)(chunks * kChunk);
   a.inv_split = (uint32_t)(((1ull << 32) + split - 1) / split);
-  const size_t smem = (RES ? (size_t)a.slice : (size_t)warps * kChunk) * 16 + (OP == kLogprob ? 0 : List::bytes(a.k));
-  auto* kernel = voc_stream_kernel<T, OP, MODE, RES>;
-  if (smem > (32 << 10) &&                        // beyond what needs no leave, with the static part
+  const size_t smem = (RES ? (size_t)a.slice : (size_t)warps * kChunk) * 16 + (OP == kLogprob ? 0 : List::bytes(a.k)) +
+                      (TOP ? (size_t)(split == 1 ? warps * 128 : split * warps * 32) * 4 + sizeof(TopShared) : 0);
+  auto* kernel = voc_stream_kernel<T, OP, MODE, RES, TOP>;
+  if (smem > kPlainBytes &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return GSPARSE_ERR_CUDA;
@@ -2114,7 +1901,7 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
 constexpr int64_t kSliceBytes = 48 << 10;         // four CTAs per SM
 constexpr int64_t kSliceMost = 200 << 10;         // one
 
-template <class T, int OP, int MODE>
+template <class T, int OP, int MODE, bool TOP>
 int voc_stream(const VocArgs& a, cudaStream_t st) {
   const int64_t nv = cdiv(a.vocab, Elem<T>::N);
   // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
@@ -2123,62 +1910,42 @@ int voc_stream(const VocArgs& a, cudaStream_t st) {
   if constexpr (MODE == kFused) {
     const int64_t need = cdiv(nv * 16, kSliceBytes);
     if (split < need) split = need < 8 ? (int)need : 8;
-    if (nv * 16 <= split * kSliceMost) return voc_stream_launch<T, OP, MODE, true>(a, nv, split, st);
+    if (nv * 16 <= split * kSliceMost) return voc_stream_launch<T, OP, MODE, true, false>(a, nv, split, st);
   }
-  return voc_stream_launch<T, OP, MODE, false>(a, nv, split, st);
+  return voc_stream_launch<T, OP, MODE, false, TOP>(a, nv, split, st);
 }
 
-template <class T, int OP, bool TOP, int MODE>
-int voc_of_type(VocArgs a, cudaStream_t st) {
-  if constexpr (!TOP && MODE != kBackward)
-    return voc_stream<T, OP, MODE>(a, st);
-  else {
+template <class T, int OP>
+int voc_backward(VocArgs a, cudaStream_t st) {
   const int64_t nv = cdiv(a.vocab, Elem<T>::N);
   // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
   int split = 1;
   while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
-  if (MODE == kFused)                             // a slice whose second read still finds it in L2
-    while (split < 8 && nv * 16 > split * (200 << 10)) split *= 2;
   a.split = split;
   a.inv_split = (uint32_t)(((1ull << 32) + split - 1) / split);
   int threads = 64;
-  while (threads < 256 && (int64_t)threads * kUnroll * split < nv) threads *= 2;
-  if (TOP) while (threads < kVocThreads && threads < 2 * a.k) threads *= 2;
-  size_t smem = ring_bytes(threads);
-  if (OP != kLogprob || MODE == kBackward) smem += List::bytes(OP == kLogprob ? a.k + 1 : a.k);
-  if (TOP) smem = MODE == kFused ? smem + sizeof(TopShared) : smem > sizeof(TopShared) ? smem : sizeof(TopShared);
-  auto* kernel = voc_kernel<T, OP, TOP, MODE>;
-  if (smem > (32 << 10) &&                        // beyond what needs no leave, with the static part
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+  while (threads < kVocThreads && (int64_t)threads * kUnroll * split < nv) threads *= 2;
+  const size_t smem = ring_bytes(threads) + List::bytes(OP == kLogprob ? a.k + 1 : a.k);
+  auto* kernel = voc_backward_kernel<T, OP>;
+  if (smem > kPlainBytes && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return GSPARSE_ERR_CUDA;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.rows * a.split));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.split;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = MODE != kBackward && a.split > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
-    cudaGetLastError();
-    return GSPARSE_ERR_CUDA;
-  }
+  launch(kernel, (unsigned)((int64_t)a.rows * split), (unsigned)threads, smem, st, a);
   return launch_status();
-  }
 }
 
-template <int OP, bool TOP, int MODE>
+template <class T, int OP, int MODE, bool TOP>
+int voc_of_type(const VocArgs& a, cudaStream_t st) {
+  if constexpr (MODE == kBackward) return voc_backward<T, OP>(a, st);
+  else return voc_stream<T, OP, MODE, TOP>(a, st);
+}
+
+template <int OP, int MODE, bool TOP = false>
 int voc_by_type(int32_t dtype, const VocArgs& a, cudaStream_t st) {
-  if (dtype == GSPARSE_F32) return voc_of_type<float, OP, TOP, MODE>(a, st);
-  if (dtype == GSPARSE_BF16) return voc_of_type<__nv_bfloat16, OP, TOP, MODE>(a, st);
-  return voc_of_type<__half, OP, TOP, MODE>(a, st);
+  if (dtype == GSPARSE_F32) return voc_of_type<float, OP, MODE, TOP>(a, st);
+  if (dtype == GSPARSE_BF16) return voc_of_type<__nv_bfloat16, OP, MODE, TOP>(a, st);
+  return voc_of_type<__half, OP, MODE, TOP>(a, st);
 }
 
 bool voc_dtype(int32_t t) { return t == GSPARSE_F32 || t == GSPARSE_BF16 || t == GSPARSE_F16; }
@@ -2246,9 +2013,14 @@ int gsparse_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int6
   a.weight = grad_logprob;
   a.weight_entropy = grad_entropy;
   cudaStream_t s = (cudaStream_t)stream;
-  if (dlogits)
-    return top_k ? voc_by_type<kLogprob, true, kFused>(dtype, a, s) : voc_by_type<kLogprob, false, kFused>(dtype, a, s);
-  return top_k ? voc_by_type<kLogprob, true, kForward>(dtype, a, s) : voc_by_type<kLogprob, false, kForward>(dtype, a, s);
+  if (top_k && dlogits) {                         // the alternatives first: the gradient may take the logits' place
+    VocArgs t = a;
+    t.out = t.entropy = t.stats = nullptr;
+    const int e = voc_by_type<kLogprob, kForward, true>(dtype, t, s);
+    if (e != GSPARSE_OK) return e;
+  }
+  if (dlogits) return voc_by_type<kLogprob, kFused>(dtype, a, s);
+  return top_k ? voc_by_type<kLogprob, kForward, true>(dtype, a, s) : voc_by_type<kLogprob, kForward>(dtype, a, s);
 }
 
 int gsparse_token_logprobs_backward(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
@@ -2273,7 +2045,7 @@ int gsparse_token_logprobs_backward(const void* logits, int32_t dtype, int64_t r
   a.k = top_k;
   a.list_idx = top_idx;
   a.list_val = grad_top;
-  return voc_by_type<kLogprob, false, kBackward>(dtype, a, (cudaStream_t)stream);
+  return voc_by_type<kLogprob, kBackward>(dtype, a, (cudaStream_t)stream);
 }
 
 int gsparse_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
@@ -2299,8 +2071,8 @@ int gsparse_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64_
   a.weight = grad_loss;
   cudaStream_t s = (cudaStream_t)stream;
   if (mode == GSPARSE_DISTILL_TAIL)
-    return dlogits ? voc_by_type<kTail, false, kFused>(dtype, a, s) : voc_by_type<kTail, false, kForward>(dtype, a, s);
-  return dlogits ? voc_by_type<kRenorm, false, kFused>(dtype, a, s) : voc_by_type<kRenorm, false, kForward>(dtype, a, s);
+    return dlogits ? voc_by_type<kTail, kFused>(dtype, a, s) : voc_by_type<kTail, kForward>(dtype, a, s);
+  return dlogits ? voc_by_type<kRenorm, kFused>(dtype, a, s) : voc_by_type<kRenorm, kForward>(dtype, a, s);
 }
 
 int gsparse_distill_topk_backward(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
@@ -2322,8 +2094,8 @@ int gsparse_distill_topk_backward(const void* logits, int32_t dtype, int64_t row
   a.k = k;
   a.stats_in = stats;
   a.weight = grad_loss;
-  if (mode == GSPARSE_DISTILL_TAIL) return voc_by_type<kTail, false, kBackward>(dtype, a, (cudaStream_t)stream);
-  return voc_by_type<kRenorm, false, kBackward>(dtype, a, (cudaStream_t)stream);
+  if (mode == GSPARSE_DISTILL_TAIL) return voc_by_type<kTail, kBackward>(dtype, a, (cudaStream_t)stream);
+  return voc_by_type<kRenorm, kBackward>(dtype, a, (cudaStream_t)stream);
 }
 
 }  // extern "C"
