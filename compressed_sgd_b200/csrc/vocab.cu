@@ -28,7 +28,7 @@ constexpr int kVocWarps = kVocThreads / 32;
 constexpr int kUnroll = 4;                        // vectors of 16 bytes per lane and chunk
 constexpr int kChunk = 32 * kUnroll;              // vectors per chunk
 constexpr int kChunkLog = 7;
-static_assert(kChunk == 1 << kChunkLog, "");
+static_assert(kChunk == 1 << kChunkLog && kUnroll == 4, "");
 constexpr int kStages = 3;                        // chunks per warp in shared memory
 constexpr int kCand = 2048;                       // candidates for a row's alternatives
 
@@ -846,6 +846,7 @@ struct Sums {
   // their own maximum and the difference taken first; they count where the row has no others
   float low_m, low_s, low_t;
   bool have, huge;        // rc is set; an entry is beyond -ref_min
+  bool gaps;              // -inf has been met: exponents are clamped from there on
 };
 
 // What the fast sums cannot take: -inf (0 * -inf makes t NaN), or entries far above rc. The vectors
@@ -881,12 +882,13 @@ __device__ __noinline__ void sums_slow(Sums& r, const uint4* v, f2 s, f2 t, cons
   r.rc = m.rc;
   r.s = m.s;
   r.t = m.t;
+  r.gaps = true;
 }
 
 // Adds NV vectors. Entry by entry: unpack, half a fused multiply-add, 2^q, half an addition, half a
-// fused multiply-add.
-template <class T, int NV>
-__device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs& a) {
+// fused multiply-add; GAPS: and a maximum.
+template <class T, int NV, bool GAPS>
+__device__ __forceinline__ void sums_some(Sums& r, const uint4* v, const VocArgs& a) {
   constexpr int N = Elem<T>::N;
   const f2 c2 = pair(a.c, a.c), nrc = pair(-r.rc, -r.rc);
   f2 s = r.s, t = r.t;
@@ -896,9 +898,14 @@ __device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs&
     Elem<T>::unpack(v[u], x);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const f2 q = fma2(pair(x[i], x[i + 1]), c2, nrc);
+      f2 q = fma2(pair(x[i], x[i + 1]), c2, nrc);
       float q0, q1;
       unpair(q, &q0, &q1);
+      if (GAPS) {
+        q0 = max_nan(q0, -kFarBits);
+        q1 = max_nan(q1, -kFarBits);
+        q = pair(q0, q1);
+      }
       const f2 e = pair(ex2(q0), ex2(q1));
       s = add2(s, e);
       t = fma2(e, q, t);
@@ -917,6 +924,12 @@ __device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs&
     r.s = s;
     r.t = t;
   }
+}
+
+template <class T, int NV>
+__device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs& a, bool gaps = false) {
+  if (r.gaps || gaps) sums_some<T, NV, true>(r, v, a);
+  else sums_some<T, NV, false>(r, v, a);
 }
 
 // A chunk before rc is set whose largest entry over the warp, top, is not from ref_min to -ref_min.
@@ -952,6 +965,13 @@ __device__ __forceinline__ bool sums_start(Sums& r, const uint4* v, const VocArg
     r.have = true;
     return true;
   }
+  bool all = true;                                // nothing but -inf
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const uint32_t no = Elem<T>::nothing().x;
+    all = all && v[u].x == no && v[u].y == no && v[u].z == no && v[u].w == no;
+  }
+  if (__all_sync(kFull, all)) return false;
   Sums again = r;
   uint4 w[NV];
 #pragma unroll
@@ -985,8 +1005,9 @@ constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at m
 
 struct StreamShared {
   uint64_t listed, weighed, sums, ready;          // the list's indices; its weights; all partial sums; results in 64 bits
-  uint64_t bounded, pushed;                       // alternatives: the bound is there; all candidates
-  uint32_t bound;
+  uint64_t bounded, pushed;                       // alternatives: the CTAs' bounds are there; all candidates
+  uint32_t bounds[8], tops[2][kRowWarps], least[2][kRowWarps];
+  int reach[2][kRowWarps], owners;
   int nan, scratch[kRowWarps + 1];
   float top_ref;
   double top_log_s;
@@ -1059,11 +1080,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   uint4* const buf = RES ? dyn : dyn + warp * kChunk;
   List L;
   if constexpr (LIST) L.carve(dyn + (RES ? a.slice : W * kChunk), a.k);
-  // alternatives: the largest entries of parts of the row (a lane's vectors, for one CTA a lane's vectors of
-  // one place in the chunks), later their keys
-  float* maxima = reinterpret_cast<float*>(dyn + W * kChunk);
-  const int n_maxima = C == 1 ? W * 128 : C * W * 32;
-  TopShared& top = *reinterpret_cast<TopShared*>(maxima + n_maxima);
+  // alternatives: parts of the slice that hold candidates (a part is what a lane reads at one place of its
+  // chunks), and the candidates
+  uint16_t* owners = reinterpret_cast<uint16_t*>(dyn + W * kChunk);
+  TopShared& top = *reinterpret_cast<TopShared*>(owners + W * 128);
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.listed, 1);
@@ -1071,9 +1091,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     mbar_init(&sh.sums, GRAD || part == 0 ? C * W : 1);
     mbar_init(&sh.ready, 1);
     if (TOP) {
-      mbar_init(&sh.bounded, 1);
+      mbar_init(&sh.bounded, C);
       mbar_init(&sh.pushed, part == 0 ? C * W : 1);
       top.count = 0;
+      sh.owners = 0;
     }
     fence_mbarrier_init();
   }
@@ -1230,34 +1251,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 
     // -- the row's results in 64 bits ------------------------------------------------------------------
     wait(&sh.sums);
-    if constexpr (TOP) {
-      // Each maximum is an entry, so a value that k of them reach is a lower bound of the row's k-th
-      // largest: the largest such one, or one that a few more reach.
-      uint32_t* keys = reinterpret_cast<uint32_t*>(maxima);
-      for (int i = lane; i < n_maxima; i += 32) keys[i] = order_key(maxima[i]);
-      __syncwarp();
-      auto reach = [&](uint32_t t) {
-        int n = 0;
-#pragma unroll 4
-        for (int i = lane; i < n_maxima; i += 32) n += keys[i] >= t;
-        return __reduce_add_sync(kFull, n);
-      };
-      uint32_t bound = kKeyNegInf + 1;
-      if (reach(bound) >= a.k) {
-        uint32_t res = 0;
-        for (int b = 31; b >= 0; --b) {
-          const uint32_t trial = res | (1u << b);
-          const int n = reach(trial);
-          if (n >= a.k) res = trial;
-          if (n >= a.k && n <= a.k + a.k / 4 + 2) break;
-        }
-        bound = max(bound, res);
-      }
-      if (lane < C) {
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(&sh.bound, lane)), "r"(bound) : "memory");
-        peer_arrive(&sh.bounded, lane);
-      }
-    }
     int kind = 0;
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
@@ -1419,7 +1412,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   if (OP == kTail) wait(&sh.listed);
   Sums run;
   run.s = run.t = pair(0.0f, 0.0f);
-  run.have = run.huge = false;
+  run.have = run.huge = run.gaps = false;
   run.rc = run.low_s = run.low_t = 0.0f;
   run.low_m = -INFINITY;
   typename Elem<T>::Max high[U];
@@ -1457,13 +1450,13 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = chunk[u * 32 + lane];
       }
-      if (run.have || sums_start<T, U>(run, v, a)) sums_add<T, U>(run, v, a);
+      if (run.have || sums_start<T, U>(run, v, a)) sums_add<T, U>(run, v, a, hit);
     } else {
 #pragma unroll 1
       for (int u = lane; u - lane < left; u += 32) {
         const uint4 one = u < left ? chunk[u] : Elem<T>::nothing();
         if (run.have || sums_start<T, 1>(run, &one, a))
-          if (u < left) sums_add<T, 1>(run, &one, a);
+          if (u < left) sums_add<T, 1>(run, &one, a, hit);
       }
     }
   }
@@ -1501,17 +1494,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
     }
     started();
-    if constexpr (TOP) {
-      if (C == 1) {
-        reinterpret_cast<float4*>(maxima)[warp * 32 + lane] =
-            make_float4(Elem<T>::top(high[0]), Elem<T>::top(high[1]), Elem<T>::top(high[2]), Elem<T>::top(high[3]));
-      } else {
-        const float m = fmaxf(fmaxf(Elem<T>::top(high[0]), Elem<T>::top(high[1])), fmaxf(Elem<T>::top(high[2]), Elem<T>::top(high[3])));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(&maxima[(part * W + warp) * 32 + lane], 0)), "f"(m) : "memory");
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-      }
-      __syncwarp();
-    }
     if (lane < (GRAD ? C : 1)) {
       peer_store(&sh.part[part * W + warp], lane, make_float4(ref, s0, t0, __int_as_float(kind)));
       peer_arrive(&sh.sums, lane);
@@ -1519,40 +1501,89 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   }
 
   // -- candidates for the alternatives ------------------------------------------------------------------
-  // Only parts whose maximum reaches the bound hold any; those are read again, from L2.
+  // The largest entry of a part is an entry, so a value that k parts reach is a lower bound of the
+  // slice's, and so of the row's, k-th largest. The warps look for the largest such value by bisection on
+  // the keys (a value that a few more parts reach will do), and the CTAs take the largest of theirs. Then
+  // the parts that reach it are read again, from L2, shared out among the warps: the likely tokens of a
+  // vocabulary sorted by frequency all lie in one warp's chunks.
   if constexpr (TOP) {
-    wait(&sh.bounded);
-    const uint32_t bound = sh.bound;
-    const int chunks = (own + kChunk - 1) / kChunk, mine = chunks > warp ? (chunks - warp + W - 1) / W : 0;
-    const int each = C == 1 ? mine : mine * U;    // vectors of a part
-    const int width = each <= 8 ? 8 : each <= 16 ? 16 : 32;
-    for (int place = 0; place < (C == 1 ? U : 1); ++place) {
-      float m;
-      if (C == 1) {
-        m = place == 0 ? Elem<T>::top(high[0]) : place == 1 ? Elem<T>::top(high[1])
-            : place == 2 ? Elem<T>::top(high[2]) : Elem<T>::top(high[3]);
-      } else {
-        m = fmaxf(fmaxf(Elem<T>::top(high[0]), Elem<T>::top(high[1])), fmaxf(Elem<T>::top(high[2]), Elem<T>::top(high[3])));
-      }
-      uint32_t owners = __ballot_sync(kFull, order_key(m) >= bound);
-      while (owners) {
-        int l = -1;                               // the lane whose part this lane reads: several at once
-        for (int g = 0; g < 32 / width; ++g) {
-          if (lane / width == g && owners) l = __ffs(owners) - 1;
-          owners &= owners - 1;
-        }
-        if (l < 0) continue;
-        for (int j = lane % width; j < each; j += width) {
-          const int c = C == 1 ? j : j / U, u = C == 1 ? place : j % U;
-          const int i = (warp + W * c) * kChunk + u * 32 + l;
-          if (i >= own) break;
-          float x[N];
-          Elem<T>::unpack(ld_row(row.vec() + row.v0 + i), x);
+    auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"r"(W * 32) : "memory"); };
+    uint32_t key[U], mx = 0, mn = 0xffffffffu;
 #pragma unroll
-          for (int b = 0; b < N; ++b) {
-            const uint32_t key = order_key(x[b]);
-            if (key >= bound) peer_push(&top, key, row.head + (row.v0 + i) * N + b);
-          }
+    for (int u = 0; u < U; ++u) {
+      key[u] = order_key(Elem<T>::top(high[u]));
+      mx = max(mx, key[u]);
+      if (key[u] > kKeyNegInf) mn = min(mn, key[u]);
+    }
+    int turn = 0;
+    auto reach = [&](uint32_t t) {                // parts that reach t, over the CTA
+      int n = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) n += key[u] >= t;
+      n = __reduce_add_sync(kFull, n);
+      if (lane == 0) sh.reach[turn][warp] = n;
+      meet();
+      n = 0;
+      for (int q = 0; q < W; ++q) n += sh.reach[turn][q];
+      turn ^= 1;
+      return n;
+    };
+    mx = __reduce_max_sync(kFull, mx);
+    mn = __reduce_min_sync(kFull, mn);
+    if (lane == 0) {
+      sh.tops[0][warp] = mx;
+      sh.least[0][warp] = mn;
+    }
+    uint32_t bound = kKeyNegInf + 1;
+    if (reach(bound) >= a.k) {
+      for (int q = 0; q < W; ++q) {
+        mx = max(mx, sh.tops[0][q]);
+        mn = min(mn, sh.least[0][q]);
+      }
+      const int bits = 32 - __clz(mx ^ mn);       // below these the keys agree
+      uint32_t res = bits == 32 ? 0u : mx >> bits << bits;
+      for (int b = bits - 1; b >= 0; --b) {
+        const uint32_t trial = res | (1u << b);
+        const int n = reach(trial);
+        if (n >= a.k) {
+          res = trial;
+          if (n <= a.k + a.k / 4 + 2) break;
+        }
+      }
+      bound = max(bound, res);
+    }
+    if (C > 1) {
+      if (warp == 0 && lane < C) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(&sh.bounds[part], lane)), "r"(bound) : "memory");
+        peer_arrive(&sh.bounded, lane);
+      }
+      wait(&sh.bounded);
+      for (int q = 0; q < C; ++q) bound = max(bound, sh.bounds[q]);
+    }
+    if (lane == 0 && warp == 0) sh.bounds[0] = bound;   // (what others may still read there does not change theirs)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t who = __ballot_sync(kFull, key[u] >= bound);
+      int first = 0;
+      if (lane == 0 && who) first = atomicAdd(&sh.owners, __popc(who));
+      first = __shfl_sync(kFull, first, 0);
+      if (key[u] >= bound) owners[first + __popc(who & lanemask_lt())] = (uint16_t)(warp << 7 | u << 5 | lane);
+    }
+    meet();
+    const int n_own = sh.owners, chunks = (own + kChunk - 1) / kChunk;
+    const int most = (chunks + W - 1) / W;        // vectors of a part
+    const int width = most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    for (int q = (warp * 32 + lane) / width; q < n_own; q += W * 32 / width) {
+      const int o = owners[q], at_w = o >> 7, at_u = (o >> 5) & 3, at_l = o & 31;
+      for (int j = lane % width; j < most; j += width) {
+        const int i = (at_w + W * j) * kChunk + at_u * 32 + at_l;
+        if (i >= own) break;
+        float x[N];
+        Elem<T>::unpack(ld_row(row.vec() + row.v0 + i), x);
+#pragma unroll
+        for (int b = 0; b < N; ++b) {
+          const uint32_t k = order_key(x[b]);
+          if (k >= bound) peer_push(&top, k, row.head + (row.v0 + i) * N + b);
         }
       }
     }
@@ -1804,7 +1835,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     __syncthreads();
     if (top.count > kCand || sh.nan) {
       const Row<T> whole(row.x, a.vocab, 0, 1, 0u);
-      exact_top(whole, a.k, sh.bound, top, sh.scratch);
+      exact_top(whole, a.k, sh.bounds[0], top, sh.scratch);
     }
     int n = top.count;
     unsigned long long* cand = top.cand;
@@ -1871,7 +1902,7 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
   a.slice = (int32_t)(chunks * kChunk);
   a.inv_split = (uint32_t)(((1ull << 32) + split - 1) / split);
   const size_t smem = (RES ? (size_t)a.slice : (size_t)warps * kChunk) * 16 + (OP == kLogprob ? 0 : List::bytes(a.k)) +
-                      (TOP ? (size_t)(split == 1 ? warps * 128 : split * warps * 32) * 4 + sizeof(TopShared) : 0);
+                      (TOP ? (size_t)warps * 256 + sizeof(TopShared) : 0);
   auto* kernel = voc_stream_kernel<T, OP, MODE, RES, TOP>;
   if (smem > kPlainBytes &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
