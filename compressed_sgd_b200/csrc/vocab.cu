@@ -988,6 +988,15 @@ __device__ __forceinline__ uint4 ld_row(const uint4* p) {
   return v;
 }
 
+// Asynchronous 16-byte copies by each lane for itself.
+__device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // ---- a row per cluster, streamed -----------------------------------------------------------------------
 
 // A cluster of C CTAs takes a row; W warps of a CTA stream its slice chunk by chunk (U vectors per lane, the
@@ -1001,6 +1010,7 @@ __device__ __forceinline__ uint4 ld_row(const uint4* p) {
 // L2 costs half as much traffic again between L2 and the SMs, which is what bounds that form.
 constexpr int kRowWarps = 7;                      // streaming warps, at most
 constexpr int kRowCtas = 4;                       // per SM
+constexpr int kAhead = 2;                         // chunks per warp on their way to shared memory (RES)
 constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at most
 
 struct StreamShared {
@@ -1031,8 +1041,11 @@ __device__ __forceinline__ uint32_t peer(const void* p, int q) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
   return r;
 }
-__device__ __forceinline__ void peer_store(float4* p, int q, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer(p, q)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// The store itself counts on the barrier there: a release over the cluster before an arrival costs the warp
+// about 2000 cycles.
+__device__ __forceinline__ void peer_send(float4* p, uint64_t* bar, int q, float4 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(peer(p, q)),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(peer(bar, q))
                : "memory");
 }
 __device__ __forceinline__ void peer_arrive(uint64_t* bar, int q) {
@@ -1088,7 +1101,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   if (threadIdx.x == 0) {
     mbar_init(&sh.listed, 1);
     mbar_init(&sh.weighed, 1);
-    mbar_init(&sh.sums, GRAD || part == 0 ? C * W : 1);
+    mbar_init(&sh.sums, C == 1 ? W : 1);
     mbar_init(&sh.ready, 1);
     if (TOP) {
       mbar_init(&sh.bounded, C);
@@ -1097,6 +1110,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       sh.owners = 0;
     }
     fence_mbarrier_init();
+    if (C > 1 && (GRAD || part == 0)) mbar_arrive_expect_tx(&sh.sums, 16u * (uint32_t)(C * W));
   }
   __syncthreads();
   // the CTAs meet without waiting; what is sent to another waits for its start
@@ -1108,7 +1122,13 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   const uint4* at = row.vec() + row.v0 + warp * kChunk + lane;
   uint4 nx[U];
   auto request = [&](int left) {                  // of the slice, from the chunk's first vector on
-    if (left >= kChunk) {
+    if constexpr (RES) {                          // straight to its place
+      uint4* to = buf + (own - left) + lane;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * 32 + lane < left) copy_async(to + u * 32, at + u * 32);
+      copy_commit();
+    } else if (left >= kChunk) {
 #pragma unroll
       for (int u = 0; u < U; ++u) nx[u] = ld_row(at + u * 32);
     } else {
@@ -1118,7 +1138,8 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     }
     at += step;
   };
-  if (warp < W) request(own - warp * kChunk);
+  if (warp < W)
+    for (int q = 0; q < (RES ? kAhead : 1); ++q) request(own - warp * kChunk - q * step);
   // the first warp's lanes take the head and the tail, one entry each
   int edge = -1;
   if (warp == 0) {
@@ -1421,18 +1442,27 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     for (int u = 0; u < U; ++u) high[u] = Elem<T>::least();
   }
   for (int left = own - warp * kChunk; left > 0; left -= step) {
-    uint4 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = nx[u];
-    request(left - step);
     const int o = own - left;                     // first vector of the chunk
     const bool hit = OP == kTail && hits(o);
     uint4* chunk = RES ? buf + o : buf;
-    if (RES || hit || left < kChunk) {
-      if (!RES) __syncwarp();
+    uint4 v[U];
+    if constexpr (RES) {
+      copy_wait<kAhead - 1>();
+      request(left - kAhead * step);
+      if (!hit) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (left >= kChunk || u * 32 + lane < left) chunk[u * 32 + lane] = v[u];
+        for (int u = 0; u < U; ++u) v[u] = chunk[u * 32 + lane];
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = nx[u];
+      request(left - step);
+      if (hit || left < kChunk) {
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (left >= kChunk || u * 32 + lane < left) chunk[u * 32 + lane] = v[u];
+      }
     }
     if (hit) {                                    // the list's entries leave the sums
       T* el = reinterpret_cast<T*>(chunk);
@@ -1494,9 +1524,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
     }
     started();
-    if (lane < (GRAD ? C : 1)) {
-      peer_store(&sh.part[part * W + warp], lane, make_float4(ref, s0, t0, __int_as_float(kind)));
-      peer_arrive(&sh.sums, lane);
+    const float4 sums = make_float4(ref, s0, t0, __int_as_float(kind));
+    if (C == 1) {                                 // (no asynchronous store outside a cluster launch: it is illegal there)
+      if (lane == 0) sh.part[warp] = sums;
+      arrive(&sh.sums);
+    } else if (lane < (GRAD ? C : 1)) {
+      peer_send(&sh.part[part * W + warp], &sh.sums, lane, sums);
     }
   }
 
@@ -1929,7 +1962,7 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
   return launch_status();
 }
 
-constexpr int64_t kSliceBytes = 48 << 10;         // four CTAs per SM
+constexpr int64_t kSliceBytes = 64 << 10;         // three or four CTAs per SM
 constexpr int64_t kSliceMost = 200 << 10;         // one
 
 template <class T, int OP, int MODE, bool TOP>
@@ -1939,8 +1972,9 @@ int voc_stream(const VocArgs& a, cudaStream_t st) {
   int split = 1;
   while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
   if constexpr (MODE == kFused) {
-    const int64_t need = cdiv(nv * 16, kSliceBytes);
-    if (split < need) split = need < 8 ? (int)need : 8;
+    // Powers of two: clusters of 3 and 6 find their places later than those of 2 and 4 (2048 x 50021 fp16: 212
+    // us in three slices of 33 KB, 152 in two of 50; 8192 x 128000 bf16: 1022 us in six, 888 in four).
+    while (split < 8 && nv * 16 > split * kSliceBytes) split *= 2;
     if (nv * 16 <= split * kSliceMost) return voc_stream_launch<T, OP, MODE, true, false>(a, nv, split, st);
   }
   return voc_stream_launch<T, OP, MODE, false, TOP>(a, nv, split, st);
