@@ -1030,9 +1030,9 @@ struct StreamShared {
   float list_high;                                // kTail: largest logit at the list's entries
   double list_exp;                                // and the sum of exp(z - its z) over them
   // the results of the careful route
-  float k, A, Bl, ref, ref_row;
+  float k, A, Bl, ref;
   int wild, none;
-  double A_list, S_row, per, log_s;
+  float g_target;                                 // the gradient at the target
 };
 
 // Stores to and arrivals at another CTA of the cluster.
@@ -1348,34 +1348,58 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
     }
     double log_s = 0.0;
-    if (GRAD && kind != 1) {
-      double A, Bl = 0.0;
+    if constexpr (GRAD) {
       const double itd = (double)a.it;
-      if (OP == kLogprob) {
-        double ent = 0.0;
-        if (w_h != 0.0f) {
-          log_s = log(S_row);
-          ent = (double)(float)(log_s - 0.6931471805599453 * (Td / Sd));
+      double ent = 0.0;
+      if (w_h != 0.0f) {
+        log_s = log(S_row);
+        ent = (double)(float)(log_s - 0.6931471805599453 * (Td / Sd));
+      }
+      const double A_list = OP == kLogprob ? -itd * ((double)w + (double)w_h * ent)
+                            : itd * (double)w * (OP == kRenorm ? Q : Q + rho);
+      // the gradient at the list's entries, in 64 bits: in the place of their logits
+      const double inv = 1.0 / S_row;
+      auto entry = [&](float x, double add) {
+        const double z = ((double)x - (double)ref_row) * itd, p = exp(z) * inv;
+        double g = p * A_list + itd * add;
+        if (OP == kLogprob && w_h != 0.0f && p != 0.0) g -= itd * (double)w_h * p * (z - log_s);
+        return (float)g;
+      };
+      if constexpr (LIST) {
+        const double per = OP == kRenorm ? -(double)w / sh.list_sum : -(double)w;
+        for (int j = lane; j < a.k; j += 32) {
+          const int e = L.idx[j];
+          if (e < 0 || !row.owns(e)) continue;
+          double add = 0.0;
+          if (Q != 0.0) {
+            if (!sh.repeats) add = per * L.q[j];
+            else
+              for (int i = 0; i < a.k; ++i)
+                if (L.idx[i] == e) add += per * L.q[i];
+          }
+          L.v[j] = entry(L.x[j], add);
         }
-        A = -itd * ((double)w + (double)w_h * ent);
-        Bl = -itd * (double)w_h * 0.6931471805599453;
-      } else if (OP == kRenorm) {
-        A = itd * (double)w * Q;
-      } else {
-        const double Rr = Sd == 0.0 ? 0.0 : Sd / S_row * (ref == ref_row ? 1.0 : exp(((double)ref - (double)ref_row) * itd));
-        A = itd * (double)w * ((Q + rho) * Rr - rho);
+      } else if (lane == 0 && sh.target >= 0) {
+        sh.g_target = entry(sh.x_target, (double)w);
       }
-      if (lane == 0) {
-        dense_factors(sh, ref, Sd, A, Bl, a);
-        sh.A_list = OP == kTail ? itd * (double)w * (Q + rho) : A;
-        sh.ref_row = ref_row;
-        sh.S_row = S_row;
-        sh.log_s = log_s;
-        sh.per = OP == kRenorm ? -(double)w / sh.list_sum : -(double)w;
-        sh.none = S_row == 0.0 || (w == 0.0f && w_h == 0.0f);
+      if (kind != 1) {                            // the factors, where the warps have no way of their own
+        double A, Bl = 0.0;
+        if (OP == kLogprob) {
+          A = A_list;
+          Bl = -itd * (double)w_h * 0.6931471805599453;
+        } else if (OP == kRenorm) {
+          A = A_list;
+        } else {
+          const double Rr = Sd == 0.0 ? 0.0 : Sd / S_row * (ref == ref_row ? 1.0 : exp(((double)ref - (double)ref_row) * itd));
+          A = itd * (double)w * ((Q + rho) * Rr - rho);
+        }
+        if (lane == 0) {
+          dense_factors(sh, ref, Sd, A, Bl, a);
+          sh.none = S_row == 0.0 || (w == 0.0f && w_h == 0.0f);
+        }
       }
+      arrive(&sh.ready);
     }
-    if (GRAD) arrive(&sh.ready);
     if (lane == 0 && part == 0) {
       log_s = log(S_row);
       if constexpr (OP == kLogprob) {
@@ -1639,8 +1663,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     wait(&sh.sums);
     float kf, A, Bl, ref = 0.0f;
     bool wild = false, none;
-    double A_list, S_row, x0, log_s = 0.0;        // for the list's entries: p = exp((x - x0) it) / S_row
-    const double itd = (double)a.it, w = (double)sh.w, w_h = OP == kLogprob ? (double)sh.w_h : 0.0;
+    const float w = sh.w, w_h = OP == kLogprob ? sh.w_h : 0.0f;
     // a warp's own way to the factors: in fp32, the parts in a fixed order
     const int parts = C * W;
     const float4 p = lane < parts ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
@@ -1669,39 +1692,26 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       s = warp_sum(s);
       t = warp_sum(t);
       s = fmaf(a.fine, t, s);                     // c is rounded: to first order S + d ln2 T
-      x0 = (double)rcm * a.inv_c;
       float Af;
       Bl = 0.0f;
       if (OP == kLogprob) {
         float ent = 0.0f;
-        if (w_h != 0.0) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
-        Af = -a.it * fmaf((float)w_h, ent, (float)w);
-        Bl = -a.it * (float)w_h * 0.69314718f;
-        S_row = (double)s;
-        if (w_h != 0.0) log_s = (double)(0.69314718f * __log2f(s));
+        if (w_h != 0.0f) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
+        Af = -a.it * fmaf(w_h, ent, w);
+        Bl = -a.it * w_h * 0.69314718f;
       } else if (OP == kRenorm) {
-        Af = a.it * (float)w * (float)sh.Q;
-        S_row = (double)s;
+        Af = a.it * w * (float)sh.Q;
       } else {
         // the list's sum to the same reference; the share of the others
-        const float d = (float)(((double)sh.list_high - x0) * ((double)a.c + (double)a.c_lo));
+        const float d = (float)(((double)sh.list_high - (double)rcm * a.inv_c) * ((double)a.c + (double)a.c_lo));
         const float Q = (float)sh.Q, rho = (float)sh.rho;
-        float list = 0.0f, R = 1.0f;
-        S_row = (double)s;
+        float R = 1.0f;
         if (!(sh.list_exp == 0.0)) {
-          if (d < 100.0f) {
-            list = (float)sh.list_exp * ex2(d);
-            R = s / (s + list);
-            S_row = (double)s + (double)list;
-          } else {                                // the others are below 2^-100 of the row
-            R = s * ex2(-d) / (float)sh.list_exp;
-            x0 = (double)sh.list_high;
-            S_row = sh.list_exp;
-          }
+          // (beyond 2^100 the others are nothing beside the list)
+          R = d < 100.0f ? s / (s + (float)sh.list_exp * ex2(d)) : s * ex2(-d) / (float)sh.list_exp;
         }
-        Af = a.it * (float)w * ((Q + rho) * R - rho);
+        Af = a.it * w * ((Q + rho) * R - rho);
       }
-      A_list = OP == kTail ? itd * w * (sh.Q + sh.rho) : (double)Af;
       // p = 2^(x c - rcm) / s with s = 2^E m: 2^(x c - k) f, k = fl(rcm + E), f = 2^(k - E - rcm) / m
       const int E = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
       const float m = s * __uint_as_float((uint32_t)(127 - E) << 23);
@@ -1709,7 +1719,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       const float off = (float)((double)kf - (double)E - (double)rcm), f = __fdividef(fmaf(off, 0.69314718f, 1.0f), m);
       A = f * (Bl != 0.0f ? fmaf(Bl, off - __log2f(m), Af) : Af);
       Bl *= f;
-      none = w == 0.0 && w_h == 0.0;
+      none = w == 0.0f && w_h == 0.0f;
     } else {
       wait(&sh.ready);
       kf = sh.k;
@@ -1718,10 +1728,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       ref = sh.ref;
       wild = sh.wild;
       none = sh.none;
-      A_list = sh.A_list;
-      S_row = sh.S_row;
-      x0 = (double)sh.ref_row;
-      log_s = sh.log_s;
     }
     T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
     const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
@@ -1745,24 +1751,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       float q = fmaf(x, a.c, -kf);
       if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
       return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
-    };
-    // an entry of the list in 64 bits: `add` is what it gets besides p's part
-    auto listed_one = [&](float x, double add) {
-      const double z = ((double)x - x0) * itd, p = exp(z) / S_row;
-      double g = p * A_list + itd * add;
-      if (OP == kLogprob && w_h != 0.0 && p != 0.0) g -= itd * w_h * p * (z - log_s);
-      return Elem<T>::from((float)g);
-    };
-    auto list_entry = [&](int j) {
-      double add = 0.0;
-      if (sh.Q != 0.0) {
-        const double per = OP == kRenorm ? -w / sh.list_sum : -w;
-        if (!sh.repeats) add = per * L.q[j];
-        else
-          for (int i = 0; i < a.k; ++i)
-            if (L.idx[i] == L.idx[j]) add += per * L.q[i];
-      }
-      return listed_one(L.x[j], add);
     };
     // The whole chunks without entries of the list, in a loop of their own that holds little else (one loop
     // for all chunks took 160 instructions per chunk more); the others after it.
@@ -1830,9 +1818,15 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
             __syncwarp();
           }
           if constexpr (LIST) {
-            if (hit) listed_in(e0, n * N, [&](int e, int j) { el[e] = list_entry(j); });
+            if (hit) {
+              wait(&sh.ready);
+              listed_in(e0, n * N, [&](int e, int j) { el[e] = Elem<T>::from(L.v[j]); });
+            }
           } else {
-            if (lane == 0 && hit && sh.target - e0 < n * N) el[sh.target - e0] = listed_one(sh.x_target, w);
+            if (hit) {
+              wait(&sh.ready);
+              if (lane == 0 && sh.target - e0 < n * N) el[sh.target - e0] = Elem<T>::from(sh.g_target);
+            }
           }
           __syncwarp();
         }
@@ -1846,11 +1840,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     if (edge >= 0) {
       T g = none ? Elem<T>::from(0.0f) : grad_one(x_edge);
       if (!none) {
+        wait(&sh.ready);
         if constexpr (LIST) {
           for (int j = 0; j < a.k; ++j)
-            if (L.idx[j] == edge) g = list_entry(j);
+            if (L.idx[j] == edge) g = Elem<T>::from(L.v[j]);
         } else {
-          if (sh.target == edge) g = listed_one(sh.x_target, w);
+          if (sh.target == edge) g = Elem<T>::from(sh.g_target);
         }
       }
       dx[edge] = g;
