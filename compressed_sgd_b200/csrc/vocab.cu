@@ -1014,7 +1014,7 @@ constexpr int kAhead = 2;                         // chunks per warp on their wa
 constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at most
 
 struct StreamShared {
-  uint64_t listed, weighed, sums, ready;          // the list's indices; its weights; all partial sums; results in 64 bits
+  uint64_t listed, sums, factors, ready;          // the list's indices; all partial sums; the gradient's factors; that at the list's entries
   uint64_t bounded, pushed;                       // alternatives: the CTAs' bounds are there; all candidates
   uint32_t bounds[8], tops[2][kRowWarps], least[2][kRowWarps];
   int reach[2][kRowWarps], owners;
@@ -1100,7 +1100,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.listed, 1);
-    mbar_init(&sh.weighed, 1);
+    mbar_init(&sh.factors, 1);
     mbar_init(&sh.sums, C == 1 ? W : 1);
     mbar_init(&sh.ready, 1);
     if (TOP) {
@@ -1266,12 +1266,79 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         sh.list_exp = add;
       }
     }
-    arrive(&sh.weighed);
+    __syncwarp();
     started();
     if (!GRAD && part != 0) return;
 
     // -- the row's results in 64 bits ------------------------------------------------------------------
     wait(&sh.sums);
+    if constexpr (GRAD) {
+      // What the gradient waits for, in fp32, the parts in a fixed order (by every warp for itself this took 1400
+      // instructions per CTA)
+      const int parts = C * W;
+      const float4 p = lane < parts ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+      bool normal = __float_as_int(p.w) == 1, huge = __float_as_int(p.w) == 2;
+      float rcm = warp_max(normal ? p.x : -INFINITY);
+      float4 p1 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+      if (parts > 32) {
+        if (lane + 32 < parts) p1 = sh.part[lane + 32];
+        normal |= __float_as_int(p1.w) == 1;
+        huge |= __float_as_int(p1.w) == 2;
+        rcm = fmaxf(rcm, warp_max(__float_as_int(p1.w) == 1 ? p1.x : -INFINITY));
+      }
+      const bool plain_sums = __any_sync(kFull, normal) && !__any_sync(kFull, huge);
+      if (plain_sums) {
+        float s = 0.0f, t = 0.0f;
+        if (__float_as_int(p.w) == 1) {
+          const float d = fmaxf(p.x - rcm, -kFarBits), f = ex2(d);
+          s = f * p.y;
+          t = f * fmaf(d, p.y, p.z);
+        }
+        if (parts > 32 && __float_as_int(p1.w) == 1) {
+          const float d = fmaxf(p1.x - rcm, -kFarBits), f = ex2(d);
+          s = fmaf(f, p1.y, s);
+          t = fmaf(f, fmaf(d, p1.y, p1.z), t);
+        }
+        s = warp_sum(s);
+        t = warp_sum(t);
+        s = fmaf(a.fine, t, s);                     // c is rounded: to first order S + d ln2 T
+        float Af, Bl = 0.0f;
+        if (OP == kLogprob) {
+          float ent = 0.0f;
+          if (w_h != 0.0f) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
+          Af = -a.it * fmaf(w_h, ent, w);
+          Bl = -a.it * w_h * 0.69314718f;
+        } else if (OP == kRenorm) {
+          Af = a.it * w * (float)sh.Q;
+        } else {
+          // the list's sum to the same reference; the share of the others
+          const float d = (float)(((double)sh.list_high - (double)rcm * a.inv_c) * ((double)a.c + (double)a.c_lo));
+          const float Q = (float)sh.Q, rho = (float)sh.rho;
+          float R = 1.0f;
+          if (!(sh.list_exp == 0.0)) {
+            // (beyond 2^100 the others are nothing beside the list)
+            R = d < 100.0f ? s / (s + (float)sh.list_exp * ex2(d)) : s * ex2(-d) / (float)sh.list_exp;
+          }
+          Af = a.it * w * ((Q + rho) * R - rho);
+        }
+        // p = 2^(x c - rcm) / s with s = 2^E m: 2^(x c - k) f, k = fl(rcm + E), f = 2^(k - E - rcm) / m
+        const int E = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
+        const float m = s * __uint_as_float((uint32_t)(127 - E) << 23);
+        const float kf = rcm + (float)E;
+        const float off = (float)((double)kf - (double)E - (double)rcm), f = __fdividef(fmaf(off, 0.69314718f, 1.0f), m);
+        const float A = f * (Bl != 0.0f ? fmaf(Bl, off - __log2f(m), Af) : Af);
+        Bl *= f;
+        if (lane == 0) {
+          sh.k = kf;
+          sh.A = A;
+          sh.Bl = Bl;
+          sh.ref = 0.0f;
+          sh.wild = 0;
+          sh.none = w == 0.0f && w_h == 0.0f;
+        }
+        arrive(&sh.factors);
+      }
+    }
     int kind = 0;
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
@@ -1397,6 +1464,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
           dense_factors(sh, ref, Sd, A, Bl, a);
           sh.none = S_row == 0.0 || (w == 0.0f && w_h == 0.0f);
         }
+        arrive(&sh.factors);
       }
       arrive(&sh.ready);
     }
@@ -1659,76 +1727,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   if constexpr (GRAD) {
     at = row.vec() + row.v0 + warp * kChunk + lane;
     if (!RES) request(own - warp * kChunk);
-    wait(&sh.weighed);
-    wait(&sh.sums);
-    float kf, A, Bl, ref = 0.0f;
-    bool wild = false, none;
-    const float w = sh.w, w_h = OP == kLogprob ? sh.w_h : 0.0f;
-    // a warp's own way to the factors: in fp32, the parts in a fixed order
-    const int parts = C * W;
-    const float4 p = lane < parts ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-    bool normal = __float_as_int(p.w) == 1, huge = __float_as_int(p.w) == 2;
-    float rcm = warp_max(normal ? p.x : -INFINITY);
-    float4 p1 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-    if (parts > 32) {
-      if (lane + 32 < parts) p1 = sh.part[lane + 32];
-      normal |= __float_as_int(p1.w) == 1;
-      huge |= __float_as_int(p1.w) == 2;
-      rcm = fmaxf(rcm, warp_max(__float_as_int(p1.w) == 1 ? p1.x : -INFINITY));
-    }
-    const bool plain_sums = __any_sync(kFull, normal) && !__any_sync(kFull, huge);
-    if (plain_sums) {
-      float s = 0.0f, t = 0.0f;
-      if (__float_as_int(p.w) == 1) {
-        const float d = fmaxf(p.x - rcm, -kFarBits), f = ex2(d);
-        s = f * p.y;
-        t = f * fmaf(d, p.y, p.z);
-      }
-      if (parts > 32 && __float_as_int(p1.w) == 1) {
-        const float d = fmaxf(p1.x - rcm, -kFarBits), f = ex2(d);
-        s = fmaf(f, p1.y, s);
-        t = fmaf(f, fmaf(d, p1.y, p1.z), t);
-      }
-      s = warp_sum(s);
-      t = warp_sum(t);
-      s = fmaf(a.fine, t, s);                     // c is rounded: to first order S + d ln2 T
-      float Af;
-      Bl = 0.0f;
-      if (OP == kLogprob) {
-        float ent = 0.0f;
-        if (w_h != 0.0f) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
-        Af = -a.it * fmaf(w_h, ent, w);
-        Bl = -a.it * w_h * 0.69314718f;
-      } else if (OP == kRenorm) {
-        Af = a.it * w * (float)sh.Q;
-      } else {
-        // the list's sum to the same reference; the share of the others
-        const float d = (float)(((double)sh.list_high - (double)rcm * a.inv_c) * ((double)a.c + (double)a.c_lo));
-        const float Q = (float)sh.Q, rho = (float)sh.rho;
-        float R = 1.0f;
-        if (!(sh.list_exp == 0.0)) {
-          // (beyond 2^100 the others are nothing beside the list)
-          R = d < 100.0f ? s / (s + (float)sh.list_exp * ex2(d)) : s * ex2(-d) / (float)sh.list_exp;
-        }
-        Af = a.it * w * ((Q + rho) * R - rho);
-      }
-      // p = 2^(x c - rcm) / s with s = 2^E m: 2^(x c - k) f, k = fl(rcm + E), f = 2^(k - E - rcm) / m
-      const int E = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
-      const float m = s * __uint_as_float((uint32_t)(127 - E) << 23);
-      kf = rcm + (float)E;
-      const float off = (float)((double)kf - (double)E - (double)rcm), f = __fdividef(fmaf(off, 0.69314718f, 1.0f), m);
-      A = f * (Bl != 0.0f ? fmaf(Bl, off - __log2f(m), Af) : Af);
-      Bl *= f;
-      none = w == 0.0f && w_h == 0.0f;
-    } else {
-      wait(&sh.ready);
-      kf = sh.k;
-      A = sh.A;
-      Bl = sh.Bl;
-      ref = sh.ref;
-      wild = sh.wild;
-      none = sh.none;
-    }
+    wait(&sh.factors);
+    const float kf = sh.k, A = sh.A, Bl = sh.Bl, ref = sh.ref;
+    const bool wild = sh.wild, none = sh.none;
     T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
     const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
     const bool plain = in_step && !wild && !none;
