@@ -1016,8 +1016,9 @@ constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at m
 struct StreamShared {
   uint64_t listed, sums, factors, ready;          // the list's indices; all partial sums; the gradient's factors; that at the list's entries
   uint64_t bounded, pushed;                       // alternatives: the CTAs' bounds are there; all candidates
-  uint32_t bounds[8], tops[2][kRowWarps], least[2][kRowWarps];
-  int reach[2][kRowWarps], owners;
+  uint32_t bounds[8], tops[8], least[8];
+  alignas(16) uint32_t reach[2][8];               // parts of each warp that reach three values, ten bits each
+  int owners;
   int nan, scratch[kRowWarps + 1];
   float top_ref;
   double top_log_s;
@@ -1070,11 +1071,17 @@ __device__ __forceinline__ bool peer_wait_bounded(uint64_t* bar) {
   return true;
 }
 
-// A candidate to the first CTA of the row.
-__device__ __forceinline__ void peer_push(TopShared* top, uint32_t key, int e) {
-  uint32_t n;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(peer(&top->count, 0)) : "memory");
-  if (n < kCand) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer(&top->cand[n], 0)), "l"(cand_of(key, e)) : "memory");
+// Places for n candidates in the first CTA of the row (alone: the row has no other), and a candidate there.
+__device__ __forceinline__ uint32_t peer_places(TopShared* top, int n, bool alone) {
+  if (alone) return (uint32_t)atomicAdd(&top->count, n);
+  uint32_t at;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(peer(&top->count, 0)), "r"(n) : "memory");
+  return at;
+}
+__device__ __forceinline__ void peer_put(TopShared* top, uint32_t at, uint32_t key, int e, bool alone) {
+  if (at >= kCand) return;
+  if (alone) top->cand[at] = cand_of(key, e);
+  else asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer(&top->cand[at], 0)), "l"(cand_of(key, e)) : "memory");
 }
 
 // Shared memory: RES: the slice; else a chunk per warp for those that hold entries of the list. Then the
@@ -1633,47 +1640,56 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   // vocabulary sorted by frequency all lie in one warp's chunks.
   if constexpr (TOP) {
     auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"r"(W * 32) : "memory"); };
-    uint32_t key[U], mx = 0, mn = 0xffffffffu;
+    uint32_t key[U], mx = 0, mn = 0xffffffffu, valid = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       key[u] = order_key(Elem<T>::top(high[u]));
       mx = max(mx, key[u]);
-      if (key[u] > kKeyNegInf) mn = min(mn, key[u]);
+      if (key[u] > kKeyNegInf) {
+        mn = min(mn, key[u]);
+        ++valid;
+      }
     }
-    int turn = 0;
-    auto reach = [&](uint32_t t) {                // parts that reach t, over the CTA
-      int n = 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) n += key[u] >= t;
-      n = __reduce_add_sync(kFull, n);
-      if (lane == 0) sh.reach[turn][warp] = n;
-      meet();
-      n = 0;
-      for (int q = 0; q < W; ++q) n += sh.reach[turn][q];
-      turn ^= 1;
-      return n;
-    };
     mx = __reduce_max_sync(kFull, mx);
     mn = __reduce_min_sync(kFull, mn);
+    valid = __reduce_add_sync(kFull, valid);
+    if (warp == 0 && lane < 8) sh.reach[0][lane] = 0;   // (of warps that are not there, too)
     if (lane == 0) {
-      sh.tops[0][warp] = mx;
-      sh.least[0][warp] = mn;
+      sh.tops[warp] = mx;
+      sh.least[warp] = mn;
+      sh.reach[1][warp] = valid;
+    }
+    if (warp == 0 && lane >= W && lane < 8) sh.reach[1][lane] = 0;
+    meet();
+    valid = 0;
+    for (int q = 0; q < W; ++q) {
+      mx = max(mx, sh.tops[q]);
+      mn = min(mn, sh.least[q]);
+      valid += sh.reach[1][q];
     }
     uint32_t bound = kKeyNegInf + 1;
-    if (reach(bound) >= a.k) {
-      for (int q = 0; q < W; ++q) {
-        mx = max(mx, sh.tops[0][q]);
-        mn = min(mn, sh.least[0][q]);
-      }
-      const int bits = 32 - __clz(mx ^ mn);       // below these the keys agree
+    if ((int)valid >= a.k) {
+      // two bits of it a round: one reduction per warp and one barrier
+      const int bits = (33 - __clz(mx ^ mn)) & ~1;    // below these, rounded up to pairs, the keys agree
       uint32_t res = bits == 32 ? 0u : mx >> bits << bits;
-      for (int b = bits - 1; b >= 0; --b) {
-        const uint32_t trial = res | (1u << b);
-        const int n = reach(trial);
-        if (n >= a.k) {
-          res = trial;
-          if (n <= a.k + a.k / 4 + 2) break;
-        }
+      int turn = 0;
+      for (int b = bits - 2; b >= 0; b -= 2) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (uint32_t i = 1; i < 4; ++i) n += (key[u] > kKeyNegInf && key[u] >= res + (i << b)) << (10 * (i - 1));
+        n = __reduce_add_sync(kFull, n);
+        if (lane == 0) sh.reach[turn][warp] = n;
+        meet();
+        const uint4 lo = *reinterpret_cast<const uint4*>(&sh.reach[turn][0]), hi = *reinterpret_cast<const uint4*>(&sh.reach[turn][4]);
+        n = lo.x + lo.y + lo.z + lo.w + hi.x + hi.y + hi.z + hi.w;
+        turn ^= 1;
+        const int n1 = n & 1023, n2 = (n >> 10) & 1023, n3 = (int)(n >> 20);
+        const int up = n3 >= a.k ? 3 : n2 >= a.k ? 2 : n1 >= a.k ? 1 : 0;
+        const int got = up == 3 ? n3 : up == 2 ? n2 : n1;
+        res += (uint32_t)up << b;
+        if (up && got <= a.k + a.k / 4 + 2) break;
       }
       bound = max(bound, res);
     }
@@ -1705,17 +1721,24 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         if (i >= own) break;
         float x[N];
         Elem<T>::unpack(ld_row(row.vec() + row.v0 + i), x);
+        uint32_t hits = 0;
 #pragma unroll
-        for (int b = 0; b < N; ++b) {
-          const uint32_t k = order_key(x[b]);
-          if (k >= bound) peer_push(&top, k, row.head + (row.v0 + i) * N + b);
-        }
+        for (int b = 0; b < N; ++b) hits |= (order_key(x[b]) >= bound ? 1u : 0u) << b;
+        if (hits == 0) continue;
+        uint32_t n = peer_places(&top, __popc(hits), C == 1);
+#pragma unroll
+        for (int b = 0; b < N; ++b)
+          if ((hits >> b) & 1u) peer_put(&top, n++, order_key(x[b]), row.head + (row.v0 + i) * N + b, C == 1);
       }
     }
-    if (edge >= 0 && order_key(x_edge) >= bound) peer_push(&top, order_key(x_edge), edge);
-    if (C > 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) peer_arrive(&sh.pushed, 0);
+    if (edge >= 0 && order_key(x_edge) >= bound) peer_put(&top, peer_places(&top, 1, C == 1), order_key(x_edge), edge, C == 1);
+    if (C > 1) {
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) peer_arrive(&sh.pushed, 0);
+    } else {
+      arrive(&sh.pushed);
+    }
     if (part != 0) {
       leave();
       return;
@@ -1964,9 +1987,9 @@ constexpr int64_t kSliceMost = 200 << 10;         // one
 template <class T, int OP, int MODE, bool TOP>
 int voc_stream(const VocArgs& a, cudaStream_t st) {
   const int64_t nv = cdiv(a.vocab, Elem<T>::N);
-  // few rows: split each over up to 8 CTAs, as long as a CTA keeps 512 vectors
+  // few rows: split each over up to 8 CTAs, as long as a CTA keeps 256 vectors
   int split = 1;
-  while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 512) split *= 2;
+  while (split < 8 && (int64_t)a.rows * split < 2 * sm_count() && nv / (2 * split) >= 256) split *= 2;
   if constexpr (MODE == kFused) {
     // Powers of two: clusters of 3 and 6 find their places later than those of 2 and 4 (2048 x 50021 fp16: 212
     // us in three slices of 33 KB, 152 in two of 50; 8192 x 128000 bf16: 1022 us in six, 888 in four).
