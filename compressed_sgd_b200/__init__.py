@@ -521,7 +521,7 @@ def _new_dlogits(logits: torch.Tensor) -> torch.Tensor:
         stride = vocab                              # broadcast or far apart rows: a dense gradient
     first = (logits.data_ptr() % 16) // logits.element_size()
     if stride == vocab and first == 0:
-        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+        return logits.new_empty((rows, vocab))
     flat = torch.empty(first + max(rows, 1) * stride, dtype=logits.dtype, device=logits.device)
     return flat.as_strided((rows, vocab), (stride, 1), first)
 
@@ -571,14 +571,14 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
     logprob = entropy = stats = top_idx = top_logprob = None
     if targets is not None:
-        logprob = torch.empty(rows, dtype=torch.float32, device=dev)
+        logprob = logits.new_empty(rows, dtype=torch.float32)
     if want_entropy:
-        entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+        entropy = logits.new_empty(rows, dtype=torch.float32)
     if want_stats:
-        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        stats = logits.new_empty((rows, 2), dtype=torch.float32)
     if top_k > 0:
-        top_idx = torch.empty((rows, top_k), dtype=torch.int32, device=dev)
-        top_logprob = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+        top_idx = logits.new_empty((rows, top_k), dtype=torch.int32)
+        top_logprob = logits.new_empty((rows, top_k), dtype=torch.float32)
     if want_grad or dlogits is not None:
         dlogits = _grad_out(dlogits, logits)
     _on_device(dev, "gsparse_token_logprobs", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature), p_t,
@@ -634,8 +634,8 @@ def distill_topk(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_val: t
     lists = _teacher(teacher_idx, teacher_val, rows, dev)
     p_g = _like(grad_loss, torch.float32, (rows,), dev, "grad_loss")
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
-    loss = torch.empty(rows, dtype=torch.float32, device=dev)
-    stats = torch.empty((rows, 4 if tail else 2), dtype=torch.float32, device=dev) if want_stats else None
+    loss = logits.new_empty(rows, dtype=torch.float32)
+    stats = logits.new_empty((rows, 4 if tail else 2), dtype=torch.float32) if want_stats else None
     if want_grad or dlogits is not None:
         dlogits = _grad_out(dlogits, logits)
     _on_device(dev, "gsparse_distill_topk", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature), *lists,

@@ -2,15 +2,19 @@
 // likely tokens, and distillation from a teacher's (index, value) list, each with the gradient of the
 // logits in the same call or as a pass of its own.
 //
-// With z = x * it (it = 1 / temperature), M = max x, c = it * log2(e):
-//   S = sum 2^((x - M) c),  T = sum 2^((x - M) c) (x - M) c,  p = 2^((x - M) c - log2 S),
-//   entropy = ln2 (log2 S - T / S),  log p_t = (x_t - M) it - ln S,
-// so one pass over a row with a running maximum gives everything but the gradient, and the gradient
-// of either loss is p (A + B log2 p) per entry plus a few entries of the row's list, which are
-// computed and written apart after the dense pass.
+// With z = x * it (it = 1 / temperature), c = it * log2(e) and any reference m near the largest entry:
+//   S = sum 2^((x - m) c),  T = sum 2^((x - m) c) (x - m) c,  p = 2^((x - m) c - log2 S),
+//   entropy = ln2 (log2 S - T / S),  log p_t = (x_t - m) it - ln S,
+// so one pass over a row gives everything but the gradient, and the gradient of either loss is p (A + B
+// log2 p) per entry plus a few entries of the row's list, which are computed apart.
 //
-// One thread-block cluster of C CTAs takes a row, each CTA a slice of it; the CTAs exchange their
-// (M, S, T) through distributed shared memory. C = 1 when there are rows enough to fill the GPU.
+// What bounds them: a read of the logits (and a write of the gradient) at 6.5 TB/s, and next to it the
+// exponential unit: one 2^x per entry and pass at 16 a clock and SM is 0.7 of the time that the bytes of
+// 16-bit logits take. So the inner loops are counted in instructions: 4.7 per entry for the sums, of which one
+// is the exponential.
+//
+// Two kernels: voc_stream_kernel (losses, with or without the gradient, alternatives) and
+// voc_backward_kernel (the gradient from saved statistics).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,13 +33,13 @@ constexpr int kUnroll = 4;                        // vectors of 16 bytes per lan
 constexpr int kChunk = 32 * kUnroll;              // vectors per chunk
 constexpr int kChunkLog = 7;
 static_assert(kChunk == 1 << kChunkLog && kUnroll == 4, "");
-constexpr int kStages = 3;                        // chunks per warp in shared memory
+constexpr int kStages = 3;                        // chunks per warp in the backward kernel's rings
 constexpr int kCand = 2048;                       // candidates for a row's alternatives
 
 constexpr float kLowest = -3.402823466e38f;       // the maximum of a row that holds nothing but -inf
 constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: where a sum weighs by the exponent it is
                                                   // clamped here, so that -inf logits add 0
-constexpr float kLowestSafe = 1.0e38f;
+constexpr float kLowestSafe = 1.0e38f;            // largest size of ref_min
 constexpr float kWildBits = 1.2676506e30f;        // 2^100: maxima beyond it (in bits) take the careful route
 
 enum { kLogprob = 0, kRenorm = 1, kTail = 2 };    // what is computed
@@ -999,15 +1003,21 @@ template <int LEFT> __device__ __forceinline__ void copy_wait() {
 
 // ---- a row per cluster, streamed -----------------------------------------------------------------------
 
-// A cluster of C CTAs takes a row; W warps of a CTA stream its slice chunk by chunk (U vectors per lane, the
-// next chunk's loads in registers while one is worked on) and one more warp reads the row's list and
-// writes its results. The warps meet once: each leaves its partial sums with every CTA of the row, and
-// joins the partial sums of all by itself.
-// What was measured (4000 rows of 85000 bf16): plain loads through registers with 64 KB a SM on their way read
-// the rows in 95 us; bulk and cp.async copies with 96 to 192 KB on their way took 109 to 120 us, rings of
-// them under this kernel 133 to 190 us.
-// RES (the gradient): the slice stays in shared memory between the sums and the gradient. Reading it again from
-// L2 costs half as much traffic again between L2 and the SMs, which is what bounds that form.
+// A cluster of C CTAs takes a row; W warps of a CTA stream its slice chunk by chunk (U vectors per lane) and
+// one more warp reads the row's list, joins the partial sums and writes the results, in 64 bits where that
+// is free. The warps meet once per row: each sends its partial sums to every CTA of the row that needs them.
+// C = 1 when there are rows enough to fill the GPU and no gradient.
+//
+// Sums alone: the next chunk's loads are in registers while one is worked on, 64 KB a SM on their way. Measured on
+// 4000 rows of 85000 bf16 (680 MB): 113 us, 6.0 TB/s, 0.92 of the measured copy bandwidth. A kernel that only
+// reads takes 95 us with such loads and 109 to 120 us with cp.async rings of 64 to 192 KB a SM; this one with bulk
+// or cp.async rings took 133 to 190 us.
+//
+// RES (with the gradient): the slice goes to shared memory and stays there between the sums and the gradient:
+// 288 us, 4.7 TB/s, 0.72. Reading it again from L2 instead costs half as much traffic again between L2 and the
+// SMs (322 us), and more than about 60 MB of rows in flight no longer stay in L2. What is left is the chain of
+// a slice, about 9 us for 42 KB (loads 2, sums 3, join 1.5, gradient 2.5), of which four CTAs per SM hide two
+// thirds. Rows that eight slices of 200 KB cannot hold are read twice.
 constexpr int kRowWarps = 7;                      // streaming warps, at most
 constexpr int kRowCtas = 4;                       // per SM
 constexpr int kAhead = 2;                         // chunks per warp on their way to shared memory (RES)
@@ -1982,7 +1992,7 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
 }
 
 constexpr int64_t kSliceBytes = 64 << 10;         // three or four CTAs per SM
-constexpr int64_t kSliceMost = 200 << 10;         // one
+constexpr int64_t kSliceMost = 200 << 10;         // one CTA per SM
 
 template <class T, int OP, int MODE, bool TOP>
 int voc_stream(const VocArgs& a, cudaStream_t st) {

@@ -421,7 +421,8 @@ int gsparse_combine_local(const float* G, const float* L, float* out, int64_t n,
  * Arithmetic: the exponential of fp32 differences and sums in fp32 within a thread, joined in fp64
  * in a fixed order: the same call on the same layout gives the same bits on every run, within a few
  * fp32 roundings of the formula (a gradient in 16 bits is rounded once). 1 <= vocab <= GSPARSE_MAX_VOCAB, 0 <= rows <
- * 2^26. These calls need no workspace.
+ * 2^26. inv_temperature from 2^-64 to 2^64. These calls need no workspace. A wait of a row's CTAs for one
+ * another that gives up (about a second) raises GSPARSE_DERR_TIMEOUT; the results are then not valid.
  */
 enum gsparse_dtype { GSPARSE_F32 = 0, GSPARSE_BF16 = 1, GSPARSE_F16 = 2 };
 
@@ -434,9 +435,9 @@ enum gsparse_dtype { GSPARSE_F32 = 0, GSPARSE_BF16 = 1, GSPARSE_F16 = 2 };
  *              count as -1.
  * logprob      fp32[rows] or NULL: log p of the token.
  * entropy      fp32[rows] or NULL: -sum_v p_v log p_v.
- * stats        fp32[rows][2] or NULL, for the backward call: the row's largest logit x (before the
+ * stats        fp32[rows][2] or NULL, for the backward call: a logit m near the row's largest (before the
  *              temperature; the lowest fp32 value for a row with nothing but -inf) and the sum of
- *              exp(z - its z).
+ *              exp(z - m's z). Any m for which the sum is finite and not 0 serves the backward call.
  * top_k        0 <= top_k <= min(vocab, GSPARSE_MAX_ALTERNATIVES): the top_k largest entries of each
  *              row, largest first, ties to the lower index (-0 ties with +0, NaN ranks above +inf);
  *              top_idx int32[rows][top_k], top_logprob fp32[rows][top_k]. -inf entries are never

@@ -213,6 +213,31 @@ def test_tokens_masks(dtype, times):
     check_tokens(x, dtype, targets=np.tile([-1, 700, 0, 4, 6, 1199, 8, 1100, 41], times), grad=False)
 
 
+@pytest.mark.parametrize("times", [1, 25])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_tokens_far_apart(dtype, times):
+    """Entries far above those before them, finite masks, values at the ends of the types."""
+    V = 9000
+    x, _ = make(8, V, dtype)
+    big = 6.0e4 if dtype == "fp16" else 3.0e38
+    x[0, 1500:] += 300.0                                  # far above the first chunk
+    x[1] += (torch.arange(V, device="cuda") // 1024 * 90).to(x.dtype)   # rising from chunk to chunk
+    x[2, :4000] = -1.0e4                                  # a finite mask over whole chunks
+    x[3, ::2] = -6.0e4
+    x[4, 8000] = big                                      # one entry that is everything
+    x[5] = -big; x[5, 40] = -big / 2; x[5, 41] = -big / 2  # all below what sums are taken from
+    x[6, :8999] = torch.finfo(TYPES[dtype]).min           # the last entry alone is more than the mask
+    x[7] = big
+    x = x.repeat(times, 1)
+    t = np.tile([1600, 8999, 20, 1, 8000, 40, 8999, 3], times)
+    check_tokens(x, dtype, targets=t, top_k=5)
+    check_tokens(x, dtype, targets=t, grad=False, temperature=4.0)
+    idx = np.tile(np.array([[1600, 8999, 20, 40]], np.int32), (8 * times, 1))
+    val = np.tile(np.log(np.array([[0.4, 0.3, 0.1, 0.05]], np.float32)), (8 * times, 1))
+    keep = np.tile([True, True, True, True, False, True, True, True], times)   # row 4 has losses of 1e38
+    check_distill(x[torch.from_numpy(keep).cuda()], dtype, idx[keep], val[keep], False, w=np.ones(keep.sum(), np.float32))
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows,V", [(2, 9000), (1, 40000), (300, 2100)])
 @pytest.mark.parametrize("k", [1, 20, 256])
