@@ -1025,6 +1025,7 @@ constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at m
 
 struct StreamShared {
   uint64_t listed, sums, factors, ready;          // the list's indices; all partial sums; the gradient's factors; that at the list's entries
+  uint64_t gathered, reread;                      // the row's entries at the list have been read; by all CTAs, the row again
   uint64_t bounded, pushed;                       // alternatives: the CTAs' bounds are there; all candidates
   uint32_t bounds[8], tops[8], least[8];
   alignas(16) uint32_t reach[2][8];               // parts of each warp that reach three values, ten bits each
@@ -1118,6 +1119,8 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   if (threadIdx.x == 0) {
     mbar_init(&sh.listed, 1);
     mbar_init(&sh.factors, 1);
+    mbar_init(&sh.gathered, 1);
+    mbar_init(&sh.reread, C);
     mbar_init(&sh.sums, C == 1 ? W : 1);
     mbar_init(&sh.ready, 1);
     if (TOP) {
@@ -1222,15 +1225,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         L.v[j] = v;
         if (e >= 0) vmax = fmaxf(vmax, v);
       }
-#pragma unroll 4
-      for (int j = lane; j < a.k; j += 32) {
-        const int e = L.idx[j];
-        L.x[j] = e >= 0 ? Elem<T>::to(row.x[e]) : 0.0f;
-      }
-      vmax = fmaxf(warp_max(vmax), kLowest);
       __syncwarp();
-      bool repeats = false;
-      if (GRAD || OP == kTail) {
+      // which chunks hold entries of the list: what the tail's sums begin with
+      auto mark = [&]() {
+        bool repeats = false;
         for (int j = lane; j < a.k; j += 32) {
           const int e = L.idx[j];
           if (e < 0) continue;
@@ -1243,8 +1241,17 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         }
         repeats = __any_sync(kFull, repeats);
         if (lane == 0) sh.repeats = repeats;
+        arrive(&sh.listed);
+      };
+      if (OP == kTail) mark();
+#pragma unroll 4
+      for (int j = lane; j < a.k; j += 32) {
+        const int e = L.idx[j];
+        L.x[j] = e >= 0 ? Elem<T>::to(row.x[e]) : 0.0f;
       }
-      arrive(&sh.listed);
+      arrive(&sh.gathered);
+      if (OP != kTail && GRAD) mark();
+      vmax = fmaxf(warp_max(vmax), kLowest);
       double sum = 0.0;
       for (int j = lane; j < a.k; j += 32) {
         const int e = L.idx[j];
@@ -1283,6 +1290,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         sh.list_exp = add;
       }
     }
+    if (!LIST) arrive(&sh.gathered);
     __syncwarp();
     started();
     if (!GRAD && part != 0) return;
@@ -1395,6 +1403,11 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       careful_sums(whole, M, a, out, OP == kTail ? a.k : 0, lane, 32, Sd, Td);
       Sd = warp_sum(Sd);
       Td = warp_sum(Td);
+      if (GRAD && C > 1) {                        // (as with the sums)
+        __syncwarp();
+        if (lane < C) peer_arrive(&sh.reread, lane);
+        wait(&sh.reread);
+      }
     }
     const float ref = fmaxf(M, kLowest);
     // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
@@ -1633,6 +1646,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
     }
     started();
+    // The gradient may take the logits' place, so that no CTA of the row begins it before the others have read
+    // what they need of it.
+    if (GRAD && C > 1) wait(&sh.gathered);
     const float4 sums = make_float4(ref, s0, t0, __int_as_float(kind));
     if (C == 1) {                                 // (no asynchronous store outside a cluster launch: it is illegal there)
       if (lane == 0) sh.part[warp] = sums;

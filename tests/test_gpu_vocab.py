@@ -5,7 +5,8 @@ Tolerances count roundings, u = 2^-24 (half a step of fp32):
  - an exponential 2^q, q = (x - M) c: the hardware's 2^q is within 4 u (its documented 2^-22), and q carries
    the roundings of c and of the product, 2 |q| u, in the exponent: ln2 * 2 |q| u relative. The entries that
    carry a softmax's weight have sum p |q| <= log2 V + entropy <= 2 log2 V.
- - a thread adds at most n = max(64, V / 512) entries in fp32: n u.
+ - a CTA's seven warps hold 7 * 32 * 2 = 448 fp32 sums, of V / 448 entries each and whole chunks of up to 16, and six
+   more additions join them before 64 bits do: n u with n = max(64, V / 448 + 22).
  So log S, and with it a log probability, is within LSE(V) = (4 + 2 * 2 log2 V + n) u, plus u |result| for the
  result's own rounding; the entropy log S - T / S within LSE (2 + ln V) as T weighs the same errors by |q|.
  - a gradient p (A + B log p) + a: p is off by the exponential's error at its own q' = log2 p and by log S's,
@@ -30,7 +31,7 @@ TINY = {"fp32": 2.0 ** -126, "bf16": 2.0 ** -126, "fp16": 2.0 ** -25}   # fp32 r
 
 
 def lse_tol(V):
-    return (4 + 4 * math.log2(V + 1) + max(64, V / 512)) * U
+    return (4 + 4 * math.log2(V + 1) + max(64, V / 448 + 22)) * U
 
 
 def close(got, want, tol, what):
