@@ -505,6 +505,20 @@ def test_distill_in_place(tail):
         assert bool(((y.float() - want.dlogits.float()).abs() <= half * want.dlogits.float().abs() + 1e-6).all())
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 900_001), ("fp32", 450_003)])
+def test_rows_longer_than_eight_slices(dtype, V):
+    """Rows that shared memory cannot hold between the sums and the gradient are read twice."""
+    x, _ = make(2, V, dtype, stride=V + 3, first=1)
+    check_tokens(x, dtype, targets=np.array([V - 1, 17]), top_k=20)
+    idx, val = lists(x, 40, 1.0, True, ragged=False)
+    for tail in (False, True):
+        check_distill(x, dtype, idx, val, tail)
+    ti, tv, w = dev(idx, torch.int32), dev(val), dev(weights(2)[0])
+    want = gs.distill_topk(x, ti, tv, tail=True, grad_loss=w, want_grad=True)
+    got = gs.distill_topk(x, ti, tv, tail=True, grad_loss=w, dlogits=x)
+    assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.loss, want.loss)
+
+
 # ---- as a run ---------------------------------------------------------------------------------------
 
 def test_teacher_to_student_to_compressed_gradient():
