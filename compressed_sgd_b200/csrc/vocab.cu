@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -39,8 +40,9 @@ constexpr int kCand = 2048;                       // candidates for a row's alte
 constexpr float kLowest = -3.402823466e38f;       // the maximum of a row that holds nothing but -inf
 constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: where a sum weighs by the exponent it is
                                                   // clamped here, so that -inf logits add 0
-constexpr float kLowestSafe = 1.0e38f;            // largest size of ref_min
-constexpr float kWildBits = 1.2676506e30f;        // 2^100: maxima beyond it (in bits) take the careful route
+constexpr float kNearBits = 65536.0f;             // references m with |m c| up to here: exponents fma(x, c, -fl(m c)), which at
+                                                  // m itself is the rounding of fl(m c), at most 2^-8. Beyond: (x - m) c
+constexpr float kHugeBits = 1.2676506e30f;        // 2^100: maxima beyond it (in bits) take the careful route
 
 enum { kLogprob = 0, kRenorm = 1, kTail = 2 };    // what is computed
 enum { kForward = 0, kFused = 1, kBackward = 2 }; // loss; loss and gradient; gradient from saved statistics
@@ -55,7 +57,7 @@ struct VocArgs {
   int32_t k;                     // list length: alternatives wanted (forward), given (backward), or the teacher's
   int32_t val_dtype;
   float it, c, c_lo;             // c + c_lo = it log2(e)
-  float far, ref_min;            // kFarBits / c, -kWildBits / c
+  float far, huge;               // kFarBits / c, kHugeBits / c
   float fine;                    // ln2 c_lo / c
   double inv_c;                  // 1 / c
   const int32_t* targets;
@@ -340,23 +342,6 @@ struct Row {
   }
 };
 
-// ---- running maximum and sums -----------------------------------------------------------------
-
-struct Running {
-  float m;        // largest entry so far, -inf if none (NaN is passed over; it reaches s)
-  float rc;       // fl(max(m, ref_min) c), what the exponents are taken from
-  f2 s, t;        // sums over entries of e = 2^q and of e q, q = fl(x c - rc)
-};
-
-// Moves the sums to the reference rc2 >= rc.
-__device__ __forceinline__ void running_shift(Running& r, float rc2) {
-  const float dd = max_nan(r.rc - rc2, -kFarBits);
-  const float f = ex2(dd);
-  r.t = mul2(fma2(r.s, pair(dd, dd), r.t), pair(f, f));
-  r.s = mul2(r.s, pair(f, f));
-  r.rc = rc2;
-}
-
 // ---- list of a row ------------------------------------------------------------------------------
 
 struct List {              // in dynamic shared memory, for n entries
@@ -597,25 +582,26 @@ __device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocA
 
 constexpr int kHitWords = 16;
 
-// The factors of the dense gradient for p = 2^((x - ref) c) / S, g = p (A + Bl log2 p).
+// The factors of the dense gradient for p = 2^((x - ref) c) / S, g = p (A + Bl log2 p). A reference beyond kNearBits
+// (away) leaves the difference to the entries and k = E.
 // With S = 2^E s, 1 <= s < 2, p = 2^(x c - k) f for k = fl(fl(ref c) + E) and f = 2^(k - E - ref c) / s: no
 // logarithm, and no rounding of k is left in p.
 template <class Out>
 __device__ __forceinline__ void dense_factors(Out& R, float ref, double S, double A, double Bl, const VocArgs& a) {
   R.ref = ref;
-  R.wild = !(fabsf(ref) * a.c <= kWildBits);
+  R.away = !(fabsf(ref) * a.c <= kNearBits);
   if (S == 0.0) {                                 // -inf alone, and entries that the list writes
     R.k = R.A = R.Bl = 0.0f;
-    R.wild = 0;
+    R.away = 0;
     return;
   }
   int E;
   const double s = 2.0 * frexp(S, &E);
   E -= 1;
   const float k = ref * a.c + (float)E;
-  const double off = R.wild ? 0.0 : (double)k - (double)E - (double)ref * (double)a.c;
+  const double off = R.away ? 0.0 : (double)k - (double)E - (double)ref * (double)a.c;
   const double f = exp2_small(off) / s;
-  R.k = R.wild ? (float)E : k;                    // careful entries take (x - ref) c - E
+  R.k = R.away ? (float)E : k;
   R.A = (float)(f * (A + (Bl != 0.0 ? Bl * (off - (double)log2f((float)s)) : 0.0)));
   R.Bl = (float)(f * Bl);
 }
@@ -630,7 +616,7 @@ struct RowShared {
   float ref, ref_row;
   double S_row;
   float k, A, Bl, A_list;
-  int wild;
+  int away;
 };
 
 // Dynamic shared memory: the warps' rings, then the list.
@@ -760,31 +746,36 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
   const bool nothing = R.S_row == 0.0;            // nothing but -inf: no distribution, no gradient
   // no weight: zeros, whatever the row holds
   const bool none = nothing || (OP == kLogprob ? w_h == 0.0f && R.rho == 0.0 : w == 0.0f);
-  const bool wild = R.wild;
+  const bool away = R.away;
   T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
   const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
-  auto grad = [&](uint4 v) {
+  auto grad = [&](uint4 v, auto far) {             // far: the difference first
     float x[N];
     Elem<T>::unpack(v, x);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       float q0, q1;
-      f2 q = fma2(pair(x[i], x[i + 1]), c2, nk), g = A2;
-      unpair(q, &q0, &q1);
+      f2 q, g = A2;
+      if constexpr (far.value) {
+        q0 = max_nan((x[i] - ref) * a.c, -kFarBits) - kf;
+        q1 = max_nan((x[i + 1] - ref) * a.c, -kFarBits) - kf;
+      } else {
+        q = fma2(pair(x[i], x[i + 1]), c2, nk);
+        unpair(q, &q0, &q1);
+      }
       if (OP == kLogprob && Bl != 0.0f) g = fma2(pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), B2, A2);
       unpair(mul2(pair(ex2(q0), ex2(q1)), g), &x[i], &x[i + 1]);
     }
     return Elem<T>::pack(x);
   };
   auto grad_one = [&](float x) {
-    float q = fmaf(x, a.c, -kf);
-    if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
+    const float q = away ? max_nan((x - ref) * a.c, -kFarBits) - kf : fmaf(x, a.c, -kf);
     return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
   };
   const int e0 = row.head + row.v0 * N, e1 = row.head + row.v1 * N;
   const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
   uint4* dvec = reinterpret_cast<uint4*>(dx + row.head) + row.v0;
-  if (early && (none || wild || !in_step))
+  if (early && (none || !in_step))
     for (int q = 0; q < min(kStages, ring.n); ++q) ring.wait(q, a.d_status);
   if (none) {
     if (in_step) {
@@ -796,7 +787,7 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
     ring.drain();
     return;
   }
-  if (in_step && !wild) {
+  auto chunks = [&](auto far) {
     for (int q = 0; q < ring.n; ++q) {
       ring.wait(q, a.d_status);
       const uint4* at = ring.at(q);
@@ -804,13 +795,17 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
       const int left = own - ring.first(q);
       if (left >= kChunk) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) __stcs(to + u * 32 + lane, grad(at[u * 32 + lane]));
+        for (int u = 0; u < U; ++u) __stcs(to + u * 32 + lane, grad(at[u * 32 + lane], far));
       } else {
-        for (int u = lane; u < left; u += 32) __stcs(to + u, grad(at[u]));
+        for (int u = lane; u < left; u += 32) __stcs(to + u, grad(at[u], far));
       }
       __syncwarp();
       if (q + kStages < ring.n) ring.issue(q + kStages);
     }
+  };
+  if (in_step) {
+    if (away) chunks(std::true_type{});
+    else chunks(std::false_type{});
   } else {                                        // rows that start at different offsets from 16 bytes
     for (int e = e0 + tid; e < e1; e += B) dx[e] = grad_one(Elem<T>::to(row.x[e]));
   }
@@ -840,61 +835,103 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
 
 // ---- sums without a running maximum ---------------------------------------------------------------------
 
-// Sums over a lane's entries of e = 2^q and e q, q = fl(x c - rc). rc starts as the largest entry of the
-// warp's first chunk; fp32 takes entries far above it, and a chunk that takes the sums beyond 2^60
-// moves it. Saves half an instruction per entry and a branch per chunk against the running maximum.
+// Sums over a lane's entries of e = 2^q and e q. The reference is the largest entry m of the first chunk in which
+// the warp finds one, near 0: q = fma(x, c, -rc), rc = fl(m c), the same for every entry; away from it: q = (x - m) c.
+// fp32 takes entries far above it, and a chunk that takes the sums beyond kShiftAt moves it. Saves half an
+// instruction per entry and a branch per chunk against the running maximum. All but s and t is the warp's.
+enum { kNone = 0, kNear = 1, kHuge = 2, kAway = 3, kNan = 4 };   // what there is (parts of a row: up to kAway)
+constexpr float kShiftAt = 1.0e18f;
+
 struct Sums {
-  float rc;
+  int kind;
+  float ref;              // kNear: rc, kAway: m
   f2 s, t;
-  // entries before rc is set that are below ref_min (a row of the type's lowest value, say), with
-  // their own maximum and the difference taken first; they count where the row has no others
-  float low_m, low_s, low_t;
-  bool have, huge;        // rc is set; an entry is beyond -ref_min
-  bool gaps;              // -inf has been met: exponents are clamped from there on
+  bool gaps;              // -inf has been met (0 * -inf makes t NaN): exponents are clamped from there on
 };
 
-// What the fast sums cannot take: -inf (0 * -inf makes t NaN), or entries far above rc. The vectors
-// again, with rc moved up to them and the exponents clamped.
+// What the fast sums cannot take: a first chunk or a reference away from 0, entries far above the reference, NaN. The
+// reference follows the chunk's largest entry; exponents are clamped.
 template <class T, int NV>
-__device__ __noinline__ void sums_slow(Sums& r, const uint4* v, f2 s, f2 t, const VocArgs& a) {
+__device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& a) {
   constexpr int N = Elem<T>::N;
-  Running m{0.0f, r.rc, s, t};
   float high = -INFINITY;
+  bool nan = false;
   for (int u = 0; u < NV; ++u) {
     float x[N];
     Elem<T>::unpack(v[u], x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) high = fmaxf(high, x[i]);
+    for (int i = 0; i < N; ++i) {
+      high = fmaxf(high, x[i]);
+      nan |= x[i] != x[i];
+    }
   }
-  if (high > -a.ref_min) r.huge = true;
-  else if (high * a.c > m.rc) running_shift(m, high * a.c);
-  const f2 c2 = pair(a.c, a.c), nrc = pair(-m.rc, -m.rc);
+  if (r.kind >= kHuge && r.kind != kAway) return;
+  const float top = warp_max(high), rc = top * a.c;
+  if (__any_sync(kFull, nan)) {
+    r.kind = kNan;
+    return;
+  }
+  if (top == -INFINITY) return;
+  if (top > a.huge) {
+    r.kind = kHuge;
+    return;
+  }
+  const bool near = fabsf(rc) <= kNearBits;
+  float down = 0.0f;                              // from the new reference to the old one
+  if (r.kind == kNone) {
+    r.kind = near ? kNear : kAway;
+    r.ref = near ? rc : top;
+  } else if (r.kind == kNear && rc > r.ref) {
+    down = near ? r.ref - rc : fmaf(-top, a.c, r.ref);
+    r.kind = near ? kNear : kAway;
+    r.ref = near ? rc : top;
+  } else if (r.kind == kAway && top > r.ref) {
+    down = (r.ref - top) * a.c;
+    if (near && down < -kFarBits) {               // nothing is left of what was there
+      r.kind = kNear;
+      r.ref = rc;
+    } else {
+      r.ref = top;
+    }
+  }
+  if (down < 0.0f) {
+    down = fmaxf(down, -kFarBits);
+    const float f = ex2(down);
+    r.t = mul2(fma2(r.s, pair(down, down), r.t), pair(f, f));
+    r.s = mul2(r.s, pair(f, f));
+  }
+  const bool away = r.kind == kAway;
   for (int u = 0; u < NV; ++u) {
     float x[N];
     Elem<T>::unpack(v[u], x);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      float q0, q1;
-      unpair(fma2(pair(x[i], x[i + 1]), c2, nrc), &q0, &q1);
-      q0 = max_nan(q0, -kFarBits);
-      q1 = max_nan(q1, -kFarBits);
+      const float q0 = max_nan(away ? (x[i] - r.ref) * a.c : fmaf(x[i], a.c, -r.ref), -kFarBits);
+      const float q1 = max_nan(away ? (x[i + 1] - r.ref) * a.c : fmaf(x[i + 1], a.c, -r.ref), -kFarBits);
       const f2 e = pair(ex2(q0), ex2(q1));
-      m.s = add2(m.s, e);
-      m.t = fma2(e, pair(q0, q1), m.t);
+      r.s = add2(r.s, e);
+      r.t = fma2(e, pair(q0, q1), r.t);
     }
   }
-  r.rc = m.rc;
-  r.s = m.s;
-  r.t = m.t;
-  r.gaps = true;
 }
 
-// Adds NV vectors. Entry by entry: unpack, half a fused multiply-add, 2^q, half an addition, half a
+// The call with copies: what it may touch must not live in registers' stead.
+template <class T, int NV>
+__device__ __forceinline__ void sums_call(Sums& r, const uint4* v, const VocArgs& a) {
+  Sums again = r;
+  uint4 w[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) w[u] = v[u];
+  sums_other<T, NV>(again, w, a);
+  r = again;
+}
+
+// Adds NV vectors to sums near 0; false, and nothing added, where that is not for these sums. Entry by entry: unpack, half a fused multiply-add, 2^q, half an addition, half a
 // fused multiply-add; GAPS: and a maximum.
 template <class T, int NV, bool GAPS>
-__device__ __forceinline__ void sums_some(Sums& r, const uint4* v, const VocArgs& a) {
+__device__ __forceinline__ bool sums_some(Sums& r, const uint4* v, const VocArgs& a) {
   constexpr int N = Elem<T>::N;
-  const f2 c2 = pair(a.c, a.c), nrc = pair(-r.rc, -r.rc);
+  const f2 c2 = pair(a.c, a.c), nrc = pair(-r.ref, -r.ref);
   f2 s = r.s, t = r.t;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
@@ -917,72 +954,38 @@ __device__ __forceinline__ void sums_some(Sums& r, const uint4* v, const VocArgs
   }
   float t0, t1;
   unpair(t, &t0, &t1);
-  if (!(fabsf(t0 + t1) < 1.0e18f)) {
-    Sums again = r;                               // copies: what a call may touch must not live in registers' stead
-    uint4 w[NV];
-#pragma unroll
-    for (int u = 0; u < NV; ++u) w[u] = v[u];
-    sums_slow<T, NV>(again, w, r.s, r.t, a);
-    r = again;
-  } else {
-    r.s = s;
-    r.t = t;
-  }
+  if (__any_sync(kFull, !(t0 + t1 < kShiftAt))) return false;
+  r.s = s;
+  r.t = t;
+  return true;
 }
 
+// Adds a chunk.
 template <class T, int NV>
 __device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs& a, bool gaps = false) {
-  if (r.gaps || gaps) sums_some<T, NV, true>(r, v, a);
-  else sums_some<T, NV, false>(r, v, a);
-}
-
-// A chunk before rc is set whose largest entry over the warp, top, is not from ref_min to -ref_min.
-template <class T, int NV>
-__device__ __noinline__ void sums_odd(Sums& r, const uint4* v, float top, const VocArgs& a) {
-  constexpr int N = Elem<T>::N;
-  if (top > 0.0f) r.huge = true;
-  for (int u = 0; u < NV; ++u) {
-    float x[N];
-    Elem<T>::unpack(v[u], x);
-    for (int i = 0; i < N; ++i) {
-      if (x[i] != x[i]) r.s = pair(NAN, NAN);
-      if (!(x[i] > -INFINITY) || r.huge) continue;
-      if (x[i] > r.low_m) {
-        const float d = fmaxf((r.low_m - x[i]) * a.c, -kFarBits), f = ex2(d);
-        r.low_t = f * (r.low_t + d * r.low_s);
-        r.low_s *= f;
-        r.low_m = x[i];
-      }
-      const float d = fmaxf((x[i] - r.low_m) * a.c, -kFarBits), e = ex2(d);
-      r.low_s += e;
-      r.low_t = fmaf(e, d, r.low_t);
+  if (r.kind == kNone) {
+    const float rc = warp_max(Elem<T>::template high<NV>(v)) * a.c;
+    if (fabsf(rc) <= kNearBits) {
+      r.kind = kNear;
+      r.ref = rc;
     }
   }
-}
-
-// Sets rc from a chunk's largest entry over the warp; false if the chunk is not for the sums.
-template <class T, int NV>
-__device__ __forceinline__ bool sums_start(Sums& r, const uint4* v, const VocArgs& a) {
-  const float top = warp_max(Elem<T>::template high<NV>(v));
-  if (top >= a.ref_min && top <= -a.ref_min) {
-    r.rc = top * a.c;
-    r.have = true;
-    return true;
-  }
-  bool all = true;                                // nothing but -inf
+  if (r.kind == kNear) {
+    if (!r.gaps && !gaps && sums_some<T, NV, false>(r, v, a)) return;
+    if (sums_some<T, NV, true>(r, v, a)) {
+      r.gaps |= !gaps;
+      return;
+    }
+  } else if (r.kind == kNone) {
+    bool all = true;                              // nothing but -inf
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const uint32_t no = Elem<T>::nothing().x;
-    all = all && v[u].x == no && v[u].y == no && v[u].z == no && v[u].w == no;
+    for (int u = 0; u < NV; ++u) {
+      const uint32_t no = Elem<T>::nothing().x;
+      all = all && v[u].x == no && v[u].y == no && v[u].z == no && v[u].w == no;
+    }
+    if (__all_sync(kFull, all)) return;
   }
-  if (__all_sync(kFull, all)) return false;
-  Sums again = r;
-  uint4 w[NV];
-#pragma unroll
-  for (int u = 0; u < NV; ++u) w[u] = v[u];
-  sums_odd<T, NV>(again, w, top, a);
-  r = again;
-  return false;
+  sums_call<T, NV>(r, v, a);
 }
 
 // Reads a row's vector past L1. (Kept coherent: the gradient may take the logits' place.)
@@ -1033,7 +1036,7 @@ struct StreamShared {
   int nan, scratch[kRowWarps + 1];
   float top_ref;
   double top_log_s;
-  float4 part[kParts];                            // rc, s, t, and as an int: 0 none, 1 sums, 2 beyond range, 3 below ref_min
+  float4 part[kParts];                            // of each warp: reference, s, t, and as an int its kind
   int repeats;                                    // an index stands in the list twice
   uint32_t hit[kHitWords];                        // chunks of the slice that hold entries of the list (modulo)
   float w, w_h, x_target;
@@ -1043,7 +1046,7 @@ struct StreamShared {
   double list_exp;                                // and the sum of exp(z - its z) over them
   // the results of the careful route
   float k, A, Bl, ref;
-  int wild, none;
+  int away, none;
   float g_target;                                 // the gradient at the target
 };
 
@@ -1297,29 +1300,30 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 
     // -- the row's results in 64 bits ------------------------------------------------------------------
     wait(&sh.sums);
+    bool near = true;                             // GRAD: all parts have references near 0
     if constexpr (GRAD) {
       // What the gradient waits for, in fp32, the parts in a fixed order (by every warp for itself this took 1400
       // instructions per CTA)
       const int parts = C * W;
       const float4 p = lane < parts ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-      bool normal = __float_as_int(p.w) == 1, huge = __float_as_int(p.w) == 2;
+      bool normal = __float_as_int(p.w) == kNear, other = __float_as_int(p.w) > kNear;
       float rcm = warp_max(normal ? p.x : -INFINITY);
       float4 p1 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
       if (parts > 32) {
         if (lane + 32 < parts) p1 = sh.part[lane + 32];
-        normal |= __float_as_int(p1.w) == 1;
-        huge |= __float_as_int(p1.w) == 2;
-        rcm = fmaxf(rcm, warp_max(__float_as_int(p1.w) == 1 ? p1.x : -INFINITY));
+        normal |= __float_as_int(p1.w) == kNear;
+        other |= __float_as_int(p1.w) > kNear;
+        rcm = fmaxf(rcm, warp_max(__float_as_int(p1.w) == kNear ? p1.x : -INFINITY));
       }
-      const bool plain_sums = __any_sync(kFull, normal) && !__any_sync(kFull, huge);
-      if (plain_sums) {
+      near = __any_sync(kFull, normal) && !__any_sync(kFull, other);
+      if (near) {
         float s = 0.0f, t = 0.0f;
-        if (__float_as_int(p.w) == 1) {
+        if (__float_as_int(p.w) == kNear) {
           const float d = fmaxf(p.x - rcm, -kFarBits), f = ex2(d);
           s = f * p.y;
           t = f * fmaf(d, p.y, p.z);
         }
-        if (parts > 32 && __float_as_int(p1.w) == 1) {
+        if (parts > 32 && __float_as_int(p1.w) == kNear) {
           const float d = fmaxf(p1.x - rcm, -kFarBits), f = ex2(d);
           s = fmaf(f, p1.y, s);
           t = fmaf(f, fmaf(d, p1.y, p1.z), t);
@@ -1350,7 +1354,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         const int E = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
         const float m = s * __uint_as_float((uint32_t)(127 - E) << 23);
         const float kf = rcm + (float)E;
-        const float off = (float)((double)kf - (double)E - (double)rcm), f = __fdividef(fmaf(off, 0.69314718f, 1.0f), m);
+        const float off = (float)((double)kf - (double)E - (double)rcm), f = __fdividef(ex2(off), m);
         const float A = f * (Bl != 0.0f ? fmaf(Bl, off - __log2f(m), Af) : Af);
         Bl *= f;
         if (lane == 0) {
@@ -1358,42 +1362,66 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
           sh.A = A;
           sh.Bl = Bl;
           sh.ref = 0.0f;
-          sh.wild = 0;
+          sh.away = 0;
           sh.none = w == 0.0f && w_h == 0.0f;
         }
         arrive(&sh.factors);
       }
     }
-    int kind = 0;
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
-    {
-      const int n = C * W, k0 = lane < n ? __float_as_int(sh.part[lane].w) : 0;
-      const int k1 = lane + 32 < n ? __float_as_int(sh.part[lane + 32].w) : 0;
-      const bool huge = __any_sync(kFull, k0 == 2 || k1 == 2), normal = __any_sync(kFull, k0 == 1 || k1 == 1);
-      // of the parts with a normal reference (kind 1) where there are any, else of those below ref_min
-      const int which = normal ? 1 : 3;
-      kind = huge ? 2 : normal ? 1 : __any_sync(kFull, k0 == 3 || k1 == 3) ? 3 : 0;
-      M = warp_max(fmaxf(k0 == which ? sh.part[lane].x : -INFINITY, k1 == which ? sh.part[lane + 32].x : -INFINITY));
-      for (int q = lane; q < n; q += 32) {
+    bool careful = false;
+    const int n_parts = C * W;
+    if constexpr (!GRAD) {
+      const int k0 = lane < n_parts ? __float_as_int(sh.part[lane].w) : kNone;
+      const int k1 = lane + 32 < n_parts ? __float_as_int(sh.part[lane + 32].w) : kNone;
+      near = __any_sync(kFull, k0 == kNear || k1 == kNear) && !__any_sync(kFull, k0 > kNear || k1 > kNear);
+    }
+    if (near) {
+      for (int q = lane; q < n_parts; q += 32)
+        if (__float_as_int(sh.part[q].w) == kNear) M = fmaxf(M, sh.part[q].x);
+      M = warp_max(M);
+      for (int q = lane; q < n_parts; q += 32) {
         const float4 p = sh.part[q];
-        if (__float_as_int(p.w) != which) continue;
-        // a normal reference is fl(x c), the other an entry
-        const float off = fmaxf(normal ? p.x - M : (p.x - M) * a.c, -kFarBits), f = ex2(off);
+        if (__float_as_int(p.w) != kNear) continue;
+        const float off = fmaxf(p.x - M, -kFarBits), f = ex2(off);
         Sd += (double)f * (double)p.y;
         Td += (double)f * ((double)p.z + (double)off * (double)p.y);
       }
       Sd = warp_sum(Sd);
       Td = warp_sum(Td);
-      if (kind == 1) {
-        const double rc = (double)M;
-        M = (float)(rc * a.inv_c);
-        const double off = rc - (double)M * (double)a.c, f = exp2_small(off);
-        Td = f * (Td + off * Sd);
-        Sd *= f;
+      const double rc = (double)M;
+      M = (float)(rc * a.inv_c);
+      const double off = rc - (double)M * (double)a.c, f = exp2_small(off);
+      Td = f * (Td + off * Sd);
+      Sd *= f;
+    } else {
+      // the parts' references in bits, exact in 64 bits; the largest, and an entry at or near it
+      auto bits = [&](const float4& p) { return __float_as_int(p.w) == kAway ? (double)p.x * (double)a.c : (double)p.x; };
+      double high = -INFINITY;
+      for (int q = lane; q < n_parts; q += 32) {
+        const float4 p = sh.part[q];
+        careful |= __float_as_int(p.w) == kHuge;
+        if (__float_as_int(p.w) == kNone || !(bits(p) > high)) continue;
+        high = bits(p);
+        M = __float_as_int(p.w) == kAway ? p.x : (float)(high * a.inv_c);
       }
+      careful = __any_sync(kFull, careful);
+      double most = high;
+      for (int d = 16; d > 0; d >>= 1) most = fmax(most, __shfl_xor_sync(kFull, most, d));
+      M = warp_max(high == most ? M : -INFINITY);
+      for (int q = lane; q < n_parts; q += 32) {
+        const float4 p = sh.part[q];
+        if (__float_as_int(p.w) == kNone) continue;
+        const double off = bits(p) - (double)M * (double)a.c, s = (double)p.y, t = (double)p.z;
+        // (a part that is nothing beside the others still brings its NaN)
+        const double f = off < -2.0 * kFarBits ? 0.0 : exp2_small(off);
+        Sd += f * s;
+        Td += f == 0.0 ? f * s : f * (t + off * s);
+      }
+      Sd = warp_sum(Sd);
+      Td = warp_sum(Td);
     }
-    const bool careful = kind == 2;
     if (careful) {                                // logits beyond 2^100 / c
       const int32_t* out = nullptr;
       if constexpr (OP == kTail) out = L.idx;
@@ -1479,7 +1507,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       } else if (lane == 0 && sh.target >= 0) {
         sh.g_target = entry(sh.x_target, (double)w);
       }
-      if (kind != 1) {                            // the factors, where the warps have no way of their own
+      if (!near) {                                // the factors, where the short way above has none
         double A, Bl = 0.0;
         if (OP == kLogprob) {
           A = A_list;
@@ -1555,9 +1583,9 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
   if (OP == kTail) wait(&sh.listed);
   Sums run;
   run.s = run.t = pair(0.0f, 0.0f);
-  run.have = run.huge = run.gaps = false;
-  run.rc = run.low_s = run.low_t = 0.0f;
-  run.low_m = -INFINITY;
+  run.kind = kNone;
+  run.ref = 0.0f;
+  run.gaps = false;
   typename Elem<T>::Max high[U];
   if (TOP) {
 #pragma unroll
@@ -1579,7 +1607,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 #pragma unroll
       for (int u = 0; u < U; ++u) v[u] = nx[u];
       request(left - step);
-      if (hit || left < kChunk) {
+      if (hit) {
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -1597,20 +1625,16 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       for (int u = 0; u < U; ++u)
         if (left >= kChunk || u * 32 + lane < left) Elem<T>::rise(high[u], v[u]);
     }
-    if (left >= kChunk) {
-      if (hit) {
+    if (hit) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = chunk[u * 32 + lane];
-      }
-      if (run.have || sums_start<T, U>(run, v, a)) sums_add<T, U>(run, v, a, hit);
-    } else {
-#pragma unroll 1
-      for (int u = lane; u - lane < left; u += 32) {
-        const uint4 one = u < left ? chunk[u] : Elem<T>::nothing();
-        if (run.have || sums_start<T, 1>(run, &one, a))
-          if (u < left) sums_add<T, 1>(run, &one, a, hit);
-      }
+      for (int u = 0; u < U; ++u) v[u] = chunk[u * 32 + lane];
     }
+    if (left < kChunk) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * 32 + lane >= left) v[u] = Elem<T>::nothing();
+    }
+    sums_add<T, U>(run, v, a, hit || left < kChunk);
   }
   if (warp == 0 && __any_sync(kFull, edge >= 0)) {   // the entries before the first and after the last vector
     float x[N];
@@ -1620,36 +1644,28 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         if (L.idx[j] == edge) x[0] = -INFINITY;
 #pragma unroll
     for (int i = 1; i < N; ++i) x[i] = -INFINITY;
-    const uint4 v = Elem<T>::pack(x);
-    if ((run.have || sums_start<T, 1>(run, &v, a)) && edge >= 0) sums_add<T, 1>(run, &v, a);
+    uint4 v[U];
+    v[0] = Elem<T>::pack(x);
+#pragma unroll
+    for (int u = 1; u < U; ++u) v[u] = Elem<T>::nothing();
+    sums_call<T, U>(run, v, a);
   }
   {                                               // the lanes' sums together, to the CTAs of the row
-    const float rc = warp_max(run.rc);
-    Running all{0.0f, run.rc, run.s, run.t};
-    if (__any_sync(kFull, run.rc != rc)) running_shift(all, rc);   // (a lane that had entries far above the first chunk)
     float s0, s1, t0, t1;
-    unpair(all.s, &s0, &s1);
-    unpair(all.t, &t0, &t1);
+    unpair(run.s, &s0, &s1);
+    unpair(run.t, &t0, &t1);
     s0 = warp_sum(s0 + s1);
     t0 = warp_sum(t0 + t1);
-    float ref = rc;
-    int kind = __any_sync(kFull, run.huge) ? 2 : run.have || s0 != s0 ? 1 : 0;
-    if (kind == 0) {
-      const float low = warp_max(run.low_m);
-      if (low > -INFINITY) {
-        const float d = fmaxf((run.low_m - low) * a.c, -kFarBits), f = ex2(d);
-        const bool any = run.low_m > -INFINITY;
-        s0 = warp_sum(any ? f * run.low_s : 0.0f);
-        t0 = warp_sum(any ? f * (run.low_t + d * run.low_s) : 0.0f);
-        ref = low;
-        kind = 3;
-      }
+    if (run.kind == kNan) {
+      run.kind = kNear;
+      run.ref = 0.0f;
+      s0 = t0 = NAN;
     }
     started();
     // The gradient may take the logits' place, so that no CTA of the row begins it before the others have read
     // what they need of it.
     if (GRAD && C > 1) wait(&sh.gathered);
-    const float4 sums = make_float4(ref, s0, t0, __int_as_float(kind));
+    const float4 sums = make_float4(run.ref, s0, t0, __int_as_float(run.kind));
     if (C == 1) {                                 // (no asynchronous store outside a cluster launch: it is illegal there)
       if (lane == 0) sh.part[warp] = sums;
       arrive(&sh.sums);
@@ -1778,28 +1794,33 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     if (!RES) request(own - warp * kChunk);
     wait(&sh.factors);
     const float kf = sh.k, A = sh.A, Bl = sh.Bl, ref = sh.ref;
-    const bool wild = sh.wild, none = sh.none;
+    const bool away = sh.away, none = sh.none;
     T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
     const bool in_step = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
-    const bool plain = in_step && !wild && !none;
+    const bool plain = in_step && !away && !none;
     uint4* dvec = reinterpret_cast<uint4*>(dx + row.head) + row.v0;
     const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
-    auto grad = [&](uint4 v) {
+    auto grad = [&](uint4 v, auto far) {             // far: the difference first
       float x[N];
       Elem<T>::unpack(v, x);
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         float q0, q1;
-        f2 q = fma2(pair(x[i], x[i + 1]), c2, nk), g = A2;
-        unpair(q, &q0, &q1);
+        f2 q, g = A2;
+        if constexpr (far.value) {
+          q0 = max_nan((x[i] - ref) * a.c, -kFarBits) - kf;
+          q1 = max_nan((x[i + 1] - ref) * a.c, -kFarBits) - kf;
+        } else {
+          q = fma2(pair(x[i], x[i + 1]), c2, nk);
+          unpair(q, &q0, &q1);
+        }
         if (OP == kLogprob && Bl != 0.0f) g = fma2(pair(max_nan(q0, -kFarBits), max_nan(q1, -kFarBits)), B2, A2);
         unpair(mul2(pair(ex2(q0), ex2(q1)), g), &x[i], &x[i + 1]);
       }
       return Elem<T>::pack(x);
     };
     auto grad_one = [&](float x) {
-      float q = fmaf(x, a.c, -kf);
-      if (wild) q = max_nan(max_nan(x - ref, -a.far) * a.c, -kFarBits) - kf;   // the difference first
+      const float q = away ? max_nan((x - ref) * a.c, -kFarBits) - kf : fmaf(x, a.c, -kf);
       return Elem<T>::from(ex2(q) * (Bl != 0.0f ? fmaf(max_nan(q, -kFarBits), Bl, A) : A));
     };
     // The whole chunks without entries of the list, in a loop of their own that holds little else (one loop
@@ -1824,7 +1845,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 #pragma unroll
           for (int u = 0; u < U; ++u) v[u] = from[u * 32];
 #pragma unroll
-          for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(v[u]));
+          for (int u = 0; u < U; ++u) __stcs(to + u * 32, grad(v[u], std::false_type{}));
         }
       }
     }
@@ -1846,9 +1867,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       bool hit;
       if (LIST) hit = hits(o);
       else hit = sh.target >= e0 && sh.target < e0 + kChunk * N;
-      if (!wild) {
+      if (away) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = grad(v[u]);
+        for (int u = 0; u < U; ++u) v[u] = grad(v[u], std::true_type{});
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = grad(v[u], std::false_type{});
       }
       if (plain && !hit) {
 #pragma unroll
@@ -1863,10 +1887,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
           if (u * 32 + lane < n) chunk[u * 32 + lane] = none ? make_uint4(0, 0, 0, 0) : v[u];
         __syncwarp();
         if (!none) {
-          if (wild) {
-            for (int e = lane; e < n * N; e += 32) el[e] = grad_one(Elem<T>::to(el[e]));
-            __syncwarp();
-          }
           if constexpr (LIST) {
             if (hit) {
               wait(&sh.ready);
@@ -2079,8 +2099,8 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
   a.far = kFarBits / a.c;
   a.fine = (float)((double)a.c_lo / (double)a.c * 0.6931471805599453);
   a.inv_c = 1.0 / (double)a.c;
-  a.ref_min = -kWildBits / a.c;
-  if (a.ref_min < -kLowestSafe) a.ref_min = -kLowestSafe;
+  a.huge = kHugeBits / a.c;
+  if (a.huge > 1.0e38f) a.huge = 1.0e38f;
   a.it = inv_temperature;
   a.logits = logits;
   a.dlogits = dlogits;

@@ -519,6 +519,100 @@ def test_rows_longer_than_eight_slices(dtype, V):
     assert torch.equal(got.dlogits, want.dlogits) and torch.equal(got.loss, want.loss)
 
 
+# ---- references far from 0 ------------------------------------------------------------------------
+#
+# The exponent (x - m) c of an entry far from 0 must be 0 at the reference m itself: the rounding of the product
+# m c alone, half a step of it, is more than an exponent may be off by once |m c| is beyond about 2^20.
+
+MASKS = [-1e6, -1e7, -1e8, -1e9, -1e10, -1e11, -1e12, -1e15, -1e18, -1e20, -1e30]
+
+
+def rounded_out(want, dtype):
+    """What rounding makes of gradients beyond the type's range: infinities (fp16: from 65520 on)."""
+    return np.where(np.abs(want) >= 65520.0, np.copysign(np.inf, want), want) if dtype == "fp16" else want
+
+
+def check_all(x, dtype, temperature, targets, idx, val):
+    """Both losses in every form: alone, with the gradient, the gradient from statistics."""
+    rows, V = x.shape
+    it = float(np.float32(1.0 / temperature))
+    h = f64(x)
+    check_tokens(x, dtype, temperature, targets, top_k=4 if rows < 100 else 0, grad=False)
+    w, t = weights(rows), dev(targets, torch.int32)
+    kw = dict(grad_logprob=dev(w[0]), grad_entropy=dev(w[1]), temperature=temperature)
+    r = gs.token_logprobs(x, t, want_entropy=True, want_stats=True, want_grad=True, **kw)
+    back = gs.token_logprobs_backward(x, r.stats, t, entropy=r.entropy, **kw)
+    lp, ent, _, _ = vocab.token_logprobs(h, it, targets)
+    close(r.logprob, lp, lse_tol(V) + 4 * U * np.abs(np.where(np.isfinite(lp), lp, 0)), "logprob")
+    close(r.entropy, ent, lse_tol(V) * (2 + math.log(V + 1)) + U * np.abs(ent), "entropy")
+    want = vocab.token_logprobs_grad(h, it, targets, w[0].astype(np.float64), w[1].astype(np.float64))
+    want[(np.where(targets < 0, 0, w[0]) == 0) & (w[1] == 0)] = 0.0
+    tol = grad_tol(h, it, want, dtype, it * (np.abs(w[0]) + np.abs(w[1]) * ent), it * w[1], it * w[0])
+    close(r.dlogits, rounded_out(want, dtype), tol, "dlogits")
+    close(back, rounded_out(want, dtype), tol, "backward")
+    small = min(1.0, 1.0e4 * temperature) if dtype == "fp16" else 1.0
+    for tail in (False, True):
+        check_distill(x, dtype, idx, val, tail, temperature, w=np.full(rows, small, np.float32))
+
+
+def some_lists(rows, V):
+    idx = np.tile(np.array([[V - 3, 7, V // 2, -1]], np.int32), (rows, 1))
+    val = np.tile(np.log(np.array([[0.4, 0.3, 0.1, 0.05]], np.float32)), (rows, 1))
+    return idx, val
+
+
+# once: a row over several CTAs; six times: a CTA for each row
+@pytest.mark.parametrize("temperature,times", [(0.5, 1), (1.0, 1), (1.25, 1), (2.0, 1), (4.0, 1), (1.0, 6), (2.0, 6)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_finite_masks_of_any_size(dtype, temperature, times):
+    V, n = 9000, len(MASKS)
+    x, _ = make(5 * n, V, dtype)
+    m = torch.tensor(MASKS, device="cuda").to(x.dtype)[:, None]
+    x[:n] = m                                             # nothing but the mask
+    x[n:2 * n, :2048] = m                                 # the first entries of a vocabulary
+    x[2 * n:3 * n, :V - 1] = m                            # all entries but one
+    x[3 * n:4 * n] = -m                                   # far above 0
+    x[4 * n:, ::2] = m
+    x[4 * n:, 4096:8192] = m                              # whole chunks after ordinary ones
+    x = x.repeat(times, 1)
+    t = np.tile([3, V - 1, 2050, -1, 5], n * times)
+    check_all(x, dtype, temperature, t, *some_lists(len(t), V))
+
+
+@pytest.mark.parametrize("temperature", [1e-3, 1e-4, 1e-5, 1e-6, 1e-7, 1e-8, 1e-9])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_low_temperatures(dtype, temperature):
+    V = 9000
+    x, _ = make(12, V, dtype)
+    x[0, [20, 8000]] = 9.1                                # two equal maxima
+    x[1, [8000, 8001]] = 21.5
+    x[2] = 7.3
+    x[3] = -7.3
+    x[4, :4500] = -1.0e4
+    x[5] = float("-inf"); x[5, 4000:4002] = 3.3
+    x[6] = torch.linspace(1.0, 1.0 + 40 * temperature, V, device="cuda").to(x.dtype)
+    x[7] = 1.7 + torch.linspace(0.0, 40 * temperature, V, device="cuda").flip(0).to(x.dtype)
+    t = np.array([20, 8001, 5, 6, 8000, 4001, V - 1, 0, -1, 7, 8, 9])
+    check_all(x, dtype, temperature, t, *some_lists(12, V))
+
+
+@pytest.mark.parametrize("at", [45426.0, -45426.0, 3.0e6, -3.0e6])
+@pytest.mark.parametrize("times", [1, 40])
+def test_references_on_both_sides_of_the_border(at, times):
+    """Logits around the size where the difference is taken first (2^16 bits) and beyond, spread as ordinary ones are."""
+    V = 9000
+    x, _ = make(6, V, "fp32")
+    x += at
+    x[0, :4000] += 8.0
+    x[1, 4000:] += 8.0
+    x[2] += (torch.arange(V, device="cuda") // 512).float()
+    x[3] -= (torch.arange(V, device="cuda") // 512).float()
+    x[4, :3000] = 0.0 if at < 0 else -1e9
+    x = x.repeat(times, 1)
+    t = np.tile([3, V - 1, 2050, 17, 5, 4000], times)
+    check_all(x, "fp32", 1.0, t, *some_lists(len(t), V))
+
+
 # ---- as a run ---------------------------------------------------------------------------------------
 
 def test_teacher_to_student_to_compressed_gradient():
