@@ -42,7 +42,6 @@ constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: where a sum we
                                                   // clamped here, so that -inf logits add 0
 constexpr float kNearBits = 65536.0f;             // references m with |m c| up to here: exponents fma(x, c, -fl(m c)), which at
                                                   // m itself is the rounding of fl(m c), at most 2^-8. Beyond: (x - m) c
-constexpr float kHugeBits = 1.2676506e30f;        // 2^100: maxima beyond it (in bits) take the careful route
 
 enum { kLogprob = 0, kRenorm = 1, kTail = 2 };    // what is computed
 enum { kForward = 0, kFused = 1, kBackward = 2 }; // loss; loss and gradient; gradient from saved statistics
@@ -57,7 +56,6 @@ struct VocArgs {
   int32_t k;                     // list length: alternatives wanted (forward), given (backward), or the teacher's
   int32_t val_dtype;
   float it, c, c_lo;             // c + c_lo = it log2(e)
-  float far, huge;               // kFarBits / c, kHugeBits / c
   float fine;                    // ln2 c_lo / c
   double inv_c;                  // 1 / c
   const int32_t* targets;
@@ -542,42 +540,6 @@ struct Ring {
   }
 };
 
-// The thread's maximum over the slice, NaN passed over; the entries in `out` left out.
-template <class T>
-__device__ __noinline__ float careful_max(const Row<T>& row, const int32_t* out, int n_out, int tid, int threads) {
-  float m = -INFINITY;
-  for (int e = tid; e < row.V; e += threads) {
-    float x = Elem<T>::to(row.x[e]);
-    for (int j = 0; j < n_out; ++j)
-      if (out[j] == e) x = -INFINITY;
-    m = fmaxf(m, x);
-  }
-  return m;
-}
-
-// The thread's sums over the CTA's slice relative to M, entry by entry with the difference taken first: for rows
-// whose maximum times c is beyond 2^100, where fl(x c - rc) would overflow. out: entries left out.
-template <class T>
-__device__ __noinline__ void careful_sums(const Row<T>& row, float M, const VocArgs& a, const int32_t* out, int n_out, int tid,
-                                          int threads, double& S, double& Tt) {
-  double s = 0.0, t = 0.0;
-  auto one = [&](int e) {
-    float x = Elem<T>::to(row.x[e]);
-    for (int j = 0; j < n_out; ++j)
-      if (out[j] == e) x = -INFINITY;
-    const float q = max_nan(max_nan(x - M, -a.far) * a.c, -kFarBits), y = ex2(q);
-    s += (double)y;
-    t += (double)y * (double)q;
-  };
-  for (int e = row.head + row.v0 * Elem<T>::N + tid; e < row.head + row.v1 * Elem<T>::N; e += threads) one(e);
-  if (row.first)
-    for (int e = tid; e < row.head; e += threads) one(e);
-  if (row.last)
-    for (int e = row.tail0() + tid; e < row.V; e += threads) one(e);
-  S = s;
-  Tt = t;
-}
-
 // ---- gradient from saved statistics ----------------------------------------------------------------
 
 constexpr int kHitWords = 16;
@@ -839,7 +801,8 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
 // the warp finds one, near 0: q = fma(x, c, -rc), rc = fl(m c), the same for every entry; away from it: q = (x - m) c.
 // fp32 takes entries far above it, and a chunk that takes the sums beyond kShiftAt moves it. Saves half an
 // instruction per entry and a branch per chunk against the running maximum. All but s and t is the warp's.
-enum { kNone = 0, kNear = 1, kHuge = 2, kAway = 3, kNan = 4 };   // what there is (parts of a row: up to kAway)
+// NaN or +inf make the row NaN: nothing more is read of the warp's chunks.
+enum { kNone = 0, kNear = 1, kAway = 2, kNan = 3 };   // what there is (parts of a row: up to kAway)
 constexpr float kShiftAt = 1.0e18f;
 
 struct Sums {
@@ -865,17 +828,13 @@ __device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& 
       nan |= x[i] != x[i];
     }
   }
-  if (r.kind >= kHuge && r.kind != kAway) return;
+  if (r.kind == kNan) return;
   const float top = warp_max(high), rc = top * a.c;
-  if (__any_sync(kFull, nan)) {
+  if (top == INFINITY || __any_sync(kFull, nan)) {
     r.kind = kNan;
     return;
   }
   if (top == -INFINITY) return;
-  if (top > a.huge) {
-    r.kind = kHuge;
-    return;
-  }
   const bool near = fabsf(rc) <= kNearBits;
   float down = 0.0f;                              // from the new reference to the old one
   if (r.kind == kNone) {
@@ -1028,7 +987,7 @@ constexpr int kParts = 8 * kRowWarps;             // partial sums of a row, at m
 
 struct StreamShared {
   uint64_t listed, sums, factors, ready;          // the list's indices; all partial sums; the gradient's factors; that at the list's entries
-  uint64_t gathered, reread;                      // the row's entries at the list have been read; by all CTAs, the row again
+  uint64_t gathered;                              // the row's entries at the list have been read
   uint64_t bounded, pushed;                       // alternatives: the CTAs' bounds are there; all candidates
   uint32_t bounds[8], tops[8], least[8];
   alignas(16) uint32_t reach[2][8];               // parts of each warp that reach three values, ten bits each
@@ -1044,7 +1003,7 @@ struct StreamShared {
   double Q, rho, list_max, list_sum;
   float list_high;                                // kTail: largest logit at the list's entries
   double list_exp;                                // and the sum of exp(z - its z) over them
-  // the results of the careful route
+  // the gradient's factors
   float k, A, Bl, ref;
   int away, none;
   float g_target;                                 // the gradient at the target
@@ -1123,7 +1082,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     mbar_init(&sh.listed, 1);
     mbar_init(&sh.factors, 1);
     mbar_init(&sh.gathered, 1);
-    mbar_init(&sh.reread, C);
     mbar_init(&sh.sums, C == 1 ? W : 1);
     mbar_init(&sh.ready, 1);
     if (TOP) {
@@ -1370,7 +1328,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     }
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
-    bool careful = false;
     const int n_parts = C * W;
     if constexpr (!GRAD) {
       const int k0 = lane < n_parts ? __float_as_int(sh.part[lane].w) : kNone;
@@ -1401,12 +1358,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       double high = -INFINITY;
       for (int q = lane; q < n_parts; q += 32) {
         const float4 p = sh.part[q];
-        careful |= __float_as_int(p.w) == kHuge;
         if (__float_as_int(p.w) == kNone || !(bits(p) > high)) continue;
         high = bits(p);
         M = __float_as_int(p.w) == kAway ? p.x : (float)(high * a.inv_c);
       }
-      careful = __any_sync(kFull, careful);
       double most = high;
       for (int d = 16; d > 0; d >>= 1) most = fmax(most, __shfl_xor_sync(kFull, most, d));
       M = warp_max(high == most ? M : -INFINITY);
@@ -1421,21 +1376,6 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       }
       Sd = warp_sum(Sd);
       Td = warp_sum(Td);
-    }
-    if (careful) {                                // logits beyond 2^100 / c
-      const int32_t* out = nullptr;
-      if constexpr (OP == kTail) out = L.idx;
-      const Row<T> whole(row.x, a.vocab, 0, 1, 0u);
-      M = careful_max(whole, out, OP == kTail ? a.k : 0, lane, 32);
-      M = warp_max(M);
-      careful_sums(whole, M, a, out, OP == kTail ? a.k : 0, lane, 32, Sd, Td);
-      Sd = warp_sum(Sd);
-      Td = warp_sum(Td);
-      if (GRAD && C > 1) {                        // (as with the sums)
-        __syncwarp();
-        if (lane < C) peer_arrive(&sh.reread, lane);
-        wait(&sh.reread);
-      }
     }
     const float ref = fmaxf(M, kLowest);
     // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
@@ -2096,11 +2036,8 @@ int voc_common(VocArgs& a, const void* logits, int32_t dtype, int64_t rows, int6
   const double c = (double)inv_temperature * 1.4426950408889634;
   a.c = (float)c;
   a.c_lo = (float)(c - (double)a.c);
-  a.far = kFarBits / a.c;
   a.fine = (float)((double)a.c_lo / (double)a.c * 0.6931471805599453);
   a.inv_c = 1.0 / (double)a.c;
-  a.huge = kHugeBits / a.c;
-  if (a.huge > 1.0e38f) a.huge = 1.0e38f;
   a.it = inv_temperature;
   a.logits = logits;
   a.dlogits = dlogits;

@@ -127,7 +127,9 @@ def distill_grad(x, it, idx, val, tail, g):
             if not np.isneginf(log_r):
                 outside = np.ones(x.shape[1], bool)
                 outside[idx[r][idx[r] >= 0]] = False
-                out[r] += rho * p[r] - np.where(outside, rho * np.exp(np.where(outside, lp[r], -np.inf) - log_r), 0.0)
+                # p / R outside is a softmax of its own: from log p it would lose its digits where R is next to nothing
+                share = np.exp(log_softmax(np.where(outside, x[r], -np.inf)[None], it)[0])
+                out[r] += rho * p[r] - rho * share
         for j in range(idx.shape[1]):
             if idx[r, j] >= 0:
                 out[r, idx[r, j]] -= q[r, j]

@@ -613,6 +613,46 @@ def test_references_on_both_sides_of_the_border(at, times):
     check_all(x, "fp32", 1.0, t, *some_lists(len(t), V))
 
 
+@pytest.mark.parametrize("rows,V", [(3, 1 << 24), (9, 128001), (330, 40003)])
+def test_infinite_and_huge_entries_with_long_lists(rows, V):
+    """Rows with +inf or entries near the types' ends cost no more than others: the largest vocabulary, a list of 256."""
+    k = 256
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    x = torch.randn(rows, V, device="cuda", generator=gen).to(torch.bfloat16)
+    x[0, V - 5] = float("inf")
+    x[1, 4000] = 1.0e38
+    x[2, ::2] = -1.0e38
+    idx = np.tile((np.arange(k, dtype=np.int64) * 7919 * 2 + 1) % V, (rows, 1)).astype(np.int32)
+    idx[1, 5] = 4000
+    val = np.tile(np.log(np.full(k, 0.9 / k)).astype(np.float32), (rows, 1))
+    w = np.ones(rows, np.float32)
+    ti, tv, st = dev(idx, torch.int32), dev(val), gs.status_tensor()
+    n = min(rows, 9)                                      # the rows that are compared
+    h, v64 = f64(x[:n]), val[:n].astype(np.float64)
+    for tail in (True, False):
+        a = gs.distill_topk(x, ti, tv, tail=tail, d_status=st)
+        b = gs.distill_topk(x, ti, tv, tail=tail, want_grad=True, grad_loss=dev(w), d_status=st)
+        want = vocab.distill(h, 1.0, idx[:n], v64, tail)
+        tol = 2 * lse_tol(V) + 2 * U * np.abs(np.nan_to_num(want))
+        close(a.loss[:n], want, tol, "loss")
+        close(b.loss[:n], want, tol, "loss with the gradient")
+        grad = vocab.distill_grad(h, 1.0, idx[:n], v64, tail, w[:n].astype(np.float64))
+        # (mass + rest) p - rest p / R: terms of p's accuracy that cancel at most where R is near 1 (four times p), the
+        # second alone (the gradient itself; log2 of p / R within 64) where p vanishes beside the list; rounded to bf16
+        l2 = np.abs(np.nan_to_num(np.maximum(vocab.log_softmax(h, 1.0), -100.0))) / math.log(2)
+        rel = (16 + 8 * math.log2(V + 1)) * U + 2 * lse_tol(V)
+        body = 4 * np.exp2(-l2) * (rel + 3 * l2 * U) + np.abs(np.nan_to_num(grad)) * (rel + 3 * 64 * U)
+        close(b.dlogits[:n], grad, body + 2.0 ** -8 * (np.abs(np.nan_to_num(grad)) + body) + TINY["bf16"], "dlogits")
+    r = gs.token_logprobs(x, ti[:, 0].contiguous(), top_k=20, want_entropy=True, d_status=st)
+    lp, ent, top, _ = vocab.token_logprobs(h[:3], 1.0, idx[:3, 0], 0 if V > 1 << 20 else 20)
+    close(r.logprob[:3], lp, lse_tol(V) + 4 * U * np.abs(np.nan_to_num(lp)), "logprob")
+    close(r.entropy[:3], ent, lse_tol(V) * (2 + math.log(V + 1)), "entropy")
+    if V <= 1 << 20:
+        assert np.array_equal(r.top_idx[:3].cpu().numpy(), top)
+    assert int(st.item()) == 0
+
+
 # ---- as a run ---------------------------------------------------------------------------------------
 
 def test_teacher_to_student_to_compressed_gradient():

@@ -97,6 +97,13 @@ def test_distillation_gradient_against_differences(it, tail):
     assert (got[3] == 0).all()
 
 
+def test_the_rest_of_a_row_keeps_its_shares_beside_a_huge_entry():
+    # beside 1e38 the others have p = 0, but the mass the list leaves still goes to them by their own softmax
+    x = np.array([[1e38, np.log(1.0), np.log(3.0)]])
+    got = vocab.distill_grad(x, 1.0, np.array([[0]]), np.log([[0.75]]), True, np.ones(1))
+    assert np.allclose(got, [[1.0 - 0.75, -0.25 * 0.25, -0.25 * 0.75]])
+
+
 def test_a_student_like_its_teacher_has_no_loss():
     rng = np.random.default_rng(3)
     x = rng.normal(size=(2, 9))
