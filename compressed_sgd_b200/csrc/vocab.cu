@@ -1931,6 +1931,18 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 // ---- launch -----------------------------------------------------------------------------------------
 
 constexpr size_t kPlainBytes = 32 << 10;          // dynamic shared memory that needs no leave beside the static part
+constexpr int64_t kSliceBytes = 64 << 10;         // three or four CTAs per SM
+constexpr int64_t kSliceMost = 200 << 10;         // one CTA per SM
+
+// The leave for a launch of `smem` bytes. It belongs to the kernel, not to the call: every call sets the most that any
+// call of the kernel needs, so that one thread's small call does not take back what another's launch is about to use.
+template <class K>
+bool voc_leave(K* kernel, size_t smem, size_t most) {
+  if (smem <= kPlainBytes) return true;
+  if (smem <= most && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
 
 template <class T, int OP, int MODE, bool RES, bool TOP>
 int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
@@ -1939,14 +1951,13 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
   a.split = split;
   a.slice = (int32_t)(chunks * kChunk);
   a.inv_split = (uint32_t)(((1ull << 32) + split - 1) / split);
-  const size_t smem = (RES ? (size_t)a.slice : (size_t)warps * kChunk) * 16 + (OP == kLogprob ? 0 : List::bytes(a.k)) +
-                      (TOP ? (size_t)warps * 256 + sizeof(TopShared) : 0);
+  auto bytes = [](size_t vectors, int w, int k) {
+    return vectors * 16 + (OP == kLogprob ? 0 : List::bytes(k)) + (TOP ? (size_t)w * 256 + sizeof(TopShared) : 0);
+  };
+  const size_t smem = bytes(RES ? a.slice : warps * kChunk, warps, a.k);
+  const size_t most = bytes(RES ? kSliceMost / 16 + kChunk : kRowWarps * kChunk, kRowWarps, GSPARSE_MAX_ALTERNATIVES);
   auto* kernel = voc_stream_kernel<T, OP, MODE, RES, TOP>;
-  if (smem > kPlainBytes &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return GSPARSE_ERR_CUDA;
-  }
+  if (!voc_leave(kernel, smem, most)) return GSPARSE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.rows * split));
   cfg.blockDim = dim3((unsigned)((warps + 1) * 32));
@@ -1966,9 +1977,6 @@ int voc_stream_launch(VocArgs a, int64_t nv, int split, cudaStream_t st) {
   }
   return launch_status();
 }
-
-constexpr int64_t kSliceBytes = 64 << 10;         // three or four CTAs per SM
-constexpr int64_t kSliceMost = 200 << 10;         // one CTA per SM
 
 template <class T, int OP, int MODE, bool TOP>
 int voc_stream(const VocArgs& a, cudaStream_t st) {
@@ -1997,10 +2005,7 @@ int voc_backward(VocArgs a, cudaStream_t st) {
   while (threads < kVocThreads && (int64_t)threads * kUnroll * split < nv) threads *= 2;
   const size_t smem = ring_bytes(threads) + List::bytes(OP == kLogprob ? a.k + 1 : a.k);
   auto* kernel = voc_backward_kernel<T, OP>;
-  if (smem > kPlainBytes && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return GSPARSE_ERR_CUDA;
-  }
+  if (!voc_leave(kernel, smem, ring_bytes(kVocThreads) + List::bytes(GSPARSE_MAX_ALTERNATIVES + 1))) return GSPARSE_ERR_CUDA;
   launch(kernel, (unsigned)((int64_t)a.rows * split), (unsigned)threads, smem, st, a);
   return launch_status();
 }

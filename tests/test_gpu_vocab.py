@@ -711,6 +711,48 @@ def test_streams_and_two_calls_at_once():
         assert torch.equal(gtops[s].top_idx, tops[s].top_idx) and torch.equal(gtops[s].top_logprob, tops[s].top_logprob)
 
 
+def test_calls_of_two_threads():
+    """Host threads that call one operator with other vocabularies and lists: each launch gets the memory it asks for."""
+    import threading
+    one = torch.ones(1, device="cuda")
+    t = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sets = []
+    for V, k in [(110000, 3), (400000, 250)]:
+        x = make(1, V, "fp32", seed=40)[0]
+        r = gs.token_logprobs(x, t, top_k=k, want_stats=True, want_grad=True, grad_logprob=one)
+        g_top = torch.ones(1, k, device="cuda")
+        sets.append((x, k, r, g_top, gs.token_logprobs_backward(x, r.stats, t, one, top_idx=r.top_idx, grad_top=g_top)))
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(2)
+
+    def work(x, k, want, g_top, back):
+        try:
+            V, out, back_out = x.shape[1], torch.empty_like(x), torch.empty_like(x)
+            logprob, stream = torch.empty_like(want.logprob), torch.cuda.Stream()
+            fused = (x.data_ptr(), 0, 1, V, V, 1.0, t.data_ptr(), logprob.data_ptr(), None, None, 0, None, None,
+                     out.data_ptr(), V, one.data_ptr(), None, None, stream.cuda_stream)
+            backward = (x.data_ptr(), 0, 1, V, V, 1.0, want.stats.data_ptr(), t.data_ptr(), one.data_ptr(), None, None, k,
+                        want.top_idx.data_ptr(), g_top.data_ptr(), back_out.data_ptr(), V, None, stream.cuda_stream)
+            for f, args in [(gs.lib().gsparse_token_logprobs, fused), (gs.lib().gsparse_token_logprobs_backward, backward)]:
+                start.wait(60)
+                refused = sum(f(*args) != 0 for _ in range(10000))
+                if refused:
+                    wrong.append((f.__name__, V, refused))
+            stream.synchronize()
+            if not (torch.equal(logprob, want.logprob) and torch.equal(out, want.dlogits) and torch.equal(back_out, back)):
+                wrong.append(("results", V))
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            start.abort()
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=s) for s in sets]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong
+
+
 def test_captured_and_replayed():
     x, _ = make(3, 30000, "bf16", seed=20)
     idx, val = lists(x, 9, 1.0, True)
