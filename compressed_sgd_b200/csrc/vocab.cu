@@ -799,11 +799,13 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
 
 // Sums over a lane's entries of e = 2^q and e q. The reference is the largest entry m of the first chunk in which
 // the warp finds one, near 0: q = fma(x, c, -rc), rc = fl(m c), the same for every entry; away from it: q = (x - m) c.
-// fp32 takes entries far above it, and a chunk that takes the sums beyond kShiftAt moves it. Saves half an
-// instruction per entry and a branch per chunk against the running maximum. All but s and t is the warp's.
+// Entries above it are added as they are until a chunk takes the sums T beyond kShiftAt, which moves it. Saves half an
+// instruction per entry against the running maximum. All but s and t is the warp's.
 // NaN or +inf make the row NaN: nothing more is read of the warp's chunks.
 enum { kNone = 0, kNear = 1, kAway = 2, kNan = 3 };   // what there is (parts of a row: up to kAway)
-constexpr float kShiftAt = 1.0e18f;
+// An entry 6.4 bits above the reference moves it: T / S from a reference k bits below the row's largest entry has k
+// roundings, and the entropy log S - T / S may be next to nothing. (No slower than 2^60: 4000 x 85000 bf16 119 us.)
+constexpr float kShiftAt = 512.0f;
 
 struct Sums {
   int kind;
@@ -1288,11 +1290,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         }
         s = warp_sum(s);
         t = warp_sum(t);
+        float Af, Bl = 0.0f, ent = 0.0f;
+        if (OP == kLogprob && w_h != 0.0f) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
         s = fmaf(a.fine, t, s);                     // c is rounded: to first order S + d ln2 T
-        float Af, Bl = 0.0f;
         if (OP == kLogprob) {
-          float ent = 0.0f;
-          if (w_h != 0.0f) ent = 0.69314718f * (__log2f(s) - __fdividef(t, s));
           Af = -a.it * fmaf(w_h, ent, w);
           Bl = -a.it * w_h * 0.69314718f;
         } else if (OP == kRenorm) {
@@ -1378,7 +1379,10 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       Td = warp_sum(Td);
     }
     const float ref = fmaxf(M, kLowest);
-    // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand
+    // c is rounded: to first order 2^(q (1 + d)) = 2^q (1 + d ln2 q), with the sum of 2^q q at hand. The entropy takes S
+    // and T as they are: at a temperature off by d it is off by d times the variance of z, with S alone corrected by d times
+    // the square of z's mean.
+    const double S_raw = Sd;
     Sd += (double)a.fine * Td;
     float ref_row = ref;
     double S_row = Sd, loss = 0.0, rho = 0.0, Q = 0.0;
@@ -1418,7 +1422,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       double ent = 0.0;
       if (w_h != 0.0f) {
         log_s = log(S_row);
-        ent = (double)(float)(log_s - 0.6931471805599453 * (Td / Sd));
+        ent = (double)(float)(log(S_raw) - 0.6931471805599453 * (Td / S_raw));
       }
       const double A_list = OP == kLogprob ? -itd * ((double)w + (double)w_h * ent)
                             : itd * (double)w * (OP == kRenorm ? Q : Q + rho);
@@ -1473,7 +1477,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
           a.out[r] = sh.target < 0     ? 0.0f
                      : S_row == 0.0 ? -INFINITY
                                     : (float)(((double)sh.x_target - (double)ref) * (double)a.it - log_s);
-        if (a.entropy) a.entropy[r] = S_row == 0.0 ? 0.0f : (float)(log_s - 0.6931471805599453 * (Td / Sd));
+        if (a.entropy) a.entropy[r] = S_row == 0.0 ? 0.0f : (float)(log(S_raw) - 0.6931471805599453 * (Td / S_raw));
       } else if constexpr (OP == kRenorm) {
         a.out[r] = Q == 0.0 ? 0.0f
                             : (float)(loss / sh.list_sum - log(sh.list_sum) + (S_row == 0.0 ? (double)INFINITY : log_s));

@@ -613,6 +613,29 @@ def test_references_on_both_sides_of_the_border(at, times):
     check_all(x, "fp32", 1.0, t, *some_lists(len(t), V))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_entropy_of_rows_with_a_peak_far_above_what_came_before(dtype):
+    """The entropy log S - T / S of a row with one likely token: taken from a reference far below the peak, T / S
+    alone carries |q| u.
+
+    From a reference at the peak (36 bits or more above the rest, so that sums are moved to it) S is 1 and a rest
+    below 2^-22, with the 4 u of 2^q at the peak; |T / S| is below 2^-16, its roundings nothing; the result
+    is rounded to fp32. Together less than 8 u, where a reference 36 to 50 bits below the peak has up to 35 u."""
+    rows, V = 300, 20000
+    rng = np.random.default_rng(11)
+    x = torch.from_numpy(rng.uniform(0.0, 1.0, size=(rows, V)).astype(np.float32)).to(TYPES[dtype]).cuda()
+    at = rng.integers(8000, V, size=rows)
+    x[torch.arange(rows), torch.from_numpy(at).cuda()] = dev(rng.uniform(26.5, 35.0, size=rows)).to(x.dtype)
+    t = dev(at, torch.int32)
+    h = f64(x)
+    ent = vocab.token_logprobs(h, 1.0)[1]
+    one = torch.ones(rows, device="cuda")
+    for r in (gs.token_logprobs(x, t, want_entropy=True),
+              gs.token_logprobs(x, t, want_entropy=True, want_grad=True, grad_logprob=one)):
+        close(r.entropy, ent, 8 * U, "entropy")
+        close(r.logprob, vocab.token_logprobs(h, 1.0, at)[0], 8 * U, "logprob")
+
+
 @pytest.mark.parametrize("rows,V", [(3, 1 << 24), (9, 128001), (330, 40003)])
 def test_infinite_and_huge_entries_with_long_lists(rows, V):
     """Rows with +inf or entries near the types' ends cost no more than others: the largest vocabulary, a list of 256."""
