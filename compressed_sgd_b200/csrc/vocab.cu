@@ -800,7 +800,8 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
 // Sums over a lane's entries of e = 2^q and e q. The reference is the largest entry m of the first chunk in which
 // the warp finds one, near 0: q = fma(x, c, -rc), rc = fl(m c), the same for every entry; away from it: q = (x - m) c.
 // Entries above it are added as they are until a chunk takes the sums T beyond kShiftAt, which moves it. Saves half an
-// instruction per entry against the running maximum. All but s and t is the warp's.
+// instruction per entry against the running maximum. A chunk's entries are added up before they join s and t, so that a
+// large entry swallows those of its own chunk at most. All but s and t is the warp's.
 // NaN or +inf make the row NaN: nothing more is read of the warp's chunks.
 enum { kNone = 0, kNear = 1, kAway = 2, kNan = 3 };   // what there is (parts of a row: up to kAway)
 // An entry 6.4 bits above the reference moves it: T / S from a reference k bits below the row's largest entry has k
@@ -862,6 +863,7 @@ __device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& 
     r.s = mul2(r.s, pair(f, f));
   }
   const bool away = r.kind == kAway;
+  f2 s = pair(0.0f, 0.0f), t = s;
   for (int u = 0; u < NV; ++u) {
     float x[N];
     Elem<T>::unpack(v[u], x);
@@ -870,10 +872,12 @@ __device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& 
       const float q0 = max_nan(away ? (x[i] - r.ref) * a.c : fmaf(x[i], a.c, -r.ref), -kFarBits);
       const float q1 = max_nan(away ? (x[i + 1] - r.ref) * a.c : fmaf(x[i + 1], a.c, -r.ref), -kFarBits);
       const f2 e = pair(ex2(q0), ex2(q1));
-      r.s = add2(r.s, e);
-      r.t = fma2(e, pair(q0, q1), r.t);
+      s = add2(s, e);
+      t = fma2(e, pair(q0, q1), t);
     }
   }
+  r.s = add2(r.s, s);
+  r.t = add2(r.t, t);
 }
 
 // The call with copies: what it may touch must not live in registers' stead.
@@ -893,7 +897,7 @@ template <class T, int NV, bool GAPS>
 __device__ __forceinline__ bool sums_some(Sums& r, const uint4* v, const VocArgs& a) {
   constexpr int N = Elem<T>::N;
   const f2 c2 = pair(a.c, a.c), nrc = pair(-r.ref, -r.ref);
-  f2 s = r.s, t = r.t;
+  f2 s = pair(0.0f, 0.0f), t = s;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     float x[N];
@@ -916,8 +920,8 @@ __device__ __forceinline__ bool sums_some(Sums& r, const uint4* v, const VocArgs
   float t0, t1;
   unpair(t, &t0, &t1);
   if (__any_sync(kFull, !(t0 + t1 < kShiftAt))) return false;
-  r.s = s;
-  r.t = t;
+  r.s = add2(r.s, s);
+  r.t = add2(r.t, t);
   return true;
 }
 

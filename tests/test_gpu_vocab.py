@@ -636,6 +636,23 @@ def test_entropy_of_rows_with_a_peak_far_above_what_came_before(dtype):
         close(r.logprob, vocab.token_logprobs(h, 1.0, at)[0], 8 * U, "logprob")
 
 
+@pytest.mark.parametrize("dtype,V,rows", [("bf16", 1000000, 300), ("fp32", 300000, 300), ("bf16", 1 << 24, 2)])
+def test_many_small_entries_beside_a_large_one(dtype, V, rows):
+    """One entry of 1 and V - 1 entries e of 0.9 u (u = 2^-24): added one by one to 1 each of them would be lost, V / 448
+    of them in the sum that holds the 1. A chunk's entries are added up first: at most its own 16 are lost, and each of
+    the warp's V / 7168 chunks adds one rounding, u; then 2^q (4 u), the join of the lanes (6 u), the result (2 u)."""
+    peak = torch.tensor(-math.log(0.9 * U), device="cuda").to(TYPES[dtype])
+    x = torch.zeros(rows, V, dtype=TYPES[dtype], device="cuda")
+    at = dev(np.random.default_rng(12).integers(0, V, size=rows), torch.int32)
+    x[torch.arange(rows, device="cuda"), at.long()] = peak
+    e = math.exp(-float(peak))
+    tol = (16 + V / 7168 + 12) * U
+    one = torch.ones(rows, device="cuda")
+    for r in (gs.token_logprobs(x, at, want_stats=True),
+              gs.token_logprobs(x, at, want_stats=True, want_grad=True, grad_logprob=one)):
+        close(r.logprob, np.full(rows, -math.log1p((V - 1) * e)), tol, "logprob")
+
+
 @pytest.mark.parametrize("rows,V", [(3, 1 << 24), (9, 128001), (330, 40003)])
 def test_infinite_and_huge_entries_with_long_lists(rows, V):
     """Rows with +inf or entries near the types' ends cost no more than others: the largest vocabulary, a list of 256."""
