@@ -579,6 +579,7 @@ struct RowShared {
   double S_row;
   float k, A, Bl, A_list;
   int away;
+  int empty;           // no entry in the teacher's list
 };
 
 // Dynamic shared memory: the warps' rings, then the list.
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
   float list_max = 0.0f;
   if (OP == kRenorm) list_max = fmaxf(block_max(vmax, R.max_list), kLowest);
   else __syncthreads();
-  // sum of the probabilities (of the renormalised list: not yet divided); of the incoming gradients and
+  // sum of the probabilities (of the renormalised list: not yet divided) and how many; of the incoming gradients and
   // their sizes
   double sum = 0.0, size = 0.0;
   for (int j = tid; j < nl; j += B) {
@@ -660,6 +661,7 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
       const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)list_max) * (double)a.it : (double)L.v[j]);
       L.q[j] = q;
       sum += q;
+      size += 1.0;
     }
     if (L.add(e)) R.repeats = 1;
   }
@@ -671,6 +673,7 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
     sum_get(sum, size, R.sum_list);
     R.Q = sum;
     R.rho = size;
+    R.empty = size == 0.0;
     R.list_sum = sum;
     if (OP == kRenorm) R.Q = sum == 0.0 ? 0.0 : sum == sum ? 1.0 : sum;
     if (OP == kTail) R.rho = sum == sum ? fmax(1.0 - sum, 0.0) : sum;
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
   const float kf = R.k, A = R.A, Bl = R.Bl, ref = R.ref;
   const bool nothing = R.S_row == 0.0;            // nothing but -inf: no distribution, no gradient
   // no weight: zeros, whatever the row holds
-  const bool none = nothing || (OP == kLogprob ? w_h == 0.0f && R.rho == 0.0 : w == 0.0f);
+  const bool none = nothing || (OP == kLogprob ? w_h == 0.0f && R.rho == 0.0 : w == 0.0f || R.empty);
   const bool away = R.away;
   T* dx = static_cast<T*>(a.dlogits) + (int64_t)r * a.dstride;
   const f2 c2 = pair(a.c, a.c), nk = pair(-kf, -kf), A2 = pair(A, A), B2 = pair(Bl, Bl);
@@ -820,6 +823,7 @@ struct Sums {
 template <class T, int NV>
 __device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& a) {
   constexpr int N = Elem<T>::N;
+  if (r.kind == kNan) return;
   float high = -INFINITY;
   bool nan = false;
   for (int u = 0; u < NV; ++u) {
@@ -831,7 +835,6 @@ __device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& 
       nan |= x[i] != x[i];
     }
   }
-  if (r.kind == kNan) return;
   const float top = warp_max(high), rc = top * a.c;
   if (top == INFINITY || __any_sync(kFull, nan)) {
     r.kind = kNan;
@@ -941,6 +944,8 @@ __device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs&
       r.gaps |= !gaps;
       return;
     }
+  } else if (r.kind == kNan) {
+    return;
   } else if (r.kind == kNone) {
     bool all = true;                              // nothing but -inf
 #pragma unroll
@@ -1012,6 +1017,7 @@ struct StreamShared {
   // the gradient's factors
   float k, A, Bl, ref;
   int away, none;
+  int empty;                                      // no entry in the list
   float g_target;                                 // the gradient at the target
 };
 
@@ -1219,6 +1225,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       arrive(&sh.gathered);
       if (OP != kTail && GRAD) mark();
       vmax = fmaxf(warp_max(vmax), kLowest);
+      bool any = false;
       double sum = 0.0;
       for (int j = lane; j < a.k; j += 32) {
         const int e = L.idx[j];
@@ -1226,9 +1233,12 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         const double q = exp(OP == kRenorm ? ((double)L.v[j] - (double)vmax) * (double)a.it : (double)L.v[j]);
         L.q[j] = q;
         sum += q;
+        any = true;
       }
       sum = warp_sum(sum);
+      any = __any_sync(kFull, any);
       if (lane == 0) {
+        sh.empty = !any;
         sh.w = w;
         sh.list_max = (double)vmax;
         sh.list_sum = sum;
@@ -1326,7 +1336,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
           sh.Bl = Bl;
           sh.ref = 0.0f;
           sh.away = 0;
-          sh.none = w == 0.0f && w_h == 0.0f;
+          sh.none = (w == 0.0f && w_h == 0.0f) || (LIST && sh.empty);
         }
         arrive(&sh.factors);
       }
@@ -1468,7 +1478,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         }
         if (lane == 0) {
           dense_factors(sh, ref, Sd, A, Bl, a);
-          sh.none = S_row == 0.0 || (w == 0.0f && w_h == 0.0f);
+          sh.none = S_row == 0.0 || (w == 0.0f && w_h == 0.0f) || (LIST && sh.empty);
         }
         arrive(&sh.factors);
       }
@@ -1486,7 +1496,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
         a.out[r] = Q == 0.0 ? 0.0f
                             : (float)(loss / sh.list_sum - log(sh.list_sum) + (S_row == 0.0 ? (double)INFINITY : log_s));
       } else {
-        if (Q == 0.0 && rho == 0.0) loss = 0.0;
+        if (sh.empty || (Q == 0.0 && rho == 0.0)) loss = 0.0;
         else if (S_row == 0.0) loss = Q != 0.0 ? (double)INFINITY : 0.0;
         else {
           loss += (Q + rho) * log_s;

@@ -475,7 +475,8 @@ int gsparse_token_logprobs_backward(const void* logits, int32_t dtype, int64_t r
  *   exp(teacher_val_j), and the mass the list leaves, rho = max(0, 1 - sum q), is one more class
  *   against R = the sum of p outside the list: loss = sum_j q_j (log q_j - log p_{i_j}) + rho (log
  *   rho - log R). Where no entry outside the list has p > 0 the rho term is dropped.
- * Entries with q = 0 add nothing; an empty list has loss 0 and gradient 0. Both are the
+ * Entries with q = 0 add nothing; a list without entries has loss 0 and gradient 0, whatever the row
+ * holds. Both are the
  * Kullback-Leibler divergence from the teacher, in nats, not multiplied by the temperature.
  *
  * loss     fp32[rows].

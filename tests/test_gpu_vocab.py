@@ -473,6 +473,25 @@ def test_distill_masks_and_lists(dtype, tail, times):
                   w=np.tile(np.linspace(0.5, 1.5, 10), times).astype(np.float32))
 
 
+@pytest.mark.parametrize("rows", [3, 400])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_empty_lists_give_zeros_whatever_the_row_holds(dtype, tail, rows):
+    """Padding: rows without a list and with anything for logits."""
+    x, _ = make(rows, 3000, dtype)
+    x[0] = float("nan")
+    x[1, 2999] = float("inf")
+    idx = np.full((rows, 5), -1, np.int32)
+    idx[2] = [4, 7, -1, 1, 2000]
+    ti, tv, w = dev(idx, torch.int32), dev(np.log(np.full((rows, 5), 0.1))), dev(np.ones(rows))
+    r = gs.distill_topk(x, ti, tv, tail=tail, want_grad=True, want_stats=True, grad_loss=w)
+    back = gs.distill_topk_backward(x, r.stats, ti, tv, w, tail=tail)
+    plain = gs.distill_topk(x, ti, tv, tail=tail)
+    empty = torch.arange(rows, device="cuda") != 2
+    for out in (r.loss, plain.loss, r.dlogits, back):
+        assert bool((out[empty] == 0).all()) and bool(torch.isfinite(out[2]).all()) and bool((out[2] != 0).any())
+
+
 def test_distill_bad_indices_are_reported_and_left_out():
     x, _ = make(2, 100, "fp32")
     val = dev(np.log([[0.5, 0.2, 0.1], [0.5, 0.2, 0.1]]))
