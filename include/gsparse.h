@@ -403,9 +403,9 @@ int gsparse_combine_local(const float* G, const float* L, float* out, int64_t n,
                           gsparse_stream stream);
 
 /* ---------------------------------------------------------------------------------------------
- * Losses over vocabulary rows  (no counterpart in the pages: these calls make the gradient of an
- * output layer over a vocabulary, which the calls above compress, and the (index, value) lists a
- * teacher sends)
+ * Losses over vocabulary rows  (no counterpart in the pages: these calls make the gradient of logits
+ * over a vocabulary, from which the caller's backward pass makes the parameters' gradients that the
+ * calls above compress, and the (index, value) lists a teacher sends)
  *
  * logits       [rows] rows of `vocab` entries of type dtype, entry v of row r at logits[r * row_stride
  *              + v]; any row_stride >= 0 (0: every row the same) and any alignment of the element.
@@ -418,11 +418,18 @@ int gsparse_combine_local(const float* G, const float* L, float* out, int64_t n,
  *              stride, must not overlap it otherwise. Rows of logits and dlogits that start at the
  *              same offset from a 16-byte boundary are fastest. A row whose incoming gradients are
  *              all zero gets zeros, whatever its logits hold.
- * Arithmetic: the exponential of fp32 differences and sums in fp32 within a thread, joined in fp64
- * in a fixed order: the same call on the same layout gives the same bits on every run, within a few
- * fp32 roundings of the formula (a gradient in 16 bits is rounded once). 1 <= vocab <= GSPARSE_MAX_VOCAB, 0 <= rows <
- * 2^26. inv_temperature from 2^-64 to 2^64. These calls need no workspace. A wait of a row's CTAs for one
- * another that gives up (about a second) raises GSPARSE_DERR_TIMEOUT; the results are then not valid.
+ * Finite logits of any size are served, masks of any finite value among them.
+ * Arithmetic: the hardware's 2^x of fp32 exponents; sums in fp32 over a warp's entries (up to 32 of a
+ * lane, then the lane's partial sums, then the lanes), the warps' sums joined in fp64, and results from
+ * them in fp64. The factors of the gradient in the same call are worked out from these sums in fp32 (in
+ * fp64 where |z| of a row's largest entries exceeds about 45000), the gradient at targets and lists in
+ * fp64. The sum of a row's exponentials, and with it a log probability, is within (26 + 4 log2 vocab +
+ * vocab / 3584) 2^-24 of the formula, next to its own rounding to fp32; the entropy within (2 + ln vocab)
+ * times that; a gradient p (A + B log p) has 3 |log2 p| 2^-24 more in p and is rounded once to its type.
+ * Sums in a fixed order: the same call on the same layout gives the same bits on every run.
+ * 1 <= vocab <= GSPARSE_MAX_VOCAB, 0 <= rows < 2^26. inv_temperature from 2^-64 to 2^64. These calls
+ * need no workspace. A wait of a row's CTAs for one another that gives up (about a second) raises
+ * GSPARSE_DERR_TIMEOUT; the results are then not valid.
  */
 enum gsparse_dtype { GSPARSE_F32 = 0, GSPARSE_BF16 = 1, GSPARSE_F16 = 2 };
 

@@ -547,8 +547,9 @@ MASKS = [-1e6, -1e7, -1e8, -1e9, -1e10, -1e11, -1e12, -1e15, -1e18, -1e20, -1e30
 
 
 def rounded_out(want, dtype):
-    """What rounding makes of gradients beyond the type's range: infinities (fp16: from 65520 on)."""
-    return np.where(np.abs(want) >= 65520.0, np.copysign(np.inf, want), want) if dtype == "fp16" else want
+    """What rounding makes of values beyond the type's range: infinities (fp16 from 65520 on, fp32 from 2^128 - 2^103)."""
+    end = 65520.0 if dtype == "fp16" else 2.0 ** 128 - 2.0 ** 103
+    return np.where(np.abs(want) >= end, np.copysign(np.inf, want), want)
 
 
 def check_all(x, dtype, temperature, targets, idx, val):
@@ -556,14 +557,25 @@ def check_all(x, dtype, temperature, targets, idx, val):
     rows, V = x.shape
     it = float(np.float32(1.0 / temperature))
     h = f64(x)
-    check_tokens(x, dtype, temperature, targets, top_k=4 if rows < 100 else 0, grad=False)
-    w, t = weights(rows), dev(targets, torch.int32)
+    w, t, k = weights(rows), dev(targets, torch.int32), 4 if rows < 100 else 0
+    r = gs.token_logprobs(x, t, top_k=k, want_entropy=True, temperature=temperature)
+    lp, ent, idx4, val4 = vocab.token_logprobs(h, it, targets, k)
+
+    def logs(want):
+        return lse_tol(V) + 4 * U * np.abs(np.where(np.isfinite(want), want, 0))
+
+    def losses(r):
+        close(r.logprob, rounded_out(lp, "fp32"), logs(lp), "logprob")
+        close(r.entropy, ent, lse_tol(V) * (2 + math.log(V + 1)) + U * np.abs(ent), "entropy")
+
+    losses(r)
+    if k:
+        assert np.array_equal(r.top_idx.cpu().numpy(), idx4)
+        close(r.top_logprob, rounded_out(val4, "fp32"), logs(val4), "top_logprob")
     kw = dict(grad_logprob=dev(w[0]), grad_entropy=dev(w[1]), temperature=temperature)
     r = gs.token_logprobs(x, t, want_entropy=True, want_stats=True, want_grad=True, **kw)
     back = gs.token_logprobs_backward(x, r.stats, t, entropy=r.entropy, **kw)
-    lp, ent, _, _ = vocab.token_logprobs(h, it, targets)
-    close(r.logprob, lp, lse_tol(V) + 4 * U * np.abs(np.where(np.isfinite(lp), lp, 0)), "logprob")
-    close(r.entropy, ent, lse_tol(V) * (2 + math.log(V + 1)) + U * np.abs(ent), "entropy")
+    losses(r)
     want = vocab.token_logprobs_grad(h, it, targets, w[0].astype(np.float64), w[1].astype(np.float64))
     want[(np.where(targets < 0, 0, w[0]) == 0) & (w[1] == 0)] = 0.0
     tol = grad_tol(h, it, want, dtype, it * (np.abs(w[0]) + np.abs(w[1]) * ent), it * w[1], it * w[0])
@@ -658,14 +670,16 @@ def test_entropy_of_rows_with_a_peak_far_above_what_came_before(dtype):
 @pytest.mark.parametrize("dtype,V,rows", [("bf16", 1000000, 300), ("fp32", 300000, 300), ("bf16", 1 << 24, 2)])
 def test_many_small_entries_beside_a_large_one(dtype, V, rows):
     """One entry of 1 and V - 1 entries e of 0.9 u (u = 2^-24): added one by one to 1 each of them would be lost, V / 448
-    of them in the sum that holds the 1. A chunk's entries are added up first: at most its own 16 are lost, and each of
-    the warp's V / 7168 chunks adds one rounding, u; then 2^q (4 u), the join of the lanes (6 u), the result (2 u)."""
+    of them in the sum that holds the 1. A chunk's entries are added up first (of 7 warps, 128 vectors of N entries each):
+    at most a lane's own 2 N there are lost, and each of the warp's V / (7 * 128 N) chunks adds one rounding, u; then
+    2^q (4 u), the join of the lanes (6 u), the result (2 u)."""
     peak = torch.tensor(-math.log(0.9 * U), device="cuda").to(TYPES[dtype])
     x = torch.zeros(rows, V, dtype=TYPES[dtype], device="cuda")
     at = dev(np.random.default_rng(12).integers(0, V, size=rows), torch.int32)
     x[torch.arange(rows, device="cuda"), at.long()] = peak
     e = math.exp(-float(peak))
-    tol = (16 + V / 7168 + 12) * U
+    N = 4 if dtype == "fp32" else 8
+    tol = (2 * N + V / (7 * 128 * N) + 12) * U
     one = torch.ones(rows, device="cuda")
     for r in (gs.token_logprobs(x, at, want_stats=True),
               gs.token_logprobs(x, at, want_stats=True, want_grad=True, grad_logprob=one)):
@@ -744,6 +758,27 @@ def test_teacher_to_student_to_compressed_gradient():
     down = float((dev(w) * (r.loss - after.loss)).sum())
     square = float((r.dlogits.double() ** 2).sum())
     assert 0.9 * step * square < down < 1.0 * step * square + 1e-6
+
+
+@pytest.mark.parametrize("temperature", [2.0 ** -64, 2.0 ** 64])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_temperatures_at_the_ends(dtype, temperature):
+    V = 9000
+    x, _ = make(8, V, dtype)
+    x[0] = 0.0
+    x[1, 5000:] = 1.0e38
+    x[2] = -1.0e38; x[2, 4500] = 3.0e38
+    x[3] = torch.linspace(1.0, 2.0, V, device="cuda").to(x.dtype) * 2.0 ** -63
+    x[4] = torch.linspace(-1.0, 1.0, V, device="cuda").to(x.dtype) * 2.0 ** 63
+    x[5, 100:] = float("-inf")
+    t = np.array([3, V - 1, 4500, V - 1, 0, 99, -1, 17])
+    if temperature < 1:                                    # (the losses of rows 1, 2 and 4 are beyond fp32)
+        with_losses = [0, 3, 5, 6, 7]
+        r = gs.token_logprobs(x, dev(t, torch.int32), top_k=1, want_entropy=True, temperature=temperature)
+        assert r.logprob[4].item() == -math.inf and r.top_idx[2].item() == 4500 and r.logprob[2].item() == 0.0
+        assert abs(r.entropy[4].item() - math.log((x[4] == x[4].max()).sum().item())) < 1e-6
+        x, t = x[with_losses].contiguous(), t[with_losses]
+    check_all(x, dtype, temperature, t, *some_lists(len(t), V))
 
 
 def test_streams_and_two_calls_at_once():
