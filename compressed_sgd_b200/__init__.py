@@ -562,7 +562,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     each row, the rows' entropy, and their top_k most likely tokens (largest first, ties to the lower
     index). `want_stats`: the row statistics that token_logprobs_backward takes. `want_grad` (or a
     `dlogits` to write to, which may be the logits): also the gradient of sum(grad_logprob * logprob)
-    + sum(grad_entropy * entropy) by the logits, laid out as the logits are."""
+    + sum(grad_entropy * entropy) by the logits, laid out as the logits are. Outside autograd: results are
+    detached, and logits.backward(dlogits) is the caller's to run."""
     rows, vocab, stride, dt = _logits(logits)
     dev = logits.device
     p_t = _like(targets, torch.int32, (rows,), dev, "targets")
@@ -628,7 +629,8 @@ def distill_topk(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_val: t
     """Loss of each row against a teacher's list of tokens (teacher_idx int32[rows, k], -1: absent):
     the divergence from the list's softmax at that temperature, or with `tail` from the list's log
     probabilities with the mass the list leaves as one more class. `want_grad` (or a `dlogits` to
-    write to, which may be the logits): also the gradient of sum(grad_loss * loss)."""
+    write to, which may be the logits): also the gradient of sum(grad_loss * loss). Outside autograd, as
+    token_logprobs."""
     rows, vocab, stride, dt = _logits(logits)
     dev = logits.device
     lists = _teacher(teacher_idx, teacher_val, rows, dev)

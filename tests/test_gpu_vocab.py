@@ -760,6 +760,47 @@ def test_teacher_to_student_to_compressed_gradient():
     assert 0.9 * step * square < down < 1.0 * step * square + 1e-6
 
 
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_the_output_layers_gradient_over_steps(dtype, pad):
+    """Three steps of a student: the gradient of its output layer, made from that of the logits, goes through the
+    residual top-k; what was sent and what is carried add up to the gradients of all steps."""
+    rows, V, D, k, T = 20, 1001, 16, 8, 2.0
+    rng = np.random.default_rng(21)
+    weight = dev(rng.normal(size=(V, D)) * 0.3).requires_grad_()
+    residual = torch.zeros(V * D, device="cuda")
+    sent, total = np.zeros(V * D), np.zeros(V * D)
+    w = np.full(rows, 1.0 / rows, np.float32)
+    for step in range(3):
+        hidden = dev(rng.normal(size=(rows, D)))
+        teacher, _ = make(rows, V, dtype, seed=50 + step, stride=V + pad)
+        top = gs.token_logprobs(teacher, top_k=k, temperature=T)
+        out = (hidden @ weight.t()).to(TYPES[dtype])
+        logits, _ = make(rows, V, dtype, stride=V + pad)      # rows of a padded buffer
+        logits.copy_(out.detach())
+        r = gs.distill_topk(logits, top.top_idx, top.top_logprob, tail=True, temperature=T, want_grad=True, grad_loss=dev(w))
+        assert r.dlogits.stride(0) == V + pad and not r.loss.requires_grad
+        grad = (r.dlogits.float().t() @ hidden).reshape(-1)
+        weight.grad = None
+        out.backward(r.dlogits)                               # the same through autograd: fp32 sums of 20 products
+        size = (r.dlogits.abs().double().t() @ hidden.abs().double()).reshape(-1)
+        assert bool(((grad - weight.grad.reshape(-1)).abs() <= 2 * (rows + 1) * U * size).all())
+        before = residual.clone()
+        idx, val, off = gs.residual_topk(grad, residual, (1, 100))
+        K = int(off[-1])
+        assert K == gs.k_for(V * D, (1, 100))
+        acc = before + grad
+        at = idx[:K].long()
+        assert torch.equal(val[:K], acc[at]) and bool((residual[at] == 0).all())
+        keep = torch.ones(V * D, dtype=torch.bool, device="cuda")
+        keep[at] = False
+        assert torch.equal(residual[keep], acc[keep])
+        sent[at.cpu().numpy()] += f64(val[:K])
+        total += f64(grad)
+    # two fp32 additions per place
+    assert np.abs(sent + f64(residual) - total).max() <= 2 * U * 3 * np.abs(total).max() + 1e-12
+
+
 @pytest.mark.parametrize("temperature", [2.0 ** -64, 2.0 ** 64])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_temperatures_at_the_ends(dtype, temperature):
