@@ -2,7 +2,8 @@
 // likely tokens, and distillation from a teacher's (index, value) list, each with the gradient of the
 // logits in the same call or as a pass of its own.
 //
-// With z = x * it (it = 1 / temperature), c = it * log2(e) and any reference m near the largest entry:
+// With z = x * it (it = 1 / temperature), c = it * log2(e) and any reference m, here at most 6.4 / c below the largest
+// entry:
 //   S = sum 2^((x - m) c),  T = sum 2^((x - m) c) (x - m) c,  p = 2^((x - m) c - log2 S),
 //   entropy = ln2 (log2 S - T / S),  log p_t = (x_t - m) it - ln S,
 // so one pass over a row gives everything but the gradient, and the gradient of either loss is p (A + B
@@ -10,8 +11,8 @@
 //
 // What bounds them: a read of the logits (and a write of the gradient) at 6.5 TB/s, and next to it the
 // exponential unit: one 2^x per entry and pass at 16 a clock and SM is 0.7 of the time that the bytes of
-// 16-bit logits take. So the inner loops are counted in instructions: 4.7 per entry for the sums, of which one
-// is the exponential.
+// 16-bit logits take. So the inner loops are counted in instructions: 6.4 per entry for the whole of a score with
+// entropy (1184 x 85000 bf16), of which one is the exponential.
 //
 // Two kernels: voc_stream_kernel (losses, with or without the gradient, alternatives) and
 // voc_backward_kernel (the gradient from saved statistics).
@@ -586,7 +587,7 @@ struct RowShared {
 __host__ __device__ __forceinline__ size_t ring_bytes(int threads) { return (size_t)threads / 32 * kStages * kChunk * 16; }
 
 // C CTAs take a row, each a slice, with nothing to tell each other. One read and one write per entry:
-// 4096 x 32000 fp32 in 156 us, 6.73 TB/s; through registers, without the rings, 187 us.
+// 4096 x 32000 fp32 in 157 us, 6.69 TB/s; through registers, without the rings, 187 us.
 template <class T, int OP>
 __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __grid_constant__ VocArgs a) {
   constexpr int N = Elem<T>::N, U = kUnroll;
@@ -982,12 +983,12 @@ template <int LEFT> __device__ __forceinline__ void copy_wait() {
 // C = 1 when there are rows enough to fill the GPU and no gradient.
 //
 // Sums alone: the next chunk's loads are in registers while one is worked on, 64 KB a SM on their way. Measured on
-// 4000 rows of 85000 bf16 (680 MB): 113 us, 6.0 TB/s, 0.92 of the measured copy bandwidth. A kernel that only
+// 4000 rows of 85000 bf16 (680 MB): 119 us, 5.7 TB/s, 0.87 of the measured copy bandwidth. A kernel that only
 // reads takes 95 us with such loads and 109 to 120 us with cp.async rings of 64 to 192 KB a SM; this one with bulk
 // or cp.async rings took 133 to 190 us.
 //
 // RES (with the gradient): the slice goes to shared memory and stays there between the sums and the gradient:
-// 288 us, 4.7 TB/s, 0.72. Reading it again from L2 instead costs half as much traffic again between L2 and the
+// 302 us, 4.5 TB/s, 0.69. Reading it again from L2 instead costs half as much traffic again between L2 and the
 // SMs (322 us), and more than about 60 MB of rows in flight no longer stay in L2. What is left is the chain of
 // a slice, about 9 us for 42 KB (loads 2, sums 3, join 1.5, gradient 2.5), of which four CTAs per SM hide two
 // thirds. Rows that eight slices of 200 KB cannot hold are read twice.
