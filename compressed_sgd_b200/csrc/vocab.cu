@@ -41,8 +41,8 @@ constexpr int kCand = 2048;                       // candidates for a row's alte
 constexpr float kLowest = -3.402823466e38f;       // the maximum of a row that holds nothing but -inf
 constexpr float kFarBits = 1.0e4f;                // 2^-10^4 = 0: where a sum weighs by the exponent it is
                                                   // clamped here, so that -inf logits add 0
-constexpr float kNearBits = 65536.0f;             // references m with |m c| up to here: exponents fma(x, c, -fl(m c)), which at
-                                                  // m itself is the rounding of fl(m c), at most 2^-8. Beyond: (x - m) c
+constexpr float kNearBits = 1048576.0f;           // references m with |m c| up to 2^20: exponents fma(x, c, -fl(m c)), which at
+                                                  // m itself is the rounding of fl(m c), at most 2^-5. Beyond: (x - m) c
 
 enum { kLogprob = 0, kRenorm = 1, kTail = 2 };    // what is computed
 enum { kForward = 0, kFused = 1, kBackward = 2 }; // loss; loss and gradient; gradient from saved statistics
@@ -803,6 +803,8 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
 
 // Sums over a lane's entries of e = 2^q and e q. The reference is the largest entry m of the first chunk in which
 // the warp finds one, near 0: q = fma(x, c, -rc), rc = fl(m c), the same for every entry; away from it: q = (x - m) c.
+// (4000 x 85000 bf16, scores and with the gradient: ordinary rows 111 and 268 us, rows away from 0 124 and 369: their
+// factors are worked out in 64 bits.)
 // Entries above it are added as they are until a chunk takes the sums T beyond kShiftAt, which moves it. Saves half an
 // instruction per entry against the running maximum. A chunk's entries are added up before they join s and t, so that a
 // large entry swallows those of its own chunk at most. All but s and t is the warp's.
@@ -819,45 +821,26 @@ struct Sums {
   bool gaps;              // -inf has been met (0 * -inf makes t NaN): exponents are clamped from there on
 };
 
-// What the fast sums cannot take: a first chunk or a reference away from 0, entries far above the reference, NaN. The
-// reference follows the chunk's largest entry; exponents are clamped.
-template <class T, int NV>
-__device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& a) {
-  constexpr int N = Elem<T>::N;
-  if (r.kind == kNan) return;
-  float high = -INFINITY;
-  bool nan = false;
-  for (int u = 0; u < NV; ++u) {
-    float x[N];
-    Elem<T>::unpack(v[u], x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      high = fmaxf(high, x[i]);
-      nan |= x[i] != x[i];
-    }
-  }
-  const float top = warp_max(high), rc = top * a.c;
-  if (top == INFINITY || __any_sync(kFull, nan)) {
-    r.kind = kNan;
-    return;
-  }
-  if (top == -INFINITY) return;
+// Moves the reference to a chunk's largest entry over the warp, from kNone too.
+__device__ __noinline__ Sums sums_move(Sums r, float top, float c) {
+  const float rc = top * c;
   const bool near = fabsf(rc) <= kNearBits;
   float down = 0.0f;                              // from the new reference to the old one
-  if (r.kind == kNone) {
+  if (top == INFINITY) {
+    r.kind = kNan;
+  } else if (r.kind == kNone) {
     r.kind = near ? kNear : kAway;
     r.ref = near ? rc : top;
   } else if (r.kind == kNear && rc > r.ref) {
-    down = near ? r.ref - rc : fmaf(-top, a.c, r.ref);
+    down = near ? r.ref - rc : fmaf(-top, c, r.ref);
     r.kind = near ? kNear : kAway;
     r.ref = near ? rc : top;
   } else if (r.kind == kAway && top > r.ref) {
-    down = (r.ref - top) * a.c;
+    down = (r.ref - top) * c;
+    r.ref = top;
     if (near && down < -kFarBits) {               // nothing is left of what was there
       r.kind = kNear;
       r.ref = rc;
-    } else {
-      r.ref = top;
     }
   }
   if (down < 0.0f) {
@@ -866,41 +849,17 @@ __device__ __noinline__ void sums_other(Sums& r, const uint4* v, const VocArgs& 
     r.t = mul2(fma2(r.s, pair(down, down), r.t), pair(f, f));
     r.s = mul2(r.s, pair(f, f));
   }
-  const bool away = r.kind == kAway;
-  f2 s = pair(0.0f, 0.0f), t = s;
-  for (int u = 0; u < NV; ++u) {
-    float x[N];
-    Elem<T>::unpack(v[u], x);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float q0 = max_nan(away ? (x[i] - r.ref) * a.c : fmaf(x[i], a.c, -r.ref), -kFarBits);
-      const float q1 = max_nan(away ? (x[i + 1] - r.ref) * a.c : fmaf(x[i + 1], a.c, -r.ref), -kFarBits);
-      const f2 e = pair(ex2(q0), ex2(q1));
-      s = add2(s, e);
-      t = fma2(e, pair(q0, q1), t);
-    }
-  }
-  r.s = add2(r.s, s);
-  r.t = add2(r.t, t);
+  return r;
 }
 
-// The call with copies: what it may touch must not live in registers' stead.
-template <class T, int NV>
-__device__ __forceinline__ void sums_call(Sums& r, const uint4* v, const VocArgs& a) {
-  Sums again = r;
-  uint4 w[NV];
-#pragma unroll
-  for (int u = 0; u < NV; ++u) w[u] = v[u];
-  sums_other<T, NV>(again, w, a);
-  r = again;
-}
-
-// Adds NV vectors to sums near 0; false, and nothing added, where that is not for these sums. Entry by entry: unpack, half a fused multiply-add, 2^q, half an addition, half a
-// fused multiply-add; GAPS: and a maximum.
-template <class T, int NV, bool GAPS>
-__device__ __forceinline__ bool sums_some(Sums& r, const uint4* v, const VocArgs& a) {
+// Adds NV vectors to the sums, unless a lane's T is then beyond kShiftAt or NaN; returns that T. FAST: references near 0, no
+// -inf: entry by entry unpack, half a fused multiply-add, 2^q, half an addition, half a fused multiply-add. Else half
+// an addition (the difference with a reference away from 0) and a maximum more.
+template <class T, int NV, bool FAST>
+__device__ __forceinline__ float sums_some(Sums& r, const uint4* v, float c) {
   constexpr int N = Elem<T>::N;
-  const f2 c2 = pair(a.c, a.c), nrc = pair(-r.ref, -r.ref);
+  const float m = r.kind == kAway ? r.ref : 0.0f, rc = r.kind == kAway ? 0.0f : r.ref;
+  const f2 c2 = pair(c, c), nrc = FAST ? pair(-r.ref, -r.ref) : pair(-rc, -rc), nm = pair(-m, -m);
   f2 s = pair(0.0f, 0.0f), t = s;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
@@ -908,10 +867,12 @@ __device__ __forceinline__ bool sums_some(Sums& r, const uint4* v, const VocArgs
     Elem<T>::unpack(v[u], x);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      f2 q = fma2(pair(x[i], x[i + 1]), c2, nrc);
+      f2 q = pair(x[i], x[i + 1]);
+      if (!FAST) q = add2(q, nm);
+      q = fma2(q, c2, nrc);
       float q0, q1;
       unpair(q, &q0, &q1);
-      if (GAPS) {
+      if (!FAST) {
         q0 = max_nan(q0, -kFarBits);
         q1 = max_nan(q1, -kFarBits);
         q = pair(q0, q1);
@@ -923,40 +884,56 @@ __device__ __forceinline__ bool sums_some(Sums& r, const uint4* v, const VocArgs
   }
   float t0, t1;
   unpair(t, &t0, &t1);
-  if (__any_sync(kFull, !(t0 + t1 < kShiftAt))) return false;
-  r.s = add2(r.s, s);
-  r.t = add2(r.t, t);
-  return true;
+  t0 += t1;
+  if (__all_sync(kFull, t0 < kShiftAt)) {
+    r.s = add2(r.s, s);
+    r.t = add2(r.t, t);
+    return 0.0f;
+  }
+  return __any_sync(kFull, t0 != t0) ? NAN : kShiftAt;
 }
 
-// Adds a chunk.
+// Adds a chunk; gaps: it may hold -inf.
 template <class T, int NV>
 __device__ __forceinline__ void sums_add(Sums& r, const uint4* v, const VocArgs& a, bool gaps = false) {
+  if (r.kind == kNan) return;
+  bool move = false;
   if (r.kind == kNone) {
-    const float rc = warp_max(Elem<T>::template high<NV>(v)) * a.c;
+    const float top = warp_max(Elem<T>::template high<NV>(v)), rc = top * a.c;
     if (fabsf(rc) <= kNearBits) {
       r.kind = kNear;
       r.ref = rc;
+    } else {
+      move = true;
+      if (!(top > -INFINITY)) {                   // -inf alone, or NaN
+        bool all = true;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          const uint32_t no = Elem<T>::nothing().x;
+          all = all && v[u].x == no && v[u].y == no && v[u].z == no && v[u].w == no;
+        }
+        if (!__all_sync(kFull, all)) r.kind = kNan;
+        return;
+      }
     }
   }
-  if (r.kind == kNear) {
-    if (!r.gaps && !gaps && sums_some<T, NV, false>(r, v, a)) return;
-    if (sums_some<T, NV, true>(r, v, a)) {
-      r.gaps |= !gaps;
+  if (r.kind == kNear && !r.gaps && !gaps) {
+    const float t = sums_some<T, NV, true>(r, v, a.c);
+    if (t == 0.0f) return;
+    move = t == t;
+    r.gaps = !move;
+  }
+  while (true) {                                  // from a chunk's largest entry its T is below kShiftAt: at most twice
+    if (move) r = sums_move(r, warp_max(Elem<T>::template high<NV>(v)), a.c);
+    if (r.kind == kNan) return;
+    const float t = sums_some<T, NV, false>(r, v, a.c);
+    if (t == 0.0f) return;
+    if (move || t != t) {
+      r.kind = kNan;
       return;
     }
-  } else if (r.kind == kNan) {
-    return;
-  } else if (r.kind == kNone) {
-    bool all = true;                              // nothing but -inf
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const uint32_t no = Elem<T>::nothing().x;
-      all = all && v[u].x == no && v[u].y == no && v[u].z == no && v[u].w == no;
-    }
-    if (__all_sync(kFull, all)) return;
+    move = true;
   }
-  sums_call<T, NV>(r, v, a);
 }
 
 // Reads a row's vector past L1. (Kept coherent: the gradient may take the logits' place.)
@@ -1275,22 +1252,22 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
 
     // -- the row's results in 64 bits ------------------------------------------------------------------
     wait(&sh.sums);
-    bool near = true;                             // GRAD: all parts have references near 0
+    bool near = true;                             // the row's parts have references near 0, or are nothing beside those that have
+    auto beside = [&](const float4& p, float rcm) { return __float_as_int(p.w) == kAway && !(p.x * a.c < rcm - 2.0f * kFarBits); };
     if constexpr (GRAD) {
       // What the gradient waits for, in fp32, the parts in a fixed order (by every warp for itself this took 1400
       // instructions per CTA)
       const int parts = C * W;
       const float4 p = lane < parts ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-      bool normal = __float_as_int(p.w) == kNear, other = __float_as_int(p.w) > kNear;
+      bool normal = __float_as_int(p.w) == kNear;
       float rcm = warp_max(normal ? p.x : -INFINITY);
       float4 p1 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
       if (parts > 32) {
         if (lane + 32 < parts) p1 = sh.part[lane + 32];
         normal |= __float_as_int(p1.w) == kNear;
-        other |= __float_as_int(p1.w) > kNear;
         rcm = fmaxf(rcm, warp_max(__float_as_int(p1.w) == kNear ? p1.x : -INFINITY));
       }
-      near = __any_sync(kFull, normal) && !__any_sync(kFull, other);
+      near = __any_sync(kFull, normal) && !__any_sync(kFull, beside(p, rcm) || (parts > 32 && beside(p1, rcm)));
       if (near) {
         float s = 0.0f, t = 0.0f;
         if (__float_as_int(p.w) == kNear) {
@@ -1345,15 +1322,15 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     float M = -INFINITY;                          // what the sums are taken from
     double Sd = 0.0, Td = 0.0;
     const int n_parts = C * W;
+    for (int q = lane; q < n_parts; q += 32)
+      if (__float_as_int(sh.part[q].w) == kNear) M = fmaxf(M, sh.part[q].x);
+    M = warp_max(M);
     if constexpr (!GRAD) {
-      const int k0 = lane < n_parts ? __float_as_int(sh.part[lane].w) : kNone;
-      const int k1 = lane + 32 < n_parts ? __float_as_int(sh.part[lane + 32].w) : kNone;
-      near = __any_sync(kFull, k0 == kNear || k1 == kNear) && !__any_sync(kFull, k0 > kNear || k1 > kNear);
+      bool other = false;
+      for (int q = lane; q < n_parts; q += 32) other |= beside(sh.part[q], M);
+      near = M > -INFINITY && !__any_sync(kFull, other);
     }
     if (near) {
-      for (int q = lane; q < n_parts; q += 32)
-        if (__float_as_int(sh.part[q].w) == kNear) M = fmaxf(M, sh.part[q].x);
-      M = warp_max(M);
       for (int q = lane; q < n_parts; q += 32) {
         const float4 p = sh.part[q];
         if (__float_as_int(p.w) != kNear) continue;
@@ -1372,6 +1349,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
       // the parts' references in bits, exact in 64 bits; the largest, and an entry at or near it
       auto bits = [&](const float4& p) { return __float_as_int(p.w) == kAway ? (double)p.x * (double)a.c : (double)p.x; };
       double high = -INFINITY;
+      M = -INFINITY;
       for (int q = lane; q < n_parts; q += 32) {
         const float4 p = sh.part[q];
         if (__float_as_int(p.w) == kNone || !(bits(p) > high)) continue;
@@ -1607,7 +1585,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, kRowCtas) voc_stream_ker
     v[0] = Elem<T>::pack(x);
 #pragma unroll
     for (int u = 1; u < U; ++u) v[u] = Elem<T>::nothing();
-    sums_call<T, U>(run, v, a);
+    sums_add<T, U>(run, v, a, true);
   }
   {                                               // the lanes' sums together, to the CTAs of the row
     float s0, s1, t0, t1;

@@ -422,7 +422,7 @@ int gsparse_combine_local(const float* G, const float* L, float* out, int64_t n,
  * Arithmetic: the hardware's 2^x of fp32 exponents; sums in fp32 over a warp's entries (up to 32 of a
  * lane, then the lane's partial sums, then the lanes), the warps' sums joined in fp64, and results from
  * them in fp64. The factors of the gradient in the same call are worked out from these sums in fp32 (in
- * fp64 where |z| of a row's largest entries exceeds about 45000), the gradient at targets and lists in
+ * fp64 where |z| of a row's largest entries exceeds about 700000), the gradient at targets and lists in
  * fp64. The sum of a row's exponentials, and with it a log probability, is within (26 + 4 log2 vocab +
  * vocab / 3584) 2^-24 of the formula, next to its own rounding to fp32; the entropy within (2 + ln vocab)
  * times that; a gradient p (A + B log p) has 3 |log2 p| 2^-24 more in p and is rounded once to its type.

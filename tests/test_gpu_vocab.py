@@ -627,10 +627,10 @@ def test_low_temperatures(dtype, temperature):
     check_all(x, dtype, temperature, t, *some_lists(12, V))
 
 
-@pytest.mark.parametrize("at", [45426.0, -45426.0, 3.0e6, -3.0e6])
+@pytest.mark.parametrize("at", [45426.0, -45426.0, 726817.0, -726817.0, 3.0e6, -3.0e6])
 @pytest.mark.parametrize("times", [1, 40])
 def test_references_on_both_sides_of_the_border(at, times):
-    """Logits around the size where the difference is taken first (2^16 bits) and beyond, spread as ordinary ones are."""
+    """Logits around the size where the difference is taken first (2^20 bits) and beyond, spread as ordinary ones are."""
     V = 9000
     x, _ = make(6, V, "fp32")
     x += at
@@ -844,6 +844,43 @@ def test_streams_and_two_calls_at_once():
     for s in range(2):
         assert torch.equal(got[s].loss, want[s].loss) and torch.equal(got[s].dlogits, want[s].dlogits)
         assert torch.equal(gtops[s].top_idx, tops[s].top_idx) and torch.equal(gtops[s].top_logprob, tops[s].top_logprob)
+
+
+@pytest.mark.parametrize("rows", [6, 330])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_far_references_in_the_logits_place_and_in_graphs(dtype, rows):
+    """Rows whose sums and gradient take the difference first: the gradient over the logits, captured and replayed."""
+    V, T = 9001, 1e-4                                     # (rows at every offset from 16 bytes)
+    x, _ = make(rows, V, dtype)
+    if dtype != "fp16":
+        x[0] = -1.0e12
+        x[1, :5000] = -1.0e12
+        x[2, 4000:] = 1.0e12
+    t = dev(np.arange(rows) % V, torch.int32)
+    idx, val = some_lists(rows, V)
+    ti, tv, w = dev(idx, torch.int32), dev(val), dev(np.full(rows, 1e-4))
+
+    def forms(x, place):
+        y = [x.clone() if place else None for _ in range(4)]
+        a = gs.token_logprobs(x if y[0] is None else y[0], t, want_entropy=True, want_stats=True, temperature=T, grad_logprob=w,
+                              grad_entropy=w, want_grad=True, dlogits=y[0])
+        b = gs.token_logprobs_backward(x if y[1] is None else y[1], a.stats, t, w, a.entropy, w, temperature=T, dlogits=y[1])
+        c = gs.distill_topk(x if y[2] is None else y[2], ti, tv, tail=True, temperature=T, grad_loss=w, want_grad=True,
+                            want_stats=True, dlogits=y[2])
+        d = gs.distill_topk_backward(x if y[3] is None else y[3], c.stats, ti, tv, w, tail=True, temperature=T, dlogits=y[3])
+        return [a.logprob, a.entropy, a.dlogits, b, c.loss, c.dlogits, d]
+
+    want = forms(x, False)
+    for u, v in zip(forms(x, True), want):
+        assert torch.equal(u, v) and not bool(torch.isnan(v).any())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = forms(x, False)
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(out, want):
+            assert torch.equal(u, v)
 
 
 def test_calls_of_two_threads():
