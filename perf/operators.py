@@ -297,8 +297,10 @@ def run(state):
         if op == "distill_loss":
             return {"loss": gs.distill_topk(state["logits"], state["idx"], state["val"], tail=case["tail"],
                                             temperature=case["temperature"]).loss}
-        return {"dlogits": gs.distill_topk_backward(state["logits"], state["stats"], state["idx"], state["val"],
-                                                    state["weight"], tail=case["tail"], temperature=case["temperature"])}
+        # the renormalised loss leaves the first two statistics of each row
+        stats = state["stats"] if case["tail"] else state["stats"][:, :2].contiguous()
+        return {"dlogits": gs.distill_topk_backward(state["logits"], stats, state["idx"], state["val"], state["weight"],
+                                                    tail=case["tail"], temperature=case["temperature"])}
     if op == "score":
         return _plain_rows(state, gradient=False)
     if op == "train":
