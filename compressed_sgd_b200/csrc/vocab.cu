@@ -11,7 +11,7 @@
 //
 // What bounds them: a read of the logits (and a write of the gradient) at 6.5 TB/s, and next to it the
 // exponential unit: one 2^x per entry and pass at 16 a clock and SM is 0.7 of the time that the bytes of
-// 16-bit logits take. So the inner loops are counted in instructions: 6.4 per entry for the whole of a score with
+// 16-bit logits take. So the inner loops are counted in instructions: 6.6 per entry for the whole of a score with
 // entropy (1184 x 85000 bf16), of which one is the exponential.
 //
 // Two kernels: voc_stream_kernel (losses, with or without the gradient, alternatives) and
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kVocThreads, 4) voc_backward_kernel(const __gr
 // NaN or +inf make the row NaN: nothing more is read of the warp's chunks.
 enum { kNone = 0, kNear = 1, kAway = 2, kNan = 3 };   // what there is (parts of a row: up to kAway)
 // An entry 6.4 bits above the reference moves it: T / S from a reference k bits below the row's largest entry has k
-// roundings, and the entropy log S - T / S may be next to nothing. (No slower than 2^60: 4000 x 85000 bf16 119 us.)
+// roundings, and the entropy log S - T / S may be next to nothing. (No slower than 2^60: 4000 x 85000 bf16 118 us.)
 constexpr float kShiftAt = 512.0f;
 
 struct Sums {
@@ -960,12 +960,12 @@ template <int LEFT> __device__ __forceinline__ void copy_wait() {
 // C = 1 when there are rows enough to fill the GPU and no gradient.
 //
 // Sums alone: the next chunk's loads are in registers while one is worked on, 64 KB a SM on their way. Measured on
-// 4000 rows of 85000 bf16 (680 MB): 119 us, 5.7 TB/s, 0.87 of the measured copy bandwidth. A kernel that only
+// 4000 rows of 85000 bf16 (680 MB): 118 us, 5.8 TB/s, 0.88 of the measured copy bandwidth. A kernel that only
 // reads takes 95 us with such loads and 109 to 120 us with cp.async rings of 64 to 192 KB a SM; this one with bulk
 // or cp.async rings took 133 to 190 us.
 //
 // RES (with the gradient): the slice goes to shared memory and stays there between the sums and the gradient:
-// 302 us, 4.5 TB/s, 0.69. Reading it again from L2 instead costs half as much traffic again between L2 and the
+// 303 us, 4.5 TB/s, 0.69. Reading it again from L2 instead costs half as much traffic again between L2 and the
 // SMs (322 us), and more than about 60 MB of rows in flight no longer stay in L2. What is left is the chain of
 // a slice, about 9 us for 42 KB (loads 2, sums 3, join 1.5, gradient 2.5), of which four CTAs per SM hide two
 // thirds. Rows that eight slices of 200 KB cannot hold are read twice.
