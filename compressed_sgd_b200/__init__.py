@@ -93,6 +93,22 @@ _SIGNATURES = {
                                             _vp, _i64, _vp, _vp, _vp]),
     "gsparse_distill_topk_backward": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _i32,
                                                      _i32, _vp, _vp, _i64, _vp, _vp]),
+    "gsparse_quantize_rows": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "gsparse_dequantize_rows": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "gsparse_rms_norm": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i64, _i64, _f32, _vp, _i64, _vp, _i64, _vp,
+                                        _i64, _vp, _vp, _vp]),
+    "gsparse_rms_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "gsparse_rms_norm_backward": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp,
+                                                 _i64, _vp, _vp, _sz, _vp]),
+    "gsparse_linear_q8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "gsparse_linear_q8": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _sz, _vp,
+                                         _vp]),
+    "gsparse_linear_q8_grad_input_workspace_size": (_sz, [_vp, _i32, _i64, _i64, _i64, _i64]),
+    "gsparse_linear_q8_grad_input": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _i64,
+                                                    _vp, _sz, _vp, _vp]),
+    "gsparse_linear_q8_grad_weight_workspace_size": (_sz, [_vp, _i32, _i64, _i64, _i64, _i64]),
+    "gsparse_linear_q8_grad_weight": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
+                                                     _sz, _vp, _vp]),
 }
 
 _lib = None
@@ -662,3 +678,225 @@ def distill_topk_backward(logits: torch.Tensor, stats: torch.Tensor, teacher_idx
     _on_device(dev, "gsparse_distill_topk_backward", logits.data_ptr(), dt, rows, vocab, stride, _inverse(temperature),
                p_st, *lists, int(tail), p_g, dlogits.data_ptr(), dlogits.stride(0), p_s)
     return dlogits
+
+
+# ---------------------------------------------------------------------------------------------
+# a layer in 8 bits
+
+MAX_DEPTH = 1 << 15
+MAX_NORM_DEPTH = 1 << 14
+
+
+class QuantRows(NamedTuple):
+    """Rows in 8 bits: q int8[rows, depth], whose rows start at multiples of 16 bytes, and a scale per row (fp32)."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+class RmsNorm(NamedTuple):
+    h: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    q: Optional[QuantRows]
+    rstd: Optional[torch.Tensor]
+
+
+class RmsNormGrad(NamedTuple):
+    dx: torch.Tensor
+    dweight: Optional[torch.Tensor]
+
+
+def _matrix(t: torch.Tensor, name, like: Optional[torch.Tensor] = None):
+    """(pointer, row stride) of a matrix with contiguous rows, of the type, shape and device of `like`."""
+    if t.dim() != 2 or not t.is_cuda or t.dtype not in _DTYPES or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise GsparseError(f"{name} must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
+    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.device != like.device):
+        raise GsparseError(f"{name} must be of type {like.dtype} and shape {tuple(like.shape)} on {like.device}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _quant(rows: QuantRows, name, device=None, depth=None):
+    """(q's pointer, q's row stride, scale's pointer, rows, depth)."""
+    q, scale = rows
+    if q.dim() != 2 or not q.is_cuda or q.dtype is not torch.int8 or (q.stride(1) != 1 and q.shape[1] > 1):
+        raise GsparseError(f"{name}.q must be a CUDA matrix of int8 with contiguous rows")
+    n, k = q.shape
+    if (device is not None and q.device != device) or (depth is not None and k != depth):
+        raise GsparseError(f"{name} must be rows of {depth} entries on {device}")
+    return q.data_ptr(), _row_step(q, 16), _like(scale, torch.float32, (n,), q.device, f"{name}.scale"), n, k
+
+
+def _row_step(t: torch.Tensor, unit: int) -> int:
+    """The row stride; of a single row, whose stride says nothing, the next multiple of `unit`."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
+
+
+def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype) -> torch.Tensor:
+    """A new matrix whose rows start at multiples of 16 bytes."""
+    unit = 16 // dtype.itemsize
+    stride = -(-cols // unit) * unit
+    t = torch.empty((rows, stride), dtype=dtype, device=like.device)
+    return t if stride == cols else t[:, :cols]
+
+
+def _new_quant(like: torch.Tensor) -> QuantRows:
+    rows, depth = like.shape
+    return QuantRows(_aligned_rows(like, rows, depth, torch.int8), like.new_empty(rows, dtype=torch.float32))
+
+
+def _dtype_code(dtype) -> int:
+    if dtype not in _DTYPES:
+        raise GsparseError("the type must be fp32, bf16 or fp16")
+    return _DTYPES[dtype]
+
+
+def quantize_rows(x: torch.Tensor, out: Optional[QuantRows] = None) -> QuantRows:
+    """The rows of x in 8 bits, each with a power of two as its scale: an activation checkpoint, or weights by channel."""
+    p, stride = _matrix(x, "x")
+    if out is None:
+        out = _new_quant(x)
+    q, qs, scale, rows, depth = _quant(out, "out", x.device, x.shape[1])
+    if rows != x.shape[0]:
+        raise GsparseError(f"out must hold {x.shape[0]} rows")
+    _on_device(x.device, "gsparse_quantize_rows", p, _DTYPES[x.dtype], rows, depth, stride, q, qs, scale)
+    return out
+
+
+def dequantize_rows(rows: QuantRows, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that rows in 8 bits stand for; bf16 holds those of quantize_rows and rms_norm exactly."""
+    q, qs, scale, n, depth = _quant(rows, "rows")
+    if out is None:
+        out = torch.empty((n, depth), dtype=dtype, device=rows.q.device)
+    p, stride = _matrix(out, "out")
+    if out.shape != rows.q.shape or out.device != rows.q.device:
+        raise GsparseError(f"out must be of shape {tuple(rows.q.shape)} on {rows.q.device}")
+    _on_device(out.device, "gsparse_dequantize_rows", q, qs, scale, n, depth, p, _DTYPES[out.dtype], stride)
+    return out
+
+
+def _norm_weight(weight, depth, device):
+    _dtype_code(weight.dtype)
+    return _like(weight, weight.dtype, (depth,), device, "weight"), _DTYPES[weight.dtype]
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             want_y: bool = False, want_q: bool = False, want_rstd: bool = False, h: Optional[torch.Tensor] = None,
+             q: Optional[QuantRows] = None) -> RmsNorm:
+    """h = x + residual and its root-mean-square norm y = h / sqrt(mean(h^2) + eps) * weight, as y in x's type
+    (`want_y`) or in 8 bits (`want_q`, or `q` to write to), in one pass. `h` may be x or residual itself; without a
+    residual the returned h is x. `want_rstd`: what rms_norm_backward takes. Outside autograd."""
+    p_x, s_x = _matrix(x, "x")
+    rows, depth = x.shape
+    dev = x.device
+    p_r, s_r = (None, 0) if residual is None else _matrix(residual, "residual", x)
+    p_w, wt = _norm_weight(weight, depth, dev)
+    if h is None and residual is not None:
+        h = torch.empty((rows, depth), dtype=x.dtype, device=dev)
+    p_h, s_h = (None, 0) if h is None else _matrix(h, "h", x)
+    y = torch.empty((rows, depth), dtype=x.dtype, device=dev) if want_y else None
+    if q is None and want_q:
+        q = _new_quant(x)
+    p_q, s_q, p_s = None, 0, None
+    if q is not None:
+        p_q, s_q, p_s, n, _ = _quant(q, "q", dev, depth)
+        if n != rows:
+            raise GsparseError(f"q must hold {rows} rows")
+    rstd = x.new_empty(rows, dtype=torch.float32) if want_rstd else None
+    _on_device(dev, "gsparse_rms_norm", p_x, s_x, p_r, s_r, p_w, wt, _DTYPES[x.dtype], rows, depth, eps, p_h, s_h, _ptr(y), depth,
+               p_q, s_q, p_s, _ptr(rstd))
+    return RmsNorm(x if h is None else h, y, q, rstd)
+
+
+def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor,
+                      dh: Optional[torch.Tensor] = None, want_dweight: bool = True, dx: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> RmsNormGrad:
+    """The gradients of rms_norm by h (that is by x and by residual) and by the weight (fp32), from the gradient dy at its
+    output and dh, what reaches h on other ways. dx may be h, dy or dh itself."""
+    p_h, s_h = _matrix(h, "h")
+    rows, depth = h.shape
+    dev = h.device
+    p_w, wt = _norm_weight(weight, depth, dev)
+    p_r = _like(rstd, torch.float32, (rows,), dev, "rstd")
+    p_y, s_y = _matrix(dy, "dy", h)
+    p_d, s_d = (None, 0) if dh is None else _matrix(dh, "dh", h)
+    if dx is None:
+        dx = torch.empty((rows, depth), dtype=h.dtype, device=dev)
+    p_x, s_x = _matrix(dx, "dx", h)
+    dweight = None
+    if want_dweight:
+        dweight = h.new_empty(depth, dtype=torch.float32)
+        if workspace is None:
+            workspace = _workspace(lib().gsparse_rms_norm_backward_workspace_size(rows, depth), dev)
+    _on_device(dev, "gsparse_rms_norm_backward", p_h, s_h, p_w, wt, p_r, p_y, s_y, p_d, s_d, _DTYPES[h.dtype], rows, depth, p_x, s_x,
+               _ptr(dweight), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return RmsNormGrad(dx, dweight)
+
+
+def linear_q8(x: QuantRows, w: QuantRows, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, d_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t, n] = x.scale[t] w.scale[n] sum_k x.q[t, k] w.q[n, k]: a layer's product in 8-bit integers, exact up to the
+    rounding of the result. Rows of an `out` that is made here start at multiples of 16 bytes: where channels is no
+    multiple of that, it is a view whose stride(0) is larger, as token_logprobs and distill_topk take it."""
+    p_x, s_x, c_x, tokens, depth = _quant(x, "x")
+    dev = x.q.device
+    p_w, s_w, c_w, channels, _ = _quant(w, "w", dev, depth)
+    if out is None:
+        _dtype_code(dtype)
+        out = _aligned_rows(x.q, tokens, channels, dtype)
+    p_o, s_o = _matrix(out, "out")
+    if out.shape != (tokens, channels) or out.device != dev:
+        raise GsparseError(f"out must be of shape {(tokens, channels)} on {dev}")
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    if workspace is None:
+        workspace = _workspace(lib().gsparse_linear_q8_workspace_size(tokens, channels, depth), dev)
+    _on_device(dev, "gsparse_linear_q8", p_x, s_x, c_x, p_w, s_w, c_w, tokens, channels, depth, p_o, _DTYPES[out.dtype], s_o,
+               workspace.data_ptr(), workspace.numel(), p_s)
+    return out
+
+
+def linear_q8_grad_input(dout: torch.Tensor, w: QuantRows, dtype=None, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, d_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx[t, k] = sum_n dout[t, n] w.scale[n] w.q[n, k], in dout's type or `dtype`."""
+    p_g, s_g = _matrix(dout, "dout")
+    dev = dout.device
+    tokens, channels = dout.shape
+    p_w, s_w, c_w, n, depth = _quant(w, "w", dev)
+    if n != channels:
+        raise GsparseError(f"w must hold {channels} rows")
+    if out is None:
+        dtype = dout.dtype if dtype is None else dtype
+        _dtype_code(dtype)
+        out = torch.empty((tokens, depth), dtype=dtype, device=dev)
+    p_o, s_o = _matrix(out, "out")
+    if out.shape != (tokens, depth) or out.device != dev:
+        raise GsparseError(f"out must be of shape {(tokens, depth)} on {dev}")
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    dt = _DTYPES[dout.dtype]
+    if workspace is None:
+        workspace = _workspace(lib().gsparse_linear_q8_grad_input_workspace_size(p_g, dt, s_g, tokens, channels, depth), dev)
+    _on_device(dev, "gsparse_linear_q8_grad_input", p_g, dt, s_g, p_w, s_w, c_w, tokens, channels, depth, p_o, _DTYPES[out.dtype],
+               s_o, workspace.data_ptr(), workspace.numel(), p_s)
+    return out
+
+
+def linear_q8_grad_weight(dout: torch.Tensor, x: QuantRows, out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, d_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dweight[n, k] = sum_t dout[t, n] x.scale[t] x.q[t, k] in fp32, from the activations kept in 8 bits: what
+    residual_topk takes, as it is (out.reshape(-1): place i is the same weight in every step)."""
+    p_g, s_g = _matrix(dout, "dout")
+    dev = dout.device
+    tokens, channels = dout.shape
+    p_x, s_x, c_x, n, depth = _quant(x, "x", dev)
+    if n != tokens:
+        raise GsparseError(f"x must hold {tokens} rows")
+    if out is None:
+        out = torch.empty((channels, depth), dtype=torch.float32, device=dev)
+    p_o, s_o = _matrix(out, "out")
+    if out.shape != (channels, depth) or out.device != dev or out.dtype is not torch.float32:
+        raise GsparseError(f"out must be fp32 of shape {(channels, depth)} on {dev}")
+    p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
+    dt = _DTYPES[dout.dtype]
+    if workspace is None:
+        workspace = _workspace(lib().gsparse_linear_q8_grad_weight_workspace_size(p_g, dt, s_g, tokens, channels, depth), dev)
+    _on_device(dev, "gsparse_linear_q8_grad_weight", p_g, dt, s_g, p_x, s_x, c_x, tokens, channels, depth, p_o, s_o,
+               workspace.data_ptr(), workspace.numel(), p_s)
+    return out

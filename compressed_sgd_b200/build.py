@@ -22,6 +22,7 @@ NVCC_FLAGS = [
     "-fmad=false",               # every fp32 multiply and add is its own IEEE operation
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
+    "--threads", "0",            # the sources beside one another
 ]
 
 

@@ -1,0 +1,601 @@
+// Rows in 8 bits with one scale each, the root-mean-square norm that writes them, and its gradient.
+//
+// A row's scale is a power of two, 2^e with the smallest e from -126 to 121 for which no entry exceeds 127 * 2^e: the value q * 2^e has
+// seven bits, so bf16 holds it exactly and the products that read it (linear8.cu) lose nothing to a conversion. Against a
+// scale of max / 127 the step is up to twice as wide, 1.44 times on average.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "common.cuh"
+
+namespace gs {
+namespace {
+
+constexpr int kRowsPerBlock = 4;     // rows of a block whose rows take one warp each
+constexpr int kMostThreads = 1024;
+
+template <class T> struct Type;
+template <> struct Type<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <> struct Type<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Type<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+
+// A thread's E entries of a row of `depth`: with VEC as vectors of 16 bytes, thread after thread; else entry by entry, thread
+// after thread, so that rows of any alignment are read in whole lines too.
+template <class T, bool VEC, int E>
+struct Mine {
+  static constexpr int N = VEC ? Type<T>::N : 1;
+  static __device__ __forceinline__ int first(int j, int tid, int threads) { return (j * threads + tid) * N; }
+
+  static __device__ __forceinline__ void load(float (&v)[E], const T* row, int depth, int tid, int threads) {
+#pragma unroll
+    for (int j = 0; j < E / N; ++j) {
+      const int at = first(j, tid, threads);
+      if constexpr (VEC) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (at < depth) raw = *reinterpret_cast<const uint4*>(row + at);
+        const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[j * N + i] = Type<T>::get(e[i]);
+      } else {
+        v[j] = at < depth ? Type<T>::get(row[at]) : 0.0f;
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void store(T* row, const float (&v)[E], int depth, int tid, int threads) {
+#pragma unroll
+    for (int j = 0; j < E / N; ++j) {
+      const int at = first(j, tid, threads);
+      if (at >= depth) continue;
+      if constexpr (VEC) {
+        uint4 raw;
+        T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = Type<T>::put(v[j * N + i]);
+        *reinterpret_cast<uint4*>(row + at) = raw;
+      } else {
+        row[at] = Type<T>::put(v[j]);
+      }
+    }
+  }
+
+  // N entries of 16 bits; with VEC they start at a multiple of their own size.
+  template <class W>
+  static __device__ __forceinline__ void narrow(float* v, const W* w) {
+    W e[N];
+    if constexpr (N == 8) *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(w));
+    else if constexpr (N == 4) *reinterpret_cast<uint2*>(e) = __ldg(reinterpret_cast<const uint2*>(w));
+    else e[0] = *w;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = Type<W>::get(e[i]);
+  }
+
+  // Entries of fp32, bf16 or fp16, whatever T is (the norm's weight).
+  static __device__ __forceinline__ void load_any(float (&v)[E], const void* p, int dtype, int depth, int tid, int threads) {
+#pragma unroll
+    for (int j = 0; j < E / N; ++j) {
+      const int at = first(j, tid, threads);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[j * N + i] = 0.0f;
+      if (at >= depth) continue;
+      if (dtype == GSPARSE_F32) {
+        const float* w = static_cast<const float*>(p) + at;
+        if constexpr (N >= 4) {
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(w + i));
+            v[j * N + i] = f.x; v[j * N + i + 1] = f.y; v[j * N + i + 2] = f.z; v[j * N + i + 3] = f.w;
+          }
+        } else {
+          v[j] = *w;
+        }
+      } else if (dtype == GSPARSE_BF16) {
+        narrow(&v[j * N], static_cast<const __nv_bfloat16*>(p) + at);
+      } else {
+        narrow(&v[j * N], static_cast<const __half*>(p) + at);
+      }
+    }
+  }
+};
+
+struct RowArgs {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* h;
+  void* y;
+  int8_t* q;
+  float* scale;
+  float* rstd;
+  int64_t rows, x_stride, residual_stride, h_stride, y_stride, q_stride;
+  int depth, weight_dtype, warps;   // warps of a row
+  float eps;
+};
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); }
+
+// The exponent of the scale of a row whose largest magnitude has these (finite) bits.
+__device__ __forceinline__ int scale_exponent(uint32_t top) {
+  // top = m 2^(k - 127) with 1 <= m < 2: 127 / 64 is the border of m. What is below 2^-119 takes the smallest scale.
+  const int k = (int)(top >> 23);
+  const int e = k - 127 - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return e < -126 ? -126 : e > 121 ? 121 : e;     // 121: 64 * 2^122 is no fp32 number
+}
+
+template <bool NORM>
+struct Scaled {
+  float hi, lo;
+  // y = v r w as a sum hi + lo that is good to about 2^-46, so that an entry next to a border between two steps of the 8
+  // bits falls on the side that the formula says.
+  __device__ __forceinline__ Scaled(float v, float r_hi, float r_lo, float w) {
+    if constexpr (NORM) {
+      const float rw = __fmul_rn(r_hi, w);
+      const float rw_lo = __fmaf_rn(r_hi, w, -rw) + r_lo * w;
+      hi = __fmul_rn(v, rw);
+      lo = __fmaf_rn(v, rw, -hi) + v * rw_lo;
+    } else {
+      hi = v;
+      lo = 0.0f;
+    }
+  }
+};
+
+// One pass over the rows: the sum with the residual, the norm, the 8 bits. A row stays in its threads' registers.
+template <class T, bool VEC, int E, bool NORM, int MOST>
+__global__ void __launch_bounds__(MOST) rows_kernel(const __grid_constant__ RowArgs a) {
+  pdl_begin();
+  __shared__ double sums[kMostThreads / 32];
+  __shared__ uint32_t tops[kMostThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool one = a.warps == 1;
+  const int64_t row = one ? (int64_t)blockIdx.x * kRowsPerBlock + warp : blockIdx.x;
+  if (row >= a.rows) return;                       // whole warps, and only where no barrier follows
+  const int tid = one ? lane : threadIdx.x, threads = a.warps * 32, depth = a.depth;
+  using M = Mine<T, VEC, E>;
+  float v[E];
+  M::load(v, static_cast<const T*>(a.x) + row * a.x_stride, depth, tid, threads);
+  if constexpr (NORM) {
+    if (a.residual) {
+      float r[E];
+      M::load(r, static_cast<const T*>(a.residual) + row * a.residual_stride, depth, tid, threads);
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = Type<T>::get(Type<T>::put(v[i] + r[i]));
+    }
+    if (a.h) M::store(static_cast<T*>(a.h) + row * a.h_stride, v, depth, tid, threads);
+  }
+  float r_hi = 1.0f, r_lo = 0.0f;
+  float w[NORM ? E : 1];
+  if constexpr (NORM) {
+    M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+    // squares of any size, and a sum that is good to the last of them: 64 bits
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = __fma_rn((double)v[i], (double)v[i], ss);
+    ss = warp_sum(ss);
+    if (!one) {
+      if (lane == 0) sums[warp] = ss;
+      __syncthreads();
+      ss = lane < a.warps ? sums[lane] : 0.0;
+      ss = warp_sum(ss);
+    }
+    const double r = 1.0 / sqrt(ss / (double)depth + (double)a.eps);
+    r_hi = (float)r;
+    r_lo = (float)(r - (double)r_hi);
+    if (a.rstd && tid == 0) a.rstd[row] = r_hi;
+    if (a.y) {
+      float y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const Scaled<NORM> s(v[i], r_hi, r_lo, w[i]);
+        y[i] = s.hi + s.lo;
+      }
+      M::store(static_cast<T*>(a.y) + row * a.y_stride, y, depth, tid, threads);
+    }
+    if (!a.q) return;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) top = max(top, mag_key(Scaled<NORM>(v[i], r_hi, r_lo, NORM ? w[i] : 1.0f).hi));
+  top = __reduce_max_sync(kFull, top);
+  if (!one) {
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(kFull, lane < a.warps ? tops[lane] : 0u);
+  }
+  const bool fine = top < 0x7f800000u;             // no infinity, no NaN
+  const int e = fine ? scale_exponent(top) : 0;
+  const float up = power(-e);                      // -121 <= -e <= 126
+  if (tid == 0) a.scale[row] = fine ? power(e) : __int_as_float(0x7fc00000);
+  int8_t* out = a.q + row * a.q_stride;
+#pragma unroll
+  for (int j = 0; j < E / M::N; ++j) {
+    uint32_t packed[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < M::N; ++i) {
+      const int k = j * M::N + i;
+      const Scaled<NORM> s(v[k], r_hi, r_lo, NORM ? w[k] : 1.0f);
+      const float t = s.hi * up;
+      float n = rintf(t);
+      if constexpr (NORM) {
+        const float d = (t - n) + s.lo * up;       // the first difference is exact
+        n += d > 0.5f ? 1.0f : d < -0.5f ? -1.0f : 0.0f;
+      }
+      const int q = fine ? max(-127, min(127, (int)n)) : 0;
+      packed[i / 4] |= (uint32_t)(q & 0xff) << (8 * (i % 4));
+    }
+    const int at = M::first(j, tid, threads);
+    if (at >= depth) continue;
+    if constexpr (M::N == 8) *reinterpret_cast<uint2*>(out + at) = make_uint2(packed[0], packed[1]);
+    else if constexpr (M::N == 4) *reinterpret_cast<uint32_t*>(out + at) = packed[0];
+    else out[at] = (int8_t)packed[0];
+  }
+}
+
+// ---- read back ------------------------------------------------------------------------------------------
+
+// 16 entries a thread.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int depth,
+                                                      T* out, int64_t out_stride) {
+  pdl_begin();
+  const int64_t per = (depth + 15) / 16, all = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / per;
+    const int at = (int)(i - row * per) * 16;
+    const float s = __ldg(scale + row);
+    const int8_t* p = q + row * q_stride + at;
+    T* o = out + row * out_stride + at;
+    const int left = depth - at;
+    T v[16];
+    if (left >= 16) {
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
+      const int8_t* b = reinterpret_cast<const int8_t*>(&raw);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = Type<T>::put((float)b[k] * s);
+      if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < 16; k += Type<T>::N) *reinterpret_cast<uint4*>(o + k) = *reinterpret_cast<const uint4*>(v + k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = v[k];
+      }
+    } else {
+      for (int k = 0; k < left; ++k) o[k] = Type<T>::put((float)p[k] * s);
+    }
+  }
+}
+
+// ---- the norm's gradient ---------------------------------------------------------------------------------
+
+struct BackArgs {
+  const void* h;
+  const void* dy;
+  const void* dh;
+  const void* weight;
+  const float* rstd;
+  void* dx;
+  float* partial;                   // fp32[blocks][depth]
+  int64_t rows, h_stride, dy_stride, dh_stride, dx_stride;
+  int depth, weight_dtype, warps, groups;   // warps of a row; rows in flight of a block
+};
+
+// With xh = h r and g = dy w: dx = r (g - xh mean(g xh)) + dh, dw = sum over the rows of dy xh. A thread keeps its places'
+// weights and its sum of dw in registers over all the rows of its group.
+template <class T, bool VEC, int E, int MOST>
+__global__ void __launch_bounds__(MOST) norm_back_kernel(const __grid_constant__ BackArgs a) {
+  pdl_begin();
+  extern __shared__ float shared[];                // of groups > 1: [groups][depth]
+  __shared__ float sums[2][kMostThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool one = a.warps == 1;
+  const int tid = one ? lane : threadIdx.x, threads = a.warps * 32, depth = a.depth;
+  const int group = one ? warp : 0;
+  using M = Mine<T, VEC, E>;
+  float w[E], dw[E];
+  M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = 0.0f;
+  const float inv = 1.0f / (float)depth;
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * a.groups + group; row < a.rows; row += (int64_t)gridDim.x * a.groups, turn ^= 1) {
+    float h[E], g[E];
+    M::load(h, static_cast<const T*>(a.h) + row * a.h_stride, depth, tid, threads);
+    M::load(g, static_cast<const T*>(a.dy) + row * a.dy_stride, depth, tid, threads);
+    const float r = __ldg(a.rstd + row);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      h[i] *= r;
+      dw[i] = __fmaf_rn(g[i], h[i], dw[i]);
+      g[i] *= w[i];
+      s = __fmaf_rn(g[i], h[i], s);
+    }
+    s = warp_sum(s);
+    if (!one) {
+      if (lane == 0) sums[turn][warp] = s;
+      __syncthreads();                             // the other half is free: all have read it before they came here
+      s = warp_sum(lane < a.warps ? sums[turn][lane] : 0.0f);
+    }
+    s *= inv;
+#pragma unroll
+    for (int i = 0; i < E; ++i) g[i] = r * __fmaf_rn(-h[i], s, g[i]);
+    if (a.dh) {
+      M::load(h, static_cast<const T*>(a.dh) + row * a.dh_stride, depth, tid, threads);
+#pragma unroll
+      for (int i = 0; i < E; ++i) g[i] += h[i];
+    }
+    M::store(static_cast<T*>(a.dx) + row * a.dx_stride, g, depth, tid, threads);
+  }
+  if (!a.partial) return;
+  float* to = a.partial + (int64_t)blockIdx.x * depth;
+  if (one) {
+#pragma unroll
+    for (int j = 0; j < E / M::N; ++j)
+#pragma unroll
+      for (int i = 0; i < M::N; ++i) {
+        const int at = M::first(j, tid, threads) + i;
+        if (at < depth) shared[group * depth + at] = dw[j * M::N + i];
+      }
+    __syncthreads();
+    for (int at = threadIdx.x; at < depth; at += blockDim.x) {
+      float s = 0.0f;
+      for (int k = 0; k < a.groups; ++k) s += shared[k * depth + at];
+      to[at] = s;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < E / M::N; ++j)
+#pragma unroll
+      for (int i = 0; i < M::N; ++i) {
+        const int at = M::first(j, tid, threads) + i;
+        if (at < depth) to[at] = dw[j * M::N + i];
+      }
+  }
+}
+
+// dw = the blocks' sums, in a fixed order: 32 columns a block, 32 parts of the list of blocks each.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* partial, int blocks, int depth, float* dweight) {
+  pdl_begin();
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (at < depth)
+    for (int b = warp; b < blocks; b += 32) s += __ldg(partial + (int64_t)b * depth + at);
+  part[warp][lane] = s;
+  __syncthreads();
+  s = warp_sum(part[lane][warp]);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < depth) dweight[col] = s;
+}
+
+// ---- launches ---------------------------------------------------------------------------------------------
+
+bool known(int32_t t) { return t == GSPARSE_F32 || t == GSPARSE_BF16 || t == GSPARSE_F16; }
+size_t size_of(int32_t t) { return t == GSPARSE_F32 ? 4 : 2; }
+bool at_multiple(const void* p, size_t of) { return (reinterpret_cast<uintptr_t>(p) % of) == 0; }
+
+// Whether rows at p, `stride` entries apart, all start at 16-byte boundaries.
+bool even(const void* p, int64_t stride, int32_t dtype) {
+  return !p || (aligned16(p) && (stride * (int64_t)size_of(dtype)) % 16 == 0);
+}
+
+int rows_sizes(int32_t dtype, int64_t rows, int64_t depth, int64_t most = GSPARSE_MAX_NORM_DEPTH) {
+  if (!known(dtype) || rows < 0 || depth < 1) return GSPARSE_ERR_INVALID_ARG;
+  if (rows > GSPARSE_MAX_ROWS || depth > most) return GSPARSE_ERR_UNSUPPORTED;
+  return GSPARSE_OK;
+}
+
+// A matrix argument: present, its entries aligned, and where `write`, its rows apart.
+bool matrix(const void* p, int64_t stride, int32_t dtype, int64_t rows, int64_t depth, bool write) {
+  return p && at_multiple(p, size_of(dtype)) && stride >= (write && rows > 1 ? depth : 0);
+}
+
+// Warps of a row and entries a thread: one warp while 16 entries a lane hold the row, then 16 entries a thread; the longest rows
+// in 8 bits without a norm, 32 (more in registers with a norm's weights beside them would spill).
+struct Shape { int warps, entries; };
+Shape shape_of(int64_t depth) {
+  if (depth <= 512) return {1, depth <= 256 ? 8 : 16};
+  const int e = depth <= GSPARSE_MAX_NORM_DEPTH ? 16 : 32;
+  return {(int)cdiv(depth, 32 * e), e};
+}
+
+template <class T, bool VEC, bool NORM>
+void rows_of(const RowArgs& a, const Shape& s, cudaStream_t st) {
+  const dim3 grid((unsigned)(s.warps == 1 ? cdiv(a.rows, kRowsPerBlock) : a.rows)), block(s.warps == 1 ? kRowsPerBlock * 32 : s.warps * 32);
+  if (s.entries == 8) launch(rows_kernel<T, VEC, 8, NORM, 512>, grid, block, 0, st, a);
+  else if (s.entries == 16 && s.warps <= 16) launch(rows_kernel<T, VEC, 16, NORM, 512>, grid, block, 0, st, a);
+  else if (s.entries == 16) launch(rows_kernel<T, VEC, 16, NORM, 1024>, grid, block, 0, st, a);
+  else if constexpr (!NORM) launch(rows_kernel<T, VEC, 32, NORM, 1024>, grid, block, 0, st, a);
+}
+
+template <bool NORM>
+int rows_by_type(int32_t dtype, const RowArgs& a, bool vec, cudaStream_t st) {
+  const Shape s{a.warps, shape_of(a.depth).entries};
+  if (dtype == GSPARSE_F32) vec ? rows_of<float, true, NORM>(a, s, st) : rows_of<float, false, NORM>(a, s, st);
+  else if (dtype == GSPARSE_BF16) vec ? rows_of<__nv_bfloat16, true, NORM>(a, s, st) : rows_of<__nv_bfloat16, false, NORM>(a, s, st);
+  else vec ? rows_of<__half, true, NORM>(a, s, st) : rows_of<__half, false, NORM>(a, s, st);
+  return launch_status();
+}
+
+template <class T, bool VEC>
+void back_of(const BackArgs& a, const Shape& s, int blocks, size_t smem, cudaStream_t st) {
+  const dim3 grid((unsigned)blocks), block((unsigned)(a.groups * s.warps * 32));
+  if (s.entries == 8) launch(norm_back_kernel<T, VEC, 8, 512>, grid, block, smem, st, a);
+  else if (s.warps <= 16) launch(norm_back_kernel<T, VEC, 16, 512>, grid, block, smem, st, a);
+  else launch(norm_back_kernel<T, VEC, 16, 1024>, grid, block, smem, st, a);
+}
+
+int back_groups(const Shape& s) { return s.warps == 1 ? 8 : 1; }
+
+// Blocks of the gradient: what the SMs hold at once (about 1024 threads each), at most one a group of rows.
+int back_blocks(int64_t rows, const Shape& s) {
+  const int groups = back_groups(s), threads = groups * s.warps * 32;
+  const int64_t most = 148 * (int64_t)(threads >= 1024 ? 1 : 1024 / threads);
+  const int64_t need = cdiv(rows, groups);
+  return (int)(need < most ? need : most);
+}
+
+template <class T>
+void dequant_of(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int depth, void* out, int64_t out_stride, bool vec,
+                cudaStream_t st) {
+  const int64_t blocks = cdiv(rows * cdiv(depth, 16), 256);
+  const dim3 grid((unsigned)(blocks < 148 * 32 ? blocks : 148 * 32));
+  if (vec) launch(dequant_kernel<T, true>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride);
+  else launch(dequant_kernel<T, false>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride);
+}
+
+}  // namespace
+}  // namespace gs
+
+using namespace gs;
+
+extern "C" {
+
+int gsparse_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64_t depth, int64_t row_stride, int8_t* q, int64_t q_stride,
+                          float* scale, gsparse_stream stream) {
+  const int st = rows_sizes(dtype, rows, depth, GSPARSE_MAX_DEPTH);
+  if (st != GSPARSE_OK || rows == 0) return st;
+  if (!matrix(x, row_stride, dtype, rows, depth, false)) return GSPARSE_ERR_INVALID_ARG;
+  if (!q || !scale || !aligned16(q) || q_stride % 16 || q_stride < depth || !at_multiple(scale, 4)) return GSPARSE_ERR_INVALID_ARG;
+  RowArgs a{};
+  a.x = x;
+  a.x_stride = row_stride;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.scale = scale;
+  a.rows = rows;
+  a.depth = (int)depth;
+  a.warps = shape_of(depth).warps;
+  const bool vec = even(x, row_stride, dtype) && depth % (16 / (int64_t)size_of(dtype)) == 0;
+  return rows_by_type<false>(dtype, a, vec, (cudaStream_t)stream);
+}
+
+int gsparse_dequantize_rows(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int64_t depth, void* out, int32_t dtype,
+                            int64_t out_stride, gsparse_stream stream) {
+  const int st = rows_sizes(dtype, rows, depth, GSPARSE_MAX_DEPTH);
+  if (st != GSPARSE_OK || rows == 0) return st;
+  if (!q || !scale || !aligned16(q) || q_stride % 16 || q_stride < depth || !at_multiple(scale, 4)) return GSPARSE_ERR_INVALID_ARG;
+  if (!matrix(out, out_stride, dtype, rows, depth, true)) return GSPARSE_ERR_INVALID_ARG;
+  const bool vec = even(out, out_stride, dtype);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == GSPARSE_F32) dequant_of<float>(q, q_stride, scale, rows, (int)depth, out, out_stride, vec, s);
+  else if (dtype == GSPARSE_BF16) dequant_of<__nv_bfloat16>(q, q_stride, scale, rows, (int)depth, out, out_stride, vec, s);
+  else dequant_of<__half>(q, q_stride, scale, rows, (int)depth, out, out_stride, vec, s);
+  return launch_status();
+}
+
+int gsparse_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const void* weight,
+                     int32_t weight_dtype, int32_t dtype, int64_t rows, int64_t depth, float eps, void* h, int64_t h_stride, void* y,
+                     int64_t y_stride, int8_t* q, int64_t q_stride, float* scale, float* rstd, gsparse_stream stream) {
+  const int st = rows_sizes(dtype, rows, depth);
+  if (st != GSPARSE_OK) return st;
+  if (!known(weight_dtype) || !(eps >= 0x1p-126f) || !isfinite(eps)) return GSPARSE_ERR_INVALID_ARG;
+  if (rows == 0) return GSPARSE_OK;
+  if (!matrix(x, x_stride, dtype, rows, depth, false) || !weight || !at_multiple(weight, size_of(weight_dtype)))
+    return GSPARSE_ERR_INVALID_ARG;
+  if (residual && !matrix(residual, residual_stride, dtype, rows, depth, false)) return GSPARSE_ERR_INVALID_ARG;
+  if (h && !matrix(h, h_stride, dtype, rows, depth, true)) return GSPARSE_ERR_INVALID_ARG;
+  if (y && !matrix(y, y_stride, dtype, rows, depth, true)) return GSPARSE_ERR_INVALID_ARG;
+  if ((h && h == x && h_stride != x_stride) || (h && h == residual && h_stride != residual_stride)) return GSPARSE_ERR_INVALID_ARG;
+  if ((q != nullptr) != (scale != nullptr)) return GSPARSE_ERR_INVALID_ARG;
+  if (q && (!aligned16(q) || q_stride % 16 || q_stride < depth || !at_multiple(scale, 4))) return GSPARSE_ERR_INVALID_ARG;
+  if (!at_multiple(rstd, 4)) return GSPARSE_ERR_INVALID_ARG;
+  RowArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.h = h;
+  a.y = y;
+  a.q = q;
+  a.scale = scale;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.h_stride = h_stride;
+  a.y_stride = y_stride;
+  a.q_stride = q_stride;
+  a.depth = (int)depth;
+  a.weight_dtype = weight_dtype;
+  a.warps = shape_of(depth).warps;
+  a.eps = eps;
+  const bool vec = depth % (16 / (int64_t)size_of(dtype)) == 0 && aligned16(weight) && even(x, x_stride, dtype) &&
+                   even(residual, residual_stride, dtype) && even(h, h_stride, dtype) && even(y, y_stride, dtype);
+  return rows_by_type<true>(dtype, a, vec, (cudaStream_t)stream);
+}
+
+size_t gsparse_rms_norm_backward_workspace_size(int64_t rows, int64_t depth) {
+  if (rows_sizes(GSPARSE_F32, rows, depth) != GSPARSE_OK) return 0;
+  return 256 + (size_t)back_blocks(rows, shape_of(depth)) * (size_t)depth * sizeof(float);
+}
+
+int gsparse_rms_norm_backward(const void* h, int64_t h_stride, const void* weight, int32_t weight_dtype, const float* rstd,
+                              const void* dy, int64_t dy_stride, const void* dh, int64_t dh_stride, int32_t dtype, int64_t rows,
+                              int64_t depth, void* dx, int64_t dx_stride, float* dweight, void* workspace, size_t workspace_bytes,
+                              gsparse_stream stream) {
+  const int st = rows_sizes(dtype, rows, depth);
+  if (st != GSPARSE_OK) return st;
+  if (!known(weight_dtype) || !at_multiple(dweight, 4)) return GSPARSE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (rows == 0) {
+    if (dweight && cudaMemsetAsync(dweight, 0, (size_t)depth * sizeof(float), s) != cudaSuccess) {
+      cudaGetLastError();
+      return GSPARSE_ERR_CUDA;
+    }
+    return GSPARSE_OK;
+  }
+  if (!weight || !at_multiple(weight, size_of(weight_dtype)) || !rstd || !at_multiple(rstd, 4)) return GSPARSE_ERR_INVALID_ARG;
+  if (!matrix(h, h_stride, dtype, rows, depth, false) || !matrix(dy, dy_stride, dtype, rows, depth, false) ||
+      !matrix(dx, dx_stride, dtype, rows, depth, true))
+    return GSPARSE_ERR_INVALID_ARG;
+  if (dh && !matrix(dh, dh_stride, dtype, rows, depth, false)) return GSPARSE_ERR_INVALID_ARG;
+  if ((dx == h && dx_stride != h_stride) || (dx == dy && dx_stride != dy_stride) || (dx == dh && dx_stride != dh_stride))
+    return GSPARSE_ERR_INVALID_ARG;
+  const Shape shape = shape_of(depth);
+  const int blocks = back_blocks(rows, shape);
+  Carver c(workspace);
+  float* partial = c.take<float>((int64_t)blocks * depth);
+  if (dweight && (!workspace || !at_multiple(workspace, 256) || workspace_bytes < c.off)) return GSPARSE_ERR_WORKSPACE;
+  BackArgs a{};
+  a.h = h;
+  a.dy = dy;
+  a.dh = dh;
+  a.weight = weight;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.partial = dweight ? partial : nullptr;
+  a.rows = rows;
+  a.h_stride = h_stride;
+  a.dy_stride = dy_stride;
+  a.dh_stride = dh_stride;
+  a.dx_stride = dx_stride;
+  a.depth = (int)depth;
+  a.weight_dtype = weight_dtype;
+  a.warps = shape.warps;
+  a.groups = back_groups(shape);
+  const bool vec = depth % (16 / (int64_t)size_of(dtype)) == 0 && aligned16(weight) && even(h, h_stride, dtype) &&
+                   even(dy, dy_stride, dtype) && even(dh, dh_stride, dtype) && even(dx, dx_stride, dtype);
+  const size_t smem = shape.warps == 1 ? (size_t)a.groups * (size_t)depth * sizeof(float) : 0;   // at most 16 KB
+  if (dtype == GSPARSE_F32) vec ? back_of<float, true>(a, shape, blocks, smem, s) : back_of<float, false>(a, shape, blocks, smem, s);
+  else if (dtype == GSPARSE_BF16)
+    vec ? back_of<__nv_bfloat16, true>(a, shape, blocks, smem, s) : back_of<__nv_bfloat16, false>(a, shape, blocks, smem, s);
+  else vec ? back_of<__half, true>(a, shape, blocks, smem, s) : back_of<__half, false>(a, shape, blocks, smem, s);
+  if (dweight) launch(norm_join_kernel, dim3((unsigned)cdiv(depth, 32)), dim3(1024), 0, s, (const float*)partial, blocks, (int)depth, dweight);
+  return launch_status();
+}
+
+}  // extern "C"

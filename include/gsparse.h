@@ -507,6 +507,89 @@ int gsparse_distill_topk_backward(const void* logits, int32_t dtype, int64_t row
                                   const float* grad_loss, void* dlogits, int64_t dlogits_stride,
                                   int32_t* d_status, gsparse_stream stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A layer in 8 bits  (no counterpart in the pages: the norm, the layer and the layer's gradient, next to the
+ * losses above; the gradient of its weights is what the compression takes)
+ *
+ * Rows in 8 bits: int8 q[rows][depth], row r at q + r * q_stride (q 16-byte aligned, q_stride a multiple of 16, >= depth;
+ * what stands behind a row's depth entries is neither read nor written), and fp32 scale[rows]. A row y is held as
+ *   scale = 2^e, e the smallest integer from -126 to 121 for which no |y_k| exceeds 127 * 2^e (121 where none does);
+ *   q_k = y_k / 2^e rounded to the nearest integer, ties to even, and held within +-127.
+ * The value q_k * scale has seven bits, so bf16 holds it exactly. A row that holds NaN or an infinity has scale NaN and q = 0.
+ * Activations and checkpoints are held by token, weights by channel. The products take scales that are no powers of two too.
+ *
+ * Matrices: entry k of row r at p[r * stride + k], any alignment of the element, any stride >= 0 of what is read and >= depth
+ * of what is written. Rows that start at 16-byte boundaries are fastest. 1 <= depth <= GSPARSE_MAX_DEPTH (of the norm
+ * GSPARSE_MAX_NORM_DEPTH); 0 <= rows, tokens <= GSPARSE_MAX_ROWS; 1 <= channels <= GSPARSE_MAX_ROWS. Sums in a fixed
+ * order: the same call on the same layout gives the same bits on every run.
+ */
+#define GSPARSE_MAX_DEPTH (1 << 15)
+#define GSPARSE_MAX_NORM_DEPTH (1 << 14)
+#define GSPARSE_MAX_ROWS (1 << 26)
+
+int gsparse_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64_t depth, int64_t row_stride,
+                          int8_t* q, int64_t q_stride, float* scale, gsparse_stream stream);
+
+/* out = q * scale in the type dtype, rounded once. */
+int gsparse_dequantize_rows(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int64_t depth,
+                            void* out, int32_t dtype, int64_t out_stride, gsparse_stream stream);
+
+/* h = x + residual in the type dtype (residual NULL: x);  r = (mean of h_k^2 + eps)^(-1/2);  y_k = h_k r weight_k.
+ * weight   [depth] of type weight_dtype. eps from 2^-126, finite.
+ * h        NULL, or receives h; may be x or residual itself, with the same stride.
+ * y        NULL, or receives y in the type dtype.
+ * q, scale NULL, or receive y (before its rounding to dtype) in 8 bits; y / 2^e is worked out to 2^-40, so that an
+ *          entry next to a border between two steps falls on the side that the formula says.
+ * rstd     fp32[rows] or NULL: r, for the backward call.
+ * Squares are summed in 64 bits. */
+int gsparse_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                     const void* weight, int32_t weight_dtype, int32_t dtype, int64_t rows, int64_t depth,
+                     float eps, void* h, int64_t h_stride, void* y, int64_t y_stride, int8_t* q, int64_t q_stride,
+                     float* scale, float* rstd, gsparse_stream stream);
+
+/* The gradient by h (and so by x and by residual) and by the weight, for dy the gradient at y (the rounding to 8 bits
+ * passes it on as it is) and dh, or NULL, what reaches h on other ways:
+ *   xh_k = h_k r;  g_k = dy_k weight_k;  dx_k = r (g_k - xh_k * mean of g_j xh_j) + dh_k;
+ *   dweight_k = sum over the rows of dy_k xh_k  (fp32[depth], or NULL).
+ * h, dy, dh and dx are of the type dtype. dx may be h, dy or dh itself, with the same stride. The workspace is needed for
+ * dweight. No rows: dweight is 0. */
+size_t gsparse_rms_norm_backward_workspace_size(int64_t rows, int64_t depth);
+int gsparse_rms_norm_backward(const void* h, int64_t h_stride, const void* weight, int32_t weight_dtype,
+                              const float* rstd, const void* dy, int64_t dy_stride, const void* dh,
+                              int64_t dh_stride, int32_t dtype, int64_t rows, int64_t depth, void* dx,
+                              int64_t dx_stride, float* dweight, void* workspace, size_t workspace_bytes,
+                              gsparse_stream stream);
+
+/* out[t][n] = x_scale_t w_scale_n * sum_k x[t][k] w[n][k], the sum in 32-bit integers (exact), its product with x_scale_t
+ * (which has to be within fp32), then with w_scale_n, each rounded to fp32, and once more to out's type dtype. x: tokens
+ * rows of depth in 8 bits; w: channels rows. */
+size_t gsparse_linear_q8_workspace_size(int64_t tokens, int64_t channels, int64_t depth);
+int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, const int8_t* w, int64_t w_stride,
+                      const float* w_scale, int64_t tokens, int64_t channels, int64_t depth, void* out,
+                      int32_t dtype, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                      int32_t* d_status, gsparse_stream stream);
+
+/* Its gradients, from dout [tokens][channels] of type dtype:
+ *   dx[t][k] = sum_n dout[t][n] w_scale_n w[n][k]        (of type dx_dtype)
+ *   dweight[n][k] = sum_t dout[t][n] x_scale_t x[t][k]   (fp32; the gradient by the weights that w stands for)
+ * The 8-bit operand's values are taken as bf16 (exact where scales are powers of two, else rounded once), dout in full:
+ * bf16 as it is, fp16 as the exact sum of two and fp32 of three bf16 numbers (below 2^-100 in magnitude the smaller parts
+ * may be lost). Sums in fp32, at most 256 products in the matrix unit's own rounding (towards zero) before they are added up.
+ * No tokens: dweight is 0. The workspace's size depends on dout's alignment and stride. */
+size_t gsparse_linear_q8_grad_input_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride,
+                                                   int64_t tokens, int64_t channels, int64_t depth);
+int gsparse_linear_q8_grad_input(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* w,
+                                 int64_t w_stride, const float* w_scale, int64_t tokens, int64_t channels,
+                                 int64_t depth, void* dx, int32_t dx_dtype, int64_t dx_stride, void* workspace,
+                                 size_t workspace_bytes, int32_t* d_status, gsparse_stream stream);
+
+size_t gsparse_linear_q8_grad_weight_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride,
+                                                    int64_t tokens, int64_t channels, int64_t depth);
+int gsparse_linear_q8_grad_weight(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* x,
+                                  int64_t x_stride, const float* x_scale, int64_t tokens, int64_t channels,
+                                  int64_t depth, float* dweight, int64_t dweight_stride, void* workspace,
+                                  size_t workspace_bytes, int32_t* d_status, gsparse_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
