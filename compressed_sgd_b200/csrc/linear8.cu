@@ -1,4 +1,11 @@
-// The product of rows in 8 bits and its gradients.
+// The product of rows in 8 bits, and its gradients, on the fifth-generation tensor cores.
+//
+// One kernel serves all three: D[m][n] = sum over s of A(m, s) B(n, s), with pairs of CTAs that take 256 x 256 tiles of D.
+//   product      A = x [tokens][depth], B = w [channels][depth], both int8 and s along their rows; D in 32-bit integers.
+//   grad_input   A = dout [tokens][channels], s along its rows; B = w's values in bf16 [channels][depth], s across its rows.
+//   grad_weight  A = dout [tokens][channels] and B = x's values in bf16 [tokens][depth], s across the rows of both.
+// The values of rows in 8 bits are bf16 numbers (rows8.cu), so the gradients' products are exact in fp32.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -7,73 +14,559 @@
 namespace gs {
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kTile = 256;                 // of a pair, both ways; a CTA loads and holds 128 rows of each operand
+constexpr int kRowBytes = 128;             // of an operand's row in a stage: 128 int8 or 64 bf16 (one swizzle atom)
+constexpr int kOperand = 128 * kRowBytes;  // bytes of one operand of one CTA in a stage
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kBox = 32 * 128;             // a warp's part of the result on its way out: 32 rows of 128 bytes
 
-__device__ __forceinline__ float read_as(const void* p, int32_t dtype, int64_t at) {
-  if (dtype == GSPARSE_F32) return static_cast<const float*>(p)[at];
-  if (dtype == GSPARSE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-  return __half2float(static_cast<const __half*>(p)[at]);
-}
+// The sums in bf16 are taken out of the tensor core every 4 blocks of 64 and added up in fp32 registers: its accumulation
+// cuts off (towards zero), 16 times in a row at most then.
+constexpr int kChunk = 4;
 
-__device__ __forceinline__ void write_as(void* p, int32_t dtype, int64_t at, float v) {
-  if (dtype == GSPARSE_F32) static_cast<float*>(p)[at] = v;
-  else if (dtype == GSPARSE_BF16) static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[at] = __float2half_rn(v);
-}
-
-struct SimpleArgs {
-  const int8_t* x;
-  const float* x_scale;
-  const int8_t* w;
-  const float* w_scale;
-  const void* dout;
-  void* out;
-  int64_t x_stride, w_stride, dout_stride, out_stride;
-  int tokens, channels, depth, dtype, out_dtype;
+template <bool INT> struct Layout {
+  static constexpr int stages = INT ? 5 : 6;
+  static constexpr int boxes = INT ? 2 : 1;
+  static constexpr int stage_bytes = 2 * kOperand;
+  static constexpr int box_at = stages * stage_bytes;
+  static constexpr int scale_at = box_at + kEpilogueWarps * boxes * kBox;
+  static constexpr int bar_at = scale_at + (INT ? 2 * kTile * 4 : 0);
+  static constexpr int bytes = bar_at + 256;
 };
 
-// OP 0: out[t][n] over k; 1: dx[t][k] over n; 2: dweight[n][k] over t. A block of 16 x 16 results, a thread each.
-template <int OP>
-__global__ void __launch_bounds__(kTile * kTile) simple_kernel(const __grid_constant__ SimpleArgs a) {
-  pdl_begin();
-  __shared__ float A[kTile][kTile + 1], B[kTile][kTile + 1];
-  const int rows = OP == 2 ? a.channels : a.tokens, cols = OP == 0 ? a.channels : a.depth;
-  const int sums = OP == 0 ? a.depth : OP == 1 ? a.channels : a.tokens;
-  const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-  for (int64_t r0 = (int64_t)blockIdx.y * kTile; r0 < rows; r0 += (int64_t)gridDim.y * kTile) {
-    const int64_t row = r0 + ty, col = (int64_t)blockIdx.x * kTile + tx;
-    int whole = 0;
-    float sum = 0.0f;
-    for (int64_t s0 = 0; s0 < sums; s0 += kTile) {
-      const int64_t ra = r0 + ty, sa = s0 + tx;          // A[ty][tx]: row ra at sum place sa
-      float v = 0.0f;
-      if (ra < rows && sa < sums) {
-        if (OP == 0) v = (float)a.x[ra * a.x_stride + sa];
-        if (OP == 1) v = read_as(a.dout, a.dtype, ra * a.dout_stride + sa);
-        if (OP == 2) v = read_as(a.dout, a.dtype, sa * a.dout_stride + ra);
-      }
-      A[ty][tx] = v;
-      const int64_t cb = (int64_t)blockIdx.x * kTile + tx, sb = s0 + ty;   // B[ty][tx]: sum place sb at column cb
-      v = 0.0f;
-      if (cb < cols && sb < sums) {
-        if (OP == 0) v = (float)a.w[cb * a.w_stride + sb];
-        if (OP == 1) v = (float)a.w[sb * a.w_stride + cb] * a.w_scale[sb];
-        if (OP == 2) v = (float)a.x[sb * a.x_stride + cb] * a.x_scale[sb];
-      }
-      B[ty][tx] = v;
-      __syncthreads();
-      for (int i = 0; i < kTile; ++i) {
-        if (OP == 0) whole += (int)A[ty][i] * (int)B[i][tx];
-        else sum = __fmaf_rn(A[ty][i], B[i][tx], sum);
-      }
-      __syncthreads();
+struct TileArgs {
+  CUtensorMap a, b, out, part;
+  const float* row_scale;                  // of the integer product
+  const float* col_scale;
+  void* result;
+  int64_t result_stride;
+  int64_t as_tiles;                        // columns of D that the tensor map describes: a copy ends at a multiple of 16 bytes
+  int32_t* d_status;
+  int64_t rows, cols;                      // of D
+  int tiles_m, tiles;                      // tile t is (t % tiles_m, t / tiles_m)
+  int blocks, plane_blocks;                // of 128 bytes along s, all planes; of one plane
+  int pairs, waves;                        // tiles below waves * pairs are whole; the others are split
+  int piece;                               // blocks of a pair's part of the split tiles (0: none are split)
+  int out_dtype;
+};
+
+// ---- instructions ----------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+// Waits for a phase; false after about a second. The arrivals may come from the other CTA.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  uint32_t ok = 0;
+  const long long t0 = clock64();
+  do {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(at), "r"(parity) : "memory");
+  } while (!ok && clock64() - t0 < kWaitCycles);
+  return ok != 0;
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Copies of a box into this CTA's shared memory that count on a barrier of the pair's first CTA.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// A tile in shared memory, swizzled by 128 bytes. Rows along s (a row of 128 bytes per m): groups of 8 rows 1024 bytes apart.
+// Rows across s (a row of 64 m per s): groups of 8 s 1024 bytes apart, the next 64 m 8192 bytes on.
+__device__ __forceinline__ uint64_t tile_of(uint32_t addr, bool across) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(across ? 8192 >> 4 : 1) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+template <bool INT>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+  if constexpr (INT)
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
+                 "r"(what), "r"((uint32_t)add)
+                 : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
+                 "r"(what), "r"((uint32_t)add)
+                 : "memory");
+}
+
+// The barrier at this place in both CTAs, once what was issued before has been done.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+
+__device__ __forceinline__ void load_columns(uint32_t (&v)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]),
+        "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+        "=r"(v[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void columns_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// ---- work of a pair -----------------------------------------------------------------------------------------
+
+// The i-th part of a pair's work: blocks [from, to) of a tile, and whether they are all of it (else its place among the parts).
+struct Part {
+  int m, n, from, to, slot;
+  bool whole;
+};
+
+__device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part& p) {
+  int tile;
+  p.slot = 0;
+  if (i < a.waves || a.piece == 0) {
+    tile = pair + i * a.pairs;
+    if (tile >= a.tiles) return false;
+    p.from = 0;
+    p.to = a.blocks;
+  } else {
+    const int k = i - a.waves;                                  // a pair's range of blocks meets at most two tiles
+    const int64_t all = (int64_t)(a.tiles - a.waves * a.pairs) * a.blocks;
+    const int64_t first = (int64_t)pair * a.piece, last = min(all, first + a.piece);
+    if (first >= last) return false;
+    const int64_t t = first / a.blocks + k;
+    const int64_t from = max(first, t * a.blocks), to = min(last, (t + 1) * a.blocks);
+    if (from >= to) return false;
+    tile = a.waves * a.pairs + (int)t;
+    p.from = (int)(from - t * a.blocks);
+    p.to = (int)(to - t * a.blocks);
+    p.slot = pair * 2 + k;
+  }
+  p.whole = p.to - p.from == a.blocks;
+  p.m = tile % a.tiles_m;
+  p.n = tile / a.tiles_m;
+  return true;
+}
+
+// ---- the way out --------------------------------------------------------------------------------------------
+
+template <class T> struct Pack;
+template <> struct Pack<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ uint4 of(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <> struct Pack<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ uint32_t two(float a, float b) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&p);
+  }
+  static __device__ __forceinline__ uint4 of(const float* v) { return make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7])); }
+};
+template <> struct Pack<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ uint32_t two(float a, float b) {
+    __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&p);
+  }
+  static __device__ __forceinline__ uint4 of(const float* v) { return make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7])); }
+};
+
+// 32 of a row's results (lane = row) into the warp's box, from the 16-byte place `at` on. Rows are swizzled as the tensor maps say,
+// which also spreads the lanes over the banks.
+template <class T>
+__device__ __forceinline__ void into_box(char* box, int lane, int at, const float* v) {
+#pragma unroll
+  for (int j = 0; j < 32 / Pack<T>::N; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 128 + (((at + j) ^ (lane & 7)) << 4)) = Pack<T>::of(v + j * Pack<T>::N);
+}
+
+// A box of 32 rows that no tensor map describes: row by row, 128 bytes of entries side by side.
+template <class T>
+__device__ void box_to_rows(const char* box, int lane, T* out, int64_t stride, int64_t row, int64_t col, int64_t rows, int64_t cols) {
+  constexpr int N = 4 / (int)sizeof(T);
+  const int n = (int)min((int64_t)32, rows - row);
+  const int64_t mine = col + lane * N;
+  for (int r = 0; r < n; ++r) {
+    const uint32_t raw = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+    const T* e = reinterpret_cast<const T*>(&raw);
+    T* to = out + (row + r) * stride + mine;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (mine + i < cols) to[i] = e[i];
+  }
+}
+
+// One warp's box on its way: the boxes of a warp are used in turn.
+struct Way {
+  char* boxes;
+  int lane, count, turn;
+
+  __device__ __forceinline__ char* next() {
+    char* box = boxes + (count > 1 ? (turn & 1) * kBox : 0);
+    ++turn;
+    if (lane == 0) {
+      if (count > 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
-    if (row < rows && col < cols) {
-      if (OP == 0) sum = ((float)whole * a.x_scale[row]) * a.w_scale[col];
-      write_as(a.out, a.out_dtype, row * a.out_stride + col, sum);
+    __syncwarp();
+    return box;
+  }
+  __device__ __forceinline__ void send(const CUtensorMap* map, int64_t x, int64_t y, char* box) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) store_box(map, (int)x, (int)y, smem_u32(box));
+  }
+};
+
+// A warp's 32 x 32 results v at (row, col) of D, the `half`-th of a box of 16-bit types.
+template <class T>
+__device__ __forceinline__ void put_result(const TileArgs& a, Way& way, char*& box, int half, const float* v, int64_t row, int64_t col) {
+  constexpr bool narrow = sizeof(T) == 2;
+  if (!narrow || half == 0) box = way.next();
+  into_box<T>(box, way.lane, narrow ? half * 4 : 0, v);
+  if (narrow && half == 0) return;
+  const int64_t x = narrow ? col - 32 : col;
+  if (row >= a.rows || x >= a.cols) return;
+  if (x + 128 / (int)sizeof(T) <= a.as_tiles || a.as_tiles == a.cols) {
+    way.send(&a.out, x, row, box);
+  } else {
+    __syncwarp();
+    box_to_rows<T>(box, way.lane, static_cast<T*>(a.result), a.result_stride, row, x, a.rows, a.cols);
+    __syncwarp();
+  }
+}
+
+__device__ __forceinline__ void put(const TileArgs& a, Way& way, char*& box, int half, const float* v, int64_t row, int64_t col) {
+  if (a.out_dtype == GSPARSE_F32) put_result<float>(a, way, box, half, v, row, col);
+  else if (a.out_dtype == GSPARSE_BF16) put_result<__nv_bfloat16>(a, way, box, half, v, row, col);
+  else put_result<__half>(a, way, box, half, v, row, col);
+}
+
+// A part of a tile's sums, as they are: row r of slot k at row k * 256 + r of the workspace.
+__device__ __forceinline__ void put_part(const TileArgs& a, Way& way, const float* v, int64_t row, int col) {
+  char* box = way.next();
+  into_box<float>(box, way.lane, 0, v);
+  way.send(&a.part, col, row, box);
+}
+
+// ---- the kernel -----------------------------------------------------------------------------------------------
+
+// Warps 0 to 7 take results out (warp w the lanes 32 (w % 4) and the columns 128 (w / 4) on), warp 8 loads, warp 9 multiplies (of
+// the pair's first CTA, for both). The loads run ahead over all of a pair's parts; the tensor memory holds two tiles of sums.
+template <bool INT, bool A_ACROSS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ TileArgs a) {
+  extern __shared__ __align__(1024) char smem[];
+  using L = Layout<INT>;
+  constexpr bool kAcross = !INT;                               // B's rows
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar_at);
+  uint64_t* empty = full + L::stages;
+  uint64_t* sums_full = empty + L::stages;
+  uint64_t* sums_empty = sums_full + 2;
+  uint64_t* drained = sums_empty + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::stages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sums_full + i, 1);
+      mbar_init(sums_empty + i, 2 * kEpilogueWarps);
+    }
+    mbar_init(drained, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_begin();
+
+  bool ok = true;
+  Part p;
+  if (warp == 8) {
+    if (lane == 0) {
+      uint32_t n = 0;                                          // stages filled so far
+      for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
+        for (int kb = p.from; kb < p.to; ++kb, ++n) {
+          const int s = (int)(n % L::stages);
+          if (n >= L::stages && !(ok = wait_phase(empty + s, (n / L::stages - 1) & 1))) break;
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * L::stage_bytes);
+          const uint32_t bar = in_cta(smem_u32(full + s), 0);
+          const uint32_t at = smem_u32(smem + s * L::stage_bytes);
+          const int plane = kb / a.plane_blocks, k = kb - plane * a.plane_blocks;
+          const int m = p.m * kTile + (int)rank * 128, c = p.n * kTile + (int)rank * 128;
+          if constexpr (INT) {
+            load_box(at, &a.a, k * 128, m, bar);
+            load_box(at + kOperand, &a.b, k * 128, c, bar);
+          } else {
+            if constexpr (A_ACROSS) {
+              load_box(at, &a.a, m, k * 64, plane, bar);
+              load_box(at + kOperand / 2, &a.a, m + 64, k * 64, plane, bar);
+            } else {
+              load_box(at, &a.a, k * 64, m, plane, bar);
+            }
+            load_box(at + kOperand, &a.b, c, k * 64, bar);
+            load_box(at + kOperand + kOperand / 2, &a.b, c + 64, k * 64, bar);
+          }
+        }
+      }
+      if (!ok) {
+        raise(a.d_status, GSPARSE_DERR_TIMEOUT);
+        if (rank == 0)                                         // the copies under way, of both CTAs
+          for (uint32_t k = n > L::stages ? n - L::stages : 0; k < n; ++k) wait_phase(full + k % L::stages, (k / L::stages) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t what = (INT ? 2u << 4 : 1u << 4) | 1u << 7 | 1u << 10 | (A_ACROSS ? 1u << 15 : 0u) | (kAcross ? 1u << 16 : 0u) |
+                                (uint32_t)(kTile >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
+      uint32_t n = 0, c = 0;                                   // stages used, sums begun
+      for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
+        for (int kb = p.from; ok && kb < p.to; ++c) {
+          const int end = INT ? p.to : min(p.to, kb + kChunk);
+          const uint32_t buf = c & 1, d = tmem + buf * kTile;
+          if (c >= 2 && !(ok = wait_phase(sums_empty + buf, (c / 2 - 1) & 1))) break;
+          fence_after();
+          for (bool add = false; kb < end; ++kb, ++n) {
+            const int s = (int)(n % L::stages);
+            if (!(ok = wait_phase(full + s, (n / L::stages) & 1))) break;
+            fence_after();
+            const uint32_t at = smem_u32(smem + s * L::stage_bytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {                      // 32 bytes along s, or 16 rows across it
+              multiply<INT>(d, tile_of(at + k * (A_ACROSS ? 2048 : 32), A_ACROSS), tile_of(at + kOperand + k * (kAcross ? 2048 : 32), kAcross), what,
+                            add);
+              add = true;
+            }
+            commit(empty + s);
+          }
+          if (ok) commit(sums_full + buf);
+        }
+      }
+      if (!ok) {
+        raise(a.d_status, GSPARSE_DERR_TIMEOUT);
+        commit(drained);
+        wait_phase(drained, 0);
+      }
+    }
+  } else {
+    const int quarter = warp & 3, side = warp >> 2;
+    const int64_t first_row = (int64_t)rank * 128 + quarter * 32;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 128;
+    const uint32_t give = in_cta(smem_u32(sums_empty), 0);
+    Way way{smem + L::box_at + warp * L::boxes * kBox, lane, L::boxes, 0};
+    uint32_t c = 0;
+    // (after a wait that gave up: on to the end, since the warps of a side meet at a barrier for each part)
+    for (int i = 0; part_of(a, pair, i, p); ++i) {
+      const int64_t row = (int64_t)p.m * kTile + first_row, col = (int64_t)p.n * kTile + side * 128;
+      const int64_t part_row = (int64_t)p.slot * kTile + first_row;
+      char* box = nullptr;
+      if constexpr (INT) {
+        const uint32_t buf = c & 1;
+        // the scales of the tile's columns, for the four warps that take the same columns
+        float* scales = reinterpret_cast<float*>(smem + L::scale_at) + buf * kTile + side * 128;
+        const int64_t at = col + quarter * 32 + lane;
+        scales[quarter * 32 + lane] = at < a.cols ? __ldg(a.col_scale + at) : 0.0f;
+        const float mine = row + lane < a.rows ? __ldg(a.row_scale + row + lane) : 0.0f;
+        asm volatile("bar.sync %0, 128;" ::"r"(side + 1) : "memory");
+        if (!(ok = ok && wait_phase(sums_full + buf, (c / 2) & 1))) continue;
+        fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t raw[32];
+          load_columns(raw, lanes + buf * kTile + j * 32);
+          columns_loaded();
+          if (j == 3) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(give + buf * 8);
+          }
+          float v[32];
+          if (p.whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 s = *reinterpret_cast<const float4*>(scales + j * 32 + k);
+              v[k] = __int2float_rn((int)raw[k]) * mine * s.x;
+              v[k + 1] = __int2float_rn((int)raw[k + 1]) * mine * s.y;
+              v[k + 2] = __int2float_rn((int)raw[k + 2]) * mine * s.z;
+              v[k + 3] = __int2float_rn((int)raw[k + 3]) * mine * s.w;
+            }
+            put(a, way, box, j & 1, v, row, col + j * 32);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
+            put_part(a, way, v, part_row, side * 128 + j * 32);
+          }
+        }
+        ++c;
+      } else {
+        float sum[128];
+        for (int kb = p.from; ok && kb < p.to; kb += kChunk, ++c) {
+          const uint32_t buf = c & 1;
+          if (!(ok = wait_phase(sums_full + buf, (c / 2) & 1))) break;
+          fence_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t raw[32];
+            load_columns(raw, lanes + buf * kTile + j * 32);
+            columns_loaded();
+            if (kb == p.from) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sum[j * 32 + k] = __uint_as_float(raw[k]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sum[j * 32 + k] += __uint_as_float(raw[k]);
+            }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(give + buf * 8);
+        }
+        if (!ok) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (p.whole) put(a, way, box, j & 1, sum + j * 32, row, col + j * 32);
+          else put_part(a, way, sum + j * 32, part_row, side * 128 + j * 32);
+        }
+      }
+    }
+    if (!ok && lane == 0) raise(a.d_status, GSPARSE_DERR_TIMEOUT);
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  // nobody leaves while the other CTA may still reach into its shared or tensor memory
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ---- split tiles -------------------------------------------------------------------------------------------------
+
+struct JoinArgs {
+  const float* part;
+  const float* row_scale;
+  const float* col_scale;
+  void* out;
+  int64_t out_stride, rows, cols;
+  int tiles_m, first_tile, blocks, piece, out_dtype;
+};
+
+// The parts of a split tile added up in their order along s. A block takes 8 rows of a tile, a thread 8 entries of one row.
+template <bool INT, class T>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
+  pdl_begin();
+  const int t = blockIdx.x >> 5, tile = a.first_tile + t;
+  const int r = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
+  const int64_t from = (int64_t)t * a.blocks, to = from + a.blocks;
+  const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
+  if (first == last) return;                       // whole after all
+  const int64_t row = (int64_t)(tile % a.tiles_m) * kTile + r, col = (int64_t)(tile / a.tiles_m) * kTile + c;
+  if (row >= a.rows || col >= a.cols) return;
+  uint32_t sum[8];
+  for (int pair = first; pair <= last; ++pair) {
+    // the part that begins a pair's range is its first: only the range's first tile can be this one in the middle
+    const int k = (int64_t)pair * a.piece < from ? 1 : 0;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + ((int64_t)(pair * 2 + k) * kTile + r) * kTile + c;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p)), y = __ldg(reinterpret_cast<const uint4*>(p + 4));
+    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (pair == first) sum[i] = v[i];
+      else if constexpr (INT) sum[i] += v[i];
+      else sum[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
+    }
+  }
+  T* out = static_cast<T*>(a.out) + row * a.out_stride + col;
+  const float mine = INT ? __ldg(a.row_scale + row) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (col + i >= a.cols) break;
+    float v;
+    if constexpr (INT) v = __int2float_rn((int)sum[i]) * mine * __ldg(a.col_scale + col + i);
+    else v = __uint_as_float(sum[i]);
+    if constexpr (sizeof(T) == 4) out[i] = v;
+    else if constexpr (__is_same(T, __nv_bfloat16)) out[i] = __float2bfloat16_rn(v);
+    else out[i] = __float2half_rn(v);
+  }
+}
+
+// ---- gradients in parts of bf16 -------------------------------------------------------------------------------
+
+// x as a sum of PLANES bf16 numbers, exact (8 bits of its significand each): the first holds what is no number.
+template <class T, int PLANES>
+__global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t in_stride, int64_t rows, int64_t cols, __nv_bfloat16* out, int64_t out_stride) {
+  pdl_begin();
+  const int64_t per = (cols + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / per, at = (i - row * per) * 8;
+    const T* p = in + row * in_stride + at;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = at + k < cols ? (float)p[k] : 0.0f;
+#pragma unroll
+    for (int plane = 0; plane < PLANES; ++plane) {
+      __nv_bfloat16 e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t bits = __float_as_uint(v[k]);
+        if ((bits & 0x7f800000u) == 0x7f800000u) {             // infinite: only here; NaN stays one
+          e[k] = __float2bfloat16_rn(v[k]);
+          v[k] = 0.0f;
+        } else {
+          const float high = __uint_as_float(bits & 0xffff0000u);
+          e[k] = __float2bfloat16_rn(high);
+          v[k] -= high;
+        }
+      }
+      *reinterpret_cast<uint4*>(out + ((int64_t)plane * rows + row) * out_stride + at) = *reinterpret_cast<const uint4*>(e);
     }
   }
 }
+
+// ---- host ----------------------------------------------------------------------------------------------------------
 
 bool known(int32_t t) { return t == GSPARSE_F32 || t == GSPARSE_BF16 || t == GSPARSE_F16; }
 size_t size_of(int32_t t) { return t == GSPARSE_F32 ? 4 : 2; }
@@ -95,12 +588,159 @@ bool matrix(const void* p, int64_t stride, int32_t dtype, int64_t rows, int64_t 
 
 bool space(const void* workspace, size_t have, size_t need) { return workspace && at_multiple(workspace, 256) && have >= need; }
 
-template <int OP>
-int simple(const SimpleArgs& a, cudaStream_t st) {
-  const int rows = OP == 2 ? a.channels : a.tokens, cols = OP == 0 ? a.channels : a.depth;
-  const int64_t gy = cdiv(rows, kTile);
-  launch(simple_kernel<OP>, dim3((unsigned)cdiv(cols, kTile), (unsigned)(gy < 65535 ? gy : 65535)), dim3(kTile * kTile), 0, st, a);
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess) {
+      cudaGetLastError();
+      return (EncodeTiled) nullptr;
+    }
+    return r == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+  }();
+  return f;
+}
+
+// Rows of 8-, 16- or 32-bit entries, `stride` entries apart, in `planes` matrices one after another; boxes of 128 bytes by `high` rows.
+bool map_of(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* p, int64_t cols, int64_t rows, int64_t stride, int high,
+            int planes = 0) {
+  const EncodeTiled encode = encoder();
+  if (!encode) return false;
+  const int64_t step = (rows > 1 ? stride : round_up(cols, 16 / bytes)) * bytes;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(planes ? planes : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)step, (cuuint64_t)(step * rows)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / bytes), (cuuint32_t)high, 1}, one[3] = {1, 1, 1};
+  return encode(m, type, planes ? 3 : 2, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+CUtensorMapDataType map_type(int32_t dtype) {
+  return dtype == GSPARSE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dtype == GSPARSE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// How the tiles of D are shared out: whole tiles in waves over the pairs of SMs; what is left over is split along s.
+struct Plan {
+  int tiles_m, tiles, blocks, pairs, waves, piece;
+};
+
+Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
+  Plan p;
+  p.tiles_m = (int)cdiv(rows, kTile);
+  p.tiles = (int)(p.tiles_m * cdiv(cols, kTile));
+  p.blocks = (int)blocks;
+  p.pairs = sm_count() / 2;
+  p.waves = p.tiles / p.pairs;
+  const int64_t left = p.tiles - (int64_t)p.waves * p.pairs;
+  const int64_t piece = cdiv(left * blocks, p.pairs);
+  // Splitting costs a part's way out and back, and a launch.
+  p.piece = left && blocks - piece >= 24 ? (int)piece : 0;
+  return p;
+}
+
+int64_t part_entries(const Plan& p) { return p.piece ? 2 * (int64_t)p.pairs * kTile * kTile : 0; }
+
+bool fits(int64_t rows, int64_t cols) { return cdiv(rows, kTile) * cdiv(cols, kTile) < (1ll << 30); }
+
+template <bool INT, bool A_ACROSS>
+int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride, cudaStream_t st) {
+  using L = Layout<INT>;
+  a.tiles_m = p.tiles_m;
+  a.tiles = p.tiles;
+  a.blocks = p.blocks;
+  a.pairs = p.pairs;
+  a.waves = p.waves;
+  a.piece = p.piece;
+  const int32_t dtype = a.out_dtype;
+  const int bytes = (int)size_of(dtype);
+  const bool as_tiles = aligned16(out) && (a.rows == 1 || (out_stride * bytes) % 16 == 0);
+  a.result = out;
+  a.result_stride = out_stride;
+  a.as_tiles = as_tiles ? a.cols / (16 / bytes) * (16 / bytes) : 0;
+  if (a.as_tiles && !map_of(&a.out, map_type(dtype), bytes, out, a.as_tiles, a.rows, out_stride, 32)) return GSPARSE_ERR_CUDA;
+  if (p.piece && !map_of(&a.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, part, kTile, 2 * (int64_t)p.pairs * kTile, kTile, 32)) return GSPARSE_ERR_CUDA;
+  auto* kernel = tile_kernel<INT, A_ACROSS>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return GSPARSE_ERR_CUDA;
+  }
+  const int used = p.piece || p.waves ? p.pairs : p.tiles;
+  launch(kernel, dim3((unsigned)(2 * used)), dim3(kThreads), L::bytes, st, (const TileArgs&)a);
+  if (p.piece) {
+    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.tiles_m, p.waves * p.pairs, p.blocks, p.piece, dtype};
+    const dim3 grid((unsigned)(32 * (p.tiles - p.waves * p.pairs)));
+    if (dtype == GSPARSE_F32) launch(join_kernel<INT, float>, grid, dim3(256), 0, st, (const JoinArgs&)j);
+    else if (dtype == GSPARSE_BF16) launch(join_kernel<INT, __nv_bfloat16>, grid, dim3(256), 0, st, (const JoinArgs&)j);
+    else launch(join_kernel<INT, __half>, grid, dim3(256), 0, st, (const JoinArgs&)j);
+  }
   return launch_status();
+}
+
+// A gradient's operands in the workspace: dout in planes of bf16 where it is not bf16 rows at 16-byte boundaries already, and the
+// values of the rows in 8 bits.
+struct Grad {
+  int planes;
+  bool copied;
+  int64_t stride8, stride_a, stride_b;
+  __nv_bfloat16* a;
+  __nv_bfloat16* b;
+  float* part;
+  size_t bytes;
+};
+
+Grad grad_of(void* workspace, const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens, int64_t channels, int64_t depth, bool weight) {
+  Grad g;
+  g.planes = dtype == GSPARSE_F32 ? 3 : dtype == GSPARSE_F16 ? 2 : 1;
+  g.copied = dtype != GSPARSE_BF16 || !aligned16(dout) || (tokens > 1 && (dout_stride % 8 || dout_stride < channels));
+  g.stride_a = round_up(channels, 8);
+  g.stride_b = round_up(depth, 8);
+  Carver c(workspace);
+  g.a = c.take<__nv_bfloat16>(g.copied ? g.planes * tokens * g.stride_a : 0);
+  const int64_t along = weight ? tokens : channels;
+  g.b = c.take<__nv_bfloat16>(along * g.stride_b);
+  const Plan p = plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64));
+  g.part = c.take<float>(part_entries(p));
+  g.bytes = c.off + 256;
+  return g;
+}
+
+size_t grad_bytes(const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens, int64_t channels, int64_t depth, bool weight) {
+  if (!known(dtype) || sizes(tokens, channels, depth) != GSPARSE_OK || !fits(weight ? channels : tokens, depth)) return 0;
+  return grad_of(nullptr, dout, dtype, dout_stride, tokens, channels, depth, weight).bytes;
+}
+
+template <bool WEIGHT>
+int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* q, int64_t q_stride, const float* scale, int64_t tokens,
+             int64_t channels, int64_t depth, void* out, int32_t out_dtype, int64_t out_stride, void* workspace, int32_t* d_status,
+             cudaStream_t st) {
+  const Grad g = grad_of(workspace, dout, dtype, dout_stride, tokens, channels, depth, WEIGHT);
+  const int64_t along = WEIGHT ? tokens : channels;
+  if (g.copied) {
+    const int64_t blocks = cdiv(tokens * cdiv(channels, 8), 256);
+    const dim3 grid((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16));
+    if (dtype == GSPARSE_F32)
+      launch(planes_kernel<float, 3>, grid, dim3(256), 0, st, static_cast<const float*>(dout), dout_stride, tokens, channels, g.a, g.stride_a);
+    else if (dtype == GSPARSE_F16)
+      launch(planes_kernel<__half, 2>, grid, dim3(256), 0, st, static_cast<const __half*>(dout), dout_stride, tokens, channels, g.a, g.stride_a);
+    else
+      launch(planes_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, static_cast<const __nv_bfloat16*>(dout), dout_stride, tokens, channels, g.a,
+             g.stride_a);
+  }
+  const int e = gsparse_dequantize_rows(q, q_stride, scale, along, depth, g.b, GSPARSE_BF16, g.stride_b, (gsparse_stream)st);
+  if (e != GSPARSE_OK) return e;
+  TileArgs a{};
+  if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.copied ? g.a : dout, channels, tokens, g.copied ? g.stride_a : dout_stride,
+              WEIGHT ? 64 : 128, g.planes) ||
+      !map_of(&a.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.b, depth, along, g.stride_b, 64))
+    return GSPARSE_ERR_CUDA;
+  a.d_status = d_status;
+  a.rows = WEIGHT ? channels : tokens;
+  a.cols = depth;
+  a.plane_blocks = (int)cdiv(along, 64);
+  a.out_dtype = out_dtype;
+  return tiles<false, WEIGHT>(a, plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks), g.part, out, out_stride, st);
 }
 
 }  // namespace
@@ -111,7 +751,8 @@ using namespace gs;
 extern "C" {
 
 size_t gsparse_linear_q8_workspace_size(int64_t tokens, int64_t channels, int64_t depth) {
-  return sizes(tokens, channels, depth) == GSPARSE_OK ? 256 : 0;
+  if (sizes(tokens, channels, depth) != GSPARSE_OK || !fits(tokens, channels)) return 0;
+  return 256 + (size_t)part_entries(plan_of(tokens, channels, cdiv(depth, 128))) * sizeof(float);
 }
 
 int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, const int8_t* w, int64_t w_stride, const float* w_scale,
@@ -119,18 +760,29 @@ int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, c
                       size_t workspace_bytes, int32_t* d_status, gsparse_stream stream) {
   const int st = sizes(tokens, channels, depth);
   if (st != GSPARSE_OK) return st;
+  if (!fits(tokens, channels)) return GSPARSE_ERR_UNSUPPORTED;
   if (!known(dtype)) return GSPARSE_ERR_INVALID_ARG;
   if (tokens == 0) return GSPARSE_OK;
   if (!rows8(x, x_stride, x_scale, depth) || !rows8(w, w_stride, w_scale, depth) || !matrix(out, out_stride, dtype, tokens, channels, true))
     return GSPARSE_ERR_INVALID_ARG;
   if (!space(workspace, workspace_bytes, gsparse_linear_q8_workspace_size(tokens, channels, depth))) return GSPARSE_ERR_WORKSPACE;
-  return simple<0>({x, x_scale, w, w_scale, nullptr, out, x_stride, w_stride, 0, out_stride, (int)tokens, (int)channels, (int)depth, 0, dtype},
-                   (cudaStream_t)stream);
+  TileArgs a{};
+  if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, depth, tokens, x_stride, 128) ||
+      !map_of(&a.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, depth, channels, w_stride, 128))
+    return GSPARSE_ERR_CUDA;
+  a.row_scale = x_scale;
+  a.col_scale = w_scale;
+  a.d_status = d_status;
+  a.rows = tokens;
+  a.cols = channels;
+  a.plane_blocks = (int)cdiv(depth, 128);
+  a.out_dtype = dtype;
+  return tiles<true, false>(a, plan_of(tokens, channels, a.plane_blocks), static_cast<float*>(workspace), out, out_stride, (cudaStream_t)stream);
 }
 
 size_t gsparse_linear_q8_grad_input_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens,
                                                    int64_t channels, int64_t depth) {
-  return known(dtype) && sizes(tokens, channels, depth) == GSPARSE_OK ? 256 : 0;
+  return grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, false);
 }
 
 int gsparse_linear_q8_grad_input(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* w, int64_t w_stride,
@@ -143,15 +795,14 @@ int gsparse_linear_q8_grad_input(const void* dout, int32_t dtype, int64_t dout_s
   if (!matrix(dout, dout_stride, dtype, tokens, channels, false) || !rows8(w, w_stride, w_scale, depth) ||
       !matrix(dx, dx_stride, dx_dtype, tokens, depth, true))
     return GSPARSE_ERR_INVALID_ARG;
-  if (!space(workspace, workspace_bytes, gsparse_linear_q8_grad_input_workspace_size(dout, dtype, dout_stride, tokens, channels, depth)))
-    return GSPARSE_ERR_WORKSPACE;
-  return simple<1>({nullptr, nullptr, w, w_scale, dout, dx, 0, w_stride, dout_stride, dx_stride, (int)tokens, (int)channels, (int)depth, dtype, dx_dtype},
-                   (cudaStream_t)stream);
+  if (!space(workspace, workspace_bytes, grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, false))) return GSPARSE_ERR_WORKSPACE;
+  return gradient<false>(dout, dtype, dout_stride, w, w_stride, w_scale, tokens, channels, depth, dx, dx_dtype, dx_stride, workspace, d_status,
+                         (cudaStream_t)stream);
 }
 
 size_t gsparse_linear_q8_grad_weight_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens,
                                                     int64_t channels, int64_t depth) {
-  return known(dtype) && sizes(tokens, channels, depth) == GSPARSE_OK ? 256 : 0;
+  return grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, true);
 }
 
 int gsparse_linear_q8_grad_weight(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* x, int64_t x_stride,
@@ -170,10 +821,9 @@ int gsparse_linear_q8_grad_weight(const void* dout, int32_t dtype, int64_t dout_
     return GSPARSE_OK;
   }
   if (!matrix(dout, dout_stride, dtype, tokens, channels, false) || !rows8(x, x_stride, x_scale, depth)) return GSPARSE_ERR_INVALID_ARG;
-  if (!space(workspace, workspace_bytes, gsparse_linear_q8_grad_weight_workspace_size(dout, dtype, dout_stride, tokens, channels, depth)))
-    return GSPARSE_ERR_WORKSPACE;
-  return simple<2>({x, x_scale, nullptr, nullptr, dout, dweight, x_stride, 0, dout_stride, dweight_stride, (int)tokens, (int)channels, (int)depth, dtype, GSPARSE_F32},
-                   s);
+  if (!space(workspace, workspace_bytes, grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, true))) return GSPARSE_ERR_WORKSPACE;
+  return gradient<true>(dout, dtype, dout_stride, x, x_stride, x_scale, tokens, channels, depth, dweight, GSPARSE_F32, dweight_stride, workspace,
+                        d_status, s);
 }
 
 }  // extern "C"
