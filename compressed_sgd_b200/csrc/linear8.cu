@@ -17,23 +17,24 @@ namespace {
 constexpr int kTile = 256;                 // of a pair, both ways; a CTA loads and holds 128 rows of each operand
 constexpr int kRowBytes = 128;             // of an operand's row in a stage: 128 int8 or 64 bf16 (one swizzle atom)
 constexpr int kOperand = 128 * kRowBytes;  // bytes of one operand of one CTA in a stage
-constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = (kEpilogueWarps + 2) * 32;
 constexpr int kBox = 32 * 128;             // a warp's part of the result on its way out: 32 rows of 128 bytes
 
-// The sums in bf16 are taken out of the tensor core every 4 blocks of 64 and added up in fp32 registers: its accumulation
-// cuts off (towards zero), 16 times in a row at most then.
-constexpr int kChunk = 4;
-
+// Integers leave the tensor memory once a tile, but soon (a depth of 512 takes a pair a microsecond): 16 warps of 64 columns. Sums
+// in bf16 stay in registers over a tile: 8 warps of 128 columns, with the registers that the other warps give up.
 template <bool INT> struct Layout {
+  static constexpr int warps = INT ? 16 : 8;                   // that take results out
+  static constexpr int side = 4 * kTile / warps;               // columns of such a warp
+  static constexpr int threads = (warps + (INT ? 2 : 4)) * 32; // setmaxnreg goes by groups of four warps
   static constexpr int stages = INT ? 5 : 6;
-  static constexpr int boxes = INT ? 2 : 1;
   static constexpr int stage_bytes = 2 * kOperand;
   static constexpr int box_at = stages * stage_bytes;
-  static constexpr int scale_at = box_at + kEpilogueWarps * boxes * kBox;
+  static constexpr int scale_at = box_at + warps * kBox;
   static constexpr int bar_at = scale_at + (INT ? 2 * kTile * 4 : 0);
-  static constexpr int bytes = bar_at + 256;
+  static constexpr int shared = bar_at + 256;
 };
+using LB = Layout<false>;
+constexpr int kMore = 216, kFewer = 72;      // registers of these and of the others, out of the 168 of the launch
+static_assert(LB::warps * 32 * kMore + 128 * kFewer <= LB::threads * 168, "");
 
 struct TileArgs {
   CUtensorMap a, b, out, part;
@@ -44,8 +45,9 @@ struct TileArgs {
   int64_t as_tiles;                        // columns of D that the tensor map describes: a copy ends at a multiple of 16 bytes
   int32_t* d_status;
   int64_t rows, cols;                      // of D
-  int tiles_m, tiles;                      // tile t is (t % tiles_m, t / tiles_m)
+  int tiles_m, tiles_n, band;
   int blocks, plane_blocks;                // of 128 bytes along s, all planes; of one plane
+  int chunk;                               // blocks of bf16 that are summed in the tensor core
   int pairs, waves;                        // tiles below waves * pairs are whole; the others are split
   int piece;                               // blocks of a pair's part of the split tiles (0: none are split)
   int out_dtype;
@@ -65,21 +67,25 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Waits for a phase; false after about a second. The arrivals may come from the other CTA.
+// Waits for a phase; false after about a second. What these barriers guard is copied and multiplied by asynchronous units and read
+// from tensor memory, so neither the waits nor the arrivals order plain memory accesses over the cluster: a release of that
+// scope before each arrival was a third of the warps' time that take results out. The time that a wait may sleep (in ns) keeps the
+// warps that wait from the issue slots and from the power that the others need: 282 against 268 us for the gradient by 85000 x 512
+// weights over 4000 tokens.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_u32(bar);
   uint32_t ok = 0;
   const long long t0 = clock64();
   do {
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok) : "r"(at), "r"(parity) : "memory");
   } while (!ok && clock64() - t0 < kWaitCycles);
   return ok != 0;
 }
 
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Copies of a box into this CTA's shared memory that count on a barrier of the pair's first CTA.
@@ -141,6 +147,16 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // ---- work of a pair -----------------------------------------------------------------------------------------
 
+// Tile t: bands of `band` tiles of the shorter way, along the longer, so that the tiles under way at a time share rows of both operands.
+__device__ __forceinline__ void place_of(int t, int tiles_m, int tiles_n, int band, int& m, int& n) {
+  const bool wide = tiles_n > tiles_m;
+  const int across = wide ? tiles_m : tiles_n, along = wide ? tiles_n : tiles_m;
+  const int b = t / (band * along), left = t - b * band * along, width = min(band, across - b * band);
+  const int x = b * band + left % width, y = left / width;
+  m = wide ? x : y;
+  n = wide ? y : x;
+}
+
 // The i-th part of a pair's work: blocks [from, to) of a tile, and whether they are all of it (else its place among the parts).
 struct Part {
   int m, n, from, to, slot;
@@ -152,12 +168,12 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part
   p.slot = 0;
   if (i < a.waves || a.piece == 0) {
     tile = pair + i * a.pairs;
-    if (tile >= a.tiles) return false;
+    if (tile >= a.tiles_m * a.tiles_n) return false;
     p.from = 0;
     p.to = a.blocks;
   } else {
     const int k = i - a.waves;                                  // a pair's range of blocks meets at most two tiles
-    const int64_t all = (int64_t)(a.tiles - a.waves * a.pairs) * a.blocks;
+    const int64_t all = (int64_t)(a.tiles_m * a.tiles_n - a.waves * a.pairs) * a.blocks;
     const int64_t first = (int64_t)pair * a.piece, last = min(all, first + a.piece);
     if (first >= last) return false;
     const int64_t t = first / a.blocks + k;
@@ -169,8 +185,7 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part
     p.slot = pair * 2 + k;
   }
   p.whole = p.to - p.from == a.blocks;
-  p.m = tile % a.tiles_m;
-  p.n = tile / a.tiles_m;
+  place_of(tile, a.tiles_m, a.tiles_n, a.band, p.m, p.n);
   return true;
 }
 
@@ -225,22 +240,17 @@ __device__ void box_to_rows(const char* box, int lane, T* out, int64_t stride, i
   }
 }
 
-// One warp's box on its way: the boxes of a warp are used in turn.
+// A warp's box on its way.
 struct Way {
-  char* boxes;
-  int lane, count, turn;
+  char* box;
+  int lane;
 
-  __device__ __forceinline__ char* next() {
-    char* box = boxes + (count > 1 ? (turn & 1) * kBox : 0);
-    ++turn;
-    if (lane == 0) {
-      if (count > 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    }
+  // Once what it held has been read.
+  __device__ __forceinline__ void next() {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
-    return box;
   }
-  __device__ __forceinline__ void send(const CUtensorMap* map, int64_t x, int64_t y, char* box) {
+  __device__ __forceinline__ void send(const CUtensorMap* map, int64_t x, int64_t y) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) store_box(map, (int)x, (int)y, smem_u32(box));
@@ -249,41 +259,44 @@ struct Way {
 
 // A warp's 32 x 32 results v at (row, col) of D, the `half`-th of a box of 16-bit types.
 template <class T>
-__device__ __forceinline__ void put_result(const TileArgs& a, Way& way, char*& box, int half, const float* v, int64_t row, int64_t col) {
+__device__ __forceinline__ void put_result(const TileArgs& a, Way& way, int half, const float* v, int64_t row, int64_t col) {
   constexpr bool narrow = sizeof(T) == 2;
-  if (!narrow || half == 0) box = way.next();
-  into_box<T>(box, way.lane, narrow ? half * 4 : 0, v);
+  if (!narrow || half == 0) way.next();
+  into_box<T>(way.box, way.lane, narrow ? half * 4 : 0, v);
   if (narrow && half == 0) return;
   const int64_t x = narrow ? col - 32 : col;
   if (row >= a.rows || x >= a.cols) return;
   if (x + 128 / (int)sizeof(T) <= a.as_tiles || a.as_tiles == a.cols) {
-    way.send(&a.out, x, row, box);
+    way.send(&a.out, x, row);
   } else {
     __syncwarp();
-    box_to_rows<T>(box, way.lane, static_cast<T*>(a.result), a.result_stride, row, x, a.rows, a.cols);
+    box_to_rows<T>(way.box, way.lane, static_cast<T*>(a.result), a.result_stride, row, x, a.rows, a.cols);
     __syncwarp();
   }
 }
 
-__device__ __forceinline__ void put(const TileArgs& a, Way& way, char*& box, int half, const float* v, int64_t row, int64_t col) {
-  if (a.out_dtype == GSPARSE_F32) put_result<float>(a, way, box, half, v, row, col);
-  else if (a.out_dtype == GSPARSE_BF16) put_result<__nv_bfloat16>(a, way, box, half, v, row, col);
-  else put_result<__half>(a, way, box, half, v, row, col);
+__device__ __forceinline__ void put(const TileArgs& a, Way& way, int half, const float* v, int64_t row, int64_t col) {
+  if (a.out_dtype == GSPARSE_F32) put_result<float>(a, way, half, v, row, col);
+  else if (a.out_dtype == GSPARSE_BF16) put_result<__nv_bfloat16>(a, way, half, v, row, col);
+  else put_result<__half>(a, way, half, v, row, col);
 }
 
 // A part of a tile's sums, as they are: row r of slot k at row k * 256 + r of the workspace.
 __device__ __forceinline__ void put_part(const TileArgs& a, Way& way, const float* v, int64_t row, int col) {
-  char* box = way.next();
-  into_box<float>(box, way.lane, 0, v);
-  way.send(&a.part, col, row, box);
+  way.next();
+  into_box<float>(way.box, way.lane, 0, v);
+  way.send(&a.part, col, row);
 }
 
 // ---- the kernel -----------------------------------------------------------------------------------------------
 
-// Warps 0 to 7 take results out (warp w the lanes 32 (w % 4) and the columns 128 (w / 4) on), warp 8 loads, warp 9 multiplies (of
-// the pair's first CTA, for both). The loads run ahead over all of a pair's parts; the tensor memory holds two tiles of sums.
+// The first warps take results out (warp w the lanes 32 (w % 4) and the columns `side` (w / 4) on), the next loads, one more
+// multiplies (of the pair's first CTA, for both). The loads run ahead over all of a pair's parts; the tensor memory holds two tiles of sums.
+//
+// The sums in bf16 are taken out of the tensor core every `chunk` blocks of 64 and added up in fp32 registers, since its
+// accumulation cuts off, towards zero.
 template <bool INT, bool A_ACROSS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads, 1) tile_kernel(const __grid_constant__ TileArgs a) {
   extern __shared__ __align__(1024) char smem[];
   using L = Layout<INT>;
   constexpr bool kAcross = !INT;                               // B's rows
@@ -304,12 +317,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_ke
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sums_full + i, 1);
-      mbar_init(sums_empty + i, 2 * kEpilogueWarps);
+      mbar_init(sums_empty + i, 2 * L::warps);
     }
     mbar_init(drained, 1);
     fence_mbarrier_init();
   }
-  if (warp == 9) {
+  if (warp == L::warps + 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     fence_before();
@@ -323,18 +336,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_ke
 
   bool ok = true;
   Part p;
-  if (warp == 8) {
-    if (lane == 0) {
-      uint32_t n = 0;                                          // stages filled so far
+  if (warp >= L::warps) {
+    if constexpr (!INT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewer));
+    if (warp == L::warps && lane == 0) {
+      uint32_t n = 0, s = 0, turn = 0;                         // stages filled so far; the next, and its turn
       for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
+        const int m = p.m * kTile + (int)rank * 128, c = p.n * kTile + (int)rank * 128;
+        int plane = p.from / a.plane_blocks, k = p.from - plane * a.plane_blocks;
         for (int kb = p.from; kb < p.to; ++kb, ++n) {
-          const int s = (int)(n % L::stages);
-          if (n >= L::stages && !(ok = wait_phase(empty + s, (n / L::stages - 1) & 1))) break;
+          if (turn && !(ok = wait_phase(empty + s, (turn - 1) & 1))) break;
           if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * L::stage_bytes);
           const uint32_t bar = in_cta(smem_u32(full + s), 0);
           const uint32_t at = smem_u32(smem + s * L::stage_bytes);
-          const int plane = kb / a.plane_blocks, k = kb - plane * a.plane_blocks;
-          const int m = p.m * kTile + (int)rank * 128, c = p.n * kTile + (int)rank * 128;
           if constexpr (INT) {
             load_box(at, &a.a, k * 128, m, bar);
             load_box(at + kOperand, &a.b, k * 128, c, bar);
@@ -348,28 +361,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_ke
             load_box(at + kOperand, &a.b, c, k * 64, bar);
             load_box(at + kOperand + kOperand / 2, &a.b, c + 64, k * 64, bar);
           }
+          if (++s == L::stages) s = 0, ++turn;
+          if (++k == a.plane_blocks) k = 0, ++plane;
         }
       }
       if (!ok) {
         raise(a.d_status, GSPARSE_DERR_TIMEOUT);
         if (rank == 0)                                         // the copies under way, of both CTAs
-          for (uint32_t k = n > L::stages ? n - L::stages : 0; k < n; ++k) wait_phase(full + k % L::stages, (k / L::stages) & 1);
+          for (uint32_t b = n > L::stages ? n - L::stages : 0; b < n; ++b) wait_phase(full + b % L::stages, (b / L::stages) & 1);
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0 && rank == 0) {
+    if (warp == L::warps + 1 && lane == 0 && rank == 0) {
       constexpr uint32_t what = (INT ? 2u << 4 : 1u << 4) | 1u << 7 | 1u << 10 | (A_ACROSS ? 1u << 15 : 0u) | (kAcross ? 1u << 16 : 0u) |
                                 (uint32_t)(kTile >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
-      uint32_t n = 0, c = 0;                                   // stages used, sums begun
+      uint32_t s = 0, turn = 0, c = 0;                         // the next stage and its turn, sums begun
       for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
         for (int kb = p.from; ok && kb < p.to; ++c) {
-          const int end = INT ? p.to : min(p.to, kb + kChunk);
+          const int end = INT ? p.to : min(p.to, kb + a.chunk);
           const uint32_t buf = c & 1, d = tmem + buf * kTile;
           if (c >= 2 && !(ok = wait_phase(sums_empty + buf, (c / 2 - 1) & 1))) break;
           fence_after();
-          for (bool add = false; kb < end; ++kb, ++n) {
-            const int s = (int)(n % L::stages);
-            if (!(ok = wait_phase(full + s, (n / L::stages) & 1))) break;
+          for (bool add = false; kb < end; ++kb) {
+            if (!(ok = wait_phase(full + s, turn & 1))) break;
             fence_after();
             const uint32_t at = smem_u32(smem + s * L::stage_bytes);
 #pragma unroll
@@ -379,6 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_ke
               add = true;
             }
             commit(empty + s);
+            if (++s == L::stages) s = 0, ++turn;
           }
           if (ok) commit(sums_full + buf);
         }
@@ -390,83 +404,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_ke
       }
     }
   } else {
+    if constexpr (!INT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore));
     const int quarter = warp & 3, side = warp >> 2;
-    const int64_t first_row = (int64_t)rank * 128 + quarter * 32;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 128;
+    const int first_row = (int)rank * 128 + quarter * 32, first_col = side * L::side;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + first_col;
     const uint32_t give = in_cta(smem_u32(sums_empty), 0);
-    Way way{smem + L::box_at + warp * L::boxes * kBox, lane, L::boxes, 0};
+    Way way{smem + L::box_at + warp * kBox, lane};
     uint32_t c = 0;
     // (after a wait that gave up: on to the end, since the warps of a side meet at a barrier for each part)
-    for (int i = 0; part_of(a, pair, i, p); ++i) {
-      const int64_t row = (int64_t)p.m * kTile + first_row, col = (int64_t)p.n * kTile + side * 128;
-      const int64_t part_row = (int64_t)p.slot * kTile + first_row;
-      char* box = nullptr;
-      if constexpr (INT) {
+    if constexpr (INT) {
+      // the scales of a part's rows, and of its columns for the four warps that take the same ones: read a part ahead
+      float row_scale, col_scale;
+      auto scales_of = [&](const Part& q) {
+        const int64_t row = (int64_t)q.m * kTile + first_row + lane, col = (int64_t)q.n * kTile + first_col + (quarter & 1) * 32 + lane;
+        row_scale = row < a.rows ? __ldg(a.row_scale + row) : 0.0f;
+        col_scale = col < a.cols ? __ldg(a.col_scale + col) : 0.0f;
+      };
+      bool more = part_of(a, pair, 0, p);
+      if (more) scales_of(p);
+      for (int i = 0; more; ++c) {
         const uint32_t buf = c & 1;
-        // the scales of the tile's columns, for the four warps that take the same columns
-        float* scales = reinterpret_cast<float*>(smem + L::scale_at) + buf * kTile + side * 128;
-        const int64_t at = col + quarter * 32 + lane;
-        scales[quarter * 32 + lane] = at < a.cols ? __ldg(a.col_scale + at) : 0.0f;
-        const float mine = row + lane < a.rows ? __ldg(a.row_scale + row + lane) : 0.0f;
+        float* scales = reinterpret_cast<float*>(smem + L::scale_at) + buf * kTile + first_col;
+        if (quarter < 2) scales[quarter * 32 + lane] = col_scale;
+        const float mine = row_scale;
+        const int64_t row = (int64_t)p.m * kTile + first_row, col = (int64_t)p.n * kTile + first_col;
+        const int64_t part_row = (int64_t)p.slot * kTile + first_row;
+        const bool whole = p.whole;
+        more = part_of(a, pair, ++i, p);
+        if (more) scales_of(p);
         asm volatile("bar.sync %0, 128;" ::"r"(side + 1) : "memory");
         if (!(ok = ok && wait_phase(sums_full + buf, (c / 2) & 1))) continue;
         fence_after();
+        uint32_t raw[2][32];
+        load_columns(raw[0], lanes + buf * kTile);
+        load_columns(raw[1], lanes + buf * kTile + 32);
+        columns_loaded();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(give + buf * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t raw[32];
-          load_columns(raw, lanes + buf * kTile + j * 32);
-          columns_loaded();
-          if (j == 3) {
-            fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(give + buf * 8);
-          }
+        for (int j = 0; j < 2; ++j) {
           float v[32];
-          if (p.whole) {
+          if (whole) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
-              const float4 s = *reinterpret_cast<const float4*>(scales + j * 32 + k);
-              v[k] = __int2float_rn((int)raw[k]) * mine * s.x;
-              v[k + 1] = __int2float_rn((int)raw[k + 1]) * mine * s.y;
-              v[k + 2] = __int2float_rn((int)raw[k + 2]) * mine * s.z;
-              v[k + 3] = __int2float_rn((int)raw[k + 3]) * mine * s.w;
+              const float4 f = *reinterpret_cast<const float4*>(scales + j * 32 + k);
+              v[k] = __int2float_rn((int)raw[j][k]) * mine * f.x;
+              v[k + 1] = __int2float_rn((int)raw[j][k + 1]) * mine * f.y;
+              v[k + 2] = __int2float_rn((int)raw[j][k + 2]) * mine * f.z;
+              v[k + 3] = __int2float_rn((int)raw[j][k + 3]) * mine * f.w;
             }
-            put(a, way, box, j & 1, v, row, col + j * 32);
+            put(a, way, j, v, row, col + j * 32);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
-            put_part(a, way, v, part_row, side * 128 + j * 32);
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[j][k]);
+            put_part(a, way, v, part_row, first_col + j * 32);
           }
         }
-        ++c;
-      } else {
-        float sum[128];
-        for (int kb = p.from; ok && kb < p.to; kb += kChunk, ++c) {
+      }
+    } else {
+      for (int i = 0; part_of(a, pair, i, p); ++i) {
+        float sum[L::side];
+        for (int kb = p.from; ok && kb < p.to; kb += a.chunk, ++c) {
           const uint32_t buf = c & 1;
           if (!(ok = wait_phase(sums_full + buf, (c / 2) & 1))) break;
           fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < L::side; j += 32) {
             uint32_t raw[32];
-            load_columns(raw, lanes + buf * kTile + j * 32);
+            load_columns(raw, lanes + buf * kTile + j);
             columns_loaded();
             if (kb == p.from) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sum[j * 32 + k] = __uint_as_float(raw[k]);
+              for (int k = 0; k < 32; ++k) sum[j + k] = __uint_as_float(raw[k]);
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sum[j * 32 + k] += __uint_as_float(raw[k]);
+              for (int k = 0; k < 32; ++k) sum[j + k] += __uint_as_float(raw[k]);
             }
           }
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_at(give + buf * 8);
         }
-        if (!ok) continue;
+        if (!ok) break;
+        const int64_t row = (int64_t)p.m * kTile + first_row, col = (int64_t)p.n * kTile + first_col;
+        const int64_t part_row = (int64_t)p.slot * kTile + first_row;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (p.whole) put(a, way, box, j & 1, sum + j * 32, row, col + j * 32);
-          else put_part(a, way, sum + j * 32, part_row, side * 128 + j * 32);
+        for (int j = 0; j < L::side / 32; ++j) {
+          if (p.whole) put(a, way, j & 1, sum + j * 32, row, col + j * 32);
+          else put_part(a, way, sum + j * 32, part_row, first_col + j * 32);
         }
       }
     }
@@ -477,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) tile_ke
   // nobody leaves while the other CTA may still reach into its shared or tensor memory
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (warp == 9) {
+  if (warp == L::warps + 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
@@ -491,7 +517,7 @@ struct JoinArgs {
   const float* col_scale;
   void* out;
   int64_t out_stride, rows, cols;
-  int tiles_m, first_tile, blocks, piece, out_dtype;
+  int tiles_m, tiles_n, band, first_tile, blocks, piece;
 };
 
 // The parts of a split tile added up in their order along s. A block takes 8 rows of a tile, a thread 8 entries of one row.
@@ -503,7 +529,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   const int64_t from = (int64_t)t * a.blocks, to = from + a.blocks;
   const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
   if (first == last) return;                       // whole after all
-  const int64_t row = (int64_t)(tile % a.tiles_m) * kTile + r, col = (int64_t)(tile / a.tiles_m) * kTile + c;
+  int m, n;
+  place_of(tile, a.tiles_m, a.tiles_n, a.band, m, n);
+  const int64_t row = (int64_t)m * kTile + r, col = (int64_t)n * kTile + c;
   if (row >= a.rows || col >= a.cols) return;
   uint32_t sum[8];
   for (int pair = first; pair <= last; ++pair) {
@@ -622,14 +650,18 @@ CUtensorMapDataType map_type(int32_t dtype) {
 }
 
 // How the tiles of D are shared out: whole tiles in waves over the pairs of SMs; what is left over is split along s.
+constexpr int kBand = 8;
+
 struct Plan {
-  int tiles_m, tiles, blocks, pairs, waves, piece;
+  int tiles_m, tiles_n, tiles, band, blocks, pairs, waves, piece;
 };
 
 Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
   Plan p;
   p.tiles_m = (int)cdiv(rows, kTile);
-  p.tiles = (int)(p.tiles_m * cdiv(cols, kTile));
+  p.tiles_n = (int)cdiv(cols, kTile);
+  p.tiles = p.tiles_m * p.tiles_n;
+  p.band = min(min(p.tiles_m, p.tiles_n), kBand);
   p.blocks = (int)blocks;
   p.pairs = sm_count() / 2;
   p.waves = p.tiles / p.pairs;
@@ -646,13 +678,14 @@ bool fits(int64_t rows, int64_t cols) { return cdiv(rows, kTile) * cdiv(cols, kT
 
 template <bool INT, bool A_ACROSS>
 int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride, cudaStream_t st) {
-  using L = Layout<INT>;
   a.tiles_m = p.tiles_m;
-  a.tiles = p.tiles;
+  a.tiles_n = p.tiles_n;
+  a.band = p.band;
   a.blocks = p.blocks;
   a.pairs = p.pairs;
   a.waves = p.waves;
   a.piece = p.piece;
+  using L = Layout<INT>;
   const int32_t dtype = a.out_dtype;
   const int bytes = (int)size_of(dtype);
   const bool as_tiles = aligned16(out) && (a.rows == 1 || (out_stride * bytes) % 16 == 0);
@@ -662,14 +695,14 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
   if (a.as_tiles && !map_of(&a.out, map_type(dtype), bytes, out, a.as_tiles, a.rows, out_stride, 32)) return GSPARSE_ERR_CUDA;
   if (p.piece && !map_of(&a.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, part, kTile, 2 * (int64_t)p.pairs * kTile, kTile, 32)) return GSPARSE_ERR_CUDA;
   auto* kernel = tile_kernel<INT, A_ACROSS>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::shared) != cudaSuccess) {
     cudaGetLastError();
     return GSPARSE_ERR_CUDA;
   }
   const int used = p.piece || p.waves ? p.pairs : p.tiles;
-  launch(kernel, dim3((unsigned)(2 * used)), dim3(kThreads), L::bytes, st, (const TileArgs&)a);
+  launch(kernel, dim3((unsigned)(2 * used)), dim3(L::threads), L::shared, st, (const TileArgs&)a);
   if (p.piece) {
-    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.tiles_m, p.waves * p.pairs, p.blocks, p.piece, dtype};
+    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.tiles_m, p.tiles_n, p.band, p.waves * p.pairs, p.blocks, p.piece};
     const dim3 grid((unsigned)(32 * (p.tiles - p.waves * p.pairs)));
     if (dtype == GSPARSE_F32) launch(join_kernel<INT, float>, grid, dim3(256), 0, st, (const JoinArgs&)j);
     else if (dtype == GSPARSE_BF16) launch(join_kernel<INT, __nv_bfloat16>, grid, dim3(256), 0, st, (const JoinArgs&)j);
@@ -740,6 +773,9 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
   a.cols = depth;
   a.plane_blocks = (int)cdiv(along, 64);
   a.out_dtype = out_dtype;
+  // 512 products of bf16 in a row (32 accumulations) are off by 6e-7 of the result, as the 4000 of a plain fp32 sum are; gradients in
+  // fp32 keep to half of that, and results of 16 bits, which are rounded to 2^-9 and 2^-12, take 2048.
+  a.chunk = dtype == GSPARSE_F32 ? 4 : out_dtype == GSPARSE_F32 ? 8 : 32;
   return tiles<false, WEIGHT>(a, plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks), g.part, out, out_stride, st);
 }
 

@@ -9,9 +9,10 @@ Tolerances count roundings, u = 2^-24 (half a step of fp32), half = eps / 2 of t
    joins and 3 more roundings a term: 32 u of the mean of |g xh|. dx adds 4 roundings to each part. dweight: a chain over a
    block's rows and over the blocks' parts.
  - the product: the sum is exact, it is rounded to fp32 and two factors multiply it: 3 u, then half.
- - the gradients: sums of S products that are exact in fp32. Up to 256 of them in the matrix unit: 16 accumulations, each
-   cut off rather than rounded (2 u of what is held), and 17 aligned terms an accumulation: 64 u in all; then S / 256 + 12 additions
-   in fp32: (64 + S / 256 + 12) u of the sum of |products|, then u or half for the result."""
+ - the gradients: sums of S products that are exact in fp32, C of them in the matrix unit (256 of an fp32 gradient, else 512
+   for results in fp32 and 2048 for results of 16 bits): C / 16 accumulations, each cut off rather than rounded (2 u of what is
+   held), and 17 aligned terms in a product's own: C / 8 + 34 u; then S / C + 12 additions in fp32, all of the sum of
+   |products|, then u or half for the result."""
 import threading
 
 import numpy as np
@@ -425,9 +426,10 @@ def test_product_shares_rows(tokens):
 
 # its gradients ------------------------------------------------------------------------------------------
 
-def sums_tolerance(size, terms, dtype, want):
-    """size: the sum of |products|."""
-    part = (64 + terms / 256 + 12) * U * size
+def sums_tolerance(size, terms, dtype, want, gradient="bf16"):
+    """size: the sum of |products|; gradient: the type of dout."""
+    unit = 256 if gradient == "fp32" else 512 if dtype == "fp32" else 2048
+    part = (unit / 8 + 34 + terms / unit + 12) * U * size
     return part + half(dtype) * (np.abs(want) + part) * 1.01 + 1.01 * TINY[dtype]
 
 
@@ -461,9 +463,9 @@ def check_gradients(dout, x, w, dtype, dx_dtype=None):
     planes = {"bf16": 1, "fp16": 2, "fp32": 3}[dtype]
     want = layer.linear_grad_input(g, wq, ws)
     assert (np.abs(want) < overflow(dx_dtype)).all()
-    close(dx, want, sums_tolerance(layer.linear_grad_input(np.abs(g), np.abs(wq.astype(float)), ws), planes * channels, dx_dtype, want), "dx")
+    close(dx, want, sums_tolerance(layer.linear_grad_input(np.abs(g), np.abs(wq.astype(float)), ws), planes * channels, dx_dtype, want, dtype), "dx")
     want = layer.linear_grad_weight(g, xq, xs)
-    close(dw, want, sums_tolerance(layer.linear_grad_weight(np.abs(g), np.abs(xq.astype(float)), xs), planes * tokens, "fp32", want), "dweight")
+    close(dw, want, sums_tolerance(layer.linear_grad_weight(np.abs(g), np.abs(xq.astype(float)), xs), planes * tokens, "fp32", want, dtype), "dweight")
     return flat
 
 
@@ -557,7 +559,7 @@ def test_products_beyond_32_bits():
     dx = gs.linear_q8_grad_input(dout, w, dtype=torch.float32)
     last = gs.linear_q8_grad_input(dout[-3:], w, dtype=torch.float32)
     size = f64(dout[-3:].abs()) @ np.abs(w.q.cpu().numpy().astype(float) * f64(w.scale)[:, None])
-    close(dx[-3:], f64(last), 2 * (64 + channels / 256 + 13) * U * size, "dx")
+    close(dx[-3:], f64(last), 2 * (64 + 34 + channels / 512 + 13) * U * size, "dx")
     dw = gs.linear_q8_grad_weight(dout, x)
     cols = slice(channels - 4, channels)
     g = f64(dout[:, cols])
