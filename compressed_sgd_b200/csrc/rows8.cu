@@ -23,13 +23,19 @@ template <> struct Type<float> {
 };
 template <> struct Type<__nv_bfloat16> {
   static constexpr int N = 8;
+  using Two = __nv_bfloat162;
   static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ float2 get(Two v) { return __bfloat1622float2(v); }
+  static __device__ __forceinline__ Two put(float a, float b) { return __floats2bfloat162_rn(a, b); }
 };
 template <> struct Type<__half> {
   static constexpr int N = 8;
+  using Two = __half2;
   static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ float2 get(Two v) { return __half22float2(v); }
+  static __device__ __forceinline__ Two put(float a, float b) { return __floats2half2_rn(a, b); }
 };
 
 // A thread's E entries of a row of `depth`: with VEC as vectors of 16 bytes, thread after thread; else entry by entry, thread
@@ -39,37 +45,66 @@ struct Mine {
   static constexpr int N = VEC ? Type<T>::N : 1;
   static __device__ __forceinline__ int first(int j, int tid, int threads) { return (j * threads + tid) * N; }
 
-  static __device__ __forceinline__ void load(float (&v)[E], const T* row, int depth, int tid, int threads) {
+  // As they lie in memory, and as numbers.
+  union Raw {
+    uint4 vec[E * sizeof(T) / 16];
+    T one[E];
+    __device__ __forceinline__ Raw() {}
+  };
+
+  static __device__ __forceinline__ void fetch(Raw& raw, const T* row, int depth, int tid, int threads) {
 #pragma unroll
     for (int j = 0; j < E / N; ++j) {
       const int at = first(j, tid, threads);
-      if constexpr (VEC) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (at < depth) raw = *reinterpret_cast<const uint4*>(row + at);
-        const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j * N + i] = Type<T>::get(e[i]);
-      } else {
-        v[j] = at < depth ? Type<T>::get(row[at]) : 0.0f;
-      }
+      if constexpr (VEC) raw.vec[j] = at < depth ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0, 0, 0, 0);
+      else raw.one[j] = at < depth ? row[at] : Type<T>::put(0.0f);
     }
   }
 
-  static __device__ __forceinline__ void store(T* row, const float (&v)[E], int depth, int tid, int threads) {
+  static __device__ __forceinline__ void numbers(float (&v)[E], const Raw& raw) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const float2 f = Type<T>::get(*reinterpret_cast<const typename Type<T>::Two*>(raw.one + i));
+        v[i] = f.x;
+        v[i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = raw.one[i];
+    }
+  }
+
+  static __device__ __forceinline__ void held(Raw& raw, const float (&v)[E]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < E; i += 2) *reinterpret_cast<typename Type<T>::Two*>(raw.one + i) = Type<T>::put(v[i], v[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) raw.one[i] = v[i];
+    }
+  }
+
+  static __device__ __forceinline__ void write(T* row, const Raw& raw, int depth, int tid, int threads) {
 #pragma unroll
     for (int j = 0; j < E / N; ++j) {
       const int at = first(j, tid, threads);
       if (at >= depth) continue;
-      if constexpr (VEC) {
-        uint4 raw;
-        T* e = reinterpret_cast<T*>(&raw);
-#pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = Type<T>::put(v[j * N + i]);
-        *reinterpret_cast<uint4*>(row + at) = raw;
-      } else {
-        row[at] = Type<T>::put(v[j]);
-      }
+      if constexpr (VEC) *reinterpret_cast<uint4*>(row + at) = raw.vec[j];
+      else row[at] = raw.one[j];
     }
+  }
+
+  static __device__ __forceinline__ void load(float (&v)[E], const T* row, int depth, int tid, int threads) {
+    Raw raw;
+    fetch(raw, row, depth, tid, threads);
+    numbers(v, raw);
+  }
+
+  static __device__ __forceinline__ void store(T* row, const float (&v)[E], int depth, int tid, int threads) {
+    Raw raw;
+    held(raw, v);
+    write(row, raw, depth, tid, threads);
   }
 
   // N entries of 16 bits; with VEC they start at a multiple of their own size.
@@ -121,6 +156,7 @@ struct RowArgs {
   float* scale;
   float* rstd;
   int64_t rows, x_stride, residual_stride, h_stride, y_stride, q_stride;
+  double inv_depth;
   int depth, weight_dtype, warps;   // warps of a row
   float eps;
 };
@@ -136,27 +172,43 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {
   return e < -126 ? -126 : e > 121 ? 121 : e;     // 121: 64 * 2^122 is no fp32 number
 }
 
-template <bool NORM>
-struct Scaled {
-  float hi, lo;
-  // y = v r w as a sum hi + lo that is good to about 2^-46, so that an entry next to a border between two steps of the 8
-  // bits falls on the side that the formula says.
-  __device__ __forceinline__ Scaled(float v, float r_hi, float r_lo, float w) {
-    if constexpr (NORM) {
-      const float rw = __fmul_rn(r_hi, w);
-      const float rw_lo = __fmaf_rn(r_hi, w, -rw) + r_lo * w;
-      hi = __fmul_rn(v, rw);
-      lo = __fmaf_rn(v, rw, -hi) + v * rw_lo;
-    } else {
-      hi = v;
-      lo = 0.0f;
-    }
-  }
-};
+// (ms)^(-1/2): two steps of Newton's iteration from the fp32 value, 2^-22 -> 2^-43 -> 2^-52 or so.
+__device__ __forceinline__ double inverse_root(double ms) {
+  if (!(ms < 0x1p100)) return 1.0 / sqrt(ms);      // beyond fp32, infinite, NaN (from below eps keeps it off)
+  double r = (double)rsqrtf((float)ms);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __fma_rn(0.5 * r, __fma_rn(-ms * r, r, 1.0), r);
+  return r;
+}
+
+// The larger one, NaN where one is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kRound = 12582912.0f;              // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
+
+// An entry's number of steps, v r w / 2^e, in two parts (good to about 2^-45 of it), rounded: what the formula gives in 64 bits.
+__device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float w, float up) {
+  const float rw = __fmul_rn(r_hi, w);
+  const float rw_lo = __fmaf_rn(r_lo, w, __fmaf_rn(r_hi, w, -rw));
+  const float hi = __fmul_rn(v, rw);
+  const float lo = __fmaf_rn(v, rw_lo, __fmaf_rn(v, rw, -hi));
+  const float t = hi * up;
+  const float m = t + kRound;
+  const float d = __fmaf_rn(lo, up, t - (m - kRound));       // the difference is exact
+  return m + ((d + kRound) - kRound);                        // -1, 0 or 1 more
+}
 
 // One pass over the rows: the sum with the residual, the norm, the 8 bits. A row stays in its threads' registers.
+//
+// An entry's steps t come from three fp32 roundings, so they are off by less than 2^-15: only those that lie closer than 2^-14 to
+// the middle between two integers (one of 2^13) are worked out again in two parts. All of them in two parts, with divisions and roots in
+// 64 bits: 92 against 38 us for 8192 x 4096 bf16 with the residual (235 MB, 36 us at the measured copy bandwidth).
 template <class T, bool VEC, int E, bool NORM, int MOST>
-__global__ void __launch_bounds__(MOST) rows_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(const __grid_constant__ RowArgs a) {
   pdl_begin();
   __shared__ double sums[kMostThreads / 32];
   __shared__ uint32_t tops[kMostThreads / 32];
@@ -166,21 +218,21 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const __grid_constant__ RowA
   if (row >= a.rows) return;                       // whole warps, and only where no barrier follows
   const int tid = one ? lane : threadIdx.x, threads = a.warps * 32, depth = a.depth;
   using M = Mine<T, VEC, E>;
-  float v[E];
-  M::load(v, static_cast<const T*>(a.x) + row * a.x_stride, depth, tid, threads);
+  typename M::Raw raw;                             // h
+  float v[E], y[E];
+  M::fetch(raw, static_cast<const T*>(a.x) + row * a.x_stride, depth, tid, threads);
+  float r_hi = 1.0f, r_lo = 0.0f;
   if constexpr (NORM) {
     if (a.residual) {
-      float r[E];
-      M::load(r, static_cast<const T*>(a.residual) + row * a.residual_stride, depth, tid, threads);
+      M::load(y, static_cast<const T*>(a.residual) + row * a.residual_stride, depth, tid, threads);
+      M::numbers(v, raw);
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = Type<T>::get(Type<T>::put(v[i] + r[i]));
+      for (int i = 0; i < E; ++i) v[i] += y[i];
+      M::held(raw, v);
     }
-    if (a.h) M::store(static_cast<T*>(a.h) + row * a.h_stride, v, depth, tid, threads);
-  }
-  float r_hi = 1.0f, r_lo = 0.0f;
-  float w[NORM ? E : 1];
-  if constexpr (NORM) {
-    M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+    if (a.h) M::write(static_cast<T*>(a.h) + row * a.h_stride, raw, depth, tid, threads);
+    M::load_any(y, a.weight, a.weight_dtype, depth, tid, threads);
+    M::numbers(v, raw);
     // squares of any size, and a sum that is good to the last of them: 64 bits
     double ss = 0.0;
 #pragma unroll
@@ -192,56 +244,73 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const __grid_constant__ RowA
       ss = lane < a.warps ? sums[lane] : 0.0;
       ss = warp_sum(ss);
     }
-    const double r = 1.0 / sqrt(ss / (double)depth + (double)a.eps);
+    const double r = inverse_root(ss * a.inv_depth + (double)a.eps);
     r_hi = (float)r;
     r_lo = (float)(r - (double)r_hi);
     if (a.rstd && tid == 0) a.rstd[row] = r_hi;
-    if (a.y) {
-      float y[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const Scaled<NORM> s(v[i], r_hi, r_lo, w[i]);
-        y[i] = s.hi + s.lo;
+    for (int i = 0; i < E; ++i) y[i] = v[i] * (r_hi * y[i]);
+    if (a.y) {
+      float w[E];
+      M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {                // in two parts: rounded once
+        const float rw = __fmul_rn(r_hi, w[i]);
+        w[i] = __fmaf_rn(v[i], rw, v[i] * __fmaf_rn(r_lo, w[i], __fmaf_rn(r_hi, w[i], -rw)));
       }
-      M::store(static_cast<T*>(a.y) + row * a.y_stride, y, depth, tid, threads);
+      M::store(static_cast<T*>(a.y) + row * a.y_stride, w, depth, tid, threads);
     }
     if (!a.q) return;
+  } else {
+    M::numbers(y, raw);
   }
-  uint32_t top = 0;
+  float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) top = max(top, mag_key(Scaled<NORM>(v[i], r_hi, r_lo, NORM ? w[i] : 1.0f).hi));
-  top = __reduce_max_sync(kFull, top);
+  for (int i = 0; i < E; ++i) top = larger(top, fabsf(y[i]));
+  uint32_t bits = __reduce_max_sync(kFull, mag_key(top));    // NaN above the infinities above the numbers
   if (!one) {
-    if (lane == 0) tops[warp] = top;
+    if (lane == 0) tops[warp] = bits;
     __syncthreads();
-    top = __reduce_max_sync(kFull, lane < a.warps ? tops[lane] : 0u);
+    bits = __reduce_max_sync(kFull, lane < a.warps ? tops[lane] : 0u);
   }
-  const bool fine = top < 0x7f800000u;             // no infinity, no NaN
-  const int e = fine ? scale_exponent(top) : 0;
+  const bool fine = bits < 0x7f800000u;            // no infinity, no NaN
+  const int e = fine ? scale_exponent(bits) : 0;
   const float up = power(-e);                      // -121 <= -e <= 126
   if (tid == 0) a.scale[row] = fine ? power(e) : __int_as_float(0x7fc00000);
+  float near = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const float t = y[i] * up;                     // at most 127 and a rounding
+    y[i] = t + kRound;
+    if constexpr (NORM) near = fmaxf(near, fabsf(t - (y[i] - kRound)));
+  }
+  if constexpr (NORM) {
+    if (near > 0.5f - 0x1p-14f && fine) {
+      M::numbers(v, raw);
+      float w[E];
+      M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+#pragma unroll
+      for (int i = 0; i < E; ++i) y[i] = steps_of(v[i], r_hi, r_lo, w[i], up);
+    }
+  }
+  if (e == 121) {                                  // where entries may be above 127 * 2^121
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = fminf(fmaxf(y[i], kRound - 127.0f), kRound + 127.0f);
+  }
   int8_t* out = a.q + row * a.q_stride;
 #pragma unroll
   for (int j = 0; j < E / M::N; ++j) {
-    uint32_t packed[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < M::N; ++i) {
-      const int k = j * M::N + i;
-      const Scaled<NORM> s(v[k], r_hi, r_lo, NORM ? w[k] : 1.0f);
-      const float t = s.hi * up;
-      float n = rintf(t);
-      if constexpr (NORM) {
-        const float d = (t - n) + s.lo * up;       // the first difference is exact
-        n += d > 0.5f ? 1.0f : d < -0.5f ? -1.0f : 0.0f;
-      }
-      const int q = fine ? max(-127, min(127, (int)n)) : 0;
-      packed[i / 4] |= (uint32_t)(q & 0xff) << (8 * (i % 4));
-    }
     const int at = M::first(j, tid, threads);
+    const float* s = y + j * M::N;
+    auto four = [&](int i) {
+      const uint32_t a01 = __byte_perm(__float_as_uint(s[i]), __float_as_uint(s[i + 1]), 0x0040);
+      const uint32_t a23 = __byte_perm(__float_as_uint(s[i + 2]), __float_as_uint(s[i + 3]), 0x0040);
+      return fine ? __byte_perm(a01, a23, 0x5410) : 0u;
+    };
     if (at >= depth) continue;
-    if constexpr (M::N == 8) *reinterpret_cast<uint2*>(out + at) = make_uint2(packed[0], packed[1]);
-    else if constexpr (M::N == 4) *reinterpret_cast<uint32_t*>(out + at) = packed[0];
-    else out[at] = (int8_t)packed[0];
+    if constexpr (M::N == 8) *reinterpret_cast<uint2*>(out + at) = make_uint2(four(0), four(4));
+    else if constexpr (M::N == 4) *reinterpret_cast<uint32_t*>(out + at) = four(0);
+    else out[at] = fine ? (int8_t)__float_as_uint(s[0]) : 0;
   }
 }
 
@@ -374,6 +443,7 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* partial, i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (at < depth)
+#pragma unroll 4
     for (int b = warp; b < blocks; b += 32) s += __ldg(partial + (int64_t)b * depth + at);
   part[warp][lane] = s;
   __syncthreads();
@@ -441,11 +511,13 @@ void back_of(const BackArgs& a, const Shape& s, int blocks, size_t smem, cudaStr
 
 int back_groups(const Shape& s) { return s.warps == 1 ? 8 : 1; }
 
+constexpr int kBackRows = 2;
+
 // Blocks of the gradient: what the SMs hold at once (about 1024 threads each), at most one a group of rows.
 int back_blocks(int64_t rows, const Shape& s) {
   const int groups = back_groups(s), threads = groups * s.warps * 32;
   const int64_t most = 148 * (int64_t)(threads >= 1024 ? 1 : 1024 / threads);
-  const int64_t need = cdiv(rows, groups);
+  const int64_t need = cdiv(rows, (int64_t)groups * kBackRows);
   return (int)(need < most ? need : most);
 }
 
@@ -533,6 +605,7 @@ int gsparse_rms_norm(const void* x, int64_t x_stride, const void* residual, int6
   a.weight_dtype = weight_dtype;
   a.warps = shape_of(depth).warps;
   a.eps = eps;
+  a.inv_depth = 1.0 / (double)depth;
   const bool vec = depth % (16 / (int64_t)size_of(dtype)) == 0 && aligned16(weight) && even(x, x_stride, dtype) &&
                    even(residual, residual_stride, dtype) && even(h, h_stride, dtype) && even(y, y_stride, dtype);
   return rows_by_type<true>(dtype, a, vec, (cudaStream_t)stream);
