@@ -19,11 +19,12 @@ constexpr int kRowBytes = 128;             // of an operand's row in a stage: 12
 constexpr int kOperand = 128 * kRowBytes;  // bytes of one operand of one CTA in a stage
 constexpr int kBox = 32 * 128;             // a warp's part of the result on its way out: 32 rows of 128 bytes
 
-// Integers leave the tensor memory once a tile, but soon (a depth of 512 takes a pair a microsecond): 16 warps of 64 columns. Sums
-// in bf16 stay in registers over a tile: 8 warps of 128 columns, with the registers that the other warps give up.
+constexpr int kSide = 128;                 // columns of a warp that takes results out: eight of them take a CTA's part of a tile
+
+// Integers leave the tensor memory once a tile, but soon (a depth of 512 takes a pair a microsecond): two groups of eight warps. Sums
+// in bf16 stay in registers over a tile: one group, with the registers that the other warps give up.
 template <bool INT> struct Layout {
   static constexpr int warps = INT ? 16 : 8;                   // that take results out
-  static constexpr int side = 4 * kTile / warps;               // columns of such a warp
   static constexpr int threads = (warps + (INT ? 2 : 4)) * 32; // setmaxnreg goes by groups of four warps
   static constexpr int stages = INT ? 5 : 6;
   static constexpr int stage_bytes = 2 * kOperand;
@@ -36,6 +37,25 @@ using LB = Layout<false>;
 constexpr int kMore = 216, kFewer = 72;      // registers of these and of the others, out of the 168 of the launch
 static_assert(LB::warps * 32 * kMore + 128 * kFewer <= LB::threads * 168, "");
 
+// Division of 0 <= n < 2^31 by a divisor that the host knows: d = ceil(2^(32 + shift) / divisor) with 2^(shift - 1) < divisor <= 2^shift
+// leaves the quotient exact (the excess of d, below the divisor, times n stays below 2^(32 + shift)).
+struct Divisor {
+  uint32_t by, shift;
+  uint64_t d;
+  __device__ __forceinline__ int of(int n) const {
+    // d has 33 bits: its top bit adds n itself
+    const uint32_t high = __umulhi((uint32_t)n, (uint32_t)d);
+    return (int)(((uint64_t)high + ((d >> 32) ? (uint32_t)n : 0u)) >> shift);
+  }
+};
+
+// Tile t: bands of `band` tiles of the shorter way, along the longer, so that the tiles under way at a time share rows of both operands.
+struct Order {
+  int tiles, band, last_band, bands;       // the last band's width
+  int wide;                                // the longer way is that of the columns
+  Divisor per_band, in_band, in_last;
+};
+
 struct TileArgs {
   CUtensorMap a, b, out, part;
   const float* row_scale;                  // of the integer product
@@ -45,7 +65,7 @@ struct TileArgs {
   int64_t as_tiles;                        // columns of D that the tensor map describes: a copy ends at a multiple of 16 bytes
   int32_t* d_status;
   int64_t rows, cols;                      // of D
-  int tiles_m, tiles_n, band;
+  Order order;
   int blocks, plane_blocks;                // of 128 bytes along s, all planes; of one plane
   int chunk;                               // blocks of bf16 that are summed in the tensor core
   int pairs, waves;                        // tiles below waves * pairs are whole; the others are split
@@ -147,14 +167,13 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // ---- work of a pair -----------------------------------------------------------------------------------------
 
-// Tile t: bands of `band` tiles of the shorter way, along the longer, so that the tiles under way at a time share rows of both operands.
-__device__ __forceinline__ void place_of(int t, int tiles_m, int tiles_n, int band, int& m, int& n) {
-  const bool wide = tiles_n > tiles_m;
-  const int across = wide ? tiles_m : tiles_n, along = wide ? tiles_n : tiles_m;
-  const int b = t / (band * along), left = t - b * band * along, width = min(band, across - b * band);
-  const int x = b * band + left % width, y = left / width;
-  m = wide ? x : y;
-  n = wide ? y : x;
+__device__ __forceinline__ void place_of(int t, const Order& o, int& m, int& n) {
+  const int b = o.per_band.of(t), left = t - b * (int)o.per_band.by;
+  const bool last = b == o.bands - 1;
+  const int width = last ? o.last_band : o.band;
+  const int y = last ? o.in_last.of(left) : o.in_band.of(left), x = b * o.band + left - y * width;
+  m = o.wide ? x : y;
+  n = o.wide ? y : x;
 }
 
 // The i-th part of a pair's work: blocks [from, to) of a tile, and whether they are all of it (else its place among the parts).
@@ -168,12 +187,12 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part
   p.slot = 0;
   if (i < a.waves || a.piece == 0) {
     tile = pair + i * a.pairs;
-    if (tile >= a.tiles_m * a.tiles_n) return false;
+    if (tile >= a.order.tiles) return false;
     p.from = 0;
     p.to = a.blocks;
   } else {
     const int k = i - a.waves;                                  // a pair's range of blocks meets at most two tiles
-    const int64_t all = (int64_t)(a.tiles_m * a.tiles_n - a.waves * a.pairs) * a.blocks;
+    const int64_t all = (int64_t)(a.order.tiles - a.waves * a.pairs) * a.blocks;
     const int64_t first = (int64_t)pair * a.piece, last = min(all, first + a.piece);
     if (first >= last) return false;
     const int64_t t = first / a.blocks + k;
@@ -185,7 +204,7 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part
     p.slot = pair * 2 + k;
   }
   p.whole = p.to - p.from == a.blocks;
-  place_of(tile, a.tiles_m, a.tiles_n, a.band, p.m, p.n);
+  place_of(tile, a.order, p.m, p.n);
   return true;
 }
 
@@ -221,7 +240,7 @@ template <class T>
 __device__ __forceinline__ void into_box(char* box, int lane, int at, const float* v) {
 #pragma unroll
   for (int j = 0; j < 32 / Pack<T>::N; ++j)
-    *reinterpret_cast<uint4*>(box + lane * 128 + (((at + j) ^ (lane & 7)) << 4)) = Pack<T>::of(v + j * Pack<T>::N);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(box + lane * 128 + ((lane & 7) << 4)) ^ (uintptr_t)((at + j) << 4)) = Pack<T>::of(v + j * Pack<T>::N);
 }
 
 // A box of 32 rows that no tensor map describes: row by row, 128 bytes of entries side by side.
@@ -238,6 +257,14 @@ __device__ void box_to_rows(const char* box, int lane, T* out, int64_t stride, i
     for (int i = 0; i < N; ++i)
       if (mine + i < cols) to[i] = e[i];
   }
+}
+
+// Two sums times their row's scale, then times their columns' scales, each rounded (two numbers an instruction).
+__device__ __forceinline__ void scaled(float& u, float& v, uint32_t a, uint32_t b, float row, float x, float y) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %4};\n mov.b64 r, {%5, %6};\n mul.rn.f32x2 p, p, q;\n"
+      " mul.rn.f32x2 p, p, r;\n mov.b64 {%0, %1}, p;\n}"
+      : "=f"(u), "=f"(v)
+      : "f"(__int2float_rn((int)a)), "f"(__int2float_rn((int)b)), "f"(row), "f"(x), "f"(y));
 }
 
 // A warp's box on its way.
@@ -290,7 +317,7 @@ __device__ __forceinline__ void put_part(const TileArgs& a, Way& way, const floa
 
 // ---- the kernel -----------------------------------------------------------------------------------------------
 
-// The first warps take results out (warp w the lanes 32 (w % 4) and the columns `side` (w / 4) on), the next loads, one more
+// The first warps take results out (warp w the lanes 32 (w % 4) and the columns 128 (w / 4 % 2) on), the next loads, one more
 // multiplies (of the pair's first CTA, for both). The loads run ahead over all of a pair's parts; the tensor memory holds two tiles of sums.
 //
 // The sums in bf16 are taken out of the tensor core every `chunk` blocks of 64 and added up in fp32 registers, since its
@@ -317,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sums_full + i, 1);
-      mbar_init(sums_empty + i, 2 * L::warps);
+      mbar_init(sums_empty + i, 2 * 8);
     }
     mbar_init(drained, 1);
     fence_mbarrier_init();
@@ -405,72 +432,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
     }
   } else {
     if constexpr (!INT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore));
-    const int quarter = warp & 3, side = warp >> 2;
-    const int first_row = (int)rank * 128 + quarter * 32, first_col = side * L::side;
+    const int quarter = warp & 3, side = (warp >> 2) & 1, group = warp >> 3;
+    const int first_row = (int)rank * 128 + quarter * 32, first_col = side * kSide;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + first_col;
     const uint32_t give = in_cta(smem_u32(sums_empty), 0);
     Way way{smem + L::box_at + warp * kBox, lane};
-    uint32_t c = 0;
-    // (after a wait that gave up: on to the end, since the warps of a side meet at a barrier for each part)
     if constexpr (INT) {
-      // the scales of a part's rows, and of its columns for the four warps that take the same ones: read a part ahead
-      float row_scale, col_scale;
+      // Two groups of eight warps take the parts in turn, so that one converts while the other waits, loads or sends. The scales of
+      // a part's rows, and of its columns for the four warps that take the same ones, are read a part ahead.
+      float row_scale = 0.0f, col_scale = 0.0f;
+      const int mine_of = quarter * 32 + lane;
       auto scales_of = [&](const Part& q) {
-        const int64_t row = (int64_t)q.m * kTile + first_row + lane, col = (int64_t)q.n * kTile + first_col + (quarter & 1) * 32 + lane;
+        const int64_t row = (int64_t)q.m * kTile + first_row + lane, col = (int64_t)q.n * kTile + first_col + mine_of;
         row_scale = row < a.rows ? __ldg(a.row_scale + row) : 0.0f;
         col_scale = col < a.cols ? __ldg(a.col_scale + col) : 0.0f;
       };
-      bool more = part_of(a, pair, 0, p);
+      int i = group;
+      bool more = part_of(a, pair, i, p);
       if (more) scales_of(p);
-      for (int i = 0; more; ++c) {
-        const uint32_t buf = c & 1;
-        float* scales = reinterpret_cast<float*>(smem + L::scale_at) + buf * kTile + first_col;
-        if (quarter < 2) scales[quarter * 32 + lane] = col_scale;
+      for (uint32_t turn = 0; more; ++turn) {      // (after a wait that gave up: on to the end, since four warps meet at a barrier)
+        float* scales = reinterpret_cast<float*>(smem + L::scale_at) + group * kTile + first_col;
+        asm volatile("bar.sync %0, 128;" ::"r"(warp / 4 + 1) : "memory");      // the last part's scales have been used
+        scales[mine_of] = col_scale;
         const float mine = row_scale;
         const int64_t row = (int64_t)p.m * kTile + first_row, col = (int64_t)p.n * kTile + first_col;
         const int64_t part_row = (int64_t)p.slot * kTile + first_row;
         const bool whole = p.whole;
-        more = part_of(a, pair, ++i, p);
+        more = part_of(a, pair, i += 2, p);
         if (more) scales_of(p);
-        asm volatile("bar.sync %0, 128;" ::"r"(side + 1) : "memory");
-        if (!(ok = ok && wait_phase(sums_full + buf, (c / 2) & 1))) continue;
+        asm volatile("bar.sync %0, 128;" ::"r"(warp / 4 + 1) : "memory");
+        if (!(ok = ok && wait_phase(sums_full + group, turn & 1))) continue;
         fence_after();
-        uint32_t raw[2][32];
-        load_columns(raw[0], lanes + buf * kTile);
-        load_columns(raw[1], lanes + buf * kTile + 32);
-        columns_loaded();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(give + buf * 8);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kSide / 32; ++j) {
+          uint32_t raw[32];
+          load_columns(raw, lanes + group * kTile + j * 32);
+          columns_loaded();
+          if (j == kSide / 32 - 1) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(give + group * 8);
+          }
           float v[32];
           if (whole) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
               const float4 f = *reinterpret_cast<const float4*>(scales + j * 32 + k);
-              v[k] = __int2float_rn((int)raw[j][k]) * mine * f.x;
-              v[k + 1] = __int2float_rn((int)raw[j][k + 1]) * mine * f.y;
-              v[k + 2] = __int2float_rn((int)raw[j][k + 2]) * mine * f.z;
-              v[k + 3] = __int2float_rn((int)raw[j][k + 3]) * mine * f.w;
+              scaled(v[k], v[k + 1], raw[k], raw[k + 1], mine, f.x, f.y);
+              scaled(v[k + 2], v[k + 3], raw[k + 2], raw[k + 3], mine, f.z, f.w);
             }
-            put(a, way, j, v, row, col + j * 32);
+            put(a, way, j & 1, v, row, col + j * 32);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[j][k]);
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
             put_part(a, way, v, part_row, first_col + j * 32);
           }
         }
       }
     } else {
+      uint32_t c = 0;
       for (int i = 0; part_of(a, pair, i, p); ++i) {
-        float sum[L::side];
+        float sum[kSide];
         for (int kb = p.from; ok && kb < p.to; kb += a.chunk, ++c) {
           const uint32_t buf = c & 1;
           if (!(ok = wait_phase(sums_full + buf, (c / 2) & 1))) break;
           fence_after();
 #pragma unroll
-          for (int j = 0; j < L::side; j += 32) {
+          for (int j = 0; j < kSide; j += 32) {
             uint32_t raw[32];
             load_columns(raw, lanes + buf * kTile + j);
             columns_loaded();
@@ -490,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
         const int64_t row = (int64_t)p.m * kTile + first_row, col = (int64_t)p.n * kTile + first_col;
         const int64_t part_row = (int64_t)p.slot * kTile + first_row;
 #pragma unroll
-        for (int j = 0; j < L::side / 32; ++j) {
+        for (int j = 0; j < kSide / 32; ++j) {
           if (p.whole) put(a, way, j & 1, sum + j * 32, row, col + j * 32);
           else put_part(a, way, sum + j * 32, part_row, first_col + j * 32);
         }
@@ -517,7 +545,8 @@ struct JoinArgs {
   const float* col_scale;
   void* out;
   int64_t out_stride, rows, cols;
-  int tiles_m, tiles_n, band, first_tile, blocks, piece;
+  Order order;
+  int first_tile, blocks, piece;
 };
 
 // The parts of a split tile added up in their order along s. A block takes 8 rows of a tile, a thread 8 entries of one row.
@@ -530,7 +559,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
   if (first == last) return;                       // whole after all
   int m, n;
-  place_of(tile, a.tiles_m, a.tiles_n, a.band, m, n);
+  place_of(tile, a.order, m, n);
   const int64_t row = (int64_t)m * kTile + r, col = (int64_t)n * kTile + c;
   if (row >= a.rows || col >= a.cols) return;
   uint32_t sum[8];
@@ -652,16 +681,32 @@ CUtensorMapDataType map_type(int32_t dtype) {
 // How the tiles of D are shared out: whole tiles in waves over the pairs of SMs; what is left over is split along s.
 constexpr int kBand = 8;
 
+Divisor divisor(int64_t by) {
+  Divisor v;
+  v.by = (uint32_t)by;
+  v.shift = 0;
+  while ((1ull << v.shift) < (uint64_t)by) ++v.shift;
+  v.d = (uint64_t)((((unsigned __int128)1 << (32 + v.shift)) + by - 1) / by);
+  return v;
+}
+
 struct Plan {
-  int tiles_m, tiles_n, tiles, band, blocks, pairs, waves, piece;
+  Order order;
+  int tiles, blocks, pairs, waves, piece;
 };
 
 Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
   Plan p;
-  p.tiles_m = (int)cdiv(rows, kTile);
-  p.tiles_n = (int)cdiv(cols, kTile);
-  p.tiles = p.tiles_m * p.tiles_n;
-  p.band = min(min(p.tiles_m, p.tiles_n), kBand);
+  const int64_t m = rows > 0 ? cdiv(rows, kTile) : 1, n = cdiv(cols, kTile), across = m < n ? m : n, along = m < n ? n : m;
+  Order& o = p.order;
+  p.tiles = o.tiles = (int)(m * n);
+  o.wide = m < n;
+  o.band = (int)(across < kBand ? across : kBand);
+  o.bands = (int)cdiv(across, o.band);
+  o.last_band = (int)(across - (int64_t)(o.bands - 1) * o.band);
+  o.per_band = divisor(along * o.band);
+  o.in_band = divisor(o.band);
+  o.in_last = divisor(o.last_band);
   p.blocks = (int)blocks;
   p.pairs = sm_count() / 2;
   p.waves = p.tiles / p.pairs;
@@ -678,9 +723,7 @@ bool fits(int64_t rows, int64_t cols) { return cdiv(rows, kTile) * cdiv(cols, kT
 
 template <bool INT, bool A_ACROSS>
 int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride, cudaStream_t st) {
-  a.tiles_m = p.tiles_m;
-  a.tiles_n = p.tiles_n;
-  a.band = p.band;
+  a.order = p.order;
   a.blocks = p.blocks;
   a.pairs = p.pairs;
   a.waves = p.waves;
@@ -702,7 +745,7 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
   const int used = p.piece || p.waves ? p.pairs : p.tiles;
   launch(kernel, dim3((unsigned)(2 * used)), dim3(L::threads), L::shared, st, (const TileArgs&)a);
   if (p.piece) {
-    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.tiles_m, p.tiles_n, p.band, p.waves * p.pairs, p.blocks, p.piece};
+    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.order, p.waves * p.pairs, p.blocks, p.piece};
     const dim3 grid((unsigned)(32 * (p.tiles - p.waves * p.pairs)));
     if (dtype == GSPARSE_F32) launch(join_kernel<INT, float>, grid, dim3(256), 0, st, (const JoinArgs&)j);
     else if (dtype == GSPARSE_BF16) launch(join_kernel<INT, __nv_bfloat16>, grid, dim3(256), 0, st, (const JoinArgs&)j);

@@ -202,6 +202,17 @@ def test_no_tokens_is_no_work(gs):
     assert _grad_input(gs, tokens=0, dout=None, out=None, workspace=None) == 0
 
 
+@pytest.mark.parametrize("tokens,channels,depth", [(0, 5, 40), (1, 1, 1), (1 << 26, 1, 1), (1, 1 << 26, 1), (1 << 20, 1 << 20, 1 << 15)])
+def test_workspace_queries_of_any_size(gs, tokens, channels, depth):
+    """A size, or 0 where the call is refused or needs nothing; never an error of arithmetic."""
+    lib = gs.lib()
+    assert 0 <= lib.gsparse_linear_q8_workspace_size(tokens, channels, depth) < 1 << 50
+    for f in (lib.gsparse_linear_q8_grad_input_workspace_size, lib.gsparse_linear_q8_grad_weight_workspace_size):
+        for dtype in (F32, BF16, F16):
+            assert 0 <= f(P, dtype, channels, tokens, channels, depth) < 1 << 50
+    assert 0 <= lib.gsparse_rms_norm_backward_workspace_size(tokens, depth) < 1 << 50
+
+
 def test_workspace_queries_refuse_what_the_calls_refuse(gs):
     lib = gs.lib()
     assert lib.gsparse_rms_norm_backward_workspace_size(1000, 512) >= 512 * 4
