@@ -730,9 +730,8 @@ def _row_step(t: torch.Tensor, unit: int) -> int:
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
 
 
-def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype) -> torch.Tensor:
-    """A new matrix whose rows start at multiples of 16 bytes."""
-    unit = 16 // dtype.itemsize
+def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype, unit: int) -> torch.Tensor:
+    """A new matrix whose rows are a multiple of `unit` entries apart."""
     stride = -(-cols // unit) * unit
     t = torch.empty((rows, stride), dtype=dtype, device=like.device)
     return t if stride == cols else t[:, :cols]
@@ -740,7 +739,7 @@ def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype) -> torch.Tens
 
 def _new_quant(like: torch.Tensor) -> QuantRows:
     rows, depth = like.shape
-    return QuantRows(_aligned_rows(like, rows, depth, torch.int8), like.new_empty(rows, dtype=torch.float32))
+    return QuantRows(_aligned_rows(like, rows, depth, torch.int8, 16), like.new_empty(rows, dtype=torch.float32))
 
 
 def _dtype_code(dtype) -> int:
@@ -834,14 +833,15 @@ def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
 def linear_q8(x: QuantRows, w: QuantRows, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, d_status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out[t, n] = x.scale[t] w.scale[n] sum_k x.q[t, k] w.q[n, k]: a layer's product in 8-bit integers, exact up to the
-    rounding of the result. Rows of an `out` that is made here start at multiples of 16 bytes: where channels is no
-    multiple of that, it is a view whose stride(0) is larger, as token_logprobs and distill_topk take it."""
+    rounding of the result. Rows of an `out` that is made here start at multiples of 32 bytes (memory's sectors, which
+    other rows would write in halves): where channels is no multiple of that, it is a view whose stride(0) is larger,
+    as token_logprobs and distill_topk take it."""
     p_x, s_x, c_x, tokens, depth = _quant(x, "x")
     dev = x.q.device
     p_w, s_w, c_w, channels, _ = _quant(w, "w", dev, depth)
     if out is None:
         _dtype_code(dtype)
-        out = _aligned_rows(x.q, tokens, channels, dtype)
+        out = _aligned_rows(x.q, tokens, channels, dtype, 8 if dtype is torch.float32 else 16)
     p_o, s_o = _matrix(out, "out")
     if out.shape != (tokens, channels) or out.device != dev:
         raise GsparseError(f"out must be of shape {(tokens, channels)} on {dev}")

@@ -69,7 +69,8 @@ struct TileArgs {
   int blocks, plane_blocks;                // of 128 bytes along s, all planes; of one plane
   int chunk;                               // blocks of bf16 that are summed in the tensor core
   int pairs, waves;                        // tiles below waves * pairs are whole; the others are split
-  int piece;                               // blocks of a pair's part of the split tiles (0: none are split)
+  int piece, group;                        // blocks of a pair's part of the split tiles (0: none are split); see Plan
+  int keep_a, keep_b;                      // how long the second-level cache should keep the operands' lines
   int out_dtype;
 };
 
@@ -109,17 +110,26 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
 }
 
 // Copies of a box into this CTA's shared memory that count on a barrier of the pair's first CTA.
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t keep) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], "
+      "[%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(keep)
       : "memory");
 }
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint64_t keep) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4}], [%5], %6;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(keep)
       : "memory");
+}
+
+// Policies of the second-level cache: lines of an operand that is read again and again, of one that passes once, and of others.
+__device__ __forceinline__ uint64_t policy(int keep) {
+  uint64_t p;
+  if (keep > 0) asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  else if (keep < 0) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
@@ -192,13 +202,14 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part
     p.to = a.blocks;
   } else {
     const int k = i - a.waves;                                  // a pair's range of blocks meets at most two tiles
-    const int64_t all = (int64_t)(a.order.tiles - a.waves * a.pairs) * a.blocks;
-    const int64_t first = (int64_t)pair * a.piece, last = min(all, first + a.piece);
+    const int set = pair / a.group, member = pair - set * a.group;
+    const int64_t all = (int64_t)((a.order.tiles - a.waves * a.pairs) / a.group) * a.blocks;
+    const int64_t first = (int64_t)set * a.piece, last = min(all, first + a.piece);
     if (first >= last) return false;
     const int64_t t = first / a.blocks + k;
     const int64_t from = max(first, t * a.blocks), to = min(last, (t + 1) * a.blocks);
     if (from >= to) return false;
-    tile = a.waves * a.pairs + (int)t;
+    tile = a.waves * a.pairs + (int)t * a.group + member;
     p.from = (int)(from - t * a.blocks);
     p.to = (int)(to - t * a.blocks);
     p.slot = pair * 2 + k;
@@ -367,6 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
     if constexpr (!INT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewer));
     if (warp == L::warps && lane == 0) {
       uint32_t n = 0, s = 0, turn = 0;                         // stages filled so far; the next, and its turn
+      const uint64_t keep_a = policy(a.keep_a), keep_b = policy(a.keep_b);
       for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
         const int m = p.m * kTile + (int)rank * 128, c = p.n * kTile + (int)rank * 128;
         int plane = p.from / a.plane_blocks, k = p.from - plane * a.plane_blocks;
@@ -376,17 +388,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
           const uint32_t bar = in_cta(smem_u32(full + s), 0);
           const uint32_t at = smem_u32(smem + s * L::stage_bytes);
           if constexpr (INT) {
-            load_box(at, &a.a, k * 128, m, bar);
-            load_box(at + kOperand, &a.b, k * 128, c, bar);
+            load_box(at, &a.a, k * 128, m, bar, keep_a);
+            load_box(at + kOperand, &a.b, k * 128, c, bar, keep_b);
           } else {
             if constexpr (A_ACROSS) {
-              load_box(at, &a.a, m, k * 64, plane, bar);
-              load_box(at + kOperand / 2, &a.a, m + 64, k * 64, plane, bar);
+              load_box(at, &a.a, m, k * 64, plane, bar, keep_a);
+              load_box(at + kOperand / 2, &a.a, m + 64, k * 64, plane, bar, keep_a);
             } else {
-              load_box(at, &a.a, k * 64, m, plane, bar);
+              load_box(at, &a.a, k * 64, m, plane, bar, keep_a);
             }
-            load_box(at + kOperand, &a.b, c, k * 64, bar);
-            load_box(at + kOperand + kOperand / 2, &a.b, c + 64, k * 64, bar);
+            load_box(at + kOperand, &a.b, c, k * 64, bar, keep_b);
+            load_box(at + kOperand + kOperand / 2, &a.b, c + 64, k * 64, bar, keep_b);
           }
           if (++s == L::stages) s = 0, ++turn;
           if (++k == a.plane_blocks) k = 0, ++plane;
@@ -546,7 +558,7 @@ struct JoinArgs {
   void* out;
   int64_t out_stride, rows, cols;
   Order order;
-  int first_tile, blocks, piece;
+  int first_tile, blocks, piece, group;
 };
 
 // The parts of a split tile added up in their order along s. A block takes 8 rows of a tile, a thread 8 entries of one row.
@@ -555,25 +567,35 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   pdl_begin();
   const int t = blockIdx.x >> 5, tile = a.first_tile + t;
   const int r = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
-  const int64_t from = (int64_t)t * a.blocks, to = from + a.blocks;
+  const int set = t / a.group, member = t - set * a.group;
+  const int64_t from = (int64_t)set * a.blocks, to = from + a.blocks;
   const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
   if (first == last) return;                       // whole after all
   int m, n;
   place_of(tile, a.order, m, n);
   const int64_t row = (int64_t)m * kTile + r, col = (int64_t)n * kTile + c;
   if (row >= a.rows || col >= a.cols) return;
-  uint32_t sum[8];
-  for (int pair = first; pair <= last; ++pair) {
-    // the part that begins a pair's range is its first: only the range's first tile can be this one in the middle
-    const int k = (int64_t)pair * a.piece < from ? 1 : 0;
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + ((int64_t)(pair * 2 + k) * kTile + r) * kTile + c;
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p)), y = __ldg(reinterpret_cast<const uint4*>(p + 4));
-    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};     // -0 + 0 is 0: as good as the first part itself
+  for (int at = first; at <= last; at += 4) {      // four parts under way at a time
+    uint4 x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (pair == first) sum[i] = v[i];
-      else if constexpr (INT) sum[i] += v[i];
-      else sum[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
+    for (int i = 0; i < 4; ++i) {
+      if (at + i > last) break;
+      // a range that begins before this tile has it as its second
+      const int64_t slot = ((int64_t)(at + i) * a.group + member) * 2 + ((int64_t)(at + i) * a.piece < from ? 1 : 0);
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (slot * kTile + r) * kTile + c;
+      x[i] = __ldg(reinterpret_cast<const uint4*>(p));
+      y[i] = __ldg(reinterpret_cast<const uint4*>(p + 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (at + i > last) break;
+      const uint32_t v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (INT) sum[j] += v[j];
+        else sum[j] = __float_as_uint(__uint_as_float(sum[j]) + __uint_as_float(v[j]));
+      }
     }
   }
   T* out = static_cast<T*>(a.out) + row * a.out_stride + col;
@@ -680,6 +702,7 @@ CUtensorMapDataType map_type(int32_t dtype) {
 
 // How the tiles of D are shared out: whole tiles in waves over the pairs of SMs; what is left over is split along s.
 constexpr int kBand = 8;
+constexpr int64_t kKeep = 96 << 20;        // bytes of an operand that the second-level cache may be asked to keep (of 126 MB)
 
 Divisor divisor(int64_t by) {
   Divisor v;
@@ -692,7 +715,7 @@ Divisor divisor(int64_t by) {
 
 struct Plan {
   Order order;
-  int tiles, blocks, pairs, waves, piece;
+  int tiles, blocks, pairs, waves, piece, group;
 };
 
 Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
@@ -711,7 +734,10 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
   p.pairs = sm_count() / 2;
   p.waves = p.tiles / p.pairs;
   const int64_t left = p.tiles - (int64_t)p.waves * p.pairs;
-  const int64_t piece = cdiv(left * blocks, p.pairs);
+  // Where all tiles are split, pairs that take the tiles of a band side by side go through the same blocks at the same time, so that
+  // the operand that they share is read from memory once.
+  p.group = p.waves == 0 && o.bands == 1 && o.band < p.pairs / 2 ? o.band : 1;
+  const int64_t piece = cdiv(left / p.group * blocks, p.pairs / p.group);
   // Splitting costs a part's way out and back, and a launch.
   p.piece = left && blocks - piece >= 24 ? (int)piece : 0;
   return p;
@@ -728,6 +754,7 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
   a.pairs = p.pairs;
   a.waves = p.waves;
   a.piece = p.piece;
+  a.group = p.group;
   using L = Layout<INT>;
   const int32_t dtype = a.out_dtype;
   const int bytes = (int)size_of(dtype);
@@ -745,7 +772,7 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
   const int used = p.piece || p.waves ? p.pairs : p.tiles;
   launch(kernel, dim3((unsigned)(2 * used)), dim3(L::threads), L::shared, st, (const TileArgs&)a);
   if (p.piece) {
-    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.order, p.waves * p.pairs, p.blocks, p.piece};
+    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.order, p.waves * p.pairs, p.blocks, p.piece, p.group};
     const dim3 grid((unsigned)(32 * (p.tiles - p.waves * p.pairs)));
     if (dtype == GSPARSE_F32) launch(join_kernel<INT, float>, grid, dim3(256), 0, st, (const JoinArgs&)j);
     else if (dtype == GSPARSE_BF16) launch(join_kernel<INT, __nv_bfloat16>, grid, dim3(256), 0, st, (const JoinArgs&)j);
@@ -819,7 +846,10 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
   // 512 products of bf16 in a row (32 accumulations) are off by 6e-7 of the result, as the 4000 of a plain fp32 sum are; gradients in
   // fp32 keep to half of that, and results of 16 bits, which are rounded to 2^-9 and 2^-12, take 2048.
   a.chunk = dtype == GSPARSE_F32 ? 4 : out_dtype == GSPARSE_F32 ? 8 : 32;
-  return tiles<false, WEIGHT>(a, plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks), g.part, out, out_stride, st);
+  const Plan p = plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks);
+  a.keep_a = p.order.bands == 1 && !p.order.wide ? -1 : 0;    // the tiles of a row of them are under way together
+  a.keep_b = along * g.stride_b * 2 <= kKeep ? 1 : 0;
+  return tiles<false, WEIGHT>(a, p, g.part, out, out_stride, st);
 }
 
 }  // namespace

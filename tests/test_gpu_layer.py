@@ -409,7 +409,8 @@ def test_product_layout():
     x, w = quants(37, 9, 64), quants(38, 1001, 64)
     out = gs.linear_q8(x, w)
     assert out.shape == (9, 1001) and out.stride(0) == 1008 and out.dtype is torch.bfloat16
-    assert gs.linear_q8(x, quants(38, 1000, 64), torch.float16).is_contiguous()
+    assert gs.linear_q8(x, quants(38, 1008, 64), torch.float16).is_contiguous()
+    assert gs.linear_q8(x, quants(38, 1000, 64), torch.float32).is_contiguous()
 
 
 @pytest.mark.parametrize("tokens", [1, 7, 300])
