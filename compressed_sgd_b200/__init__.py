@@ -11,6 +11,7 @@ allocated here with torch; scratch memory ("workspace") likewise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, NamedTuple, Optional, Sequence, Tuple
 
@@ -733,13 +734,29 @@ def _row_step(t: torch.Tensor, unit: int) -> int:
 def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype, unit: int) -> torch.Tensor:
     """A new matrix whose rows are a multiple of `unit` entries apart."""
     stride = -(-cols // unit) * unit
-    t = torch.empty((rows, stride), dtype=dtype, device=like.device)
-    return t if stride == cols else t[:, :cols]
+    t = like.new_empty((rows, stride), dtype=dtype)
+    return t if stride == cols else t.as_strided((rows, cols), (stride, 1))
 
 
 def _new_quant(like: torch.Tensor) -> QuantRows:
     rows, depth = like.shape
     return QuantRows(_aligned_rows(like, rows, depth, torch.int8, 16), like.new_empty(rows, dtype=torch.float32))
+
+
+# sizes depend on the shapes alone (and on whether dout's rows can be read as they are)
+@functools.lru_cache(maxsize=1024)
+def _layer_workspace_size(name: str, *sizes) -> int:
+    return int(getattr(lib(), name)(*sizes))
+
+
+def _scratch(workspace: Optional[torch.Tensor], like: torch.Tensor, name: str, *sizes):
+    """(tensor or None, pointer, bytes): the caller's workspace, or one as large as the call asks for."""
+    if workspace is None:
+        size = _layer_workspace_size(name, *sizes)
+        if size == 0:
+            return None, None, 0
+        workspace = like.new_empty(size, dtype=torch.uint8)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _dtype_code(dtype) -> int:
@@ -764,10 +781,11 @@ def dequantize_rows(rows: QuantRows, dtype=torch.bfloat16, out: Optional[torch.T
     """The values that rows in 8 bits stand for; bf16 holds those of quantize_rows and rms_norm exactly."""
     q, qs, scale, n, depth = _quant(rows, "rows")
     if out is None:
-        out = torch.empty((n, depth), dtype=dtype, device=rows.q.device)
-    p, stride = _matrix(out, "out")
-    if out.shape != rows.q.shape or out.device != rows.q.device:
+        _dtype_code(dtype)
+        out = rows.q.new_empty((n, depth), dtype=dtype)
+    elif out.shape != rows.q.shape or out.device != rows.q.device:
         raise GsparseError(f"out must be of shape {tuple(rows.q.shape)} on {rows.q.device}")
+    p, stride = _matrix(out, "out")
     _on_device(out.device, "gsparse_dequantize_rows", q, qs, scale, n, depth, p, _DTYPES[out.dtype], stride)
     return out
 
@@ -789,9 +807,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     p_r, s_r = (None, 0) if residual is None else _matrix(residual, "residual", x)
     p_w, wt = _norm_weight(weight, depth, dev)
     if h is None and residual is not None:
-        h = torch.empty((rows, depth), dtype=x.dtype, device=dev)
+        h = x.new_empty((rows, depth))
     p_h, s_h = (None, 0) if h is None else _matrix(h, "h", x)
-    y = torch.empty((rows, depth), dtype=x.dtype, device=dev) if want_y else None
+    y = x.new_empty((rows, depth)) if want_y else None
     if q is None and want_q:
         q = _new_quant(x)
     p_q, s_q, p_s = None, 0, None
@@ -818,15 +836,14 @@ def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
     p_y, s_y = _matrix(dy, "dy", h)
     p_d, s_d = (None, 0) if dh is None else _matrix(dh, "dh", h)
     if dx is None:
-        dx = torch.empty((rows, depth), dtype=h.dtype, device=dev)
+        dx = h.new_empty((rows, depth))
     p_x, s_x = _matrix(dx, "dx", h)
-    dweight = None
+    dweight, p_ws, n_ws = None, None, 0
     if want_dweight:
         dweight = h.new_empty(depth, dtype=torch.float32)
-        if workspace is None:
-            workspace = _workspace(lib().gsparse_rms_norm_backward_workspace_size(rows, depth), dev)
+        workspace, p_ws, n_ws = _scratch(workspace, h, "gsparse_rms_norm_backward_workspace_size", rows, depth)
     _on_device(dev, "gsparse_rms_norm_backward", p_h, s_h, p_w, wt, p_r, p_y, s_y, p_d, s_d, _DTYPES[h.dtype], rows, depth, p_x, s_x,
-               _ptr(dweight), _ptr(workspace), 0 if workspace is None else workspace.numel())
+               _ptr(dweight), p_ws, n_ws)
     return RmsNormGrad(dx, dweight)
 
 
@@ -846,10 +863,9 @@ def linear_q8(x: QuantRows, w: QuantRows, dtype=torch.bfloat16, out: Optional[to
     if out.shape != (tokens, channels) or out.device != dev:
         raise GsparseError(f"out must be of shape {(tokens, channels)} on {dev}")
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
-    if workspace is None:
-        workspace = _workspace(lib().gsparse_linear_q8_workspace_size(tokens, channels, depth), dev)
+    workspace, p_ws, n_ws = _scratch(workspace, x.q, "gsparse_linear_q8_workspace_size", tokens, channels, depth)
     _on_device(dev, "gsparse_linear_q8", p_x, s_x, c_x, p_w, s_w, c_w, tokens, channels, depth, p_o, _DTYPES[out.dtype], s_o,
-               workspace.data_ptr(), workspace.numel(), p_s)
+               p_ws, n_ws, p_s)
     return out
 
 
@@ -865,16 +881,16 @@ def linear_q8_grad_input(dout: torch.Tensor, w: QuantRows, dtype=None, out: Opti
     if out is None:
         dtype = dout.dtype if dtype is None else dtype
         _dtype_code(dtype)
-        out = torch.empty((tokens, depth), dtype=dtype, device=dev)
+        out = dout.new_empty((tokens, depth), dtype=dtype)
     p_o, s_o = _matrix(out, "out")
     if out.shape != (tokens, depth) or out.device != dev:
         raise GsparseError(f"out must be of shape {(tokens, depth)} on {dev}")
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
     dt = _DTYPES[dout.dtype]
-    if workspace is None:
-        workspace = _workspace(lib().gsparse_linear_q8_grad_input_workspace_size(p_g, dt, s_g, tokens, channels, depth), dev)
+    workspace, p_ws, n_ws = _scratch(workspace, dout, "gsparse_linear_q8_grad_input_workspace_size", p_g % 16, dt, s_g, tokens,
+                                     channels, depth)
     _on_device(dev, "gsparse_linear_q8_grad_input", p_g, dt, s_g, p_w, s_w, c_w, tokens, channels, depth, p_o, _DTYPES[out.dtype],
-               s_o, workspace.data_ptr(), workspace.numel(), p_s)
+               s_o, p_ws, n_ws, p_s)
     return out
 
 
@@ -889,14 +905,14 @@ def linear_q8_grad_weight(dout: torch.Tensor, x: QuantRows, out: Optional[torch.
     if n != tokens:
         raise GsparseError(f"x must hold {tokens} rows")
     if out is None:
-        out = torch.empty((channels, depth), dtype=torch.float32, device=dev)
+        out = dout.new_empty((channels, depth), dtype=torch.float32)
     p_o, s_o = _matrix(out, "out")
     if out.shape != (channels, depth) or out.device != dev or out.dtype is not torch.float32:
         raise GsparseError(f"out must be fp32 of shape {(channels, depth)} on {dev}")
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
     dt = _DTYPES[dout.dtype]
-    if workspace is None:
-        workspace = _workspace(lib().gsparse_linear_q8_grad_weight_workspace_size(p_g, dt, s_g, tokens, channels, depth), dev)
+    workspace, p_ws, n_ws = _scratch(workspace, dout, "gsparse_linear_q8_grad_weight_workspace_size", p_g % 16, dt, s_g, tokens,
+                                     channels, depth)
     _on_device(dev, "gsparse_linear_q8_grad_weight", p_g, dt, s_g, p_x, s_x, c_x, tokens, channels, depth, p_o, s_o,
-               workspace.data_ptr(), workspace.numel(), p_s)
+               p_ws, n_ws, p_s)
     return out

@@ -23,6 +23,11 @@ constexpr int kSide = 128;                 // columns of a warp that takes resul
 
 // Integers leave the tensor memory once a tile, but soon (a depth of 512 takes a pair a microsecond): two groups of eight warps. Sums
 // in bf16 stay in registers over a tile: one group, with the registers that the other warps give up.
+// Few rows that every pair reads at about the same time are slow to come by (16 tokens against 32000 x 4096 weights: 100 us, 64
+// tokens: 31): they are copied, and the pairs read different copies.
+// The copies take about half a megabyte (8 tokens of 512 in 16 copies, 64 KB: 40 us; in 74: 17).
+constexpr int64_t kCopyBytes = 96 << 10, kCopiesBytes = 512 << 10;
+
 template <bool INT> struct Layout {
   static constexpr int warps = INT ? 16 : 8;                   // that take results out
   static constexpr int threads = (warps + (INT ? 2 : 4)) * 32; // setmaxnreg goes by groups of four warps
@@ -70,6 +75,7 @@ struct TileArgs {
   int chunk;                               // blocks of bf16 that are summed in the tensor core
   int pairs, waves;                        // tiles below waves * pairs are whole; the others are split
   int piece, group;                        // blocks of a pair's part of the split tiles (0: none are split); see Plan
+  int copies;                              // of the integer A, one after another
   int keep_a, keep_b;                      // how long the second-level cache should keep the operands' lines
   int out_dtype;
 };
@@ -379,6 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
     if (warp == L::warps && lane == 0) {
       uint32_t n = 0, s = 0, turn = 0;                         // stages filled so far; the next, and its turn
       const uint64_t keep_a = policy(a.keep_a), keep_b = policy(a.keep_b);
+      const int copy = pair % a.copies;
       for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
         const int m = p.m * kTile + (int)rank * 128, c = p.n * kTile + (int)rank * 128;
         int plane = p.from / a.plane_blocks, k = p.from - plane * a.plane_blocks;
@@ -388,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
           const uint32_t bar = in_cta(smem_u32(full + s), 0);
           const uint32_t at = smem_u32(smem + s * L::stage_bytes);
           if constexpr (INT) {
-            load_box(at, &a.a, k * 128, m, bar, keep_a);
+            load_box(at, &a.a, k * 128, m, copy, bar, keep_a);
             load_box(at + kOperand, &a.b, k * 128, c, bar, keep_b);
           } else {
             if constexpr (A_ACROSS) {
@@ -612,6 +619,107 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   }
 }
 
+// ---- few tokens ----------------------------------------------------------------------------------------------------
+
+struct FewArgs {
+  const int8_t* x;
+  const int8_t* w;
+  const float* x_scale;
+  const float* w_scale;
+  void* out;
+  int64_t x_stride, w_stride, out_stride, channels;
+  int tokens, depth, out_dtype;
+};
+
+// The last bytes of a row in 8 bits, from `at` on, and zeros: what stands behind the row is not read.
+__device__ __noinline__ uint4 last_bytes(const int8_t* row, int at, int depth) {
+  uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (at + i < depth) v[i / 4] |= (uint32_t)(uint8_t)row[at + i] << (8 * (i % 4));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// ROWS channels of the weights pass once, 16 bytes a lane, against the tokens' rows (by way of the first-level cache): the call is
+// the weights' way from memory. With SPLIT the eight warps of a block share its channels along the depth, else each has its own.
+template <int TOKENS, int ROWS, bool SPLIT>
+__global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewArgs a) {
+  pdl_begin();
+  __shared__ int parts[SPLIT ? 8 : 1][TOKENS][ROWS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = (SPLIT ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + warp) * ROWS;
+  if (first >= a.channels) return;                 // (with SPLIT the whole block)
+  const int8_t* x = a.x;
+  const int8_t* w = a.w + first * a.w_stride;
+  const int last_row = (int)min((int64_t)ROWS - 1, a.channels - 1 - first), last_token = a.tokens - 1;
+  int sum[ROWS][TOKENS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) sum[r][t] = 0;
+  for (int at = (SPLIT ? threadIdx.x : lane) * 16; at < a.depth; at += SPLIT ? 4096 : 512) {
+    uint4 wr[ROWS], xt[TOKENS];
+    const bool all = at + 16 <= a.depth;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int8_t* p = w + min(r, last_row) * a.w_stride;
+      wr[r] = all ? __ldg(reinterpret_cast<const uint4*>(p + at)) : last_bytes(p, at, a.depth);
+    }
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) {
+      const int8_t* p = x + min(t, last_token) * a.x_stride;
+      xt[t] = all ? __ldg(reinterpret_cast<const uint4*>(p + at)) : last_bytes(p, at, a.depth);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int t = 0; t < TOKENS; ++t) {
+        int s = __dp4a((int)wr[r].x, (int)xt[t].x, sum[r][t]);
+        s = __dp4a((int)wr[r].y, (int)xt[t].y, s);
+        s = __dp4a((int)wr[r].z, (int)xt[t].z, s);
+        sum[r][t] = __dp4a((int)wr[r].w, (int)xt[t].w, s);
+      }
+  }
+  // result (t, r) to lane t * ROWS + r (of the whole block with SPLIT)
+  constexpr int N = TOKENS * ROWS;
+  static_assert(N <= 32, "");
+  int mine = 0;
+#pragma unroll
+  for (int t = 0; t < TOKENS; ++t)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int s = __reduce_add_sync(kFull, sum[r][t]);
+      if (lane == t * ROWS + r) mine = s;
+    }
+  const int t = lane / ROWS, r = lane % ROWS;
+  if constexpr (SPLIT) {
+    if (lane < N) parts[warp][t][r] = mine;
+    __syncthreads();
+    if (warp != 0) return;
+    if (lane < N) {
+      mine = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mine += parts[k][t][r];
+    }
+  }
+  if (lane >= N || t > last_token || r > last_row) return;
+  const float v = __int2float_rn(mine) * __ldg(a.x_scale + t) * __ldg(a.w_scale + first + r);
+  const int64_t to = t * a.out_stride + first + r;
+  if (a.out_dtype == GSPARSE_F32) static_cast<float*>(a.out)[to] = v;
+  else if (a.out_dtype == GSPARSE_BF16) static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(a.out)[to] = __float2half_rn(v);
+}
+
+// Copies of rows in 8 bits, one after another; a block takes a row of one of them.
+__global__ void __launch_bounds__(128) copies_kernel(const int8_t* x, int64_t x_stride, int tokens, int depth, int8_t* out, int64_t out_stride) {
+  pdl_begin();
+  const int copy = blockIdx.x / tokens, t = blockIdx.x - copy * tokens;
+  const int8_t* row = x + t * x_stride;
+  int8_t* to = out + ((int64_t)copy * tokens + t) * out_stride;
+  for (int at = threadIdx.x * 16; at < depth; at += 128 * 16)
+    *reinterpret_cast<uint4*>(to + at) = at + 16 <= depth ? __ldg(reinterpret_cast<const uint4*>(row + at)) : last_bytes(row, at, depth);
+}
+
 // ---- gradients in parts of bf16 -------------------------------------------------------------------------------
 
 // x as a sum of PLANES bf16 numbers, exact (8 bits of its significand each): the first holds what is no number.
@@ -745,6 +853,24 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
 
 int64_t part_entries(const Plan& p) { return p.piece ? 2 * (int64_t)p.pairs * kTile * kTile : 0; }
 
+constexpr int64_t kFewTokens = 4;          // (8 tokens against 85000 x 512: 34 us there, 4: 16; the tiles take 17)
+
+template <int TOKENS, int ROWS>
+void few_of(const FewArgs& a, cudaStream_t st) {
+  // Channels for fewer than 32 warps on each SM, and a depth that leaves every warp of a block something: split.
+  const bool split = a.channels < (int64_t)ROWS * 32 * sm_count() && a.depth >= 1024;
+  const dim3 grid((unsigned)cdiv(a.channels, split ? ROWS : 8 * ROWS));
+  if (split) launch(few_kernel<TOKENS, ROWS, true>, grid, dim3(256), 0, st, a);
+  else launch(few_kernel<TOKENS, ROWS, false>, grid, dim3(256), 0, st, a);
+}
+
+int few(const FewArgs& a, cudaStream_t st) {
+  if (a.tokens == 1) few_of<1, 4>(a, st);
+  else if (a.tokens == 2) few_of<2, 4>(a, st);
+  else few_of<4, 4>(a, st);
+  return launch_status();
+}
+
 bool fits(int64_t rows, int64_t cols) { return cdiv(rows, kTile) * cdiv(cols, kTile) < (1ll << 30); }
 
 template <bool INT, bool A_ACROSS>
@@ -779,6 +905,28 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
     else launch(join_kernel<INT, __half>, grid, dim3(256), 0, st, (const JoinArgs&)j);
   }
   return launch_status();
+}
+
+// What the product keeps in the workspace.
+struct Product {
+  Plan plan;
+  int copies;
+  int8_t* copy;
+  float* part;
+  size_t bytes;
+};
+
+Product product_of(void* workspace, int64_t tokens, int64_t channels, int64_t depth) {
+  Product p{};
+  if (tokens <= kFewTokens) return p;
+  p.plan = plan_of(tokens, channels, cdiv(depth, 128));
+  const int64_t x = tokens * round_up(depth, 16);
+  Carver c(workspace);
+  p.copies = x <= kCopyBytes ? (int)min(cdiv(kCopiesBytes, x), (int64_t)p.plan.pairs) : 1;
+  if (p.copies > 1) p.copy = c.take<int8_t>(p.copies * x);
+  if (part_entries(p.plan)) p.part = c.take<float>(part_entries(p.plan));
+  p.bytes = c.off;
+  return p;
 }
 
 // A gradient's operands in the workspace: dout in planes of bf16 where it is not bf16 rows at 16-byte boundaries already, and the
@@ -861,7 +1009,7 @@ extern "C" {
 
 size_t gsparse_linear_q8_workspace_size(int64_t tokens, int64_t channels, int64_t depth) {
   if (sizes(tokens, channels, depth) != GSPARSE_OK || !fits(tokens, channels)) return 0;
-  return 256 + (size_t)part_entries(plan_of(tokens, channels, cdiv(depth, 128))) * sizeof(float);
+  return product_of(nullptr, tokens, channels, depth).bytes;
 }
 
 int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, const int8_t* w, int64_t w_stride, const float* w_scale,
@@ -874,11 +1022,19 @@ int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, c
   if (tokens == 0) return GSPARSE_OK;
   if (!rows8(x, x_stride, x_scale, depth) || !rows8(w, w_stride, w_scale, depth) || !matrix(out, out_stride, dtype, tokens, channels, true))
     return GSPARSE_ERR_INVALID_ARG;
-  if (!space(workspace, workspace_bytes, gsparse_linear_q8_workspace_size(tokens, channels, depth))) return GSPARSE_ERR_WORKSPACE;
+  const Product p = product_of(workspace, tokens, channels, depth);
+  if (p.bytes && !space(workspace, workspace_bytes, p.bytes)) return GSPARSE_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (tokens <= kFewTokens)
+    return few({x, w, x_scale, w_scale, out, x_stride, w_stride, out_stride, channels, (int)tokens, (int)depth, dtype}, s);
+  const int64_t copy_stride = round_up(depth, 16);
+  if (p.copy)
+    launch(copies_kernel, dim3((unsigned)(p.copies * tokens)), dim3(128), 0, s, x, x_stride, (int)tokens, (int)depth, p.copy, copy_stride);
   TileArgs a{};
-  if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, depth, tokens, x_stride, 128) ||
+  if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.copy ? p.copy : x, depth, tokens, p.copy ? copy_stride : x_stride, 128, p.copies) ||
       !map_of(&a.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, depth, channels, w_stride, 128))
     return GSPARSE_ERR_CUDA;
+  a.copies = p.copies;
   a.row_scale = x_scale;
   a.col_scale = w_scale;
   a.d_status = d_status;
@@ -886,7 +1042,7 @@ int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, c
   a.cols = channels;
   a.plane_blocks = (int)cdiv(depth, 128);
   a.out_dtype = dtype;
-  return tiles<true, false>(a, plan_of(tokens, channels, a.plane_blocks), static_cast<float*>(workspace), out, out_stride, (cudaStream_t)stream);
+  return tiles<true, false>(a, p.plan, p.part, out, out_stride, s);
 }
 
 size_t gsparse_linear_q8_grad_input_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens,

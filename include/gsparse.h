@@ -562,7 +562,7 @@ int gsparse_rms_norm_backward(const void* h, int64_t h_stride, const void* weigh
 
 /* out[t][n] = x_scale_t w_scale_n * sum_k x[t][k] w[n][k], the sum in 32-bit integers (exact), its product with x_scale_t
  * (which has to be within fp32), then with w_scale_n, each rounded to fp32, and once more to out's type dtype. x: tokens
- * rows of depth in 8 bits; w: channels rows. */
+ * rows of depth in 8 bits; w: channels rows. The workspace may be NULL where its size is 0. */
 size_t gsparse_linear_q8_workspace_size(int64_t tokens, int64_t channels, int64_t depth);
 int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, const int8_t* w, int64_t w_stride,
                       const float* w_scale, int64_t tokens, int64_t channels, int64_t depth, void* out,

@@ -148,7 +148,7 @@ def test_no_rows_is_no_work(gs, call):
 
 
 def _product(gs, **kw):
-    a = dict(x=P, x_stride=48, xs=P, w=P, w_stride=48, ws=P, tokens=3, channels=5, depth=40, out=P, out_dtype=F32, out_stride=5,
+    a = dict(x=P, x_stride=48, xs=P, w=P, w_stride=48, ws=P, tokens=30, channels=5, depth=40, out=P, out_dtype=F32, out_stride=5,
              workspace=P, bytes=1 << 40) | kw
     return gs.lib().gsparse_linear_q8(a["x"], a["x_stride"], a["xs"], a["w"], a["w_stride"], a["ws"], a["tokens"], a["channels"],
                                       a["depth"], a["out"], a["out_dtype"], a["out_stride"], a["workspace"], a["bytes"], None, None)
@@ -217,7 +217,7 @@ def test_workspace_queries_refuse_what_the_calls_refuse(gs):
     lib = gs.lib()
     assert lib.gsparse_rms_norm_backward_workspace_size(1000, 512) >= 512 * 4
     assert lib.gsparse_rms_norm_backward_workspace_size(-1, 512) == 0 and lib.gsparse_rms_norm_backward_workspace_size(1, 0) == 0
-    assert lib.gsparse_linear_q8_workspace_size(3, 5, 40) > 0 and lib.gsparse_linear_q8_workspace_size(3, 0, 40) == 0
+    assert lib.gsparse_linear_q8_workspace_size(30, 5, 40) > 0 and lib.gsparse_linear_q8_workspace_size(3, 0, 40) == 0
     for f in (lib.gsparse_linear_q8_grad_input_workspace_size, lib.gsparse_linear_q8_grad_weight_workspace_size):
         assert f(P, F32, 5, 3, 5, 40) > 0 and f(P, 3, 5, 3, 5, 40) == 0 and f(P, F32, 5, 3, 5, 0) == 0
 
