@@ -722,17 +722,32 @@ __global__ void __launch_bounds__(128) copies_kernel(const int8_t* x, int64_t x_
 
 // ---- gradients in parts of bf16 -------------------------------------------------------------------------------
 
-// x as a sum of PLANES bf16 numbers, exact (8 bits of its significand each): the first holds what is no number.
+struct OperandArgs {
+  const void* dout;
+  __nv_bfloat16* a;                        // its planes, or null: its rows are read as they are
+  const int8_t* q;
+  const float* scale;
+  __nv_bfloat16* b;
+  int64_t dout_stride, a_stride, tokens, channels, q_stride, b_stride, along;
+  int depth, a_blocks;                     // blocks of the grid that make the planes
+};
+
+template <class T> __device__ __forceinline__ float as_float(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (__is_same(T, __nv_bfloat16)) return __bfloat162float(v);
+  else return __half2float(v);
+}
+
+// 8 entries of x as a sum of PLANES bf16 numbers each, exact (8 bits of the significand in each): the first holds what is no number.
 template <class T, int PLANES>
-__global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t in_stride, int64_t rows, int64_t cols, __nv_bfloat16* out, int64_t out_stride) {
-  pdl_begin();
-  const int64_t per = (cols + 7) / 8;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * blockDim.x) {
+__device__ __forceinline__ void planes(const OperandArgs& a, int64_t block, int64_t blocks) {
+  const int64_t per = (a.channels + 7) / 8;
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < a.tokens * per; i += blocks * blockDim.x) {
     const int64_t row = i / per, at = (i - row * per) * 8;
-    const T* p = in + row * in_stride + at;
+    const T* p = static_cast<const T*>(a.dout) + row * a.dout_stride + at;
     float v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = at + k < cols ? (float)p[k] : 0.0f;
+    for (int k = 0; k < 8; ++k) v[k] = at + k < a.channels ? as_float<T>(p[k]) : 0.0f;
 #pragma unroll
     for (int plane = 0; plane < PLANES; ++plane) {
       __nv_bfloat16 e[8];
@@ -748,8 +763,33 @@ __global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t in_str
           v[k] -= high;
         }
       }
-      *reinterpret_cast<uint4*>(out + ((int64_t)plane * rows + row) * out_stride + at) = *reinterpret_cast<const uint4*>(e);
+      *reinterpret_cast<uint4*>(a.a + ((int64_t)plane * a.tokens + row) * a.a_stride + at) = *reinterpret_cast<const uint4*>(e);
     }
+  }
+}
+
+// What a gradient's tiles read, in one launch: the planes of dout, and the values of the rows in 8 bits.
+template <class T, int PLANES>
+__global__ void __launch_bounds__(256) operands_kernel(const __grid_constant__ OperandArgs a) {
+  pdl_begin();
+  if ((int)blockIdx.x < a.a_blocks) {
+    planes<T, PLANES>(a, blockIdx.x, a.a_blocks);
+    return;
+  }
+  const int64_t per = (a.depth + 15) / 16, blocks = gridDim.x - a.a_blocks;
+  for (int64_t i = (int64_t)(blockIdx.x - a.a_blocks) * blockDim.x + threadIdx.x; i < a.along * per; i += blocks * blockDim.x) {
+    const int64_t row = i / per;
+    const int at = (int)(i - row * per) * 16;
+    const float s = __ldg(a.scale + row);
+    const int8_t* p = a.q + row * a.q_stride;
+    const uint4 raw = at + 16 <= a.depth ? __ldg(reinterpret_cast<const uint4*>(p + at)) : last_bytes(p, at, a.depth);
+    const int8_t* b = reinterpret_cast<const int8_t*>(&raw);
+    __nv_bfloat16 v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __float2bfloat16_rn((float)b[k] * s);
+    uint4* to = reinterpret_cast<uint4*>(a.b + row * a.b_stride + at);
+    to[0] = reinterpret_cast<const uint4*>(v)[0];
+    if (at + 8 < a.b_stride) to[1] = reinterpret_cast<const uint4*>(v)[1];
   }
 }
 
@@ -968,19 +1008,13 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
              cudaStream_t st) {
   const Grad g = grad_of(workspace, dout, dtype, dout_stride, tokens, channels, depth, WEIGHT);
   const int64_t along = WEIGHT ? tokens : channels;
-  if (g.copied) {
-    const int64_t blocks = cdiv(tokens * cdiv(channels, 8), 256);
-    const dim3 grid((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16));
-    if (dtype == GSPARSE_F32)
-      launch(planes_kernel<float, 3>, grid, dim3(256), 0, st, static_cast<const float*>(dout), dout_stride, tokens, channels, g.a, g.stride_a);
-    else if (dtype == GSPARSE_F16)
-      launch(planes_kernel<__half, 2>, grid, dim3(256), 0, st, static_cast<const __half*>(dout), dout_stride, tokens, channels, g.a, g.stride_a);
-    else
-      launch(planes_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, static_cast<const __nv_bfloat16*>(dout), dout_stride, tokens, channels, g.a,
-             g.stride_a);
-  }
-  const int e = gsparse_dequantize_rows(q, q_stride, scale, along, depth, g.b, GSPARSE_BF16, g.stride_b, (gsparse_stream)st);
-  if (e != GSPARSE_OK) return e;
+  OperandArgs o{dout, g.a, q, scale, g.b, dout_stride, g.stride_a, tokens, channels, q_stride, g.stride_b, along, (int)depth, 0};
+  auto blocks_of = [](int64_t vectors) { return (int)(vectors < 256ll * 148 * 16 ? cdiv(vectors, 256) : 148 * 16); };
+  if (g.copied) o.a_blocks = blocks_of(tokens * cdiv(channels, 8));
+  const dim3 grid((unsigned)(o.a_blocks + blocks_of(along * cdiv(depth, 16))));
+  if (dtype == GSPARSE_F32) launch(operands_kernel<float, 3>, grid, dim3(256), 0, st, (const OperandArgs&)o);
+  else if (dtype == GSPARSE_F16) launch(operands_kernel<__half, 2>, grid, dim3(256), 0, st, (const OperandArgs&)o);
+  else launch(operands_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, (const OperandArgs&)o);
   TileArgs a{};
   if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.copied ? g.a : dout, channels, tokens, g.copied ? g.stride_a : dout_stride,
               WEIGHT ? 64 : 128, g.planes) ||
