@@ -38,12 +38,22 @@ template <> struct Type<__half> {
   static __device__ __forceinline__ Two put(float a, float b) { return __floats2half2_rn(a, b); }
 };
 
-// A thread's E entries of a row of `depth`: with VEC as vectors of 16 bytes, thread after thread; else entry by entry, thread
-// after thread, so that rows of any alignment are read in whole lines too.
-template <class T, bool VEC, int E>
+// How a row's entries are shared out. kVectors: every row starts at a 16-byte boundary and is whole vectors. kShifted: rows start
+// anywhere, but all matrices' rows at the same place between two boundaries; vectors lie between boundaries, those at the row's ends
+// are read and written entry by entry. kEntries: rows of any alignment, entry by entry.
+enum { kVectors, kShifted, kEntries };
+
+// A thread's E entries of a row of `depth`, vector after vector (entry after entry), thread after thread. `off`: the row's start
+// behind a boundary, in entries (kShifted only).
+template <class T, int MODE, int E>
 struct Mine {
-  static constexpr int N = VEC ? Type<T>::N : 1;
-  static __device__ __forceinline__ int first(int j, int tid, int threads) { return (j * threads + tid) * N; }
+  static constexpr int N = MODE == kEntries ? 1 : Type<T>::N;
+  int tid, threads, depth, off;
+
+  __device__ __forceinline__ int first(int j) const { return (j * threads + tid) * N - (MODE == kShifted ? off : 0); }
+  __device__ __forceinline__ bool whole(int at) const { return MODE == kShifted ? at >= 0 && at + N <= depth : at < depth; }
+  __device__ __forceinline__ bool none(int at) const { return at >= depth || (MODE == kShifted && at + N <= 0); }
+  __device__ __forceinline__ bool in(int at) const { return at < depth && (MODE != kShifted || at >= 0); }
 
   // As they lie in memory, and as numbers.
   union Raw {
@@ -52,12 +62,21 @@ struct Mine {
     __device__ __forceinline__ Raw() {}
   };
 
-  static __device__ __forceinline__ void fetch(Raw& raw, const T* row, int depth, int tid, int threads) {
+  __device__ __forceinline__ void fetch(Raw& raw, const T* row) const {
 #pragma unroll
     for (int j = 0; j < E / N; ++j) {
-      const int at = first(j, tid, threads);
-      if constexpr (VEC) raw.vec[j] = at < depth ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0, 0, 0, 0);
-      else raw.one[j] = at < depth ? row[at] : Type<T>::put(0.0f);
+      const int at = first(j);
+      if constexpr (MODE == kEntries) {
+        raw.one[j] = at < depth ? row[at] : Type<T>::put(0.0f);
+      } else {
+        raw.vec[j] = make_uint4(0, 0, 0, 0);
+        if (whole(at)) raw.vec[j] = *reinterpret_cast<const uint4*>(row + at);
+        else if (MODE == kShifted && !none(at)) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (in(at + i)) raw.one[j * N + i] = row[at + i];
+        }
+      }
     }
   }
 
@@ -85,62 +104,116 @@ struct Mine {
     }
   }
 
-  static __device__ __forceinline__ void write(T* row, const Raw& raw, int depth, int tid, int threads) {
+  __device__ __forceinline__ void write(T* row, const Raw& raw) const {
 #pragma unroll
     for (int j = 0; j < E / N; ++j) {
-      const int at = first(j, tid, threads);
-      if (at >= depth) continue;
-      if constexpr (VEC) *reinterpret_cast<uint4*>(row + at) = raw.vec[j];
-      else row[at] = raw.one[j];
+      const int at = first(j);
+      if constexpr (MODE == kEntries) {
+        if (at < depth) row[at] = raw.one[j];
+      } else {
+        if (whole(at)) *reinterpret_cast<uint4*>(row + at) = raw.vec[j];
+        else if (MODE == kShifted && !none(at)) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (in(at + i)) row[at + i] = raw.one[j * N + i];
+        }
+      }
     }
   }
 
-  static __device__ __forceinline__ void load(float (&v)[E], const T* row, int depth, int tid, int threads) {
+  __device__ __forceinline__ void load(float (&v)[E], const T* row) const {
     Raw raw;
-    fetch(raw, row, depth, tid, threads);
+    fetch(raw, row);
     numbers(v, raw);
   }
 
-  static __device__ __forceinline__ void store(T* row, const float (&v)[E], int depth, int tid, int threads) {
+  __device__ __forceinline__ void store(T* row, const float (&v)[E]) const {
     Raw raw;
     held(raw, v);
-    write(row, raw, depth, tid, threads);
+    write(row, raw);
   }
 
-  // N entries of 16 bits; with VEC they start at a multiple of their own size.
+  // N entries of 16 bits; with kVectors they start at a multiple of their own size.
   template <class W>
-  static __device__ __forceinline__ void narrow(float* v, const W* w) {
+  __device__ __forceinline__ void narrow(float* v, const W* w, int at) const {
     W e[N];
-    if constexpr (N == 8) *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(w));
-    else if constexpr (N == 4) *reinterpret_cast<uint2*>(e) = __ldg(reinterpret_cast<const uint2*>(w));
-    else e[0] = *w;
+    if constexpr (MODE == kVectors && N == 8) *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(w + at));
+    else if constexpr (MODE == kVectors) *reinterpret_cast<uint2*>(e) = __ldg(reinterpret_cast<const uint2*>(w + at));
+    else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = in(at + i) ? w[at + i] : Type<W>::put(0.0f);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = Type<W>::get(e[i]);
   }
 
   // Entries of fp32, bf16 or fp16, whatever T is (the norm's weight).
-  static __device__ __forceinline__ void load_any(float (&v)[E], const void* p, int dtype, int depth, int tid, int threads) {
+  __device__ __forceinline__ void load_any(float (&v)[E], const void* p, int dtype) const {
 #pragma unroll
     for (int j = 0; j < E / N; ++j) {
-      const int at = first(j, tid, threads);
+      const int at = first(j);
 #pragma unroll
       for (int i = 0; i < N; ++i) v[j * N + i] = 0.0f;
-      if (at >= depth) continue;
+      if (none(at)) continue;
       if (dtype == GSPARSE_F32) {
-        const float* w = static_cast<const float*>(p) + at;
-        if constexpr (N >= 4) {
+        const float* w = static_cast<const float*>(p);
+        if constexpr (MODE == kVectors) {
 #pragma unroll
           for (int i = 0; i < N; i += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(w + i));
+            const float4 f = __ldg(reinterpret_cast<const float4*>(w + at + i));
             v[j * N + i] = f.x; v[j * N + i + 1] = f.y; v[j * N + i + 2] = f.z; v[j * N + i + 3] = f.w;
           }
         } else {
-          v[j] = *w;
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[j * N + i] = in(at + i) ? w[at + i] : 0.0f;
         }
       } else if (dtype == GSPARSE_BF16) {
-        narrow(&v[j * N], static_cast<const __nv_bfloat16*>(p) + at);
+        narrow(&v[j * N], static_cast<const __nv_bfloat16*>(p), at);
       } else {
-        narrow(&v[j * N], static_cast<const __half*>(p) + at);
+        narrow(&v[j * N], static_cast<const __half*>(p), at);
+      }
+    }
+  }
+
+  // The entries' low bytes (of y's bits) into a row in 8 bits, which starts at a 16-byte boundary; zeros where not `fine`.
+  __device__ __forceinline__ void bytes(int8_t* out, const float (&y)[E], bool fine) const {
+#pragma unroll
+    for (int j = 0; j < E / N; ++j) {
+      const int at = first(j);
+      const float* s = y + j * N;
+      auto four = [&](int i) {
+        const uint32_t a01 = __byte_perm(__float_as_uint(s[i]), __float_as_uint(s[i + 1]), 0x0040);
+        const uint32_t a23 = __byte_perm(__float_as_uint(s[i + 2]), __float_as_uint(s[i + 3]), 0x0040);
+        return fine ? __byte_perm(a01, a23, 0x5410) : 0u;
+      };
+      if constexpr (MODE == kEntries) {
+        if (at < depth) out[at] = fine ? (int8_t)__float_as_uint(s[0]) : 0;
+      } else if constexpr (MODE == kVectors) {
+        if (at >= depth) continue;
+        if constexpr (N == 8) *reinterpret_cast<uint2*>(out + at) = make_uint2(four(0), four(4));
+        else *reinterpret_cast<uint32_t*>(out + at) = four(0);
+      } else {
+        // The row's groups of N bytes between boundaries take this vector's last N - off entries and the next one's first: the next
+        // lane's, but for the warp's last lane, which writes its own alone, as the first lane does with what the last one lacks.
+        const int lane = threadIdx.x & 31;
+        uint64_t mine = N == 8 ? (uint64_t)four(0) | (uint64_t)four(N == 8 ? 4 : 0) << 32 : four(0);
+        const uint64_t next = N == 8 ? __shfl_down_sync(kFull, (unsigned long long)mine, 1) : __shfl_down_sync(kFull, (uint32_t)mine, 1);
+        const int group = at + off;                // (off 0: the whole of this vector)
+        if (off && lane == 0) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i < off && in(at + i)) out[at + i] = (int8_t)(mine >> (8 * i));
+        }
+        const uint64_t both = mine >> (8 * off) | (off ? next << (8 * (N - off)) : 0);
+        const int have = off && lane == 31 ? N - off : N;
+        if (have == N && group + N <= depth) {
+          if constexpr (N == 8) *reinterpret_cast<uint64_t*>(out + group) = both;
+          else *reinterpret_cast<uint32_t*>(out + group) = (uint32_t)both;
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i < have && group + i < depth) out[group + i] = (int8_t)(both >> (8 * i));
+        }
       }
     }
   }
@@ -207,8 +280,8 @@ __device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float
 // An entry's steps t come from three fp32 roundings, so they are off by less than 2^-15: only those that lie closer than 2^-14 to
 // the middle between two integers (one of 2^13) are worked out again in two parts. All of them in two parts, with divisions and roots in
 // 64 bits: 92 against 38 us for 8192 x 4096 bf16 with the residual (235 MB, 36 us at the measured copy bandwidth).
-template <class T, bool VEC, int E, bool NORM, int MOST>
-__global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(const __grid_constant__ RowArgs a) {
+template <class T, int MODE, int E, bool NORM, int MOST>
+__global__ void __launch_bounds__(MOST, MODE != kEntries && MOST == 512 ? 2 : 1) rows_kernel(const __grid_constant__ RowArgs a) {
   pdl_begin();
   __shared__ double sums[kMostThreads / 32];
   __shared__ uint32_t tops[kMostThreads / 32];
@@ -216,22 +289,24 @@ __global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(
   const bool one = a.warps == 1;
   const int64_t row = one ? (int64_t)blockIdx.x * kRowsPerBlock + warp : blockIdx.x;
   if (row >= a.rows) return;                       // whole warps, and only where no barrier follows
-  const int tid = one ? lane : threadIdx.x, threads = a.warps * 32, depth = a.depth;
-  using M = Mine<T, VEC, E>;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  using M = Mine<T, MODE, E>;
+  const M mine{one ? lane : (int)threadIdx.x, a.warps * 32, a.depth,
+               MODE == kShifted ? (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)) : 0};
   typename M::Raw raw;                             // h
   float v[E], y[E];
-  M::fetch(raw, static_cast<const T*>(a.x) + row * a.x_stride, depth, tid, threads);
+  mine.fetch(raw, x);
   float r_hi = 1.0f, r_lo = 0.0f;
   if constexpr (NORM) {
     if (a.residual) {
-      M::load(y, static_cast<const T*>(a.residual) + row * a.residual_stride, depth, tid, threads);
+      mine.load(y, static_cast<const T*>(a.residual) + row * a.residual_stride);
       M::numbers(v, raw);
 #pragma unroll
       for (int i = 0; i < E; ++i) v[i] += y[i];
       M::held(raw, v);
     }
-    if (a.h) M::write(static_cast<T*>(a.h) + row * a.h_stride, raw, depth, tid, threads);
-    M::load_any(y, a.weight, a.weight_dtype, depth, tid, threads);
+    if (a.h) mine.write(static_cast<T*>(a.h) + row * a.h_stride, raw);
+    mine.load_any(y, a.weight, a.weight_dtype);
     M::numbers(v, raw);
     // squares of any size, and a sum that is good to the last of them: 64 bits
     double ss = 0.0;
@@ -247,18 +322,18 @@ __global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(
     const double r = inverse_root(ss * a.inv_depth + (double)a.eps);
     r_hi = (float)r;
     r_lo = (float)(r - (double)r_hi);
-    if (a.rstd && tid == 0) a.rstd[row] = r_hi;
+    if (a.rstd && mine.tid == 0) a.rstd[row] = r_hi;
 #pragma unroll
     for (int i = 0; i < E; ++i) y[i] = v[i] * (r_hi * y[i]);
     if (a.y) {
       float w[E];
-      M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+      mine.load_any(w, a.weight, a.weight_dtype);
 #pragma unroll
       for (int i = 0; i < E; ++i) {                // in two parts: rounded once
         const float rw = __fmul_rn(r_hi, w[i]);
         w[i] = __fmaf_rn(v[i], rw, v[i] * __fmaf_rn(r_lo, w[i], __fmaf_rn(r_hi, w[i], -rw)));
       }
-      M::store(static_cast<T*>(a.y) + row * a.y_stride, w, depth, tid, threads);
+      mine.store(static_cast<T*>(a.y) + row * a.y_stride, w);
     }
     if (!a.q) return;
   } else {
@@ -276,7 +351,7 @@ __global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(
   const bool fine = bits < 0x7f800000u;            // no infinity, no NaN
   const int e = fine ? scale_exponent(bits) : 0;
   const float up = power(-e);                      // -121 <= -e <= 126
-  if (tid == 0) a.scale[row] = fine ? power(e) : __int_as_float(0x7fc00000);
+  if (mine.tid == 0) a.scale[row] = fine ? power(e) : __int_as_float(0x7fc00000);
   float near = 0.0f;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
@@ -288,7 +363,7 @@ __global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(
     if (near > 0.5f - 0x1p-14f && fine) {
       M::numbers(v, raw);
       float w[E];
-      M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+      mine.load_any(w, a.weight, a.weight_dtype);
 #pragma unroll
       for (int i = 0; i < E; ++i) y[i] = steps_of(v[i], r_hi, r_lo, w[i], up);
     }
@@ -297,27 +372,13 @@ __global__ void __launch_bounds__(MOST, VEC && MOST == 512 ? 2 : 1) rows_kernel(
 #pragma unroll
     for (int i = 0; i < E; ++i) y[i] = fminf(fmaxf(y[i], kRound - 127.0f), kRound + 127.0f);
   }
-  int8_t* out = a.q + row * a.q_stride;
-#pragma unroll
-  for (int j = 0; j < E / M::N; ++j) {
-    const int at = M::first(j, tid, threads);
-    const float* s = y + j * M::N;
-    auto four = [&](int i) {
-      const uint32_t a01 = __byte_perm(__float_as_uint(s[i]), __float_as_uint(s[i + 1]), 0x0040);
-      const uint32_t a23 = __byte_perm(__float_as_uint(s[i + 2]), __float_as_uint(s[i + 3]), 0x0040);
-      return fine ? __byte_perm(a01, a23, 0x5410) : 0u;
-    };
-    if (at >= depth) continue;
-    if constexpr (M::N == 8) *reinterpret_cast<uint2*>(out + at) = make_uint2(four(0), four(4));
-    else if constexpr (M::N == 4) *reinterpret_cast<uint32_t*>(out + at) = four(0);
-    else out[at] = fine ? (int8_t)__float_as_uint(s[0]) : 0;
-  }
+  mine.bytes(a.q + row * a.q_stride, y, fine);
 }
 
 // ---- read back ------------------------------------------------------------------------------------------
 
-// 16 entries a thread.
-template <class T, bool VEC>
+// Rows of `out` that start at 16-byte boundaries: 16 entries a thread.
+template <class T>
 __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int depth,
                                                       T* out, int64_t out_stride) {
   pdl_begin();
@@ -329,22 +390,67 @@ __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* q, int64_t q
     const int8_t* p = q + row * q_stride + at;
     T* o = out + row * out_stride + at;
     const int left = depth - at;
-    T v[16];
     if (left >= 16) {
       const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
       const int8_t* b = reinterpret_cast<const int8_t*>(&raw);
+      union { uint4 vec[sizeof(T)]; T one[16]; } e;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = Type<T>::put((float)b[k] * s);
-      if constexpr (VEC) {
+      for (int k = 0; k < 16; ++k) e.one[k] = Type<T>::put((float)b[k] * s);
 #pragma unroll
-        for (int k = 0; k < 16; k += Type<T>::N) *reinterpret_cast<uint4*>(o + k) = *reinterpret_cast<const uint4*>(v + k);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = v[k];
-      }
+      for (int k = 0; k < (int)sizeof(T); ++k) reinterpret_cast<uint4*>(o)[k] = e.vec[k];
     } else {
       for (int k = 0; k < left; ++k) o[k] = Type<T>::put((float)p[k] * s);
     }
+  }
+}
+
+// Rows of any alignment. A thread makes the vectors of 16 bytes of `out` between two boundaries, from the row's N bytes that they stand for: with rows that
+// start off a boundary those are parts of two groups of N.
+template <class T>
+__global__ void __launch_bounds__(256) dequant_shifted_kernel(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int depth,
+                                                              T* out, int64_t out_stride, int per) {
+  pdl_begin();
+  constexpr int N = Type<T>::N;
+  const int64_t all = rows * per, step = (int64_t)gridDim.x * blockDim.x;
+  int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= all) return;
+  // (a division once; the steps after it add up)
+  const int64_t step_rows = step / per;
+  const int step_at = (int)(step - step_rows * per);
+  int64_t row = i / per;
+  int v = (int)(i - row * per);
+  for (; i < all; i += step) {
+    T* to = out + row * out_stride;
+    const int8_t* from = q + row * q_stride;
+    const float s = __ldg(scale + row);
+    const int off = (int)((reinterpret_cast<uintptr_t>(to) & 15) / sizeof(T)), at = v * N - off;
+    auto group = [&](int g) -> uint64_t {          // bytes [g, g + N) of the row, 0 where it has none; g a multiple of N
+      if (g < 0 || g >= depth) return 0;
+      if (g + N <= depth) {
+        if constexpr (N == 8) return __ldg(reinterpret_cast<const unsigned long long*>(from + g));
+        else return __ldg(reinterpret_cast<const uint32_t*>(from + g));
+      }
+      uint64_t b = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (g + k < depth) b |= (uint64_t)(uint8_t)from[g + k] << (8 * k);
+      return b;
+    };
+    if (at < depth) {
+      const uint64_t b = off ? group(at + off - N) >> (8 * (N - off)) | group(at + off) << (8 * off) : group(at);
+      union { uint4 vec; T one[N]; } e;
+#pragma unroll
+      for (int k = 0; k < N; ++k) e.one[k] = Type<T>::put((float)(int8_t)(b >> (8 * k)) * s);
+      if (at >= 0 && at + N <= depth) *reinterpret_cast<uint4*>(to + at) = e.vec;
+      else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (at + k >= 0 && at + k < depth) to[at + k] = e.one[k];
+      }
+    }
+    row += step_rows;
+    v += step_at;
+    if (v >= per) v -= per, ++row;
   }
 }
 
@@ -364,7 +470,7 @@ struct BackArgs {
 
 // With xh = h r and g = dy w: dx = r (g - xh mean(g xh)) + dh, dw = sum over the rows of dy xh. A thread keeps its places'
 // weights and its sum of dw in registers over all the rows of its group.
-template <class T, bool VEC, int E, int MOST>
+template <class T, int MODE, int E, int MOST>
 __global__ void __launch_bounds__(MOST) norm_back_kernel(const __grid_constant__ BackArgs a) {
   pdl_begin();
   extern __shared__ float shared[];                // of groups > 1: [groups][depth]
@@ -373,17 +479,18 @@ __global__ void __launch_bounds__(MOST) norm_back_kernel(const __grid_constant__
   const bool one = a.warps == 1;
   const int tid = one ? lane : threadIdx.x, threads = a.warps * 32, depth = a.depth;
   const int group = one ? warp : 0;
-  using M = Mine<T, VEC, E>;
+  using M = Mine<T, MODE, E>;
+  const M mine{tid, threads, depth, 0};
   float w[E], dw[E];
-  M::load_any(w, a.weight, a.weight_dtype, depth, tid, threads);
+  mine.load_any(w, a.weight, a.weight_dtype);
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = 0.0f;
   const float inv = 1.0f / (float)depth;
   int turn = 0;
   for (int64_t row = (int64_t)blockIdx.x * a.groups + group; row < a.rows; row += (int64_t)gridDim.x * a.groups, turn ^= 1) {
     float h[E], g[E];
-    M::load(h, static_cast<const T*>(a.h) + row * a.h_stride, depth, tid, threads);
-    M::load(g, static_cast<const T*>(a.dy) + row * a.dy_stride, depth, tid, threads);
+    mine.load(h, static_cast<const T*>(a.h) + row * a.h_stride);
+    mine.load(g, static_cast<const T*>(a.dy) + row * a.dy_stride);
     const float r = __ldg(a.rstd + row);
     float s = 0.0f;
 #pragma unroll
@@ -403,11 +510,11 @@ __global__ void __launch_bounds__(MOST) norm_back_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < E; ++i) g[i] = r * __fmaf_rn(-h[i], s, g[i]);
     if (a.dh) {
-      M::load(h, static_cast<const T*>(a.dh) + row * a.dh_stride, depth, tid, threads);
+      mine.load(h, static_cast<const T*>(a.dh) + row * a.dh_stride);
 #pragma unroll
       for (int i = 0; i < E; ++i) g[i] += h[i];
     }
-    M::store(static_cast<T*>(a.dx) + row * a.dx_stride, g, depth, tid, threads);
+    mine.store(static_cast<T*>(a.dx) + row * a.dx_stride, g);
   }
   if (!a.partial) return;
   float* to = a.partial + (int64_t)blockIdx.x * depth;
@@ -416,7 +523,7 @@ __global__ void __launch_bounds__(MOST) norm_back_kernel(const __grid_constant__
     for (int j = 0; j < E / M::N; ++j)
 #pragma unroll
       for (int i = 0; i < M::N; ++i) {
-        const int at = M::first(j, tid, threads) + i;
+        const int at = mine.first(j) + i;
         if (at < depth) shared[group * depth + at] = dw[j * M::N + i];
       }
     __syncthreads();
@@ -430,7 +537,7 @@ __global__ void __launch_bounds__(MOST) norm_back_kernel(const __grid_constant__
     for (int j = 0; j < E / M::N; ++j)
 #pragma unroll
       for (int i = 0; i < M::N; ++i) {
-        const int at = M::first(j, tid, threads) + i;
+        const int at = mine.first(j) + i;
         if (at < depth) to[at] = dw[j * M::N + i];
       }
   }
@@ -475,38 +582,66 @@ bool matrix(const void* p, int64_t stride, int32_t dtype, int64_t rows, int64_t 
 }
 
 // Warps of a row and entries a thread: one warp while 16 entries a lane hold the row, then 16 entries a thread; the longest rows
-// in 8 bits without a norm, 32 (more in registers with a norm's weights beside them would spill).
+// in 8 bits without a norm, 32 (more in registers with a norm's weights beside them would spill). `more`: places that a shifted row
+// takes before its first entry.
 struct Shape { int warps, entries; };
-Shape shape_of(int64_t depth) {
-  if (depth <= 512) return {1, depth <= 256 ? 8 : 16};
-  const int e = depth <= GSPARSE_MAX_NORM_DEPTH ? 16 : 32;
-  return {(int)cdiv(depth, 32 * e), e};
+Shape shape_of(int64_t depth, int more = 0) {
+  const int64_t places = depth + more;
+  if (places <= 512) return {1, places <= 256 ? 8 : 16};
+  const int e = places <= GSPARSE_MAX_NORM_DEPTH ? 16 : 32;
+  return {(int)cdiv(places, 32 * e), e};
 }
 
-template <class T, bool VEC, bool NORM>
+template <class T, int MODE, bool NORM>
 void rows_of(const RowArgs& a, const Shape& s, cudaStream_t st) {
   const dim3 grid((unsigned)(s.warps == 1 ? cdiv(a.rows, kRowsPerBlock) : a.rows)), block(s.warps == 1 ? kRowsPerBlock * 32 : s.warps * 32);
-  if (s.entries == 8) launch(rows_kernel<T, VEC, 8, NORM, 512>, grid, block, 0, st, a);
-  else if (s.entries == 16 && s.warps <= 16) launch(rows_kernel<T, VEC, 16, NORM, 512>, grid, block, 0, st, a);
-  else if (s.entries == 16) launch(rows_kernel<T, VEC, 16, NORM, 1024>, grid, block, 0, st, a);
-  else if constexpr (!NORM) launch(rows_kernel<T, VEC, 32, NORM, 1024>, grid, block, 0, st, a);
+  if (s.entries == 8) launch(rows_kernel<T, MODE, 8, NORM, 512>, grid, block, 0, st, a);
+  else if (s.entries == 16 && s.warps <= 16) launch(rows_kernel<T, MODE, 16, NORM, 512>, grid, block, 0, st, a);
+  else if (s.entries == 16) launch(rows_kernel<T, MODE, 16, NORM, 1024>, grid, block, 0, st, a);
+  else if constexpr (!NORM) launch(rows_kernel<T, MODE, 32, NORM, 1024>, grid, block, 0, st, a);
 }
 
+template <class T, bool NORM>
+void rows_by_mode(const RowArgs& a, const Shape& s, int mode, cudaStream_t st) {
+  if (mode == kVectors) rows_of<T, kVectors, NORM>(a, s, st);
+  else if (mode == kShifted) rows_of<T, kShifted, NORM>(a, s, st);
+  else rows_of<T, kEntries, NORM>(a, s, st);
+}
+
+// The mode of rows whose matrices all start `place` behind a boundary and are `step` apart (modulo 16 bytes), or do not (-1).
+struct Places {
+  int place = -1, step = -1;
+  bool same = true;
+  void add(const void* p, int64_t stride, int32_t dtype) {
+    if (!p) return;
+    const int a = (int)(reinterpret_cast<uintptr_t>(p) & 15), b = (int)((stride * (int64_t)size_of(dtype)) & 15);
+    if (place < 0) place = a, step = b;
+    same = same && a == place && b == step;
+  }
+  bool boundaries() const { return same && place == 0 && step == 0; }
+};
+
 template <bool NORM>
-int rows_by_type(int32_t dtype, const RowArgs& a, bool vec, cudaStream_t st) {
-  const Shape s{a.warps, shape_of(a.depth).entries};
-  if (dtype == GSPARSE_F32) vec ? rows_of<float, true, NORM>(a, s, st) : rows_of<float, false, NORM>(a, s, st);
-  else if (dtype == GSPARSE_BF16) vec ? rows_of<__nv_bfloat16, true, NORM>(a, s, st) : rows_of<__nv_bfloat16, false, NORM>(a, s, st);
-  else vec ? rows_of<__half, true, NORM>(a, s, st) : rows_of<__half, false, NORM>(a, s, st);
+int rows_by_type(int32_t dtype, RowArgs& a, const Places& p, cudaStream_t st) {
+  const int n = 16 / (int)size_of(dtype);
+  const bool vectors = p.boundaries() && a.depth % n == 0 && (!a.weight || aligned16(a.weight));
+  Shape s = shape_of(a.depth, vectors || !p.same ? 0 : n - 1);
+  // (the longest rows of their kernels leave no place for a shift)
+  const int mode = vectors ? kVectors : p.same && s.warps <= 32 && (!NORM || s.entries <= 16) ? kShifted : kEntries;
+  if (mode == kEntries) s = shape_of(a.depth);
+  a.warps = s.warps;
+  if (dtype == GSPARSE_F32) rows_by_mode<float, NORM>(a, s, mode, st);
+  else if (dtype == GSPARSE_BF16) rows_by_mode<__nv_bfloat16, NORM>(a, s, mode, st);
+  else rows_by_mode<__half, NORM>(a, s, mode, st);
   return launch_status();
 }
 
-template <class T, bool VEC>
+template <class T, int MODE>
 void back_of(const BackArgs& a, const Shape& s, int blocks, size_t smem, cudaStream_t st) {
   const dim3 grid((unsigned)blocks), block((unsigned)(a.groups * s.warps * 32));
-  if (s.entries == 8) launch(norm_back_kernel<T, VEC, 8, 512>, grid, block, smem, st, a);
-  else if (s.warps <= 16) launch(norm_back_kernel<T, VEC, 16, 512>, grid, block, smem, st, a);
-  else launch(norm_back_kernel<T, VEC, 16, 1024>, grid, block, smem, st, a);
+  if (s.entries == 8) launch(norm_back_kernel<T, MODE, 8, 512>, grid, block, smem, st, a);
+  else if (s.warps <= 16) launch(norm_back_kernel<T, MODE, 16, 512>, grid, block, smem, st, a);
+  else launch(norm_back_kernel<T, MODE, 16, 1024>, grid, block, smem, st, a);
 }
 
 int back_groups(const Shape& s) { return s.warps == 1 ? 8 : 1; }
@@ -522,12 +657,14 @@ int back_blocks(int64_t rows, const Shape& s) {
 }
 
 template <class T>
-void dequant_of(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int depth, void* out, int64_t out_stride, bool vec,
-                cudaStream_t st) {
-  const int64_t blocks = cdiv(rows * cdiv(depth, 16), 256);
-  const dim3 grid((unsigned)(blocks < 148 * 32 ? blocks : 148 * 32));
-  if (vec) launch(dequant_kernel<T, true>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride);
-  else launch(dequant_kernel<T, false>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride);
+void dequant_of(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int depth, void* out, int64_t out_stride, cudaStream_t st) {
+  constexpr int N = Type<T>::N;
+  const bool even = aligned16(out) && (rows == 1 || (out_stride * (int64_t)sizeof(T)) % 16 == 0);
+  const int per = even ? (int)cdiv(depth, 16) : (int)cdiv(depth + N - 1, N);
+  const int64_t blocks = cdiv(rows * per, 256), most = 148 * (even ? 32 : 64);
+  const dim3 grid((unsigned)(blocks < most ? blocks : most));
+  if (even) launch(dequant_kernel<T>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride);
+  else launch(dequant_shifted_kernel<T>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride, per);
 }
 
 }  // namespace
@@ -551,9 +688,9 @@ int gsparse_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64_t de
   a.scale = scale;
   a.rows = rows;
   a.depth = (int)depth;
-  a.warps = shape_of(depth).warps;
-  const bool vec = even(x, row_stride, dtype) && depth % (16 / (int64_t)size_of(dtype)) == 0;
-  return rows_by_type<false>(dtype, a, vec, (cudaStream_t)stream);
+  Places p;
+  p.add(x, row_stride, dtype);
+  return rows_by_type<false>(dtype, a, p, (cudaStream_t)stream);
 }
 
 int gsparse_dequantize_rows(const int8_t* q, int64_t q_stride, const float* scale, int64_t rows, int64_t depth, void* out, int32_t dtype,
@@ -562,11 +699,10 @@ int gsparse_dequantize_rows(const int8_t* q, int64_t q_stride, const float* scal
   if (st != GSPARSE_OK || rows == 0) return st;
   if (!q || !scale || !aligned16(q) || q_stride % 16 || q_stride < depth || !at_multiple(scale, 4)) return GSPARSE_ERR_INVALID_ARG;
   if (!matrix(out, out_stride, dtype, rows, depth, true)) return GSPARSE_ERR_INVALID_ARG;
-  const bool vec = even(out, out_stride, dtype);
   cudaStream_t s = (cudaStream_t)stream;
-  if (dtype == GSPARSE_F32) dequant_of<float>(q, q_stride, scale, rows, (int)depth, out, out_stride, vec, s);
-  else if (dtype == GSPARSE_BF16) dequant_of<__nv_bfloat16>(q, q_stride, scale, rows, (int)depth, out, out_stride, vec, s);
-  else dequant_of<__half>(q, q_stride, scale, rows, (int)depth, out, out_stride, vec, s);
+  if (dtype == GSPARSE_F32) dequant_of<float>(q, q_stride, scale, rows, (int)depth, out, out_stride, s);
+  else if (dtype == GSPARSE_BF16) dequant_of<__nv_bfloat16>(q, q_stride, scale, rows, (int)depth, out, out_stride, s);
+  else dequant_of<__half>(q, q_stride, scale, rows, (int)depth, out, out_stride, s);
   return launch_status();
 }
 
@@ -603,12 +739,14 @@ int gsparse_rms_norm(const void* x, int64_t x_stride, const void* residual, int6
   a.q_stride = q_stride;
   a.depth = (int)depth;
   a.weight_dtype = weight_dtype;
-  a.warps = shape_of(depth).warps;
   a.eps = eps;
   a.inv_depth = 1.0 / (double)depth;
-  const bool vec = depth % (16 / (int64_t)size_of(dtype)) == 0 && aligned16(weight) && even(x, x_stride, dtype) &&
-                   even(residual, residual_stride, dtype) && even(h, h_stride, dtype) && even(y, y_stride, dtype);
-  return rows_by_type<true>(dtype, a, vec, (cudaStream_t)stream);
+  Places p;
+  p.add(x, x_stride, dtype);
+  p.add(residual, residual_stride, dtype);
+  p.add(h, h_stride, dtype);
+  p.add(y, y_stride, dtype);
+  return rows_by_type<true>(dtype, a, p, (cudaStream_t)stream);
 }
 
 size_t gsparse_rms_norm_backward_workspace_size(int64_t rows, int64_t depth) {
@@ -663,10 +801,10 @@ int gsparse_rms_norm_backward(const void* h, int64_t h_stride, const void* weigh
   const bool vec = depth % (16 / (int64_t)size_of(dtype)) == 0 && aligned16(weight) && even(h, h_stride, dtype) &&
                    even(dy, dy_stride, dtype) && even(dh, dh_stride, dtype) && even(dx, dx_stride, dtype);
   const size_t smem = shape.warps == 1 ? (size_t)a.groups * (size_t)depth * sizeof(float) : 0;   // at most 16 KB
-  if (dtype == GSPARSE_F32) vec ? back_of<float, true>(a, shape, blocks, smem, s) : back_of<float, false>(a, shape, blocks, smem, s);
+  if (dtype == GSPARSE_F32) vec ? back_of<float, kVectors>(a, shape, blocks, smem, s) : back_of<float, kEntries>(a, shape, blocks, smem, s);
   else if (dtype == GSPARSE_BF16)
-    vec ? back_of<__nv_bfloat16, true>(a, shape, blocks, smem, s) : back_of<__nv_bfloat16, false>(a, shape, blocks, smem, s);
-  else vec ? back_of<__half, true>(a, shape, blocks, smem, s) : back_of<__half, false>(a, shape, blocks, smem, s);
+    vec ? back_of<__nv_bfloat16, kVectors>(a, shape, blocks, smem, s) : back_of<__nv_bfloat16, kEntries>(a, shape, blocks, smem, s);
+  else vec ? back_of<__half, kVectors>(a, shape, blocks, smem, s) : back_of<__half, kEntries>(a, shape, blocks, smem, s);
   if (dweight) launch(norm_join_kernel, dim3((unsigned)cdiv(depth, 32)), dim3(1024), 0, s, (const float*)partial, blocks, (int)depth, dweight);
   return launch_status();
 }

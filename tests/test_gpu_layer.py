@@ -208,6 +208,33 @@ def test_norm_sizes(dtype, rows, depth):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,depth", [(9, 1), (9, 3), (17, 9), (11, 249), (9, 250), (10, 257), (9, 505), (9, 506), (9, 513), (17, 1023), (9, 3086),
+                                        (9, 8191), (9, 8186), (9, 16377), (9, 16378), (9, 16383)])
+def test_norm_rows_between_boundaries(dtype, rows, depth):
+    """Contiguous rows of an odd length: every place between two 16-byte boundaries, in all of x, residual, h and y."""
+    x, res = dev(normal(120, rows, depth, scale=2.0), TYPES[dtype]), dev(normal(121, rows, depth, scale=2.0), TYPES[dtype])
+    w = dev(1 + 0.1 * normal(122, depth))
+    a = check_norm(x, w, dtype, res)
+    apart, _ = laid(f64(x), TYPES[dtype], stride=depth + 11, first=3)        # the same entry by entry
+    b = gs.rms_norm(apart, w, res, want_y=True, want_q=True, want_rstd=True)
+    assert torch.equal(a.h, b.h) and torch.equal(a.q.q, b.q.q) and torch.equal(a.q.scale, b.q.scale)
+    q, buf = laid(np.full((rows, depth), 55), torch.int8, stride=-(-depth // 16) * 16 + 16, fill=55)
+    h, hbuf = laid(np.zeros((rows, depth)), TYPES[dtype], stride=depth, first=16)
+    gs.rms_norm(x, w, res, h=h, q=gs.QuantRows(q, torch.empty(rows, device="cuda")))
+    assert torch.equal(q, a.q.q) and torch.equal(h, a.h)
+    untouched(q, buf, 55)
+    untouched(h, hbuf, float("nan"))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,depth", [(9, 1), (9, 7), (9, 8), (17, 15), (9, 249), (9, 257), (9, 511), (9, 5459), (9, 32761), (9, 32762), (9, 32767)])
+def test_quantize_rows_between_boundaries(dtype, rows, depth):
+    for stride, first in ((depth, 0), (depth, 3), (depth + 2, 5)):
+        x, _ = laid(normal(123, rows, depth), TYPES[dtype], stride, first)
+        check_quantize(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("weight_dtype", TYPES)
 @pytest.mark.parametrize("depth", [24, 1001, 2048])
 def test_norm_weight_types(dtype, weight_dtype, depth):
