@@ -266,13 +266,24 @@ __device__ void box_to_rows(const char* box, int lane, T* out, int64_t stride, i
   constexpr int N = 4 / (int)sizeof(T);
   const int n = (int)min((int64_t)32, rows - row);
   const int64_t mine = col + lane * N;
-  for (int r = 0; r < n; ++r) {
-    const uint32_t raw = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-    const T* e = reinterpret_cast<const T*>(&raw);
-    T* to = out + (row + r) * stride + mine;
+  const int have = (int)max((int64_t)0, min((int64_t)N, cols - mine));
+  T* to = out + row * stride + mine;
+  const char* from = box + (lane & 3) * 4;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (mine + i < cols) to[i] = e[i];
+  for (int r0 = 0; r0 < 32; r0 += 8) {             // eight rows under way at a time
+    uint32_t raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(from + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const T* e = reinterpret_cast<const T*>(&raw[i]);
+      if (r0 + i < n) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (k < have) to[k] = e[k];
+      }
+      to += stride;
+    }
   }
 }
 
@@ -720,6 +731,184 @@ __global__ void __launch_bounds__(128) copies_kernel(const int8_t* x, int64_t x_
     *reinterpret_cast<uint4*>(to + at) = at + 16 <= depth ? __ldg(reinterpret_cast<const uint4*>(row + at)) : last_bytes(row, at, depth);
 }
 
+// ---- gradients of few tokens ------------------------------------------------------------------------------------
+
+struct FewGradArgs {
+  const void* dout;
+  const int8_t* q;                         // w for the input's gradient, x for the weights'
+  const float* scale;
+  float* part;                             // fp32[splits][tokens][depth]
+  void* out;
+  int64_t dout_stride, q_stride, out_stride, channels, rows;   // rows: channels of a split
+  int tokens, depth, splits;
+};
+
+template <class T> __device__ __forceinline__ float as_float(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (__is_same(T, __nv_bfloat16)) return __bfloat162float(v);
+  else return __half2float(v);
+}
+
+template <class T> __device__ __forceinline__ void put_as(T* p, float v) {
+  if constexpr (sizeof(T) == 4) *p = v;
+  else if constexpr (__is_same(T, __nv_bfloat16)) *p = __float2bfloat16_rn(v);
+  else *p = __float2half_rn(v);
+}
+
+// dx of up to TOKENS tokens: a thread holds 8 columns of the weights, a warp 256, a block's eight warps share a split's channels; the
+// weights pass once, as they are, a step ahead, and the gradients' few entries times their scales come by way of shared memory.
+constexpr int kFewChannels = 32;           // of a step of a block
+constexpr int kFewColumns = 256;
+constexpr int64_t kFewBlocks = 2, kFewWeightBlocks = 12;   // of an SM
+
+template <class T, int TOKENS>
+__global__ void __launch_bounds__(256) few_input_kernel(const __grid_constant__ FewGradArgs a) {
+  pdl_begin();
+  constexpr int STEPS = kFewChannels / 8, MINE = (kFewChannels * TOKENS + 255) / 256;
+  __shared__ float g[2][kFewChannels][TOKENS];
+  __shared__ float joined[8][kFewColumns];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * kFewColumns + lane * 8;
+  const int64_t first = blockIdx.y * a.rows, last = min(first + a.rows, a.channels);
+  float sum[TOKENS][8];
+#pragma unroll
+  for (int t = 0; t < TOKENS; ++t)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[t][k] = 0.0f;
+  uint2 w[STEPS];
+  float mine[MINE];
+  auto ahead = [&](int64_t n0) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int64_t n = n0 + i * 8 + warp;
+      w[i] = make_uint2(0, 0);
+      if (n >= last || col >= a.depth) continue;
+      const int8_t* p = a.q + n * a.q_stride;
+      if (col + 8 <= a.depth) {
+        w[i] = __ldg(reinterpret_cast<const uint2*>(p + col));
+      } else {
+        const uint4 v = last_bytes(p, col, a.depth);
+        w[i] = make_uint2(v.x, v.y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int at = threadIdx.x + i * 256, t = at / kFewChannels;
+      const int64_t n = n0 + at % kFewChannels;
+      mine[i] = t < a.tokens && n < last ? as_float<T>(static_cast<const T*>(a.dout)[t * a.dout_stride + n]) * __ldg(a.scale + n) : 0.0f;
+    }
+  };
+  ahead(first);
+  int buf = 0;
+  for (int64_t n0 = first; n0 < last; n0 += kFewChannels, buf ^= 1) {
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int at = threadIdx.x + i * 256;
+      if (at < kFewChannels * TOKENS) g[buf][at % kFewChannels][at / kFewChannels] = mine[i];
+    }
+    uint2 now[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) now[i] = w[i];
+    __syncthreads();                               // (the other half is free: all have left it before they came here)
+    if (n0 + kFewChannels < last) ahead(n0 + kFewChannels);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = (float)(int8_t)(now[i].x >> (8 * k));
+        v[k + 4] = (float)(int8_t)(now[i].y >> (8 * k));
+      }
+#pragma unroll
+      for (int t = 0; t < TOKENS; ++t) {
+        const float f = g[buf][i * 8 + warp][t];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[t][k] = __fmaf_rn(f, v[k], sum[t][k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TOKENS; ++t) {
+    if (t >= a.tokens) break;
+    __syncthreads();
+    *reinterpret_cast<float4*>(&joined[warp][lane * 8]) = make_float4(sum[t][0], sum[t][1], sum[t][2], sum[t][3]);
+    *reinterpret_cast<float4*>(&joined[warp][lane * 8 + 4]) = make_float4(sum[t][4], sum[t][5], sum[t][6], sum[t][7]);
+    __syncthreads();
+    const int c = blockIdx.x * kFewColumns + threadIdx.x;
+    if (c >= a.depth) continue;
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += joined[k][threadIdx.x];
+    a.part[((int64_t)blockIdx.y * a.tokens + t) * a.depth + c] = s;
+  }
+}
+
+// The splits' sums in their order; a warp takes 32 entries of dx, eight warps the splits.
+template <class T>
+__global__ void __launch_bounds__(256) few_join_kernel(const __grid_constant__ FewGradArgs a) {
+  pdl_begin();
+  __shared__ float joined[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t all = (int64_t)a.tokens * a.depth, at = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (at < all) {
+#pragma unroll 8
+    for (int k = warp; k < a.splits; k += 8) s += __ldg(a.part + k * all + at);
+  }
+  joined[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || at >= all) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) s += joined[k][lane];
+  const int t = (int)(at / a.depth);
+  put_as(static_cast<T*>(a.out) + t * a.out_stride + (at - (int64_t)t * a.depth), s);
+}
+
+// dweight of up to TOKENS tokens: the call is the weights' way to memory. A thread holds 4 columns of the activations' values and goes
+// down its block's channels, whose gradients lie in shared memory; a warp writes 128 entries of a row at a time.
+constexpr int kFewRowsAtOnce = 128;
+
+template <class T, int TOKENS, bool VEC>
+__global__ void __launch_bounds__(256) few_weight_kernel(const __grid_constant__ FewGradArgs a) {
+  pdl_begin();
+  __shared__ __align__(16) float g[kFewRowsAtOnce][TOKENS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 128 + (VEC ? lane * 4 : lane), apart = VEC ? 1 : 32;
+  float x[TOKENS][4];
+#pragma unroll
+  for (int t = 0; t < TOKENS; ++t) {
+    const float s = t < a.tokens ? __ldg(a.scale + t) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[t][k] = t < a.tokens && col + k * apart < a.depth ? (float)a.q[t * a.q_stride + col + k * apart] * s : 0.0f;
+  }
+  const int64_t first = blockIdx.y * a.rows, last = min(first + a.rows, a.channels);
+  for (int64_t n0 = first; n0 < last; n0 += kFewRowsAtOnce) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFewRowsAtOnce * TOKENS; i += 256) {
+      const int t = i / kFewRowsAtOnce, r = i % kFewRowsAtOnce;
+      g[r][t] = t < a.tokens && n0 + r < last ? as_float<T>(static_cast<const T*>(a.dout)[t * a.dout_stride + n0 + r]) : 0.0f;
+    }
+    __syncthreads();
+    const int rows = (int)min((int64_t)kFewRowsAtOnce, last - n0);
+#pragma unroll 4
+    for (int r = warp; r < rows; r += 8) {
+      float v[4];
+#pragma unroll
+      for (int t = 0; t < TOKENS; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = t == 0 ? g[r][0] * x[0][k] : __fmaf_rn(g[r][t], x[t][k], v[k]);
+      float* to = static_cast<float*>(a.out) + (n0 + r) * a.out_stride + col;
+      if (VEC && col + 4 <= a.depth) {
+        *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (col + k * apart < a.depth) to[k * apart] = v[k];
+      }
+    }
+  }
+}
+
 // ---- gradients in parts of bf16 -------------------------------------------------------------------------------
 
 struct OperandArgs {
@@ -731,12 +920,6 @@ struct OperandArgs {
   int64_t dout_stride, a_stride, tokens, channels, q_stride, b_stride, along;
   int depth, a_blocks;                     // blocks of the grid that make the planes
 };
-
-template <class T> __device__ __forceinline__ float as_float(T v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else if constexpr (__is_same(T, __nv_bfloat16)) return __bfloat162float(v);
-  else return __half2float(v);
-}
 
 // 8 entries of x as a sum of PLANES bf16 numbers each, exact (8 bits of the significand in each): the first holds what is no number.
 template <class T, int PLANES>
@@ -969,6 +1152,57 @@ Product product_of(void* workspace, int64_t tokens, int64_t channels, int64_t de
   return p;
 }
 
+// Gradients of few tokens: a block takes some columns and a split of the channels.
+FewGradArgs few_grad(const void* dout, int64_t dout_stride, const int8_t* q, int64_t q_stride, const float* scale, int64_t tokens, int64_t channels,
+                     int64_t depth, bool weight) {
+  FewGradArgs a{dout, q, scale, nullptr, nullptr, dout_stride, q_stride, 0, channels, 0, (int)tokens, (int)depth, 0};
+  const int64_t across = cdiv(depth, weight ? 128 : kFewColumns), want = cdiv((weight ? kFewWeightBlocks : kFewBlocks) * sm_count(), across);
+  a.rows = round_up(cdiv(channels, want), kFewChannels);
+  a.splits = (int)cdiv(channels, a.rows);
+  return a;
+}
+
+template <class T>
+void few_input_of(const FewGradArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.depth, kFewColumns), (unsigned)a.splits);
+  if (a.tokens <= 1) launch(few_input_kernel<T, 1>, grid, dim3(256), 0, st, a);
+  else if (a.tokens <= 2) launch(few_input_kernel<T, 2>, grid, dim3(256), 0, st, a);
+  else if (a.tokens <= 4) launch(few_input_kernel<T, 4>, grid, dim3(256), 0, st, a);
+  else launch(few_input_kernel<T, 8>, grid, dim3(256), 0, st, a);
+}
+
+template <class T, bool VEC>
+void few_weight_of(const FewGradArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.depth, 128), (unsigned)a.splits);
+  if (a.tokens <= 1) launch(few_weight_kernel<T, 1, VEC>, grid, dim3(256), 0, st, a);
+  else if (a.tokens <= 2) launch(few_weight_kernel<T, 2, VEC>, grid, dim3(256), 0, st, a);
+  else if (a.tokens <= 4) launch(few_weight_kernel<T, 4, VEC>, grid, dim3(256), 0, st, a);
+  else launch(few_weight_kernel<T, 8, VEC>, grid, dim3(256), 0, st, a);
+}
+
+constexpr int64_t kFewGradTokens = 8;
+
+int few_gradient(bool weight, FewGradArgs a, int32_t dtype, void* out, int32_t out_dtype, int64_t out_stride, float* part, cudaStream_t st) {
+  a.out = out;
+  a.out_stride = out_stride;
+  a.part = part;
+  if (weight) {
+    const bool vec = aligned16(out) && (a.channels == 1 || out_stride % 4 == 0);
+    if (dtype == GSPARSE_F32) vec ? few_weight_of<float, true>(a, st) : few_weight_of<float, false>(a, st);
+    else if (dtype == GSPARSE_BF16) vec ? few_weight_of<__nv_bfloat16, true>(a, st) : few_weight_of<__nv_bfloat16, false>(a, st);
+    else vec ? few_weight_of<__half, true>(a, st) : few_weight_of<__half, false>(a, st);
+    return launch_status();
+  }
+  if (dtype == GSPARSE_F32) few_input_of<float>(a, st);
+  else if (dtype == GSPARSE_BF16) few_input_of<__nv_bfloat16>(a, st);
+  else few_input_of<__half>(a, st);
+  const dim3 grid((unsigned)cdiv((int64_t)a.tokens * a.depth, 32));
+  if (out_dtype == GSPARSE_F32) launch(few_join_kernel<float>, grid, dim3(256), 0, st, (const FewGradArgs&)a);
+  else if (out_dtype == GSPARSE_BF16) launch(few_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, (const FewGradArgs&)a);
+  else launch(few_join_kernel<__half>, grid, dim3(256), 0, st, (const FewGradArgs&)a);
+  return launch_status();
+}
+
 // A gradient's operands in the workspace: dout in planes of bf16 where it is not bf16 rows at 16-byte boundaries already, and the
 // values of the rows in 8 bits.
 struct Grad {
@@ -982,12 +1216,17 @@ struct Grad {
 };
 
 Grad grad_of(void* workspace, const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens, int64_t channels, int64_t depth, bool weight) {
-  Grad g;
+  Grad g{};
   g.planes = dtype == GSPARSE_F32 ? 3 : dtype == GSPARSE_F16 ? 2 : 1;
   g.copied = dtype != GSPARSE_BF16 || !aligned16(dout) || (tokens > 1 && (dout_stride % 8 || dout_stride < channels));
   g.stride_a = round_up(channels, 8);
   g.stride_b = round_up(depth, 8);
   Carver c(workspace);
+  if (tokens <= kFewGradTokens) {
+    if (!weight) g.part = c.take<float>(few_grad(dout, 0, nullptr, 0, nullptr, tokens, channels, depth, false).splits * tokens * depth);
+    g.bytes = c.off;
+    return g;
+  }
   g.a = c.take<__nv_bfloat16>(g.copied ? g.planes * tokens * g.stride_a : 0);
   const int64_t along = weight ? tokens : channels;
   g.b = c.take<__nv_bfloat16>(along * g.stride_b);
@@ -1002,12 +1241,21 @@ size_t grad_bytes(const void* dout, int32_t dtype, int64_t dout_stride, int64_t 
   return grad_of(nullptr, dout, dtype, dout_stride, tokens, channels, depth, weight).bytes;
 }
 
+bool grad_space(const void* workspace, size_t have, const void* dout, int32_t dtype, int64_t dout_stride, int64_t tokens, int64_t channels,
+                int64_t depth, bool weight) {
+  const size_t need = grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, weight);
+  return !need || space(workspace, have, need);
+}
+
 template <bool WEIGHT>
 int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* q, int64_t q_stride, const float* scale, int64_t tokens,
              int64_t channels, int64_t depth, void* out, int32_t out_dtype, int64_t out_stride, void* workspace, int32_t* d_status,
              cudaStream_t st) {
   const Grad g = grad_of(workspace, dout, dtype, dout_stride, tokens, channels, depth, WEIGHT);
   const int64_t along = WEIGHT ? tokens : channels;
+  if (tokens <= kFewGradTokens)
+    return few_gradient(WEIGHT, few_grad(dout, dout_stride, q, q_stride, scale, tokens, channels, depth, WEIGHT), dtype, out, out_dtype, out_stride, g.part,
+                        st);
   OperandArgs o{dout, g.a, q, scale, g.b, dout_stride, g.stride_a, tokens, channels, q_stride, g.stride_b, along, (int)depth, 0};
   auto blocks_of = [](int64_t vectors) { return (int)(vectors < 256ll * 148 * 16 ? cdiv(vectors, 256) : 148 * 16); };
   if (g.copied) o.a_blocks = blocks_of(tokens * cdiv(channels, 8));
@@ -1094,7 +1342,7 @@ int gsparse_linear_q8_grad_input(const void* dout, int32_t dtype, int64_t dout_s
   if (!matrix(dout, dout_stride, dtype, tokens, channels, false) || !rows8(w, w_stride, w_scale, depth) ||
       !matrix(dx, dx_stride, dx_dtype, tokens, depth, true))
     return GSPARSE_ERR_INVALID_ARG;
-  if (!space(workspace, workspace_bytes, grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, false))) return GSPARSE_ERR_WORKSPACE;
+  if (!grad_space(workspace, workspace_bytes, dout, dtype, dout_stride, tokens, channels, depth, false)) return GSPARSE_ERR_WORKSPACE;
   return gradient<false>(dout, dtype, dout_stride, w, w_stride, w_scale, tokens, channels, depth, dx, dx_dtype, dx_stride, workspace, d_status,
                          (cudaStream_t)stream);
 }
@@ -1120,7 +1368,7 @@ int gsparse_linear_q8_grad_weight(const void* dout, int32_t dtype, int64_t dout_
     return GSPARSE_OK;
   }
   if (!matrix(dout, dout_stride, dtype, tokens, channels, false) || !rows8(x, x_stride, x_scale, depth)) return GSPARSE_ERR_INVALID_ARG;
-  if (!space(workspace, workspace_bytes, grad_bytes(dout, dtype, dout_stride, tokens, channels, depth, true))) return GSPARSE_ERR_WORKSPACE;
+  if (!grad_space(workspace, workspace_bytes, dout, dtype, dout_stride, tokens, channels, depth, true)) return GSPARSE_ERR_WORKSPACE;
   return gradient<true>(dout, dtype, dout_stride, x, x_stride, x_scale, tokens, channels, depth, dweight, GSPARSE_F32, dweight_stride, workspace,
                         d_status, s);
 }

@@ -760,7 +760,7 @@ def test_arguments_of_the_binding():
         lambda: gs.rms_norm(torch.empty((4, 32), device="cuda"), torch.empty(32, device="cuda"), eps=0.0),
         lambda: gs.rms_norm_backward(torch.empty((4, 32), device="cuda"), torch.empty(32, device="cuda"), torch.empty(5, device="cuda"),
                                      torch.empty((4, 32), device="cuda")),
-        lambda: gs.linear_q8_grad_weight(torch.empty((4, 6), device="cuda"), x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+        lambda: gs.linear_q8_grad_input(torch.empty((4, 6), device="cuda"), w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
     ]
     for call in bad:
         with pytest.raises(gs.GsparseError):
