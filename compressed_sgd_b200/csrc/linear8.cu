@@ -21,13 +21,13 @@ constexpr int kBox = 32 * 128;             // a warp's part of the result on its
 
 constexpr int kSide = 128;                 // columns of a warp that takes results out: eight of them take a CTA's part of a tile
 
-// Integers leave the tensor memory once a tile, but soon (a depth of 512 takes a pair a microsecond): two groups of eight warps. Sums
-// in bf16 stay in registers over a tile: one group, with the registers that the other warps give up.
 // Few rows that every pair reads at about the same time are slow to come by (16 tokens against 32000 x 4096 weights: 100 us, 64
 // tokens: 31): they are copied, and the pairs read different copies.
 // The copies take about half a megabyte (8 tokens of 512 in 16 copies, 64 KB: 40 us; in 74: 17).
 constexpr int64_t kCopyBytes = 96 << 10, kCopiesBytes = 512 << 10;
 
+// Integers leave the tensor memory once a tile, but soon (a depth of 512 takes a pair a microsecond): two groups of eight warps, which
+// take the tiles in turn. Sums in bf16 stay in registers over a tile: one group, with the registers that the other warps give up.
 template <bool INT> struct Layout {
   static constexpr int warps = INT ? 16 : 8;                   // that take results out
   static constexpr int threads = (warps + (INT ? 2 : 4)) * 32; // setmaxnreg goes by groups of four warps
@@ -396,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
     if (warp == L::warps && lane == 0) {
       uint32_t n = 0, s = 0, turn = 0;                         // stages filled so far; the next, and its turn
       const uint64_t keep_a = policy(a.keep_a), keep_b = policy(a.keep_b);
-      const int copy = pair % a.copies;
+      const int copy = INT ? pair % a.copies : 0;
       for (int i = 0; ok && part_of(a, pair, i, p); ++i) {
         const int m = p.m * kTile + (int)rank * 128, c = p.n * kTile + (int)rank * 128;
         int plane = p.from / a.plane_blocks, k = p.from - plane * a.plane_blocks;

@@ -509,6 +509,31 @@ def test_gradient_sizes(dtype, tokens, channels, depth):
         check_gradients(dout, x, w, dtype)
 
 
+@pytest.mark.parametrize("tokens,channels,depth", [(2500, 2700, 96), (2300, 2900, 8192), (5000, 700, 300), (700, 5000, 520)])
+def test_product_of_many_tiles(tokens, channels, depth):
+    """More tiles than pairs of SMs, in several bands either way, the last ones split or not: against 64 bits on the GPU."""
+    x, w = quants(63, tokens, depth, spread=2), quants(64, channels, depth, spread=2)
+    st = gs.status_tensor()
+    out = gs.linear_q8(x, w, torch.float32, d_status=st)
+    status_ok(st)
+    want = (x.q.double() * x.scale.double()[:, None]) @ (w.q.double() * w.scale.double()[:, None]).t()
+    assert bool(((out.double() - want).abs() <= 1.01 * U * want.abs()).all())      # powers of two: one rounding
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,channels,depth", [(2500, 2700, 2816), (1500, 5000, 700), (5000, 1500, 264)])
+def test_gradients_of_many_tiles(dtype, tokens, channels, depth):
+    x, w = quants(65, tokens, depth, spread=2), quants(66, channels, depth, spread=2)
+    dout = dev(gradient(67, tokens, channels) / 64, TYPES[dtype])
+    st = gs.status_tensor()
+    dx, dw = gs.linear_q8_grad_input(dout, w, dtype=torch.float32, d_status=st), gs.linear_q8_grad_weight(dout, x, d_status=st)
+    status_ok(st)
+    g, xv, wv = dout.double(), x.q.double() * x.scale.double()[:, None], w.q.double() * w.scale.double()[:, None]
+    planes = {"bf16": 1, "fp16": 2, "fp32": 3}[dtype]
+    for got, want, size, terms in ((dx, g @ wv, g.abs() @ wv.abs(), channels), (dw, g.t() @ xv, g.t().abs() @ xv.abs(), tokens)):
+        close(got, f64(want), sums_tolerance(f64(size), planes * terms, "fp32", f64(want), dtype), "gradient")
+
+
 @pytest.mark.parametrize("dtype,dx_dtype", [("bf16", "fp32"), ("fp32", "bf16"), ("fp16", "fp32")])
 def test_gradient_input_types(dtype, dx_dtype):
     x, w = quants(44, 140, 300), quants(45, 90, 300)
