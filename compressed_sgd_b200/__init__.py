@@ -556,7 +556,7 @@ def _on_device(device, name, *args):
     """Calls the entry point with the tensors' device current, on that device's current stream."""
     fn = getattr(_lib or lib(), name)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
@@ -565,6 +565,8 @@ def _on_device(device, name, *args):
         _check(st, name)
 
 
+# the current device without the check that CUDA is there (a tensor of it is at hand)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # the current stream's handle without the Stream object around it (2 us less per call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -708,9 +710,10 @@ class RmsNormGrad(NamedTuple):
 
 def _matrix(t: torch.Tensor, name, like: Optional[torch.Tensor] = None):
     """(pointer, row stride) of a matrix with contiguous rows, of the type, shape and device of `like`."""
-    if t.dim() != 2 or not t.is_cuda or t.dtype not in _DTYPES or (t.stride(1) != 1 and t.shape[1] > 1):
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda or t.dtype not in _DTYPES or (t.stride(1) != 1 and shape[1] > 1):
         raise GsparseError(f"{name} must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
-    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.device != like.device):
+    if like is not None and (t.dtype is not like.dtype or shape != like.shape or t.device != like.device):
         raise GsparseError(f"{name} must be of type {like.dtype} and shape {tuple(like.shape)} on {like.device}")
     return t.data_ptr(), t.stride(0)
 
@@ -718,17 +721,17 @@ def _matrix(t: torch.Tensor, name, like: Optional[torch.Tensor] = None):
 def _quant(rows: QuantRows, name, device=None, depth=None):
     """(q's pointer, q's row stride, scale's pointer, rows, depth)."""
     q, scale = rows
-    if q.dim() != 2 or not q.is_cuda or q.dtype is not torch.int8 or (q.stride(1) != 1 and q.shape[1] > 1):
+    shape = q.shape
+    if len(shape) != 2 or not q.is_cuda or q.dtype is not torch.int8 or (q.stride(1) != 1 and shape[1] > 1):
         raise GsparseError(f"{name}.q must be a CUDA matrix of int8 with contiguous rows")
-    n, k = q.shape
-    if (device is not None and q.device != device) or (depth is not None and k != depth):
+    n, k = shape
+    on = q.device
+    if (device is not None and on != device) or (depth is not None and k != depth):
         raise GsparseError(f"{name} must be rows of {depth} entries on {device}")
-    return q.data_ptr(), _row_step(q, 16), _like(scale, torch.float32, (n,), q.device, f"{name}.scale"), n, k
-
-
-def _row_step(t: torch.Tensor, unit: int) -> int:
-    """The row stride; of a single row, whose stride says nothing, the next multiple of `unit`."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
+    if scale.dtype is not torch.float32 or scale.device != on or scale.shape != (n,) or not scale.is_contiguous():
+        raise GsparseError(f"{name}.scale must be a contiguous {torch.float32} tensor of the shape {(n,)} on {on}")
+    # of a single row, whose stride says nothing, the next multiple of 16
+    return q.data_ptr(), q.stride(0) if n > 1 else k + 15 & ~15, scale.data_ptr(), n, k
 
 
 def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype, unit: int) -> torch.Tensor:
@@ -738,9 +741,12 @@ def _aligned_rows(like: torch.Tensor, rows: int, cols: int, dtype, unit: int) ->
     return t if stride == cols else t.as_strided((rows, cols), (stride, 1))
 
 
-def _new_quant(like: torch.Tensor) -> QuantRows:
+def _new_quant(like: torch.Tensor):
+    """New rows in 8 bits for those of `like`, and what _quant says of them."""
     rows, depth = like.shape
-    return QuantRows(_aligned_rows(like, rows, depth, torch.int8, 16), like.new_empty(rows, dtype=torch.float32))
+    q = _aligned_rows(like, rows, depth, torch.int8, 16)
+    scale = like.new_empty(rows, dtype=torch.float32)
+    return QuantRows(q, scale), (q.data_ptr(), depth + 15 & ~15, scale.data_ptr(), rows, depth)
 
 
 # sizes depend on the shapes alone (and on whether dout's rows can be read as they are)
@@ -768,12 +774,15 @@ def _dtype_code(dtype) -> int:
 def quantize_rows(x: torch.Tensor, out: Optional[QuantRows] = None) -> QuantRows:
     """The rows of x in 8 bits, each with a power of two as its scale: an activation checkpoint, or weights by channel."""
     p, stride = _matrix(x, "x")
+    dev = x.device
     if out is None:
-        out = _new_quant(x)
-    q, qs, scale, rows, depth = _quant(out, "out", x.device, x.shape[1])
+        out, held = _new_quant(x)
+    else:
+        held = _quant(out, "out", dev, x.shape[1])
+    q, qs, scale, rows, depth = held
     if rows != x.shape[0]:
         raise GsparseError(f"out must hold {x.shape[0]} rows")
-    _on_device(x.device, "gsparse_quantize_rows", p, _DTYPES[x.dtype], rows, depth, stride, q, qs, scale)
+    _on_device(dev, "gsparse_quantize_rows", p, _DTYPES[x.dtype], rows, depth, stride, q, qs, scale)
     return out
 
 
@@ -781,12 +790,15 @@ def dequantize_rows(rows: QuantRows, dtype=torch.bfloat16, out: Optional[torch.T
     """The values that rows in 8 bits stand for; bf16 holds those of quantize_rows and rms_norm exactly."""
     q, qs, scale, n, depth = _quant(rows, "rows")
     if out is None:
-        _dtype_code(dtype)
+        code = _dtype_code(dtype)
         out = rows.q.new_empty((n, depth), dtype=dtype)
-    elif out.shape != rows.q.shape or out.device != rows.q.device:
-        raise GsparseError(f"out must be of shape {tuple(rows.q.shape)} on {rows.q.device}")
-    p, stride = _matrix(out, "out")
-    _on_device(out.device, "gsparse_dequantize_rows", q, qs, scale, n, depth, p, _DTYPES[out.dtype], stride)
+        p, stride = out.data_ptr(), depth
+    else:
+        if out.shape != rows.q.shape or out.device != rows.q.device:
+            raise GsparseError(f"out must be of shape {tuple(rows.q.shape)} on {rows.q.device}")
+        p, stride = _matrix(out, "out")
+        code = _DTYPES[out.dtype]
+    _on_device(out.device, "gsparse_dequantize_rows", q, qs, scale, n, depth, p, code, stride)
     return out
 
 
@@ -806,17 +818,21 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     dev = x.device
     p_r, s_r = (None, 0) if residual is None else _matrix(residual, "residual", x)
     p_w, wt = _norm_weight(weight, depth, dev)
-    if h is None and residual is not None:
+    if h is not None:
+        p_h, s_h = _matrix(h, "h", x)
+    elif residual is not None:
         h = x.new_empty((rows, depth))
-    p_h, s_h = (None, 0) if h is None else _matrix(h, "h", x)
+        p_h, s_h = h.data_ptr(), depth
+    else:
+        p_h, s_h = None, 0
     y = x.new_empty((rows, depth)) if want_y else None
-    if q is None and want_q:
-        q = _new_quant(x)
     p_q, s_q, p_s = None, 0, None
     if q is not None:
         p_q, s_q, p_s, n, _ = _quant(q, "q", dev, depth)
         if n != rows:
             raise GsparseError(f"q must hold {rows} rows")
+    elif want_q:
+        q, (p_q, s_q, p_s, _, _) = _new_quant(x)
     rstd = x.new_empty(rows, dtype=torch.float32) if want_rstd else None
     _on_device(dev, "gsparse_rms_norm", p_x, s_x, p_r, s_r, p_w, wt, _DTYPES[x.dtype], rows, depth, eps, p_h, s_h, _ptr(y), depth,
                p_q, s_q, p_s, _ptr(rstd))
@@ -837,7 +853,9 @@ def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
     p_d, s_d = (None, 0) if dh is None else _matrix(dh, "dh", h)
     if dx is None:
         dx = h.new_empty((rows, depth))
-    p_x, s_x = _matrix(dx, "dx", h)
+        p_x, s_x = dx.data_ptr(), depth
+    else:
+        p_x, s_x = _matrix(dx, "dx", h)
     dweight, p_ws, n_ws = None, None, 0
     if want_dweight:
         dweight = h.new_empty(depth, dtype=torch.float32)
@@ -857,15 +875,19 @@ def linear_q8(x: QuantRows, w: QuantRows, dtype=torch.bfloat16, out: Optional[to
     dev = x.q.device
     p_w, s_w, c_w, channels, _ = _quant(w, "w", dev, depth)
     if out is None:
-        _dtype_code(dtype)
-        out = _aligned_rows(x.q, tokens, channels, dtype, 8 if dtype is torch.float32 else 16)
-    p_o, s_o = _matrix(out, "out")
-    if out.shape != (tokens, channels) or out.device != dev:
-        raise GsparseError(f"out must be of shape {(tokens, channels)} on {dev}")
+        code = _dtype_code(dtype)
+        unit = 7 if code == 0 else 15
+        out = _aligned_rows(x.q, tokens, channels, dtype, unit + 1)
+        p_o, s_o = out.data_ptr(), channels + unit & ~unit
+    else:
+        p_o, s_o = _matrix(out, "out")
+        if out.shape != (tokens, channels) or out.device != dev:
+            raise GsparseError(f"out must be of shape {(tokens, channels)} on {dev}")
+        code = _DTYPES[out.dtype]
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
     workspace, p_ws, n_ws = _scratch(workspace, x.q, "gsparse_linear_q8_workspace_size", tokens, channels, depth)
-    _on_device(dev, "gsparse_linear_q8", p_x, s_x, c_x, p_w, s_w, c_w, tokens, channels, depth, p_o, _DTYPES[out.dtype], s_o,
-               p_ws, n_ws, p_s)
+    _on_device(dev, "gsparse_linear_q8", p_x, s_x, c_x, p_w, s_w, c_w, tokens, channels, depth, p_o, code, s_o, p_ws, n_ws,
+               p_s)
     return out
 
 
@@ -882,9 +904,11 @@ def linear_q8_grad_input(dout: torch.Tensor, w: QuantRows, dtype=None, out: Opti
         dtype = dout.dtype if dtype is None else dtype
         _dtype_code(dtype)
         out = dout.new_empty((tokens, depth), dtype=dtype)
-    p_o, s_o = _matrix(out, "out")
-    if out.shape != (tokens, depth) or out.device != dev:
-        raise GsparseError(f"out must be of shape {(tokens, depth)} on {dev}")
+        p_o, s_o = out.data_ptr(), depth
+    else:
+        p_o, s_o = _matrix(out, "out")
+        if out.shape != (tokens, depth) or out.device != dev:
+            raise GsparseError(f"out must be of shape {(tokens, depth)} on {dev}")
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
     dt = _DTYPES[dout.dtype]
     workspace, p_ws, n_ws = _scratch(workspace, dout, "gsparse_linear_q8_grad_input_workspace_size", p_g % 16, dt, s_g, tokens,
@@ -906,9 +930,11 @@ def linear_q8_grad_weight(dout: torch.Tensor, x: QuantRows, out: Optional[torch.
         raise GsparseError(f"x must hold {tokens} rows")
     if out is None:
         out = dout.new_empty((channels, depth), dtype=torch.float32)
-    p_o, s_o = _matrix(out, "out")
-    if out.shape != (channels, depth) or out.device != dev or out.dtype is not torch.float32:
-        raise GsparseError(f"out must be fp32 of shape {(channels, depth)} on {dev}")
+        p_o, s_o = out.data_ptr(), depth
+    else:
+        p_o, s_o = _matrix(out, "out")
+        if out.shape != (channels, depth) or out.device != dev or out.dtype is not torch.float32:
+            raise GsparseError(f"out must be fp32 of shape {(channels, depth)} on {dev}")
     p_s = _like(d_status, torch.int32, (1,), dev, "d_status")
     dt = _DTYPES[dout.dtype]
     workspace, p_ws, n_ws = _scratch(workspace, dout, "gsparse_linear_q8_grad_weight_workspace_size", p_g % 16, dt, s_g, tokens,
