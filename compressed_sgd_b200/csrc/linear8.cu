@@ -1032,7 +1032,8 @@ CUtensorMapDataType map_type(int32_t dtype) {
 }
 
 // How the tiles of D are shared out: whole tiles in waves over the pairs of SMs; what is left over is split along s.
-constexpr int kBand = 8;
+// Tiles side by side: 16 of the product (8192 x 32003 x 4096: 754 us, 8: 775), 8 of the gradients (4000 x 85000 x 512: 313, 16: 318).
+constexpr int kProductBand = 16, kGradBand = 8;
 constexpr int64_t kKeep = 96 << 20;        // bytes of an operand that the second-level cache may be asked to keep (of 126 MB)
 
 Divisor divisor(int64_t by) {
@@ -1049,13 +1050,13 @@ struct Plan {
   int tiles, blocks, pairs, waves, piece, group;
 };
 
-Plan plan_of(int64_t rows, int64_t cols, int64_t blocks) {
+Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band) {
   Plan p;
   const int64_t m = rows > 0 ? cdiv(rows, kTile) : 1, n = cdiv(cols, kTile), across = m < n ? m : n, along = m < n ? n : m;
   Order& o = p.order;
   p.tiles = o.tiles = (int)(m * n);
   o.wide = m < n;
-  o.band = (int)(across < kBand ? across : kBand);
+  o.band = (int)(across < band ? across : band);
   o.bands = (int)cdiv(across, o.band);
   o.last_band = (int)(across - (int64_t)(o.bands - 1) * o.band);
   o.per_band = divisor(along * o.band);
@@ -1142,7 +1143,7 @@ struct Product {
 Product product_of(void* workspace, int64_t tokens, int64_t channels, int64_t depth) {
   Product p{};
   if (tokens <= kFewTokens) return p;
-  p.plan = plan_of(tokens, channels, cdiv(depth, 128));
+  p.plan = plan_of(tokens, channels, cdiv(depth, 128), kProductBand);
   const int64_t x = tokens * round_up(depth, 16);
   Carver c(workspace);
   p.copies = x <= kCopyBytes ? (int)min(cdiv(kCopiesBytes, x), (int64_t)p.plan.pairs) : 1;
@@ -1230,7 +1231,7 @@ Grad grad_of(void* workspace, const void* dout, int32_t dtype, int64_t dout_stri
   g.a = c.take<__nv_bfloat16>(g.copied ? g.planes * tokens * g.stride_a : 0);
   const int64_t along = weight ? tokens : channels;
   g.b = c.take<__nv_bfloat16>(along * g.stride_b);
-  const Plan p = plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64));
+  const Plan p = plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64), kGradBand);
   g.part = c.take<float>(part_entries(p));
   g.bytes = c.off + 256;
   return g;
@@ -1276,7 +1277,7 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
   // 512 products of bf16 in a row (32 accumulations) are off by 6e-7 of the result, as the 4000 of a plain fp32 sum are; gradients in
   // fp32 keep to half of that, and results of 16 bits, which are rounded to 2^-9 and 2^-12, take 2048.
   a.chunk = dtype == GSPARSE_F32 ? 4 : out_dtype == GSPARSE_F32 ? 8 : 32;
-  const Plan p = plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks);
+  const Plan p = plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks, kGradBand);
   a.keep_a = p.order.bands == 1 && !p.order.wide ? -1 : 0;    // the tiles of a row of them are under way together
   a.keep_b = along * g.stride_b * 2 <= kKeep ? 1 : 0;
   return tiles<false, WEIGHT>(a, p, g.part, out, out_stride, st);
