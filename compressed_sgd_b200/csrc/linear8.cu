@@ -336,8 +336,9 @@ __device__ __forceinline__ void put(const TileArgs& a, Way& way, int half, const
   else put_result<__half>(a, way, half, v, row, col);
 }
 
-// A part of a tile's sums, as they are: row r of slot k at row k * 256 + r of the workspace.
-__device__ __forceinline__ void put_part(const TileArgs& a, Way& way, const float* v, int64_t row, int col) {
+// A part of a tile's sums, as they are: row r of slot k at row k * 256 + r of the workspace. What lies outside D is left out.
+__device__ __forceinline__ void put_part(const TileArgs& a, Way& way, const float* v, int64_t row, int col, bool inside) {
+  if (!inside) return;
   way.next();
   into_box<float>(way.box, way.lane, 0, v);
   way.send(&a.part, col, row);
@@ -515,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
           } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
-            put_part(a, way, v, part_row, first_col + j * 32);
+            put_part(a, way, v, part_row, first_col + j * 32, row < a.rows && col + j * 32 < a.cols);
           }
         }
       }
@@ -550,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<INT>::threads
 #pragma unroll
         for (int j = 0; j < kSide / 32; ++j) {
           if (p.whole) put(a, way, j & 1, sum + j * 32, row, col + j * 32);
-          else put_part(a, way, sum + j * 32, part_row, first_col + j * 32);
+          else put_part(a, way, sum + j * 32, part_row, first_col + j * 32, row < a.rows && col + j * 32 < a.cols);
         }
       }
     }
@@ -579,12 +580,15 @@ struct JoinArgs {
   int first_tile, blocks, piece, group;
 };
 
-// The parts of a split tile added up in their order along s. A block takes 8 rows of a tile, a thread 8 entries of one row.
-template <bool INT, class T>
+// The parts of a split tile added up, along s: WARPS warps take a row of it, parts warp, warp + WARPS, ... each, 8 entries a lane.
+template <bool INT, class T, int WARPS>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
   pdl_begin();
-  const int t = blockIdx.x >> 5, tile = a.first_tile + t;
-  const int r = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
+  __shared__ uint32_t joined[WARPS > 1 ? WARPS : 1][WARPS > 1 ? kTile : 1];
+  constexpr int kRows = 8 / WARPS, kBlocks = kTile / kRows;    // rows of a block, blocks of a tile
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x / kBlocks, tile = a.first_tile + t;
+  const int r = (blockIdx.x % kBlocks) * kRows + warp / WARPS, c = lane * 8;
   const int set = t / a.group, member = t - set * a.group;
   const int64_t from = (int64_t)set * a.blocks, to = from + a.blocks;
   const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
@@ -592,30 +596,45 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   int m, n;
   place_of(tile, a.order, m, n);
   const int64_t row = (int64_t)m * kTile + r, col = (int64_t)n * kTile + c;
-  if (row >= a.rows || col >= a.cols) return;
+  if (row >= a.rows || (WARPS == 1 && col >= a.cols)) return;  // (with more warps they all do, or none)
   uint32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};     // -0 + 0 is 0: as good as the first part itself
-  for (int at = first; at <= last; at += 4) {      // four parts under way at a time
+  for (int at = first + warp % WARPS; at <= last && col < a.cols; at += 4 * WARPS) {   // four parts under way at a time
     uint4 x[4], y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (at + i > last) break;
+      if (at + i * WARPS > last) break;
       // a range that begins before this tile has it as its second
-      const int64_t slot = ((int64_t)(at + i) * a.group + member) * 2 + ((int64_t)(at + i) * a.piece < from ? 1 : 0);
+      const int64_t part = at + i * WARPS, slot = (part * a.group + member) * 2 + (part * a.piece < from ? 1 : 0);
       const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (slot * kTile + r) * kTile + c;
       x[i] = __ldg(reinterpret_cast<const uint4*>(p));
       y[i] = __ldg(reinterpret_cast<const uint4*>(p + 4));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (at + i > last) break;
+      if (at + i * WARPS > last) break;
       const uint32_t v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (INT) sum[j] += v[j];
-        else sum[j] = __float_as_uint(__uint_as_float(sum[j]) + __uint_as_float(v[j]));
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (INT) sum[k] += v[k];
+        else sum[k] = __float_as_uint(__uint_as_float(sum[k]) + __uint_as_float(v[k]));
       }
     }
   }
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) joined[warp][k * 32 + lane] = sum[k];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t v = joined[w][k * 32 + lane];
+        if constexpr (INT) sum[k] += v;
+        else sum[k] = __float_as_uint(__uint_as_float(sum[k]) + __uint_as_float(v));
+      }
+  }
+  if (col >= a.cols) return;
   T* out = static_cast<T*>(a.out) + row * a.out_stride + col;
   const float mine = INT ? __ldg(a.row_scale + row) : 1.0f;
 #pragma unroll
@@ -1045,6 +1064,9 @@ Divisor divisor(int64_t by) {
   return v;
 }
 
+// A part has at least 4 blocks (88 tokens of 8383 x 103 bf16: 14 us, with parts of 2 and each row joined by one warp 28).
+constexpr int64_t kPiece = 4;
+
 struct Plan {
   Order order;
   int tiles, blocks, pairs, waves, piece, group;
@@ -1069,7 +1091,7 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band) {
   // Where all tiles are split, pairs that take the tiles of a band side by side go through the same blocks at the same time, so that
   // the operand that they share is read from memory once.
   p.group = p.waves == 0 && o.bands == 1 && o.band < p.pairs / 2 ? o.band : 1;
-  const int64_t piece = cdiv(left / p.group * blocks, p.pairs / p.group);
+  const int64_t even = cdiv(left / p.group * blocks, p.pairs / p.group), piece = even < kPiece ? kPiece : even;
   // Splitting costs a part's way out and back, and a launch.
   p.piece = left && blocks - piece >= 24 ? (int)piece : 0;
   return p;
@@ -1097,6 +1119,14 @@ int few(const FewArgs& a, cudaStream_t st) {
 
 bool fits(int64_t rows, int64_t cols) { return cdiv(rows, kTile) * cdiv(cols, kTile) < (1ll << 30); }
 
+template <bool INT, int WARPS>
+void join_of(const JoinArgs& j, int tiles, int32_t dtype, cudaStream_t st) {
+  const dim3 grid((unsigned)(32 * WARPS * tiles));
+  if (dtype == GSPARSE_F32) launch(join_kernel<INT, float, WARPS>, grid, dim3(256), 0, st, j);
+  else if (dtype == GSPARSE_BF16) launch(join_kernel<INT, __nv_bfloat16, WARPS>, grid, dim3(256), 0, st, j);
+  else launch(join_kernel<INT, __half, WARPS>, grid, dim3(256), 0, st, j);
+}
+
 template <bool INT, bool A_ACROSS>
 int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride, cudaStream_t st) {
   a.order = p.order;
@@ -1123,10 +1153,9 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
   launch(kernel, dim3((unsigned)(2 * used)), dim3(L::threads), L::shared, st, (const TileArgs&)a);
   if (p.piece) {
     JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.order, p.waves * p.pairs, p.blocks, p.piece, p.group};
-    const dim3 grid((unsigned)(32 * (p.tiles - p.waves * p.pairs)));
-    if (dtype == GSPARSE_F32) launch(join_kernel<INT, float>, grid, dim3(256), 0, st, (const JoinArgs&)j);
-    else if (dtype == GSPARSE_BF16) launch(join_kernel<INT, __nv_bfloat16>, grid, dim3(256), 0, st, (const JoinArgs&)j);
-    else launch(join_kernel<INT, __half>, grid, dim3(256), 0, st, (const JoinArgs&)j);
+    const int parts = (int)cdiv(p.blocks, p.piece);
+    if (parts > 8) join_of<INT, 8>(j, p.tiles - p.waves * p.pairs, dtype, st);
+    else join_of<INT, 1>(j, p.tiles - p.waves * p.pairs, dtype, st);
   }
   return launch_status();
 }
