@@ -75,6 +75,7 @@ struct TileArgs {
   int chunk;                               // blocks of bf16 that are summed in the tensor core
   int pairs, waves;                        // tiles below waves * pairs are whole; the others are split
   int piece, group;                        // blocks of a pair's part of the split tiles (0: none are split); see Plan
+  int stacked;                             // the planes are rows of A: every tile is a part
   int copies;                              // of the integer A, one after another
   int keep_a, keep_b;                      // how long the second-level cache should keep the operands' lines
   int out_dtype;
@@ -220,7 +221,7 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part
     p.to = (int)(to - t * a.blocks);
     p.slot = pair * 2 + k;
   }
-  p.whole = p.to - p.from == a.blocks;
+  p.whole = p.to - p.from == a.blocks && !a.stacked;
   place_of(tile, a.order, p.m, p.n);
   return true;
 }
@@ -578,6 +579,7 @@ struct JoinArgs {
   int64_t out_stride, rows, cols;
   Order order;
   int first_tile, blocks, piece, group;
+  int planes, plane_rows;                  // of stacked planes: rows r, plane_rows + r, ... are added up
 };
 
 // The parts of a split tile added up, along s: WARPS warps take a row of it, parts warp, warp + WARPS, ... each, 8 entries a lane.
@@ -592,26 +594,28 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   const int set = t / a.group, member = t - set * a.group;
   const int64_t from = (int64_t)set * a.blocks, to = from + a.blocks;
   const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
-  if (first == last) return;                       // whole after all
+  if (first == last && a.planes == 1) return;      // whole after all
+  const int parts = last - first + 1, all = parts * a.planes;
   int m, n;
   place_of(tile, a.order, m, n);
   const int64_t row = (int64_t)m * kTile + r, col = (int64_t)n * kTile + c;
   if (row >= a.rows || (WARPS == 1 && col >= a.cols)) return;  // (with more warps they all do, or none)
   uint32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};     // -0 + 0 is 0: as good as the first part itself
-  for (int at = first + warp % WARPS; at <= last && col < a.cols; at += 4 * WARPS) {   // four parts under way at a time
+  for (int at = warp % WARPS; at < all && col < a.cols; at += 4 * WARPS) {   // four parts under way at a time
     uint4 x[4], y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (at + i * WARPS > last) break;
+      if (at + i * WARPS >= all) break;
       // a range that begins before this tile has it as its second
-      const int64_t part = at + i * WARPS, slot = (part * a.group + member) * 2 + (part * a.piece < from ? 1 : 0);
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (slot * kTile + r) * kTile + c;
+      const int plane = (at + i * WARPS) / parts;
+      const int64_t part = first + (at + i * WARPS - plane * parts), slot = (part * a.group + member) * 2 + (part * a.piece < from ? 1 : 0);
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (slot * kTile + plane * a.plane_rows + r) * kTile + c;
       x[i] = __ldg(reinterpret_cast<const uint4*>(p));
       y[i] = __ldg(reinterpret_cast<const uint4*>(p + 4));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (at + i * WARPS > last) break;
+      if (at + i * WARPS >= all) break;
       const uint32_t v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -1072,7 +1076,7 @@ struct Plan {
   int tiles, blocks, pairs, waves, piece, group;
 };
 
-Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band) {
+Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band, bool stacked = false) {
   Plan p;
   const int64_t m = rows > 0 ? cdiv(rows, kTile) : 1, n = cdiv(cols, kTile), across = m < n ? m : n, along = m < n ? n : m;
   Order& o = p.order;
@@ -1092,8 +1096,8 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band) {
   // the operand that they share is read from memory once.
   p.group = p.waves == 0 && o.bands == 1 && o.band < p.pairs / 2 ? o.band : 1;
   const int64_t even = cdiv(left / p.group * blocks, p.pairs / p.group), piece = even < kPiece ? kPiece : even;
-  // Splitting costs a part's way out and back, and a launch.
-  p.piece = left && blocks - piece >= 24 ? (int)piece : 0;
+  // Splitting costs a part's way out and back, and a launch. (Stacked planes are added up in any case.)
+  p.piece = stacked ? (int)(piece < blocks ? piece : blocks) : left && blocks - piece >= 24 ? (int)piece : 0;
   return p;
 }
 
@@ -1152,8 +1156,13 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
   const int used = p.piece || p.waves ? p.pairs : p.tiles;
   launch(kernel, dim3((unsigned)(2 * used)), dim3(L::threads), L::shared, st, (const TileArgs&)a);
   if (p.piece) {
-    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.order, p.waves * p.pairs, p.blocks, p.piece, p.group};
-    const int parts = (int)cdiv(p.blocks, p.piece);
+    JoinArgs j{part, a.row_scale, a.col_scale, out, out_stride, a.rows, a.cols, p.order, p.waves * p.pairs, p.blocks, p.piece, p.group, 1, 0};
+    if (a.stacked) {
+      j.planes = a.stacked;
+      j.rows = a.rows / a.stacked;
+      j.plane_rows = (int)j.rows;
+    }
+    const int parts = (int)cdiv(p.blocks, p.piece) * j.planes;
     if (parts > 8) join_of<INT, 8>(j, p.tiles - p.waves * p.pairs, dtype, st);
     else join_of<INT, 1>(j, p.tiles - p.waves * p.pairs, dtype, st);
   }
@@ -1236,6 +1245,8 @@ int few_gradient(bool weight, FewGradArgs a, int32_t dtype, void* out, int32_t o
 // A gradient's operands in the workspace: dout in planes of bf16 where it is not bf16 rows at 16-byte boundaries already, and the
 // values of the rows in 8 bits.
 struct Grad {
+  Plan plan;
+  bool stacked;
   int planes;
   bool copied;
   int64_t stride8, stride_a, stride_b;
@@ -1260,7 +1271,10 @@ Grad grad_of(void* workspace, const void* dout, int32_t dtype, int64_t dout_stri
   g.a = c.take<__nv_bfloat16>(g.copied ? g.planes * tokens * g.stride_a : 0);
   const int64_t along = weight ? tokens : channels;
   g.b = c.take<__nv_bfloat16>(along * g.stride_b);
-  const Plan p = plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64), kGradBand);
+  // The planes of few tokens as rows of one tile: the weights are read once, not once a plane.
+  g.stacked = !weight && g.planes > 1 && g.planes * tokens <= kTile && cdiv(depth, kTile) <= sm_count() / 2;
+  const Plan& p = g.plan = g.stacked ? plan_of(g.planes * tokens, depth, cdiv(along, 64), kGradBand, true)
+                                     : plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64), kGradBand);
   g.part = c.take<float>(part_entries(p));
   g.bytes = c.off + 256;
   return g;
@@ -1294,19 +1308,20 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
   else if (dtype == GSPARSE_F16) launch(operands_kernel<__half, 2>, grid, dim3(256), 0, st, (const OperandArgs&)o);
   else launch(operands_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, (const OperandArgs&)o);
   TileArgs a{};
-  if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.copied ? g.a : dout, channels, tokens, g.copied ? g.stride_a : dout_stride,
-              WEIGHT ? 64 : 128, g.planes) ||
+  if (!map_of(&a.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.copied ? g.a : dout, channels, g.stacked ? g.planes * tokens : tokens,
+              g.copied ? g.stride_a : dout_stride, WEIGHT ? 64 : 128, g.stacked ? 1 : g.planes) ||
       !map_of(&a.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.b, depth, along, g.stride_b, 64))
     return GSPARSE_ERR_CUDA;
   a.d_status = d_status;
-  a.rows = WEIGHT ? channels : tokens;
+  a.stacked = g.stacked ? g.planes : 0;
+  a.rows = WEIGHT ? channels : g.stacked ? g.planes * tokens : tokens;
   a.cols = depth;
   a.plane_blocks = (int)cdiv(along, 64);
   a.out_dtype = out_dtype;
   // 512 products of bf16 in a row (32 accumulations) are off by 6e-7 of the result, as the 4000 of a plain fp32 sum are; gradients in
   // fp32 keep to half of that, and results of 16 bits, which are rounded to 2^-9 and 2^-12, take 2048.
   a.chunk = dtype == GSPARSE_F32 ? 4 : out_dtype == GSPARSE_F32 ? 8 : 32;
-  const Plan p = plan_of(a.rows, depth, (int64_t)g.planes * a.plane_blocks, kGradBand);
+  const Plan& p = g.plan;
   a.keep_a = p.order.bands == 1 && !p.order.wide ? -1 : 0;    // the tiles of a row of them are under way together
   a.keep_b = along * g.stride_b * 2 <= kKeep ? 1 : 0;
   return tiles<false, WEIGHT>(a, p, g.part, out, out_stride, st);
