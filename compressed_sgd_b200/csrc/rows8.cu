@@ -40,7 +40,9 @@ template <> struct Type<__half> {
 
 // How a row's entries are shared out. kVectors: every row starts at a 16-byte boundary and is whole vectors. kShifted: rows start
 // anywhere, but all matrices' rows at the same place between two boundaries; vectors lie between boundaries, those at the row's ends
-// are read and written entry by entry. kEntries: rows of any alignment, entry by entry.
+// are read and written entry by entry. Rows in 8 bits start at boundaries of their own, so a group of their bytes takes a vector's end
+// and the next one's start: a warp takes 31 vectors, and its last lane holds the next warp's first once more, for its bytes.
+// kEntries: rows of any alignment, entry by entry.
 enum { kVectors, kShifted, kEntries };
 
 // A thread's E entries of a row of `depth`, vector after vector (entry after entry), thread after thread. `off`: the row's start
@@ -50,7 +52,12 @@ struct Mine {
   static constexpr int N = MODE == kEntries ? 1 : Type<T>::N;
   int tid, threads, depth, off;
 
-  __device__ __forceinline__ int first(int j) const { return (j * threads + tid) * N - (MODE == kShifted ? off : 0); }
+  __device__ __forceinline__ int first(int j) const {
+    if constexpr (MODE == kShifted) return (j * (threads / 32 * 31) + tid - (tid >> 5)) * N - off;
+    return (j * threads + tid) * N;
+  }
+  // Whether this thread's entries are its own, and not the next warp's.
+  __device__ __forceinline__ bool own() const { return MODE != kShifted || (tid & 31) < 31; }
   __device__ __forceinline__ bool whole(int at) const { return MODE == kShifted ? at >= 0 && at + N <= depth : at < depth; }
   __device__ __forceinline__ bool none(int at) const { return at >= depth || (MODE == kShifted && at + N <= 0); }
   __device__ __forceinline__ bool in(int at) const { return at < depth && (MODE != kShifted || at >= 0); }
@@ -105,6 +112,7 @@ struct Mine {
   }
 
   __device__ __forceinline__ void write(T* row, const Raw& raw) const {
+    if (!own()) return;
 #pragma unroll
     for (int j = 0; j < E / N; ++j) {
       const int at = first(j);
@@ -163,6 +171,14 @@ struct Mine {
             const float4 f = __ldg(reinterpret_cast<const float4*>(w + at + i));
             v[j * N + i] = f.x; v[j * N + i + 1] = f.y; v[j * N + i + 2] = f.z; v[j * N + i + 3] = f.w;
           }
+        } else if (MODE == kShifted && at >= 3 && at + N + 3 <= depth && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+          // N floats from anywhere out of whole vectors; the place is the row's
+          float f[N + 4];
+          const int d = at & 3;
+#pragma unroll
+          for (int i = 0; i < N + 4; i += 4) *reinterpret_cast<float4*>(f + i) = __ldg(reinterpret_cast<const float4*>(w + at - d + i));
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[j * N + i] = d == 0 ? f[i] : d == 1 ? f[i + 1] : d == 2 ? f[i + 2] : f[i + 3];
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) v[j * N + i] = in(at + i) ? w[at + i] : 0.0f;
@@ -193,26 +209,16 @@ struct Mine {
         if constexpr (N == 8) *reinterpret_cast<uint2*>(out + at) = make_uint2(four(0), four(4));
         else *reinterpret_cast<uint32_t*>(out + at) = four(0);
       } else {
-        // The row's groups of N bytes between boundaries take this vector's last N - off entries and the next one's first: the next
-        // lane's, but for the warp's last lane, which writes its own alone, as the first lane does with what the last one lacks.
-        const int lane = threadIdx.x & 31;
-        uint64_t mine = N == 8 ? (uint64_t)four(0) | (uint64_t)four(N == 8 ? 4 : 0) << 32 : four(0);
+        const uint64_t mine = N == 8 ? (uint64_t)four(0) | (uint64_t)four(N == 8 ? 4 : 0) << 32 : four(0);
         const uint64_t next = N == 8 ? __shfl_down_sync(kFull, (unsigned long long)mine, 1) : __shfl_down_sync(kFull, (uint32_t)mine, 1);
-        const int group = at + off;                // (off 0: the whole of this vector)
-        if (off && lane == 0) {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (i < off && in(at + i)) out[at + i] = (int8_t)(mine >> (8 * i));
-        }
         const uint64_t both = mine >> (8 * off) | (off ? next << (8 * (N - off)) : 0);
-        const int have = off && lane == 31 ? N - off : N;
-        if (have == N && group + N <= depth) {
+        const int group = at + off;
+        if (!own() || group >= depth) continue;    // (after the exchange)
+        if (group + N <= depth) {
           if constexpr (N == 8) *reinterpret_cast<uint64_t*>(out + group) = both;
           else *reinterpret_cast<uint32_t*>(out + group) = (uint32_t)both;
         } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (i < have && group + i < depth) out[group + i] = (int8_t)(both >> (8 * i));
+          for (int i = 0; group + i < depth; ++i) out[group + i] = (int8_t)(both >> (8 * i));
         }
       }
     }
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(MOST, MODE != kEntries && MOST == 512 ? 2 : 1)
     double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < E; ++i) ss = __fma_rn((double)v[i], (double)v[i], ss);
-    ss = warp_sum(ss);
+    ss = warp_sum(mine.own() ? ss : 0.0);
     if (!one) {
       if (lane == 0) sums[warp] = ss;
       __syncthreads();
@@ -438,9 +444,10 @@ __global__ void __launch_bounds__(256) dequant_shifted_kernel(const int8_t* q, i
     };
     if (at < depth) {
       const uint64_t b = off ? group(at + off - N) >> (8 * (N - off)) | group(at + off) << (8 * off) : group(at);
+      const uint32_t half[2] = {(uint32_t)b, (uint32_t)(b >> 32)};
       union { uint4 vec; T one[N]; } e;
 #pragma unroll
-      for (int k = 0; k < N; ++k) e.one[k] = Type<T>::put((float)(int8_t)(b >> (8 * k)) * s);
+      for (int k = 0; k < N; ++k) e.one[k] = Type<T>::put((float)(int8_t)(half[k / 4] >> (8 * (k % 4))) * s);
       if (at >= 0 && at + N <= depth) *reinterpret_cast<uint4*>(to + at) = e.vec;
       else {
 #pragma unroll
@@ -583,13 +590,13 @@ bool matrix(const void* p, int64_t stride, int32_t dtype, int64_t rows, int64_t 
 
 // Warps of a row and entries a thread: one warp while 16 entries a lane hold the row, then 16 entries a thread; the longest rows
 // in 8 bits without a norm, 32 (more in registers with a norm's weights beside them would spill). `more`: places that a shifted row
-// takes before its first entry.
+// takes before its first entry; its warps have 31 lanes.
 struct Shape { int warps, entries; };
 Shape shape_of(int64_t depth, int more = 0) {
-  const int64_t places = depth + more;
-  if (places <= 512) return {1, places <= 256 ? 8 : 16};
-  const int e = places <= GSPARSE_MAX_NORM_DEPTH ? 16 : 32;
-  return {(int)cdiv(places, 32 * e), e};
+  const int64_t places = depth + more, lanes = more ? 31 : 32;
+  if (places <= lanes * 16) return {1, places <= lanes * 8 ? 8 : 16};
+  const int e = places <= 32 * lanes * 16 ? 16 : 32;
+  return {(int)cdiv(places, lanes * e), e};
 }
 
 template <class T, int MODE, bool NORM>
@@ -626,8 +633,10 @@ int rows_by_type(int32_t dtype, RowArgs& a, const Places& p, cudaStream_t st) {
   const int n = 16 / (int)size_of(dtype);
   const bool vectors = p.boundaries() && a.depth % n == 0 && (!a.weight || aligned16(a.weight));
   Shape s = shape_of(a.depth, vectors || !p.same ? 0 : n - 1);
-  // (the longest rows of their kernels leave no place for a shift)
-  const int mode = vectors ? kVectors : p.same && s.warps <= 32 && (!NORM || s.entries <= 16) ? kShifted : kEntries;
+  // The longest rows of their kernels leave no place for a shift; and with the sum in the place of x or residual a warp's last lane
+  // might find the next warp's sum there.
+  const bool in_place = a.h && (a.h == a.x || a.h == a.residual);
+  const int mode = vectors ? kVectors : p.same && s.warps <= 32 && (!NORM || s.entries <= 16) && !in_place ? kShifted : kEntries;
   if (mode == kEntries) s = shape_of(a.depth);
   a.warps = s.warps;
   if (dtype == GSPARSE_F32) rows_by_mode<float, NORM>(a, s, mode, st);
