@@ -782,7 +782,9 @@ template <class T> __device__ __forceinline__ void put_as(T* p, float v) {
 // weights pass once, as they are, a step ahead, and the gradients' few entries times their scales come by way of shared memory.
 constexpr int kFewChannels = 32;           // of a step of a block
 constexpr int kFewColumns = 256;
-constexpr int64_t kFewBlocks = 2, kFewWeightBlocks = 12;   // of an SM
+// Blocks of an SM: more of them make more parts of dx to join (8 tokens of 85000 x 512: 33 us with 2, 39 with 4), or keep more rows of
+// dweight on their way (3 tokens of 67555 x 1078: 77 us with 4, 70 with 8, 63 with 16; 8 tokens of 85000 x 512: 39, 42, 43).
+constexpr int64_t kFewBlocks = 2, kFewWeightBlocks = 12;
 
 template <class T, int TOKENS>
 __global__ void __launch_bounds__(256) few_input_kernel(const __grid_constant__ FewGradArgs a) {
@@ -1057,7 +1059,9 @@ CUtensorMapDataType map_type(int32_t dtype) {
 // How the tiles of D are shared out: whole tiles in waves over the pairs of SMs; what is left over is split along s.
 // Tiles side by side: 16 of the product (8192 x 32003 x 4096: 754 us, 8: 775), 8 of the gradients (4000 x 85000 x 512: 313, 16: 318).
 constexpr int kProductBand = 16, kGradBand = 8;
-constexpr int64_t kKeep = 96 << 20;        // bytes of an operand that the second-level cache may be asked to keep (of 126 MB)
+// Bytes of an operand that the second-level cache may be asked to keep (of 126 MB), while the other passes once: gradient by the weights
+// of 85000 x 512 over 4000 tokens 313 us, without either hint 361 (long runs).
+constexpr int64_t kKeep = 96 << 20;
 
 Divisor divisor(int64_t by) {
   Divisor v;
@@ -1096,8 +1100,9 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band, bool stacked 
   // the operand that they share is read from memory once.
   p.group = p.waves == 0 && o.bands == 1 && o.band < p.pairs / 2 ? o.band : 1;
   const int64_t even = cdiv(left / p.group * blocks, p.pairs / p.group), piece = even < kPiece ? kPiece : even;
-  // Splitting costs a part's way out and back, and a launch. (Stacked planes are added up in any case.)
-  p.piece = stacked ? (int)(piece < blocks ? piece : blocks) : left && blocks - piece >= 24 ? (int)piece : 0;
+  // Splitting costs a part's way out and back, and a launch: worth it where it saves 36 blocks (2300 x 2900 x 8192 integers, where it
+  // saves 31 of 64: 56 us split, 49 whole; 42 x 117 x 6965, 51 of 55: 11 split, 23 whole). Stacked planes are added up in any case.
+  p.piece = stacked ? (int)(piece < blocks ? piece : blocks) : left && blocks - piece >= 36 ? (int)piece : 0;
   return p;
 }
 
@@ -1107,7 +1112,8 @@ constexpr int64_t kFewTokens = 4;          // (8 tokens against 85000 x 512: 34 
 
 template <int TOKENS, int ROWS>
 void few_of(const FewArgs& a, cudaStream_t st) {
-  // Channels for fewer than 32 warps on each SM, and a depth that leaves every warp of a block something: split.
+  // Channels for fewer than 32 warps on each SM, and a depth that leaves every warp of a block something: split (a token of
+  // 1000 x 2048: 2.5 us, 3.1 without; of 85000 x 512, which is not: 10).
   const bool split = a.channels < (int64_t)ROWS * 32 * sm_count() && a.depth >= 1024;
   const dim3 grid((unsigned)cdiv(a.channels, split ? ROWS : 8 * ROWS));
   if (split) launch(few_kernel<TOKENS, ROWS, true>, grid, dim3(256), 0, st, a);
@@ -1163,6 +1169,7 @@ int tiles(TileArgs& a, const Plan& p, float* part, void* out, int64_t out_stride
       j.plane_rows = (int)j.rows;
     }
     const int parts = (int)cdiv(p.blocks, p.piece) * j.planes;
+    // (5 parts a row, 184 x 1373 x 3872 fp32: 29 us with a warp a row, 33 with eight; 33 parts, 88 x 8383 x 103: 28 and 14)
     if (parts > 8) join_of<INT, 8>(j, p.tiles - p.waves * p.pairs, dtype, st);
     else join_of<INT, 1>(j, p.tiles - p.waves * p.pairs, dtype, st);
   }
@@ -1219,6 +1226,7 @@ void few_weight_of(const FewGradArgs& a, cudaStream_t st) {
   else launch(few_weight_kernel<T, 8, VEC>, grid, dim3(256), 0, st, a);
 }
 
+// (8 tokens of 85000 x 512 bf16: dx 33 us and 64 in the tiles, dweight 42 and 38; of 1000 x 2048: 6 and 27, 8 and 12)
 constexpr int64_t kFewGradTokens = 8;
 
 int few_gradient(bool weight, FewGradArgs a, int32_t dtype, void* out, int32_t out_dtype, int64_t out_stride, float* part, cudaStream_t st) {

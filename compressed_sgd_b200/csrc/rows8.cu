@@ -655,6 +655,7 @@ void back_of(const BackArgs& a, const Shape& s, int blocks, size_t smem, cudaStr
 
 int back_groups(const Shape& s) { return s.warps == 1 ? 8 : 1; }
 
+// Rows that a group takes at least: 4000 x 512 bf16 12.4, 9.6 and 10.2 us with 1, 2 and 4 (fewer parts to join, fewer rows at a time).
 constexpr int kBackRows = 2;
 
 // Blocks of the gradient: what the SMs hold at once (about 1024 threads each), at most one a group of rows.
