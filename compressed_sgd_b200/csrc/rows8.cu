@@ -58,6 +58,8 @@ __device__ __forceinline__ void store_wide(void* p, const uint32_t* v) {
                : "memory");
 }
 
+template <int V> struct Constant { static constexpr int value = V; };
+
 // A thread's E entries of a row of `depth`, vector after vector (entry after entry), thread after thread. `off`: the row's start
 // behind a boundary, in entries (kShifted only).
 template <class T, int MODE, int E>
@@ -205,8 +207,14 @@ struct Mine {
           const int d = at & 3;
 #pragma unroll
           for (int i = 0; i < N + 4; i += 4) *reinterpret_cast<float4*>(f + i) = __ldg(reinterpret_cast<const float4*>(w + at - d + i));
+          auto take = [&](auto from) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) v[j * N + i] = d == 0 ? f[i] : d == 1 ? f[i + 1] : d == 2 ? f[i + 2] : f[i + 3];
+            for (int i = 0; i < N; ++i) v[j * N + i] = f[i + decltype(from)::value];
+          };
+          if (d == 0) take(Constant<0>());
+          else if (d == 1) take(Constant<1>());
+          else if (d == 2) take(Constant<2>());
+          else take(Constant<3>());
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) v[j * N + i] = in(at + i) ? w[at + i] : 0.0f;
@@ -308,9 +316,9 @@ __device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float
   const float hi = __fmul_rn(v, rw);
   const float lo = __fmaf_rn(v, rw_lo, __fmaf_rn(v, rw, -hi));
   const float t = hi * up;
-  const float m = t + kRound;
-  const float d = __fmaf_rn(lo, up, t - (m - kRound));       // the difference is exact
-  return m + ((d + kRound) - kRound);                        // -1, 0 or 1 more
+  const float m = t + kRound, f = t - (m - kRound);          // within a half, exact
+  // past a half with the small part? The distances to it are exact, so the signs of these sums are.
+  return m + (__fmaf_rn(lo, up, f - 0.5f) > 0.0f ? 1.0f : __fmaf_rn(lo, up, f + 0.5f) < 0.0f ? -1.0f : 0.0f);
 }
 
 // One pass over the rows: the sum with the residual, the norm, the 8 bits. A row stays in its threads' registers.
@@ -319,7 +327,7 @@ __device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float
 // the middle between two integers (one of 2^13) are worked out again in two parts. All of them in two parts, with divisions and roots in
 // 64 bits: 92 against 38 us for 8192 x 4096 bf16 with the residual (235 MB, 36 us at the measured copy bandwidth).
 template <class T, int MODE, int E, bool NORM, int MOST>
-__global__ void __launch_bounds__(MOST, MODE != kEntries && MOST == 512 ? 2 : 1) rows_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 : MOST == 512 ? 2 : 1) rows_kernel(const __grid_constant__ RowArgs a) {
   pdl_begin();
   __shared__ double sums[kMostThreads / 32];
   __shared__ uint32_t tops[kMostThreads / 32];
@@ -653,12 +661,19 @@ Shape shape_of(int64_t depth, int more = 0) {
   return {(int)cdiv(places, lanes * e), e};
 }
 
+// Whether rows of 9 to 12 warps are held to the registers of three blocks on an SM (5480 x 5344 bf16: 54 us, 65 with two; 5000 x 5120 fp32,
+// which spills then: 71, 68).
+template <class T, int MODE, bool NORM>
+constexpr bool kThree = NORM && MODE != kEntries && sizeof(T) == 2;
+
 template <class T, int MODE, bool NORM>
 void rows_of(const RowArgs& a, const Shape& s, cudaStream_t st) {
   const dim3 grid((unsigned)(s.warps == 1 ? cdiv(a.rows, kRowsPerBlock) : a.rows)), block(s.warps == 1 ? kRowsPerBlock * 32 : s.warps * 32);
   if (s.entries == 8) {
     if constexpr (MODE != kWide) launch(rows_kernel<T, MODE, 8, NORM, 512>, grid, block, 0, st, a);
-  } else if (s.entries == 16 && s.warps <= 16) launch(rows_kernel<T, MODE, 16, NORM, 512>, grid, block, 0, st, a);
+  } else if (s.entries == 16 && kThree<T, MODE, NORM> && s.warps > 8 && s.warps <= 12)
+    launch(rows_kernel<T, MODE, 16, NORM, kThree<T, MODE, NORM> ? 384 : 512>, grid, block, 0, st, a);
+  else if (s.entries == 16 && s.warps <= 16) launch(rows_kernel<T, MODE, 16, NORM, 512>, grid, block, 0, st, a);
   else if (s.entries == 16) launch(rows_kernel<T, MODE, 16, NORM, 1024>, grid, block, 0, st, a);
   else if constexpr (!NORM) {
     if (MODE == kWide && s.warps <= 8) launch(rows_kernel<T, MODE, 32, NORM, MODE == kWide ? 256 : 1024>, grid, block, 0, st, a);

@@ -235,6 +235,21 @@ def test_quantize_rows_between_boundaries(dtype, rows, depth):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,depth", [(16384, 2048), (30000, 200), (40000, 333)])
+def test_norm_borders(dtype, rows, depth):
+    """Millions of entries, some of them within 10^-8 steps of a border: 64 bits on the GPU (2^-38, as above)."""
+    gen = torch.Generator(device="cuda")
+    for seed in range(3):
+        gen.manual_seed(seed)
+        x, res = (torch.randn(rows, depth, device="cuda", generator=gen).to(TYPES[dtype]) for _ in range(2))
+        w = 1 + 0.2 * torch.randn(depth, device="cuda", generator=gen)
+        r = gs.rms_norm(x, w, res, eps=1e-5, want_q=True)
+        h = r.h.double()
+        y = h / torch.sqrt(h.square().mean(-1, keepdim=True) + float(np.float32(1e-5))) * w.double()
+        assert float(((r.q.q.double() - y / r.q.scale.double()[:, None]).abs() - 0.5).max()) <= 2.0 ** -38
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("weight_dtype", TYPES)
 @pytest.mark.parametrize("depth", [24, 1001, 2048])
 def test_norm_weight_types(dtype, weight_dtype, depth):
