@@ -1267,7 +1267,7 @@ struct Grad {
   bool stacked;
   int planes;
   bool copied;
-  int64_t stride8, stride_a, stride_b;
+  int64_t stride_a, stride_b;
   __nv_bfloat16* a;
   __nv_bfloat16* b;
   float* part;

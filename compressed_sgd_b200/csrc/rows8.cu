@@ -283,11 +283,13 @@ struct RowArgs {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); }
 
+constexpr uint32_t kScaleBorder = 0x7e0000u;       // the significand's bits of 127 * 2^e
+
 // The exponent of the scale of a row whose largest magnitude has these (finite) bits.
 __device__ __forceinline__ int scale_exponent(uint32_t top) {
   // top = m 2^(k - 127) with 1 <= m < 2: 127 / 64 is the border of m. What is below 2^-119 takes the smallest scale.
   const int k = (int)(top >> 23);
-  const int e = k - 127 - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  const int e = k - 127 - 6 + ((top & 0x7fffffu) > kScaleBorder ? 1 : 0);
   return e < -126 ? -126 : e > 121 ? 121 : e;     // 121: 64 * 2^122 is no fp32 number
 }
 
@@ -309,13 +311,18 @@ __device__ __forceinline__ float larger(float a, float b) {
 
 constexpr float kRound = 12582912.0f;              // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
 
-// An entry's number of steps, v r w / 2^e, in two parts (good to about 2^-45 of it), rounded: what the formula gives in 64 bits.
-__device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float w, float up) {
+// v r w in two parts, good to about 2^-45 of it.
+__device__ __forceinline__ float2 in_parts(float v, float r_hi, float r_lo, float w) {
   const float rw = __fmul_rn(r_hi, w);
   const float rw_lo = __fmaf_rn(r_lo, w, __fmaf_rn(r_hi, w, -rw));
   const float hi = __fmul_rn(v, rw);
-  const float lo = __fmaf_rn(v, rw_lo, __fmaf_rn(v, rw, -hi));
-  const float t = hi * up;
+  return make_float2(hi, __fmaf_rn(v, rw_lo, __fmaf_rn(v, rw, -hi)));
+}
+
+// An entry's number of steps, v r w / 2^e, rounded: what the formula gives in 64 bits.
+__device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float w, float up) {
+  const float2 y = in_parts(v, r_hi, r_lo, w);
+  const float t = y.x * up, lo = y.y;
   const float m = t + kRound, f = t - (m - kRound);          // within a half, exact
   // past a half with the small part? The distances to it are exact, so the signs of these sums are.
   return m + (__fmaf_rn(lo, up, f - 0.5f) > 0.0f ? 1.0f : __fmaf_rn(lo, up, f + 0.5f) < 0.0f ? -1.0f : 0.0f);
@@ -325,7 +332,7 @@ __device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float
 //
 // An entry's steps t come from three fp32 roundings, so they are off by less than 2^-15: only those that lie closer than 2^-14 to
 // the middle between two integers (one of 2^13) are worked out again in two parts. All of them in two parts, with divisions and roots in
-// 64 bits: 92 against 38 us for 8192 x 4096 bf16 with the residual (235 MB, 36 us at the measured copy bandwidth).
+// 64 bits: 92 against 52 us for 8192 x 4096 bf16 with the residual (235 MB, 36 us at the measured copy bandwidth).
 template <class T, int MODE, int E, bool NORM, int MOST>
 __global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 : MOST == 512 ? 2 : 1) rows_kernel(const __grid_constant__ RowArgs a) {
   pdl_begin();
@@ -395,6 +402,24 @@ __global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 :
     bits = __reduce_max_sync(kFull, lane < a.warps ? tops[lane] : 0u);
   }
   const bool fine = bits < 0x7f800000u;            // no infinity, no NaN
+  if constexpr (NORM) {
+    // The largest entry at the border between two scales, up to its roundings: whether one is above it, in two parts.
+    if (fine && (bits & 0x7fffffu) - (kScaleBorder - 4) <= 8u) {
+      const uint32_t at = (bits & 0x7f800000u) | kScaleBorder;
+      const float border = __uint_as_float(at);
+      float w[E];
+      mine.load_any(w, a.weight, a.weight_dtype);
+      mine.numbers(v, raw);
+      bool over = false;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float2 p = in_parts(fabsf(v[i]), r_hi, r_lo, fabsf(w[i]));
+        over = over || (p.x - border) + p.y > 0.0f;            // (of entries near the border the difference is exact)
+      }
+      over = one ? __any_sync(kFull, over) : __syncthreads_or(over);
+      bits = at + (over ? 1u : 0u);
+    }
+  }
   const int e = fine ? scale_exponent(bits) : 0;
   const float up = power(-e);                      // -121 <= -e <= 126
   if (mine.tid == 0) a.scale[row] = fine ? power(e) : __int_as_float(0x7fc00000);

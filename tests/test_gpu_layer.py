@@ -235,6 +235,26 @@ def test_quantize_rows_between_boundaries(dtype, rows, depth):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("depth", [8, 13, 700])
+def test_norm_scales_at_their_border(dtype, depth):
+    """The largest entry a step of fp32 or two from 127 * 2^e, on either side: the scale is the formula's."""
+    rng = np.random.default_rng(124)
+    for k in range(40):
+        x = rng.normal(size=(1, depth)).astype(np.float32)
+        x[0, depth // 2] = 2.0 + 6.0 * rng.random()
+        t = dev(x, TYPES[dtype])
+        h = f64(t)
+        rstd = 1.0 / np.sqrt(np.mean(h * h) + float(np.float32(1e-6)))
+        at = np.float32(127 * 2.0 ** rng.integers(-9, 3) / (h[0, depth // 2] * rstd))
+        for step in range(-3, 4):
+            w = np.full(depth, at / 64, np.float32)
+            w[depth // 2] = np.float32(at + step * np.spacing(at))
+            y, _ = layer.rms_norm(h, w.astype(np.float64), float(np.float32(1e-6)))
+            r = gs.rms_norm(t, dev(w), want_q=True)
+            assert float(r.q.scale[0]) == layer.scale_of(float(np.abs(y).max())), (k, step)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,depth", [(16384, 2048), (30000, 200), (40000, 333)])
 def test_norm_borders(dtype, rows, depth):
     """Millions of entries, some of them within 10^-8 steps of a border: 64 bits on the GPU (2^-38, as above)."""
