@@ -9,12 +9,11 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "tiles.cuh"
 
 namespace gs {
 namespace {
 
-constexpr int kTile = 256;                 // of a pair, both ways; a CTA loads and holds 128 rows of each operand
 constexpr int kRowBytes = 128;             // of an operand's row in a stage: 128 int8 or 64 bf16 (one swizzle atom)
 constexpr int kOperand = 128 * kRowBytes;  // bytes of one operand of one CTA in a stage
 constexpr int kBox = 32 * 128;             // a warp's part of the result on its way out: 32 rows of 128 bytes
@@ -41,25 +40,6 @@ template <bool INT> struct Layout {
 using LB = Layout<false>;
 constexpr int kMore = 216, kFewer = 72;      // registers of these and of the others, out of the 168 of the launch
 static_assert(LB::warps * 32 * kMore + 128 * kFewer <= LB::threads * 168, "");
-
-// Division of 0 <= n < 2^31 by a divisor that the host knows: d = ceil(2^(32 + shift) / divisor) with 2^(shift - 1) < divisor <= 2^shift
-// leaves the quotient exact (the excess of d, below the divisor, times n stays below 2^(32 + shift)).
-struct Divisor {
-  uint32_t by, shift;
-  uint64_t d;
-  __device__ __forceinline__ int of(int n) const {
-    // d has 33 bits: its top bit adds n itself
-    const uint32_t high = __umulhi((uint32_t)n, (uint32_t)d);
-    return (int)(((uint64_t)high + ((d >> 32) ? (uint32_t)n : 0u)) >> shift);
-  }
-};
-
-// Tile t: bands of `band` tiles of the shorter way, along the longer, so that the tiles under way at a time share rows of both operands.
-struct Order {
-  int tiles, band, last_band, bands;       // the last band's width
-  int wide;                                // the longer way is that of the columns
-  Divisor per_band, in_band, in_last;
-};
 
 struct TileArgs {
   CUtensorMap a, b, out, part;
@@ -181,50 +161,6 @@ __device__ __forceinline__ void load_columns(uint32_t (&v)[32], uint32_t at) {
 __device__ __forceinline__ void columns_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// ---- work of a pair -----------------------------------------------------------------------------------------
-
-__device__ __forceinline__ void place_of(int t, const Order& o, int& m, int& n) {
-  const int b = o.per_band.of(t), left = t - b * (int)o.per_band.by;
-  const bool last = b == o.bands - 1;
-  const int width = last ? o.last_band : o.band;
-  const int y = last ? o.in_last.of(left) : o.in_band.of(left), x = b * o.band + left - y * width;
-  m = o.wide ? x : y;
-  n = o.wide ? y : x;
-}
-
-// The i-th part of a pair's work: blocks [from, to) of a tile, and whether they are all of it (else its place among the parts).
-struct Part {
-  int m, n, from, to, slot;
-  bool whole;
-};
-
-__device__ __forceinline__ bool part_of(const TileArgs& a, int pair, int i, Part& p) {
-  int tile;
-  p.slot = 0;
-  if (i < a.waves || a.piece == 0) {
-    tile = pair + i * a.pairs;
-    if (tile >= a.order.tiles) return false;
-    p.from = 0;
-    p.to = a.blocks;
-  } else {
-    const int k = i - a.waves;                                  // a pair's range of blocks meets at most two tiles
-    const int set = pair / a.group, member = pair - set * a.group;
-    const int64_t all = (int64_t)((a.order.tiles - a.waves * a.pairs) / a.group) * a.span;
-    const int64_t first = (int64_t)set * a.piece, last = min(all, first + a.piece);
-    if (first >= last) return false;
-    const int64_t t = first / a.span + k;
-    const int64_t from = max(first, t * a.span), to = min(last, t * a.span + a.blocks);
-    if (from >= to) return false;
-    tile = a.waves * a.pairs + (int)t * a.group + member;
-    p.from = (int)(from - t * a.span);
-    p.to = (int)(to - t * a.span);
-    p.slot = pair * 2 + k;
-  }
-  p.whole = p.to - p.from == a.blocks && !a.stacked;
-  place_of(tile, a.order, p.m, p.n);
-  return true;
-}
 
 // ---- the way out --------------------------------------------------------------------------------------------
 
@@ -591,11 +527,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x / kBlocks, tile = a.first_tile + t;
   const int r = (blockIdx.x % kBlocks) * kRows + warp / WARPS, c = lane * 8;
-  const int set = t / a.group, member = t - set * a.group;
-  const int64_t from = (int64_t)set * a.span, to = from + a.blocks;
-  const int first = (int)(from / a.piece), last = (int)((to - 1) / a.piece);
-  if (first == last && a.planes == 1) return;      // whole after all
-  const int parts = last - first + 1, all = parts * a.planes;
+  const Parts parts = parts_of(t, a.blocks, a.piece, a.group, a.span);
+  if (parts.count == 1 && a.planes == 1) return;   // whole after all
+  const int all = parts.count * a.planes;
   int m, n;
   place_of(tile, a.order, m, n);
   const int64_t row = (int64_t)m * kTile + r, col = (int64_t)n * kTile + c;
@@ -606,9 +540,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (at + i * WARPS >= all) break;
-      // a range that begins before this tile has it as its second
-      const int plane = (at + i * WARPS) / parts;
-      const int64_t part = first + (at + i * WARPS - plane * parts), slot = (part * a.group + member) * 2 + (part * a.piece < from ? 1 : 0);
+      const int plane = (at + i * WARPS) / parts.count;
+      const int64_t slot = parts.slot(at + i * WARPS - plane * parts.count);
       const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (slot * kTile + plane * a.plane_rows + r) * kTile + c;
       x[i] = __ldg(reinterpret_cast<const uint4*>(p));
       y[i] = __ldg(reinterpret_cast<const uint4*>(p + 4));
@@ -1063,58 +996,6 @@ constexpr int kProductBand = 16, kGradBand = 8;
 // of 85000 x 512 over 4000 tokens 313 us, without either hint 361 (long runs).
 constexpr int64_t kKeep = 96 << 20;
 
-Divisor divisor(int64_t by) {
-  Divisor v;
-  v.by = (uint32_t)by;
-  v.shift = 0;
-  while ((1ull << v.shift) < (uint64_t)by) ++v.shift;
-  v.d = (uint64_t)((((unsigned __int128)1 << (32 + v.shift)) + by - 1) / by);
-  return v;
-}
-
-// A part has at least 4 blocks (88 tokens of 8383 x 103 bf16: 14 us, with parts of 2 and each row joined by one warp 28).
-constexpr int64_t kPiece = 4;
-
-struct Plan {
-  Order order;
-  int tiles, blocks, pairs, waves, piece, group, span;
-};
-
-Plan plan_of(int64_t rows, int64_t cols, int64_t blocks, int band, bool stacked = false) {
-  Plan p;
-  const int64_t m = rows > 0 ? cdiv(rows, kTile) : 1, n = cdiv(cols, kTile), across = m < n ? m : n, along = m < n ? n : m;
-  Order& o = p.order;
-  p.tiles = o.tiles = (int)(m * n);
-  o.wide = m < n;
-  o.band = (int)(across < band ? across : band);
-  o.bands = (int)cdiv(across, o.band);
-  o.last_band = (int)(across - (int64_t)(o.bands - 1) * o.band);
-  o.per_band = divisor(along * o.band);
-  o.in_band = divisor(o.band);
-  o.in_last = divisor(o.last_band);
-  p.blocks = (int)blocks;
-  p.pairs = sm_count() / 2;
-  p.waves = p.tiles / p.pairs;
-  const int64_t left = p.tiles - (int64_t)p.waves * p.pairs;
-  // Where all tiles are split, pairs that take the tiles of a band side by side go through the same blocks at the same time, so that
-  // the operand that they share is read from memory once.
-  p.group = p.waves == 0 && o.bands == 1 && o.band < p.pairs / 2 ? o.band : 1;
-  const int64_t even = cdiv(left / p.group * blocks, p.pairs / p.group), piece = even < kPiece ? kPiece : even;
-  // Splitting costs a part's way out and back, and a launch: worth it where it saves 36 blocks (2300 x 2900 x 8192 integers, where it
-  // saves 31 of 64: 56 us split, 49 whole; 42 x 117 x 6965, 51 of 55: 11 split, 23 whole). Stacked planes are added up in any case.
-  p.piece = stacked ? (int)(piece < blocks ? piece : blocks) : left && blocks - piece >= 36 ? (int)piece : 0;
-  // Where a whole number of parts a tile keeps four fifths of the pairs busy, the tiles are cut at the same places, and all pairs go
-  // through the same blocks at the same time: both operands are read from memory once (gradient by the input of 4000 x 85000 x 512: 296 us
-  // with 64 of 74 pairs, 333 with all and ranges that begin anywhere).
-  p.span = p.blocks;
-  const int64_t cuts = p.waves == 0 ? p.pairs / p.tiles : 0;
-  if (p.piece && cuts > 1 && cuts * p.tiles * 5 >= 4 * p.pairs && cdiv(blocks, cuts) >= kPiece) {
-    p.piece = (int)cdiv(blocks, cuts);
-    p.span = (int)(cuts * p.piece);
-  }
-  return p;
-}
-
 int64_t part_entries(const Plan& p) { return p.piece ? 2 * (int64_t)p.pairs * kTile * kTile : 0; }
 
 constexpr int64_t kFewTokens = 4;          // (8 tokens against 85000 x 512: 34 us there, 4: 16; the tiles take 17)
@@ -1198,7 +1079,7 @@ struct Product {
 Product product_of(void* workspace, int64_t tokens, int64_t channels, int64_t depth) {
   Product p{};
   if (tokens <= kFewTokens) return p;
-  p.plan = plan_of(tokens, channels, cdiv(depth, 128), kProductBand);
+  p.plan = plan_of(tokens, channels, cdiv(depth, 128), kProductBand, sm_count() / 2);
   const int64_t x = tokens * round_up(depth, 16);
   Carver c(workspace);
   p.copies = x <= kCopyBytes ? (int)min(cdiv(kCopiesBytes, x), (int64_t)p.plan.pairs) : 1;
@@ -1291,8 +1172,9 @@ Grad grad_of(void* workspace, const void* dout, int32_t dtype, int64_t dout_stri
   g.b = c.take<__nv_bfloat16>(along * g.stride_b);
   // The planes of few tokens as rows of one tile: the weights are read once, not once a plane.
   g.stacked = !weight && g.planes > 1 && g.planes * tokens <= kTile && cdiv(depth, kTile) <= sm_count() / 2;
-  const Plan& p = g.plan = g.stacked ? plan_of(g.planes * tokens, depth, cdiv(along, 64), kGradBand, true)
-                                     : plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64), kGradBand);
+  const int pairs = sm_count() / 2;
+  const Plan& p = g.plan = g.stacked ? plan_of(g.planes * tokens, depth, cdiv(along, 64), kGradBand, pairs, true)
+                                     : plan_of(weight ? channels : tokens, depth, g.planes * cdiv(along, 64), kGradBand, pairs);
   g.part = c.take<float>(part_entries(p));
   g.bytes = c.off + 256;
   return g;
