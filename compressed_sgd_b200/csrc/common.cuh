@@ -100,6 +100,10 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(p)));
 }
 
+// n entries from `at` on, read as whole groups of four (the group of the first one on, n + 4 entries in all; n a multiple of 4): whether
+// all that is read lies in [0, depth).
+__host__ __device__ constexpr bool fours_within(int at, int n, int depth) { return at >= 0 && at - (at & 3) + n + 4 <= depth; }
+
 // Upper bound search: number of entries of a[0..len) that are <= x (a ascending).
 __device__ __forceinline__ int64_t upper_bound_i64(const int64_t* a, int64_t len, int64_t x) {
   int64_t lo = 0, hi = len;

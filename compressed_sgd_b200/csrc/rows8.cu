@@ -201,7 +201,7 @@ struct Mine {
             const float4 f = __ldg(reinterpret_cast<const float4*>(w + at + i));
             v[j * N + i] = f.x; v[j * N + i + 1] = f.y; v[j * N + i + 2] = f.z; v[j * N + i + 3] = f.w;
           }
-        } else if (MODE == kShifted && at >= 3 && at + N + 3 <= depth && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+        } else if (MODE == kShifted && fours_within(at, N, depth) && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
           // N floats from anywhere out of whole vectors; the place is the row's
           float f[N + 4];
           const int d = at & 3;

@@ -6,7 +6,8 @@ import torch
 
 import compressed_sgd_b200 as gs
 from oracle import layer
-from test_gpu_layer import TYPES, close, f64, gradient, laid, quants, status_ok, sums_tolerance, untouched
+from test_gpu_layer import (TYPES, check_norm, close, dev, f64, gradient, laid, normal, quants, status_ok, sums_tolerance,
+                            untouched)
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,13 @@ def test_gradient_input_of_wide_rows(dtype, tokens, channels, depth):
     want = layer.linear_grad_input(g, wq, ws)
     planes = {"fp16": 2, "fp32": 3}[dtype]
     close(dx, want, sums_tolerance(layer.linear_grad_input(np.abs(g), np.abs(wq.astype(float)), ws), planes * channels, dtype, want, dtype), "dx")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("depth", [7, 11, 15, 1003, 1007, 4095])
+def test_norm_weight_that_ends_at_its_last_entry(dtype, depth):
+    """Contiguous rows of an odd length; behind the weight, in the same 16 bytes, stands something else."""
+    x, buf = dev(normal(202, 9, depth, scale=2.0), TYPES[dtype]), torch.full((depth + 5,), float("nan"), device="cuda")
+    w = buf[:depth]
+    w.copy_(dev(1 + 0.1 * normal(203, depth)))
+    check_norm(x, w, dtype)
