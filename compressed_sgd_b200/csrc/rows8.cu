@@ -311,7 +311,7 @@ __device__ __forceinline__ float larger(float a, float b) {
 
 constexpr float kRound = 12582912.0f;              // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
 
-// v r w in two parts, good to about 2^-45 of it.
+// v r w in two parts, good to about 2^-45 of it where far_off (below) is false.
 __device__ __forceinline__ float2 in_parts(float v, float r_hi, float r_lo, float w) {
   const float rw = __fmul_rn(r_hi, w);
   const float rw_lo = __fmaf_rn(r_lo, w, __fmaf_rn(r_hi, w, -rw));
@@ -326,6 +326,61 @@ __device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float
   const float m = t + kRound, f = t - (m - kRound);          // within a half, exact
   // past a half with the small part? The distances to it are exact, so the signs of these sums are.
   return m + (__fmaf_rn(lo, up, f - 0.5f) > 0.0f ? 1.0f : __fmaf_rn(lo, up, f + 0.5f) < 0.0f ? -1.0f : 0.0f);
+}
+
+// Rows whose r or whose entries' r v would leave the second part of in_parts (or even r w itself) below fp32's smallest steps: in 64
+// bits, entry by entry, from h as it was written or summed again. Kept apart and last, over what the others' way has written, so that
+// other rows pay for two comparisons (8192 x 4096 bf16 with the residual: 70.8 us with the reading back, 70.5 without). With ms the
+// mean square, such rows have ms + eps beyond 2^+-48 or ms below 2^-60 of it; for the others and weights of magnitudes from 2^-64 to 2^64,
+// r w is at least 2^-88 and the entries that have steps at all (2^-8 of the largest) at least 2^-102, whose last bits in two parts
+// (2^-45 of them) are 2^-147: fp32 still has those. Rows without any entry stay with the others.
+__device__ __forceinline__ bool far_off(double ms, double eps) {
+  const double t = ms + eps;
+  return ms > 0.0 && t < 0x1p1000 && !(t >= 0x1p-48 && t <= 0x1p48 && ms >= t * 0x1p-60);
+}
+
+template <class T>
+__device__ __noinline__ void far_row(const RowArgs& a, int64_t row, double r, int tid, double* tops) {
+  const int threads = a.warps * 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool one = a.warps == 1;
+  if (one) __syncwarp();
+  else __syncthreads();                            // h, y and q are written, and the sums in `tops` have been read
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const T* residual = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
+  const T* h = a.h ? static_cast<const T*>(a.h) + row * a.h_stride : nullptr;
+  auto y_of = [&](int k) {
+    const float v = h ? Type<T>::get(h[k]) : residual ? Type<T>::get(Type<T>::put(Type<T>::get(x[k]) + Type<T>::get(residual[k]))) : Type<T>::get(x[k]);
+    const float w = a.weight_dtype == GSPARSE_F32    ? static_cast<const float*>(a.weight)[k]
+                    : a.weight_dtype == GSPARSE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.weight)[k])
+                                                     : __half2float(static_cast<const __half*>(a.weight)[k]);
+    return (double)v * r * (double)w;
+  };
+  const double infinite = __longlong_as_double(0x7ff0000000000000ll);
+  double top = 0.0;
+  for (int k = tid; k < a.depth; k += threads) {
+    const double y = y_of(k);
+    if (a.y) static_cast<T*>(a.y)[row * a.y_stride + k] = Type<T>::put((float)y);
+    top = fabs(y) < infinite ? fmax(top, fabs(y)) : infinite;  // (NaN too)
+  }
+  if (!a.q) return;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, d));
+  if (!one) {
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    top = lane < a.warps ? tops[lane] : 0.0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, d));
+  }
+  const bool fine = top < infinite;
+  // as scale_exponent, of a number of 64 bits
+  const long long bits = __double_as_longlong(top);
+  int e = (int)(bits >> 52) - 1023 - 6 + ((bits & 0xfffffffffffffll) > ((long long)kScaleBorder << 29) ? 1 : 0);
+  e = !fine ? 0 : e < -126 ? -126 : e > 121 ? 121 : e;
+  if (tid == 0) a.scale[row] = fine ? power(e) : __int_as_float(0x7fc00000);
+  const double up = __longlong_as_double((long long)(1023 - e) << 52);
+  int8_t* q = a.q + row * a.q_stride;
+  for (int k = tid; k < a.depth; k += threads) q[k] = fine ? (int8_t)__double2int_rn(fmin(fmax(y_of(k) * up, -127.0), 127.0)) : 0;
 }
 
 // One pass over the rows: the sum with the residual, the norm, the 8 bits. A row stays in its threads' registers.
@@ -350,6 +405,7 @@ __global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 :
   float v[E], y[E];
   mine.fetch(raw, x);
   float r_hi = 1.0f, r_lo = 0.0f;
+  bool far = false;
   if constexpr (NORM) {
     if (a.residual) {
       mine.load(y, static_cast<const T*>(a.residual) + row * a.residual_stride);
@@ -372,10 +428,15 @@ __global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 :
       ss = lane < a.warps ? sums[lane] : 0.0;
       ss = warp_sum(ss);
     }
-    const double r = inverse_root(ss * a.inv_depth + (double)a.eps);
+    const double ms = ss * a.inv_depth, r = inverse_root(ms + (double)a.eps);
     r_hi = (float)r;
     r_lo = (float)(r - (double)r_hi);
     if (a.rstd && mine.tid == 0) a.rstd[row] = r_hi;
+    far = far_off(ms, (double)a.eps);
+    if (far) {                                     // kept for far_row: r is at least 2^-128 here, and r 2^32 has a second part
+      r_hi = (float)(r * 0x1p32);
+      r_lo = (float)(r * 0x1p32 - (double)r_hi);
+    }
 #pragma unroll
     for (int i = 0; i < E; ++i) y[i] = v[i] * (r_hi * y[i]);
     if (a.y) {
@@ -388,7 +449,10 @@ __global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 :
       }
       mine.store(static_cast<T*>(a.y) + row * a.y_stride, w);
     }
-    if (!a.q) return;
+    if (!a.q) {
+      if (far) far_row<T>(a, row, ((double)r_hi + (double)r_lo) * 0x1p-32, mine.tid, sums);
+      return;
+    }
   } else {
     M::numbers(y, raw);
   }
@@ -444,6 +508,9 @@ __global__ void __launch_bounds__(MOST, MODE == kEntries ? 1 : MOST == 384 ? 3 :
     for (int i = 0; i < E; ++i) y[i] = fminf(fmaxf(y[i], kRound - 127.0f), kRound + 127.0f);
   }
   mine.bytes(a.q + row * a.q_stride, y, fine);
+  if constexpr (NORM) {
+    if (far) far_row<T>(a, row, ((double)r_hi + (double)r_lo) * 0x1p-32, mine.tid, sums);
+  }
 }
 
 // ---- read back ------------------------------------------------------------------------------------------

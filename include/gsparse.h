@@ -540,9 +540,9 @@ int gsparse_dequantize_rows(const int8_t* q, int64_t q_stride, const float* scal
  * weight   [depth] of type weight_dtype. eps from 2^-126, finite.
  * h        NULL, or receives h; may be x or residual itself, with the same stride.
  * y        NULL, or receives y in the type dtype.
- * q, scale NULL, or receive y (before its rounding to dtype) in 8 bits; y is worked out to 2^-40 of it, so that
- *          an entry next to a border between two steps, and the row's largest next to one between two scales, fall on the
- *          side that the formula says.
+ * q, scale NULL, or receive y (before its rounding to dtype) in 8 bits; y is worked out to 2^-40 of it, whatever the size of h
+ *          and eps, for weights of 0 or from 2^-64 to 2^64 in magnitude, so that an entry next to a border between two
+ *          steps, and the row's largest next to one between two scales, fall on the side that the formula says.
  * rstd     fp32[rows] or NULL: r, for the backward call.
  * Squares are summed in 64 bits. */
 int gsparse_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
