@@ -749,16 +749,20 @@ def _new_quant(like: torch.Tensor):
     return QuantRows(q, scale), (q.data_ptr(), depth + 15 & ~15, scale.data_ptr(), rows, depth)
 
 
-# sizes depend on the shapes alone (and on whether dout's rows can be read as they are)
+# sizes depend on the shapes, on whether dout's rows can be read as they are, and on the device, whose SMs share the work
 @functools.lru_cache(maxsize=1024)
-def _layer_workspace_size(name: str, *sizes) -> int:
-    return int(getattr(lib(), name)(*sizes))
+def _layer_workspace_size(index: int, name: str, *sizes) -> int:
+    fn = getattr(lib(), name)
+    if index == _current_device():
+        return int(fn(*sizes))
+    with torch.cuda.device(index):
+        return int(fn(*sizes))
 
 
 def _scratch(workspace: Optional[torch.Tensor], like: torch.Tensor, name: str, *sizes):
     """(tensor or None, pointer, bytes): the caller's workspace, or one as large as the call asks for."""
     if workspace is None:
-        size = _layer_workspace_size(name, *sizes)
+        size = _layer_workspace_size(like.device.index, name, *sizes)
         if size == 0:
             return None, None, 0
         workspace = like.new_empty(size, dtype=torch.uint8)

@@ -230,3 +230,44 @@ def test_the_binding_takes_device_tensors_only(gs):
                  lambda: gs.linear_q8_grad_input(torch.zeros(3, 2), q), lambda: gs.linear_q8_grad_weight(torch.zeros(2, 3), q)):
         with pytest.raises(gs.GsparseError, match="CUDA"):
             call()
+
+
+class _Device:
+    """A stand-in for the switch of the current device."""
+    current = 0
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.before, _Device.current = _Device.current, self.index
+
+    def __exit__(self, *_):
+        _Device.current = self.before
+
+
+def test_workspace_sizes_are_those_of_the_tensors_device(gs, monkeypatch):
+    """Two devices with other numbers of SMs: each call gets its own device's size, whichever was asked first."""
+    class Lib:
+        @staticmethod
+        def gsparse_linear_q8_workspace_size(tokens, channels, depth):
+            return 1000 * (1 + _Device.current) + tokens
+
+    monkeypatch.setattr(gs, "lib", lambda: Lib)
+    monkeypatch.setattr(gs, "_current_device", lambda: _Device.current)
+    monkeypatch.setattr(gs.torch.cuda, "device", _Device)
+    gs._layer_workspace_size.cache_clear()
+    try:
+        class Like:
+            def __init__(self, index):
+                self.device = torch.device("cuda", index)
+
+            def new_empty(self, size, dtype):
+                return torch.empty(size, dtype=dtype)
+
+        for _ in range(2):
+            for index in (0, 1, 0):
+                assert gs._scratch(None, Like(index), "gsparse_linear_q8_workspace_size", 30, 5, 40)[2] == 1000 * (1 + index) + 30
+                assert _Device.current == 0
+    finally:
+        gs._layer_workspace_size.cache_clear()
