@@ -766,7 +766,9 @@ def _scratch(workspace: Optional[torch.Tensor], like: torch.Tensor, name: str, *
         if size == 0:
             return None, None, 0
         workspace = like.new_empty(size, dtype=torch.uint8)
-    return workspace, workspace.data_ptr(), workspace.numel()
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise GsparseError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def _dtype_code(dtype) -> int:

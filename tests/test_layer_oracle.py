@@ -271,3 +271,21 @@ def test_workspace_sizes_are_those_of_the_tensors_device(gs, monkeypatch):
                 assert _Device.current == 0
     finally:
         gs._layer_workspace_size.cache_clear()
+
+
+def test_workspaces_of_another_device_or_with_shared_entries_are_refused(gs):
+    class Like:
+        device = torch.device("cuda", 0)
+
+    class Workspace:                       # as torch shows one
+        def __init__(self, device, t):
+            self.device, self.t = torch.device(device), t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    t = torch.empty(64, dtype=torch.float32)
+    for bad in (t, Workspace("cuda:1", t), Workspace("cuda:0", t[:1].expand(1 << 20)), Workspace("cuda:0", t[::2])):
+        with pytest.raises(gs.GsparseError, match="workspace"):
+            gs._scratch(bad, Like, "gsparse_linear_q8_workspace_size", 30, 5, 40)
+    assert gs._scratch(Workspace("cuda:0", t), Like, "gsparse_linear_q8_workspace_size", 30, 5, 40)[1:] == (t.data_ptr(), 256)
