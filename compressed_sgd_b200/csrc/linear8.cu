@@ -1191,6 +1191,16 @@ bool grad_space(const void* workspace, size_t have, const void* dout, int32_t dt
   return !need || space(workspace, have, need);
 }
 
+// Blocks of 64 products that the matrix unit adds before they are rounded to the nearest: it cuts off, so that C products in a row are
+// off by about C 1.3e-9 of the sum, in one direction. A plain fp32 product's error grows with the root of the sum's length S (S = 256:
+// 2.1e-7, 1000: 5.2e-7, 4000: 1.06e-6, 2-norms against 64 bits); C keeps to it: 128 (1.8e-7) for up to 7 blocks, 256 (3.4e-7) for up
+// to 31 and for gradients in fp32, 512 (6.4e-7) for the others. Results of 16 bits take 512 at any length (4000 x 85000 x 512 bf16 by the
+// input 297 us, 291 with 2048; by the weights 1000 x 8192 x 4096 68 us with 256, 65 with 512; 500 tokens 53 with 128, 43 with 256).
+int chunk_of(int32_t dtype, int32_t out_dtype, int blocks) {
+  const int chunk = out_dtype != GSPARSE_F32 || blocks >= 32 ? 8 : blocks >= 8 ? 4 : 2;
+  return dtype == GSPARSE_F32 && chunk > 4 ? 4 : chunk;
+}
+
 template <bool WEIGHT>
 int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t* q, int64_t q_stride, const float* scale, int64_t tokens,
              int64_t channels, int64_t depth, void* out, int32_t out_dtype, int64_t out_stride, void* workspace, int32_t* d_status,
@@ -1218,9 +1228,7 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
   a.cols = depth;
   a.plane_blocks = (int)cdiv(along, 64);
   a.out_dtype = out_dtype;
-  // 512 products of bf16 in a row (32 accumulations) are off by 6e-7 of the result, as the 4000 of a plain fp32 sum are; gradients in
-  // fp32 keep to half of that, and results of 16 bits, which are rounded to 2^-9 and 2^-12, take 2048.
-  a.chunk = dtype == GSPARSE_F32 ? 4 : out_dtype == GSPARSE_F32 ? 8 : 32;
+  a.chunk = chunk_of(dtype, out_dtype, a.plane_blocks);
   const Plan& p = g.plan;
   a.keep_a = p.order.bands == 1 && !p.order.wide ? -1 : 0;    // the tiles of a row of them are under way together
   a.keep_b = along * g.stride_b * 2 <= kKeep ? 1 : 0;

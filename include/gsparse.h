@@ -577,8 +577,8 @@ int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, c
  *   dweight[n][k] = sum_t dout[t][n] x_scale_t x[t][k]   (fp32; the gradient by the weights that w stands for)
  * The 8-bit operand's values are taken as bf16 (exact where scales are powers of two, else rounded once), dout in full:
  * bf16 as it is, fp16 as the exact sum of two and fp32 of three bf16 numbers (below 2^-100 in magnitude the smaller parts
- * may be lost). Sums in fp32; the matrix unit, which rounds towards zero, adds at most 256 products of an fp32 dout, else 512 for
- * results in fp32 and 2048 for results of 16 bits, before they are added up with rounding to the nearest.
+ * may be lost). Sums in fp32; the matrix unit, which rounds towards zero, adds at most 512 products (256 of an fp32 dout; for results in
+ * fp32 also 256 of sums of up to 1984, and 128 of up to 448) before they are added up with rounding to the nearest.
  * No tokens: dweight is 0. The workspace's size depends on dout's alignment and stride. */
 size_t gsparse_linear_q8_grad_input_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride,
                                                    int64_t tokens, int64_t channels, int64_t depth);

@@ -100,3 +100,39 @@ def test_norm_of_large_rows_among_others(dtype, depth):
         for other, sc in ((b.q.q, b.q.scale), (q[:, :depth], scale)):
             assert torch.equal(other, a.q.q) and torch.equal(sc.nan_to_num(7.0), a.q.scale.nan_to_num(7.0))
         assert torch.equal(u.nan_to_num(7.0), a.h.nan_to_num(7.0)) and bool((q[:, depth:] == 0).all())
+
+
+def parts_of_a_sum(products, at):
+    """(dout's column, q's column): 2^24, then 1.5 in one of every 16 products, as many as `products` hold; at: another small one."""
+    g, q = np.zeros(products, np.float32), np.zeros(products)
+    g[5::16], q[5::16] = 1.5, 1
+    g[0], q[0] = 2.0 ** 18, 64
+    if at is not None:
+        g[at], q[at] = 2.0 ** 15, 2
+    return g, q
+
+
+# The matrix unit cuts each 1.5 off a sum of 2^24, whose last bit is 2; the sums that it gives out later are added with rounding. So no
+# more than the 1.5s of its first C products may be lost, and a last bit's half at each addition. (C goes by whole blocks of 64
+# products: 128 for up to 7 of them, 256 for up to 31. 500 products are 8 blocks, of which 15 of 16 1.5s may be lost at C = 256: 22.5.)
+@pytest.mark.parametrize("products,unit", [(300, 128), (500, 256), (600, 256), (1900, 256), (4100, 512)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_sums_leave_the_matrix_unit(dtype, products, unit):
+    g, q = parts_of_a_sum(products, None)
+    unit = min(unit, 256) if dtype == "fp32" else unit
+    tol = 1.5 * unit / 16 + products / unit + 1
+    want = float(np.sum(g.astype(np.float64) * q))
+    dout, rows = dev(g[:, None] * np.ones((1, 40)), TYPES[dtype]), gs.QuantRows(dev(q[:, None] * np.ones((1, 32)), torch.int8), torch.ones(products, device="cuda"))
+    assert float((gs.linear_q8_grad_weight(dout, rows).double() - want).abs().max()) <= tol
+    dx = gs.linear_q8_grad_input(dout.t().contiguous(), rows, dtype=torch.float32)
+    assert float((dx.double() - want).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("depth", [32, 32768])       # the latter has tiles that one pair sums from end to end
+def test_gradient_sums_of_16_bits_leave_the_matrix_unit(depth):
+    """2^24 + 2^16 lies in the middle between two bf16 numbers: 190 more, of which 48 may be lost, and it is the upper one."""
+    g, q = parts_of_a_sum(2048, 1)
+    g, q = np.concatenate([g, np.zeros(2000, np.float32)]), np.concatenate([q, np.zeros(2000)])
+    rows = gs.QuantRows(dev(q[:, None], torch.int8).expand(4048, depth).contiguous(), torch.ones(4048, device="cuda"))
+    dx = gs.linear_q8_grad_input(dev(np.ones((40, 1)) * g, torch.bfloat16), rows)
+    assert bool((dx == 2.0 ** 24 + 2.0 ** 17).all())
