@@ -136,3 +136,16 @@ def test_gradient_sums_of_16_bits_leave_the_matrix_unit(depth):
     rows = gs.QuantRows(dev(q[:, None], torch.int8).expand(4048, depth).contiguous(), torch.ones(4048, device="cuda"))
     dx = gs.linear_q8_grad_input(dev(np.ones((40, 1)) * g, torch.bfloat16), rows)
     assert bool((dx == 2.0 ** 24 + 2.0 ** 17).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("depth", [1001, 1024])
+def test_norm_weight_gradient_in_short_chains(dtype, depth):
+    """2^24 in row 0 and 0.5 in each of 2046 others. A block takes two rows, b and b + 1024: 2^24 (a half is lost) or 1. Each of the
+    join's 32 warps adds 32 blocks in four chains of 8, so the chain with the 2^24 loses up to 7 ones to its last bit of 2; the
+    joins of the chains and of the warps round 2 + 5 times by up to 1."""
+    dy = torch.full((2047, depth), 0.5, device="cuda", dtype=TYPES[dtype])
+    dy[0] = 2.0 ** 24
+    ones = torch.ones((2047, depth), device="cuda", dtype=TYPES[dtype])
+    r = gs.rms_norm_backward(ones, torch.ones(depth, device="cuda"), torch.ones(2047, device="cuda"), dy)
+    assert float((r.dweight.double() - (2.0 ** 24 + 1023)).abs().max()) <= 0.5 + 7 + 7
