@@ -149,3 +149,20 @@ def test_norm_weight_gradient_in_short_chains(dtype, depth):
     ones = torch.ones((2047, depth), device="cuda", dtype=TYPES[dtype])
     r = gs.rms_norm_backward(ones, torch.ones(depth, device="cuda"), torch.ones(2047, device="cuda"), dy)
     assert float((r.dweight.double() - (2.0 ** 24 + 1023)).abs().max()) <= 0.5 + 7 + 7
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens", [1, 2, 3, 8, 9, 50])
+def test_gradients_with_scales_that_are_no_powers_of_two(dtype, tokens):
+    """Up to 8 tokens in fp32: a rounding of the scaled factor, chains of at most 4 and 8 of each of two splits, a dozen joins; then
+    the 8-bit operand's values in fp32 (u) and bf16 (2^-8)."""
+    x, w = quants(207, tokens, 72), quants(208, 60, 72)
+    rng = np.random.default_rng(209)
+    x, w = gs.QuantRows(x.q, dev(rng.uniform(0.5, 2.0, tokens))), gs.QuantRows(w.q, dev(rng.uniform(0.5, 2.0, 60)))
+    dout = dev(gradient(210, tokens, 60), TYPES[dtype])
+    g, xq, xs, wq, ws = f64(dout), x.q.cpu().numpy(), f64(x.scale), w.q.cpu().numpy(), f64(w.scale)
+    part = 50 * U if tokens <= 8 else 2.0 ** -8 + 100 * U
+    close(gs.linear_q8_grad_weight(dout, x), layer.linear_grad_weight(g, xq, xs), part * layer.linear_grad_weight(np.abs(g), np.abs(xq.astype(float)), xs),
+          "dweight")
+    close(gs.linear_q8_grad_input(dout, w, dtype=torch.float32), layer.linear_grad_input(g, wq, ws),
+          part * layer.linear_grad_input(np.abs(g), np.abs(wq.astype(float)), ws), "dx")
