@@ -1211,7 +1211,10 @@ int gradient(const void* dout, int32_t dtype, int64_t dout_stride, const int8_t*
     return few_gradient(WEIGHT, few_grad(dout, dout_stride, q, q_stride, scale, tokens, channels, depth, WEIGHT), dtype, out, out_dtype, out_stride, g.part,
                         st);
   OperandArgs o{dout, g.a, q, scale, g.b, dout_stride, g.stride_a, tokens, channels, q_stride, g.stride_b, along, (int)depth, 0};
-  auto blocks_of = [](int64_t vectors) { return (int)(vectors < 256ll * 148 * 16 ? cdiv(vectors, 256) : 148 * 16); };
+  auto blocks_of = [](int64_t vectors) {
+    const int64_t need = cdiv(vectors, 256), most = (int64_t)sm_count() * 16;
+    return (int)(need < most ? need : most);
+  };
   if (g.copied) o.a_blocks = blocks_of(tokens * cdiv(channels, 8));
   const dim3 grid((unsigned)(o.a_blocks + blocks_of(along * cdiv(depth, 16))));
   if (dtype == GSPARSE_F32) launch(operands_kernel<float, 3>, grid, dim3(256), 0, st, (const OperandArgs&)o);

@@ -847,7 +847,7 @@ constexpr int kBackRows = 2;
 // Blocks of the gradient: what the SMs hold at once (about 1024 threads each), at most one a group of rows.
 int back_blocks(int64_t rows, const Shape& s) {
   const int groups = back_groups(s), threads = groups * s.warps * 32;
-  const int64_t most = 148 * (int64_t)(threads >= 1024 ? 1 : 1024 / threads);
+  const int64_t most = sm_count() * (int64_t)(threads >= 1024 ? 1 : 1024 / threads);
   const int64_t need = cdiv(rows, (int64_t)groups * kBackRows);
   return (int)(need < most ? need : most);
 }
@@ -857,7 +857,7 @@ void dequant_of(const int8_t* q, int64_t q_stride, const float* scale, int64_t r
   constexpr int N = Type<T>::N;
   const bool even = aligned16(out) && (rows == 1 || (out_stride * (int64_t)sizeof(T)) % 16 == 0);
   const int per = even ? (int)cdiv(depth, 16) : (int)cdiv(depth + N - 1, N);
-  const int64_t blocks = cdiv(rows * per, 256), most = 148 * (even ? 32 : 64);
+  const int64_t blocks = cdiv(rows * per, 256), most = (int64_t)sm_count() * (even ? 32 : 64);
   const dim3 grid((unsigned)(blocks < most ? blocks : most));
   if (even) launch(dequant_kernel<T>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride);
   else launch(dequant_shifted_kernel<T>, grid, dim3(256), 0, st, q, q_stride, scale, rows, depth, static_cast<T*>(out), out_stride, per);
