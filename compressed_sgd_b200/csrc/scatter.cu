@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(kCombThreads, 4) sa_combine_kernel(Lists L, in
       }
     }
     if (own >= 0) {
-      // partial mode: the worker's own sent values leave G before the combination
+      // partial mode: the worker's own sent values leave G before the combination, and after every thread has taken its part of
+      // the dense tile
+      if (dense) __syncthreads();
       const int32_t* ix = L.idx[own];
       const float* vv = L.val[own];
       const float u = (vv || !L.uni[own]) ? 0.0f : *L.uni[own];
