@@ -1194,10 +1194,11 @@ bool grad_space(const void* workspace, size_t have, const void* dout, int32_t dt
 // Blocks of 64 products that the matrix unit adds before they are rounded to the nearest: it cuts off, so that C products in a row are
 // off by about C 1.3e-9 of the sum, in one direction. A plain fp32 product's error grows with the root of the sum's length S (S = 256:
 // 2.1e-7, 1000: 5.2e-7, 4000: 1.06e-6, 2-norms against 64 bits); C keeps to it: 128 (1.8e-7) for up to 7 blocks, 256 (3.4e-7) for up
-// to 31 and for gradients in fp32, 512 (6.4e-7) for the others. Results of 16 bits take 512 at any length (4000 x 85000 x 512 bf16 by the
-// input 297 us, 291 with 2048; by the weights 1000 x 8192 x 4096 68 us with 256, 65 with 512; 500 tokens 53 with 128, 43 with 256).
+// to 31 and for gradients in fp32, 512 (6.4e-7) for the others. Results of 16 bits take 512 from 8 blocks on (4000 x 85000 x 512 bf16 by the
+// input 297 us, 291 with 2048, and 4000 x 1900 x 4096 55 us, 60 with 256; by the weights 1000 x 8192 x 4096 68 us with 256, 65 with 512; 500
+// tokens 53 with 128, 43 with 256; 2000 x 400 x 2048 by the input 12.4 with 128 as with 512).
 int chunk_of(int32_t dtype, int32_t out_dtype, int blocks) {
-  const int chunk = out_dtype != GSPARSE_F32 || blocks >= 32 ? 8 : blocks >= 8 ? 4 : 2;
+  const int chunk = blocks < 8 ? 2 : blocks < 32 && out_dtype == GSPARSE_F32 ? 4 : 8;
   return dtype == GSPARSE_F32 && chunk > 4 ? 4 : chunk;
 }
 

@@ -577,11 +577,12 @@ int gsparse_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scale, c
  *   dweight[n][k] = sum_t dout[t][n] x_scale_t x[t][k]   (fp32; the gradient by the weights that w stands for)
  * Of more than 8 tokens the 8-bit operand's values are taken as bf16 (exact where scales are powers of two, else rounded to fp32
  * and then to bf16, 2^-8 of each value at most), dout in full: bf16 as it is, fp16 as the exact sum of two and fp32 of three
- * bf16 numbers (below 2^-100 in magnitude the smaller parts may be lost). Sums in fp32; the matrix unit, which rounds towards zero, adds at most 512 products (256 of an fp32 dout; for results in
- * fp32 also 256 of sums of up to 1984, and 128 of up to 448) before they are added up with rounding to the nearest.
- * Of up to 8 tokens all is fp32: dout[t][n] w_scale_n (which has to be within fp32) or x_scale_t x[t][k] is rounded, its product with
- * the other factor is not, and sums round to the nearest. So scales that are no powers of two give results that differ by 2^-8 of
- * their terms between 8 tokens and 9; those that quantize_rows and rms_norm make do not.
+ * bf16 numbers (below 2^-100 in magnitude the smaller parts may be lost). Sums in fp32; the matrix unit, which rounds towards zero,
+ * adds at most 512 products (256 of an fp32 dout, and of sums of up to 1984 for results in fp32; 128 of sums of up to 448) before
+ * they are added up with rounding to the nearest.
+ * Of up to 8 tokens all is fp32, rounded to the nearest: dout[t][n] w_scale_n (which has to be within fp32) or x_scale_t x[t][k],
+ * times the other factor, and the sums. So scales that are no powers of two give results that differ by 2^-8 of their terms
+ * between 8 tokens and 9; those that quantize_rows and rms_norm make do not.
  * No tokens: dweight is 0. The workspace's size depends on dout's alignment and stride. */
 size_t gsparse_linear_q8_grad_input_workspace_size(const void* dout, int32_t dtype, int64_t dout_stride,
                                                    int64_t tokens, int64_t channels, int64_t depth);

@@ -138,6 +138,14 @@ def test_gradient_sums_of_16_bits_leave_the_matrix_unit(depth):
     assert bool((dx == 2.0 ** 24 + 2.0 ** 17).all())
 
 
+def test_short_gradient_sums_of_16_bits_leave_the_matrix_unit():
+    """The same with 27 more, of which 12 may be lost (C = 128)."""
+    g, q = parts_of_a_sum(300, 1)
+    rows = gs.QuantRows(dev(q[:, None] * np.ones((1, 32)), torch.int8), torch.ones(300, device="cuda"))
+    dx = gs.linear_q8_grad_input(dev(np.ones((40, 1)) * g, torch.bfloat16), rows)
+    assert bool((dx == 2.0 ** 24 + 2.0 ** 17).all())
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("depth", [1001, 1024])
 def test_norm_weight_gradient_in_short_chains(dtype, depth):
