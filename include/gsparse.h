@@ -522,8 +522,9 @@ int gsparse_distill_topk_backward(const void* logits, int32_t dtype, int64_t row
  * of what is written. Rows that start at 16-byte boundaries are fastest. 1 <= depth <= GSPARSE_MAX_DEPTH (of the norm
  * GSPARSE_MAX_NORM_DEPTH); 0 <= rows, tokens <= GSPARSE_MAX_ROWS; 1 <= channels <= GSPARSE_MAX_ROWS (and of
  * the product tokens * channels below 2^46). Outputs must not overlap inputs where nothing else is said. Sums in a fixed
- * order: the same call on the same layout gives the same bits on every run. Workspace sizes are those of the current device. A wait of the products' kernels for their copies or
- * products that gives up (about a second) raises GSPARSE_DERR_TIMEOUT; the results are then not valid.
+ * order: the same call on the same layout gives the same bits on every run. Workspace sizes are those of the current device.
+ * A wait of the products' kernels for their copies or products that gives up (about a second) raises GSPARSE_DERR_TIMEOUT;
+ * the results are then not valid.
  */
 #define GSPARSE_MAX_DEPTH (1 << 15)
 #define GSPARSE_MAX_NORM_DEPTH (1 << 14)
