@@ -333,7 +333,7 @@ __device__ __forceinline__ float steps_of(float v, float r_hi, float r_lo, float
 // other rows pay for two comparisons (8192 x 4096 bf16 with the residual: 70.8 us with the reading back, 70.5 without). With ms the
 // mean square, such rows have ms + eps beyond 2^+-48 or ms below 2^-60 of it; for the others and weights of magnitudes from 2^-64 to 2^64,
 // r w is at least 2^-88 and the entries that have steps at all (2^-8 of the largest) at least 2^-102, whose last bits in two parts
-// (2^-45 of them) are 2^-147: fp32 still has those. Rows without any entry stay with the others.
+// (2^-45 of them) are 2^-147: fp32 still has those. Rows of zeros stay with the others.
 __device__ __forceinline__ bool far_off(double ms, double eps) {
   const double t = ms + eps;
   return ms > 0.0 && t < 0x1p1000 && !(t >= 0x1p-48 && t <= 0x1p48 && ms >= t * 0x1p-60);
